@@ -208,6 +208,86 @@ int pfop_set_gemm_pairs(int32_t mode);
 int32_t pfop_qkv_row_order(int32_t Hq, int32_t Hkv, int32_t hd, int32_t with_kv, int32_t* order, int32_t cap);
 int64_t pfop_repack_q4(const void* w_host, int32_t N, int32_t K, int32_t bn, void* dst, int64_t dst_bytes);
 
+/* ---- several sequences in one call ----
+   The calls below work on rows of several sequences over the unified cache of
+   prefill_ubatch_seqs.  Unlike the calls above they only enqueue work on
+   `stream` (of the current device), allocate nothing and may be recorded
+   into a CUDA graph; arguments are checked on the host before any CUDA call.
+
+   A run is n_rows consecutive rows of one sequence that continue it at
+   position pos0; the sequence's position p lives in cache cell cell0 + p.
+   The rows of run r follow those of run r-1 in q and out (runs with
+   n_rows 0 are allowed and skipped).  K and V of the run's own rows are in
+   the cache already, at cells cell0 + pos0 .. cell0 + pos0 + n_rows - 1. */
+typedef struct pfop_attn_run {
+  int32_t n_rows;
+  int32_t pos0;
+  int32_t cell0;
+} pfop_attn_run;
+
+/* Causal GQA attention of up to 128 runs in one call: q fp16 [T][Hq*hd], T
+   the runs' rows in all, K/V fp16 [n_cells][Hkv*hd], out bf16 [T][Hq*hd]
+   (rows from T on are not touched).  Row i of a run sees its sequence's
+   positions 0 .. pos0 + i.  Cells of no run's positions 0 .. pos0 + n_rows
+   - 1 are never used, whatever they hold; the runs' own cells must hold
+   finite values.  Probabilities are rounded to fp16 before P V, sums and
+   states are fp32.  A row's bits depend on its position, its keys and the
+   shapes of the call's runs, not on the other runs' values; a repeated call
+   gives the same bits.
+   work_dev: device scratch of the call, 256-byte aligned, work_bytes of it
+   at least pfop_attention_work_bytes of the runs; its first 256 bytes must
+   be zero before its first call.  Calls that share a scratch must not
+   overlap on the GPU (one stream, or events; two recorded graphs that share
+   one may not run at once).
+   PF_E_ARG: hd other than 64 or 256; n_head not a multiple of n_head_kv
+   with a group size dividing 16; more than 128 runs or 2^20 rows; a run
+   past n_cells; q, k, v, out not 16-byte aligned; a scratch too small. */
+int pfop_attention_packed(const void* q_dev, const void* k_dev, const void* v_dev, int64_t n_cells, int32_t Hq,
+                          int32_t Hkv, int32_t hd, const pfop_attn_run* runs, int32_t n_runs, void* out_dev,
+                          void* work_dev, int64_t work_bytes, void* stream);
+
+/* Attention of drafted token trees over the runs' caches (one row per
+   drafted token): like pfop_attention_packed, but row i of a run sees its
+   sequence's positions 0 .. pos0 - 1 (the context) and those drafted tokens
+   j of its run (position pos0 + j) whose bit j % 64 of
+   mask_dev[row * mask_words + j / 64] is set.  mask_dev: uint64, device, a
+   row for every row of q; mask_words 1 .. 4 (at most 256 drafted tokens a
+   run, n_rows <= 64 * mask_words); bits from n_rows on are ignored.  A row
+   that sees nothing (pos0 0 and no bit set) gives zeros.  One row with its
+   own bit set is a plain decoding step. */
+int pfop_attention_tree(const void* q_dev, const void* k_dev, const void* v_dev, int64_t n_cells, int32_t Hq,
+                        int32_t Hkv, int32_t hd, const pfop_attn_run* runs, int32_t n_runs, const uint64_t* mask_dev,
+                        int32_t mask_words, void* out_dev, void* work_dev, int64_t work_bytes, void* stream);
+
+/* Scratch bytes that either call needs for these runs on the current device
+   (host only; without a device, as on a GB300), or PF_E_ARG. */
+int64_t pfop_attention_work_bytes(int32_t Hq, int32_t Hkv, int32_t hd, const pfop_attn_run* runs, int32_t n_runs);
+
+/* Wait for `stream` and report whether a call using this scratch gave up a
+   bounded wait (PF_E_DEVICE_TIMEOUT: its results are invalid); clears the
+   report. */
+int pfop_attention_status(void* work_dev, void* stream);
+
+/* Log probabilities over a vocabulary, for every row of logits [rows][ld]
+   (the first `vocab` values of each row; ltype PF_L_F32 or PF_L_BF16):
+     logp[r]    = x[tok[r]] - logsumexp(x)     (tok, logp NULL: skipped)
+     entropy[r] = -sum_v p[v] log p[v]         (NULL: skipped)
+     top_id[r][i], top_logp[r][i], i < n_top: the n_top most probable tokens
+       and their log probabilities, most probable first, the lower id first
+       where two are equal (n_top 0: skipped; at most 32, at most vocab).
+   All outputs are fp32 (top_id int32), rows dense.  -inf logits are allowed
+   (probability 0).  A token outside [0, vocab) gives logp NaN.  A row
+   without a distribution (a NaN, +inf, or only -inf) gives NaN throughout
+   and top_id -1.  Enqueue only, no scratch, recordable.
+   PF_E_ARG: rows < 0, vocab < 1 or >= 2^30, ld < vocab, n_top outside
+   [0, min(32, vocab)], missing or misaligned buffers (logits to their
+   element, outputs to 4 bytes). */
+#define PF_L_F32 0
+#define PF_L_BF16 1
+int pfop_logprobs(int32_t ltype, const void* logits_dev, int64_t ld, int32_t rows, int32_t vocab,
+                  const int32_t* tok_dev, int32_t n_top, float* logp_dev, float* entropy_dev, int32_t* top_id_dev,
+                  float* top_logp_dev, void* stream);
+
 /* Last error message of a pfop_* call on this thread. */
 const char* pfop_last_error(void);
 

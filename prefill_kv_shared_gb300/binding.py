@@ -34,6 +34,8 @@ PF_PRUNE_OFF_PLAIN = 2
 
 PF_W_F32 = 0
 PF_W_Q4_0 = 2
+PF_L_F32 = 0
+PF_L_BF16 = 1
 PF_FFN_GEGLU = 0
 PF_FFN_SWIGLU = 1
 
@@ -49,7 +51,8 @@ EXPORTS = (
     "kv_save_file", "kv_load_file", "prefill_kv_file_check", "pfop_linear_row", "prefill_set_output",
     "pfop_linear_wait_test", "prefill_ubatch_seqs", "prefill_seq_n_pos", "prefill_seq_reset",
     "prefill_graph_capture", "prefill_graph_launch", "pfop_set_gemm_pairs", "pfop_qkv_row_order",
-    "pfop_repack_q4",
+    "pfop_repack_q4", "pfop_attention_packed", "pfop_attention_tree", "pfop_attention_work_bytes",
+    "pfop_attention_status", "pfop_logprobs",
 )
 
 
@@ -88,6 +91,10 @@ class LayerWeights(C.Structure):
 
 class SeqRun(C.Structure):
     _fields_ = [("seq_id", C.c_int32), ("n_tokens", C.c_int32), ("is_last", C.c_int32)]
+
+
+class AttnRun(C.Structure):
+    _fields_ = [("n_rows", C.c_int32), ("pos0", C.c_int32), ("cell0", C.c_int32)]
 
 
 class Weights(C.Structure):
@@ -161,6 +168,12 @@ def load(path: str = LIB_PATH) -> C.CDLL:
         "pfop_set_gemm_pairs": (C.c_int, [i32]),
         "pfop_qkv_row_order": (i32, [i32, i32, i32, i32, vp, i32]),
         "pfop_repack_q4": (i64, [vp, i32, i32, i32, vp, i64]),
+        "pfop_attention_packed": (C.c_int, [vp, vp, vp, i64, i32, i32, i32, C.POINTER(AttnRun), i32, vp, vp, i64, vp]),
+        "pfop_attention_tree": (C.c_int, [vp, vp, vp, i64, i32, i32, i32, C.POINTER(AttnRun), i32, vp, i32, vp, vp,
+                                          i64, vp]),
+        "pfop_attention_work_bytes": (i64, [i32, i32, i32, C.POINTER(AttnRun), i32]),
+        "pfop_attention_status": (C.c_int, [vp, vp]),
+        "pfop_logprobs": (C.c_int, [i32, vp, i64, i32, i32, vp, i32, vp, vp, vp, vp, vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -316,6 +329,128 @@ def repack_q4(w, bn: int):
     if rc != need:
         raise PrefillError(rc, load().pfop_last_error().decode())
     return out
+
+
+# ---------------------------------------------------------------------------
+# several sequences in one call: attention and log probabilities
+
+
+def _on_device(t, what: str, dtype: str, shape, device) -> int:
+    """Address of a contiguous CUDA tensor on `device` of the given type and
+    shape (None in a shape: any size)."""
+    if str(t.dtype) != "torch." + dtype:
+        raise ValueError(f"{what}: element type must be {dtype}, got {t.dtype}")
+    if len(t.shape) != len(shape) or any(w is not None and w != n for w, n in zip(shape, t.shape)):
+        raise ValueError(f"{what}: shape {tuple(t.shape)} does not fit {tuple(shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{what}: buffer must be contiguous")
+    if t.device != device:
+        raise ValueError(f"{what}: must be on {device}, is on {t.device}")
+    return t.data_ptr()
+
+
+def _call_on(device, stream, fn, *args):
+    """fn(*args, stream) with `device` current; stream None: the device's
+    current torch stream (so the call is ordered with the torch work around
+    it)."""
+    import torch
+    if torch.cuda.current_device() != device.index:
+        with torch.cuda.device(device):
+            return _call_on(device, stream, fn, *args)
+    s = torch.cuda.current_stream(device).cuda_stream if stream is None else _stream(stream)
+    check_op(fn(*args, s))
+
+
+class AttnRuns:
+    """The runs of an attention_packed / attention_tree call and the call's
+    scratch: runs = [(n_rows, pos0, cell0), ...] (see pfop_attn_run), for
+    n_head / n_head_kv heads of head_dim.  Kept by a program for as many
+    calls as have these runs; calls that use one AttnRuns share its scratch,
+    so they must not overlap on the GPU (one stream, or events between them;
+    graphs recorded with the same AttnRuns may not run at once)."""
+
+    def __init__(self, runs, n_head: int, n_head_kv: int, head_dim: int, device=None):
+        import torch
+        self._lib = load()
+        self.shape = (n_head, n_head_kv, head_dim)
+        runs = [(int(n), int(p), int(c)) for n, p, c in runs]
+        self.n_runs = len(runs)
+        self.n_rows = sum(r[0] for r in runs)
+        self.runs = (AttnRun * max(1, len(runs)))(*[AttnRun(*r) for r in runs])
+        self.device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+        with torch.cuda.device(self.device):
+            self.device = torch.device("cuda", torch.cuda.current_device())
+            need = int(self._lib.pfop_attention_work_bytes(n_head, n_head_kv, head_dim, self.runs, self.n_runs))
+            if need < 0:
+                check_op(need)
+            self.work = torch.empty(need, dtype=torch.uint8, device=self.device)
+            self.work[:256].zero_()
+        self.work_bytes = need
+
+    def check(self, stream=None):
+        """Wait for the stream (None: the current one) and raise if a call
+        gave up a bounded wait."""
+        _call_on(self.device, stream, self._lib.pfop_attention_status, self.work.data_ptr())
+
+    def _args(self, q, k, v, out):
+        hq, hkv, hd = self.shape
+        if q.shape[0] < self.n_rows or out.shape[0] < self.n_rows:
+            raise ValueError(f"q and out: the runs have {self.n_rows} rows")
+        d = self.device
+        return (_on_device(q, "q", "float16", (None, hq, hd), d), _on_device(k, "k", "float16", (None, hkv, hd), d),
+                _on_device(v, "v", "float16", (k.shape[0], hkv, hd), d), k.shape[0], hq, hkv, hd, self.runs,
+                self.n_runs), (_on_device(out, "out", "bfloat16", (None, hq, hd), d), self.work.data_ptr(),
+                               self.work_bytes)
+
+
+def attention_packed(q, k, v, runs: AttnRuns, out, stream=None):
+    """Causal attention of several sequences' rows (pfop_attention_packed):
+    q [T, n_head, head_dim] and k, v [n_cells, n_head_kv, head_dim] float16,
+    out [T, n_head, head_dim] bfloat16, all on the runs' device.  Enqueued on
+    `stream` (None: the current torch stream)."""
+    a, b = runs._args(q, k, v, out)
+    _call_on(runs.device, stream, runs._lib.pfop_attention_packed, *a, *b)
+
+
+def attention_tree(q, k, v, runs: AttnRuns, mask, out, stream=None):
+    """Attention of drafted token trees (pfop_attention_tree): as
+    attention_packed, with mask [T, words] int64, bit j % 64 of word j / 64
+    set where the row sees drafted token j of its run."""
+    if len(mask.shape) != 2 or mask.shape[0] < runs.n_rows:
+        raise ValueError(f"mask: needs [{runs.n_rows}, words]")
+    a, b = runs._args(q, k, v, out)
+    m = _on_device(mask, "mask", "int64", (None, None), runs.device)
+    _call_on(runs.device, stream, runs._lib.pfop_attention_tree, *a, m, mask.shape[1], *b)
+
+
+def logprobs(logits, tokens=None, logp=None, entropy=None, top_id=None, top_logp=None, stream=None):
+    """Log probabilities over the vocabulary (pfop_logprobs): logits [rows,
+    vocab] float32 or bfloat16 (rows may be strided: a view of wider rows);
+    tokens [rows] int32 with logp [rows] float32; entropy [rows] float32;
+    top_id [rows, n] int32 with top_logp [rows, n] float32.  Outputs left
+    None are skipped.  Enqueued on `stream` (None: the current torch
+    stream)."""
+    if len(logits.shape) != 2 or (logits.shape[1] > 1 and logits.stride(1) != 1):
+        raise ValueError("logits: needs [rows, vocab] with dense rows")
+    kinds = {"torch.float32": PF_L_F32, "torch.bfloat16": PF_L_BF16}
+    if str(logits.dtype) not in kinds:
+        raise ValueError(f"logits: element type must be float32 or bfloat16, got {logits.dtype}")
+    if (tokens is None) != (logp is None) or (top_id is None) != (top_logp is None):
+        raise ValueError("tokens and logp, top_id and top_logp go together")
+    if not logits.is_cuda:
+        raise ValueError(f"logits: must be on a CUDA device, is on {logits.device}")
+    rows, vocab = logits.shape
+    d = logits.device
+    n_top = 0 if top_id is None else top_id.shape[1]
+
+    def at(t, what, dtype, shape):
+        return None if t is None else _on_device(t, what, dtype, shape, d)
+
+    args = (kinds[str(logits.dtype)], logits.data_ptr(), logits.stride(0) if rows > 1 else vocab, rows, vocab,
+            at(tokens, "tokens", "int32", (rows,)), n_top, at(logp, "logp", "float32", (rows,)),
+            at(entropy, "entropy", "float32", (rows,)), at(top_id, "top_id", "int32", (rows, n_top)),
+            at(top_logp, "top_logp", "float32", (rows, n_top)))
+    _call_on(d, stream, load().pfop_logprobs, *args)
 
 
 # ---------------------------------------------------------------------------

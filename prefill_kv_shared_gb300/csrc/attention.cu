@@ -40,6 +40,7 @@
 // the tensor cores work while the row warps run the softmax of chunk j.  All
 // waits are bounded (PF_WAIT_CYCLES); a timed-out wait flags the error word
 // and the CTA unwinds.
+#include "attn.cuh"
 #include "common.cuh"
 #include "kernels.h"
 
@@ -48,12 +49,6 @@
 namespace pf {
 
 constexpr int CHUNK = 64;
-
-__device__ __forceinline__ float ex2_approx(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 
 // partials layout: [row t][query head][group (ATTN_MAX_GROUPS)][HD + 4] =
 // o[HD] (not normalised), m, l, 2 pad (16-byte aligned rows)
@@ -90,11 +85,6 @@ static int attn_row_ctas(const AttnArgs& a) { return (a.M * (a.Hq / a.Hkv) + 127
 // groups that hold keys of the row at position pos
 __host__ __device__ __forceinline__ int attn_row_groups(int pos, int gc) { return (pos / CHUNK) / gc + 1; }
 
-template <int HD>
-__host__ __device__ constexpr float attn_c() {
-  return 1.4426950408889634f / (HD == 256 ? 16.0f : HD == 128 ? 11.313708498984761f : 8.0f);
-}
-
 // ---------------------------------------------------------------------------
 // the tcgen05 kernel
 
@@ -116,53 +106,6 @@ struct AttnTcCfg {
   static constexpr int THREADS = 224;
   static_assert(SMEM <= 232448, "shared memory");
 };
-
-// 128-byte-swizzled operand descriptor with explicit leading / stride byte
-// offsets (MN-major: LBO = bytes between 64-element atoms along MN, SBO =
-// bytes between 8-row groups along K)
-__device__ __forceinline__ uint64_t sdesc_sw128_lbo_sbo(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
-  uint64_t d = 0;
-  d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
-  d |= static_cast<uint64_t>(lbo >> 4) << 16;
-  d |= static_cast<uint64_t>(sbo >> 4) << 32;
-  d |= static_cast<uint64_t>(1) << 46;
-  d |= static_cast<uint64_t>(2) << 61;
-  return d;
-}
-
-// D[tmem] (+)= A[tmem] * B[smem] (kind::f16), A in TMEM: its rows are the
-// TMEM lanes, two 16-bit elements of a row per 32-bit column (the lower k
-// in the low half), K = 16 per instruction (8 columns)
-__device__ __forceinline__ void tc_mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
-                                              uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-
-// kind::f16 instruction descriptor, fp16 A and B, fp32 accumulator; b_mn:
-// B is MN-major (V stored [key][dim] is the B operand of P V)
-__host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, bool b_mn) {
-  return (1u << 4) | (b_mn ? (1u << 16) : 0u) | (static_cast<uint32_t>(N >> 3) << 17) |
-         (static_cast<uint32_t>(M >> 4) << 24);
-}
-
-// 32 lanes x 32 consecutive 32-bit columns from registers (thread i -> lane i)
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
-      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
-      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
-      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
-      : "memory");
-}
-__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // let issued MMAs finish before TMEM is freed on an error path (bounded;
 // `bar` completes once, on the commit that follows them)
