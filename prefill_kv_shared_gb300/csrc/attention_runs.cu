@@ -1,68 +1,784 @@
 // Attention of several sequences' rows in one call (pfop_attention_packed,
 // pfop_attention_tree): causal over each sequence's own keys, or over a
-// context and a tree of drafted tokens.
+// context and a tree of drafted tokens, on the 5th-generation tensor cores.
+//
+// MMA rows are (row, head-in-group) pairs of a run: row R = t*G + g is the
+// run's row t and query head kvh*G + g, so the G heads of a KV head share its
+// K/V.  A pair of CTAs (a 2-CTA cluster, tcgen05 .cta_group::2) takes 256
+// rows of one run and KV head and a group of gc consecutive 128-key chunks
+// of the run's positions, and runs one online softmax over the group:
+//     S = Q K^T, m' = max(m, max_k s_k), p_k = 2^((s_k - m') c),
+//     l' = l 2^((m - m') c) + sum_k p_k, O' = O 2^((m - m') c) + fp16(P) V
+// with c = log2(e)/sqrt(hd), S, O, m, l in fp32.  A row whose keys lie in one
+// group writes O/l; otherwise each group leaves (O, m, l) in the scratch and
+// attn_runs_merge_kernel joins them in group order.
+//
+// Why pairs: 128 rows against a chunk need 64 bytes of K/V per SM clock at
+// the full tensor rate, more than L2 delivers to all SMs at once; 256 rows
+// over a pair, each CTA holding half of every K chunk (64 keys) and half of
+// every V chunk (hd/2 dims), need 32, and the halves leave room for 2.5
+// chunks in flight beside Q at hd 256.
+//
+// Roles of a CTA: warp 1 copies Q and the K/V halves by TMA (one ring of
+// stages, in the order in which the MMAs use them); warp 0 of the even CTA
+// issues the MMAs of the pair, warp 0 of the odd CTA passes its ring's
+// arrivals on to it; warps 2..5 own the CTA's 128 rows (thread = TMEM lane =
+// row): softmax, P (fp16, over the columns of S that it came from), the
+// rescale of O, the output.  With hd 256 there are two S buffers, so S of
+// the next chunk is formed while P of this one is; with hd 64 there is one,
+// and two CTAs on an SM keep its tensor cores and exponentials busy.  All
+// waits are bounded (PF_WAIT_CYCLES): one that gives up flags the scratch's
+// error word and the pair unwinds.
 #include "../../include/prefill_ops.h"
 #include "attn.cuh"
 #include "common.cuh"
 #include "kernels.h"
 
+#include <algorithm>
 #include <string>
 
 namespace pf {
 
 constexpr int RUNS_MAX = 128;
+constexpr int RCH = 128;    // keys of a chunk
+constexpr int RROWS = 256;  // MMA rows of a pair
 
 // the call's runs, passed in the kernel's parameters
 struct RunTable {
   int n_runs = 0;
   int row0[RUNS_MAX];  // first packed row
   int n[RUNS_MAX], pos0[RUNS_MAX], cell0[RUNS_MAX];
+  int item0[RUNS_MAX];  // first work item; a run has (row blocks) x (groups) of them
+  int groups[RUNS_MAX];
 };
 
-// A warp per (row, query head): lane owns HD/32 dims, keys in ascending
-// order, one online softmax.
+struct RunsShape {
+  int Hq, Hkv, log_g;  // G = 1 << log_g query heads per KV head
+  int gc;              // chunks per group
+  int slot_rows;       // rows of a state slot in the scratch
+  int items;           // work items per KV head
+};
+
+template <int HD>
+struct RunsCfg {
+  static constexpr int Q_BYTES = 128 * HD * 2;  // [64-dim box][128 rows][128 B]
+  static constexpr int STAGE = 64 * HD * 2;     // half a chunk: K [box][64 keys][128 B], V [box][128 keys][hd/2 dims]
+  static constexpr int NST = HD == 256 ? 5 : 8;
+  static constexpr int NSB = HD == 256 ? 2 : 1;  // S buffers
+  static constexpr int OCC = HD == 256 ? 1 : 2;  // CTAs per SM
+  static constexpr int OFF_ST = Q_BYTES;
+  static constexpr int OFF_BAR = OFF_ST + NST * STAGE;
+  static constexpr int SMEM = OFF_BAR + 256 + 1024;  // + barriers, + alignment slack
+  static constexpr int TMEM_S = 0;
+  static constexpr int TMEM_O = NSB * RCH;
+  static constexpr int TMEM_COLS = TMEM_O + HD <= 256 ? 256 : 512;
+  static_assert(TMEM_O + HD <= TMEM_COLS && TMEM_COLS * OCC <= 512, "TMEM");
+  static constexpr int THREADS = 192;
+  static_assert(SMEM <= 232448, "shared memory");
+};
+
+// floats of one row's state: o[HD], m, l, 2 pad
+__host__ __device__ constexpr int runs_state_stride(int hd) { return hd + 4; }
+
+// 64-byte-swizzled MN-major operand descriptor: rows (K) of 64 bytes, 8-row
+// groups of 512 bytes, one 32-element atom along MN
+__device__ __forceinline__ uint64_t sdesc_sw64_mn(uint32_t saddr) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+  d |= static_cast<uint64_t>(512 >> 4) << 16;
+  d |= static_cast<uint64_t>(512 >> 4) << 32;
+  d |= static_cast<uint64_t>(1) << 46;
+  d |= static_cast<uint64_t>(4) << 61;
+  return d;
+}
+
+// A pair's D (+)= A[tmem] * B[smem]: each CTA's 128 rows of A lie in its own TMEM
+__device__ __forceinline__ void tc_mma_f16_ts_pair(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                                   uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// two fp32 operations in one instruction
+__device__ __forceinline__ uint64_t pack_f32x2(float a, float b) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
+  return d;
+}
+__device__ __forceinline__ float2 unpack_f32x2(uint64_t v) {
+  float2 f;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
+  return f;
+}
+__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
+// bounded wait for a barrier on an error path (about 0.2 s)
+__device__ __forceinline__ void runs_drain(uint64_t* bar, uint32_t parity) {
+  const uint32_t a = smem_u32(bar);
+  const long long t0 = clock64();
+  while (!mbar_try_wait(a, parity)) {
+    if (clock64() - t0 > 400000000ll) return;
+  }
+}
+
+// The run of work item (or row) `it`: the last one whose first is not above it.
+__device__ __forceinline__ int find_run(const int* first, int n_runs, int it) {
+  int lo = 0, hi = n_runs - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (first[mid] <= it)
+      lo = mid;
+    else
+      hi = mid - 1;
+  }
+  return lo;
+}
+
+// bits of the keys kk .. kk+31 (positions) that the row sees: the context
+// [0, pos0), then its mask's bits for the drafted tokens [0, n)
+__device__ __forceinline__ uint32_t tree_bits(const uint64_t* row_mask, int words, int pos0, int n, int kk) {
+  const int d = kk - pos0;  // drafted token of the word's first bit
+  if (d <= -32) return 0xffffffffu;
+  if (d >= n) return 0u;
+  uint64_t w;
+  if (d < 0) {
+    w = (__ldg(row_mask) << -d) | ((1ull << -d) - 1ull);
+  } else {
+    w = __ldg(row_mask + (d >> 6)) >> (d & 63);
+    if ((d & 63) > 32 && (d >> 6) + 1 < words) w |= __ldg(row_mask + (d >> 6) + 1) << (64 - (d & 63));
+  }
+  if (n - d < 32) w &= (1ull << (n - d)) - 1ull;
+  return static_cast<uint32_t>(w);
+}
+
+// scores of 32 keys of this thread's row: the ones it does not see to -inf
+__device__ __forceinline__ void mask_scores(uint32_t (&x)[32], uint32_t bits) {
+#pragma unroll
+  for (int k = 0; k < 32; ++k)
+    if (!(bits >> k & 1u)) x[k] = 0xff800000u;
+}
+__device__ __forceinline__ void max_scores(const uint32_t (&x)[32], float (&mx)[4]) {
+#pragma unroll
+  for (int k = 0; k < 32; k += 8) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      mx[q] = fmaxf(mx[q], fmaxf(__uint_as_float(x[k + 2 * q]), __uint_as_float(x[k + 2 * q + 1])));
+  }
+}
+// p = 2^(s c - mc) of 32 keys, as 16 fp16 pairs, and their sum
+__device__ __forceinline__ void exp_scores(const uint32_t (&x)[32], uint64_t c2, uint64_t nmc2, uint32_t* pw,
+                                           uint64_t (&ls)[4]) {
+#pragma unroll
+  for (int k = 0; k < 16; ++k) {
+    const float2 e = unpack_f32x2(
+        fma_f32x2(pack_f32x2(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1])), c2, nmc2));
+    const float p0 = ex2_approx(e.x), p1 = ex2_approx(e.y);
+    const __half2 h = __floats2half2_rn(p0, p1);
+    pw[k] = *reinterpret_cast<const uint32_t*>(&h);
+    ls[k & 3] = add_f32x2(ls[k & 3], pack_f32x2(p0, p1));
+  }
+}
+
 template <int HD, bool TREE>
-__global__ void __launch_bounds__(256) attn_runs_kernel(const __grid_constant__ RunTable rt, const __half* q,
-                                                        const __half* k, const __half* v, int Hq, int Hkv,
-                                                        const uint64_t* mask, int words, int total,
-                                                        __nv_bfloat16* out) {
+__global__ void __launch_bounds__(RunsCfg<HD>::THREADS, RunsCfg<HD>::OCC)
+    attn_runs_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                     const __grid_constant__ CUtensorMap tmV, const __grid_constant__ RunTable rt, const RunsShape sh,
+                     const uint64_t* __restrict__ mask, int words, __nv_bfloat16* __restrict__ out,
+                     float* __restrict__ part, int* err) {
+  using C = RunsCfg<HD>;
+  constexpr float cexp = attn_c<HD>();
+  extern __shared__ uint8_t smem_raw[];
+  // The two CTAs' buffers lie at the same shared-memory offset (one
+  // descriptor addresses both): same kernel, same alignment rounding.
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
+  uint64_t* q_full = bars;
+  uint64_t* full = bars + 1;     // NST: a stage has landed (in the even CTA: in both CTAs)
+  uint64_t* empty = bars + 9;    // NST: the MMAs have read it
+  uint64_t* s_full = bars + 17;  // NSB
+  uint64_t* p_full = bars + 19;  // NSB, the even CTA's counts the warps of both
+  uint64_t* pv_done = bars + 21;  // 2, by chunk parity
+  uint64_t* drain = bars + 23;    // error path only
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 24);
+  static_assert(C::NST <= 8 && C::NSB <= 2, "barrier layout");
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = static_cast<int>(cluster_ctarank());
+  pdl_launch();
+
+  // ---- the pair's work item
+  const int idx = static_cast<int>(blockIdx.x >> 1);
+  const int kvh = idx % sh.Hkv, it = idx / sh.Hkv;
+  const int run = find_run(rt.item0, rt.n_runs, it);
+  const int n_rows = rt.n[run], pos0 = rt.pos0[run], row0 = rt.row0[run];
+  const int total_rows = n_rows << sh.log_g;
+  const int nb = (total_rows + RROWS - 1) / RROWS;
+  const int local = it - rt.item0[run];
+  const int grp = local / nb;
+  const int R0 = (nb - 1 - local % nb) * RROWS;  // blocks with the most keys first
+  const int t_last = min(n_rows - 1, (R0 + RROWS - 1) >> sh.log_g);
+  const int keys = TREE ? pos0 + n_rows : pos0 + t_last + 1;
+  const int ch_first = grp * sh.gc;
+  const int n = min((keys + RCH - 1) / RCH, ch_first + sh.gc) - ch_first;  // chunks
+  if (n <= 0) {  // no keys of this group reach the block's rows
+    pdl_wait();
+    return;
+  }
+  const int run_keys = pos0 + n_rows;
+  const int RC = R0 + rank * 128;  // this CTA's first row
+  // warps of rows, here and in the other CTA
+  auto row_warps = [&](int r) { return min(4, max(0, (total_rows - R0 - r * 128 + 31) >> 5)); };
+
+  if (threadIdx.x == 0) {
+    const uint32_t both = rank == 0 ? 2 : 1;  // the odd CTA's arrival is passed on
+    mbar_init(q_full, both);
+    for (int b = 0; b < C::NST; ++b) {
+      mbar_init(&full[b], both);
+      mbar_init(&empty[b], 1);
+    }
+    for (int b = 0; b < C::NSB; ++b) {
+      mbar_init(&s_full[b], 1);
+      mbar_init(&p_full[b], row_warps(0) + row_warps(1));
+    }
+    mbar_init(&pv_done[0], 1);
+    mbar_init(&pv_done[1], 1);
+    mbar_init(drain, 1);
+    fence_mbar_init();
+  }
+  if (warp == 1 && lane == 0) {
+    prefetch_tensormap(&tmQ);
+    prefetch_tensormap(&tmK);
+    prefetch_tensormap(&tmV);
+  }
+  if (warp == 0) tmem_alloc_pair(tmem_slot, C::TMEM_COLS);
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  pdl_wait();
+
+  // K(i) and V(i) in the order of their use: with two S buffers S(i+1) is
+  // formed before P(i) V(i)
+  const int n_seq = 2 * n;
+  auto seq_is_k = [&](int u) { return C::NSB == 2 ? (u == 0 || (u < n_seq - 1 && (u & 1))) : !(u & 1); };
+  auto seq_chunk = [&](int u) {
+    if (C::NSB == 2) return u == 0 ? 0 : u == n_seq - 1 ? n - 1 : (u & 1) ? (u + 1) / 2 : u / 2 - 1;
+    return u / 2;
+  };
+  // zero the V rows of keys past the run in a landed stage: P is 0 there,
+  // but what lies in those cells may be an infinity or NaN
+  auto clear_tail = [&](int u) {
+    const int left = run_keys - (ch_first + seq_chunk(u)) * RCH;
+    if (left >= RCH) return;
+    constexpr int VB = HD == 256 ? 128 : 64;  // bytes of a key's row in a box
+    uint8_t* v = smem + C::OFF_ST + (u % C::NST) * C::STAGE;
+    for (int box = 0; box < C::STAGE / (RCH * VB); ++box)
+      for (int o = left * VB + lane * 16; o < RCH * VB; o += 512)
+        *reinterpret_cast<uint4*>(v + box * RCH * VB + o) = make_uint4(0u, 0u, 0u, 0u);
+    fence_proxy_async_smem();
+    __syncwarp();
+  };
+
+  if (warp == 1) {
+    // ---------------- TMA producer (each CTA its own rows and halves)
+    if (lane == 0) {
+      mbar_arrive_expect_tx(q_full, C::Q_BYTES);
+      tma_load_4d(smem, &tmQ, q_full, 0, kvh << sh.log_g, row0 + (RC >> sh.log_g), 0);
+      bool ok = true;
+      int u = 0;
+      for (; u < n_seq && ok; ++u) {
+        const int s = u % C::NST;
+        if (u >= C::NST) ok = mbar_wait<true>(&empty[s], ((u - C::NST) / C::NST) & 1, err, PF_DEV_TIMEOUT_PRODUCER);
+        if (!ok) break;
+        uint8_t* dst = smem + C::OFF_ST + s * C::STAGE;
+        const int cell = rt.cell0[run] + (ch_first + seq_chunk(u)) * RCH;
+        mbar_arrive_expect_tx(&full[s], C::STAGE);
+        if (seq_is_k(u))
+          tma_load_3d(dst, &tmK, &full[s], kvh * HD, cell + rank * 64, 0);
+        else
+          tma_load_3d(dst, &tmV, &full[s], kvh * HD + rank * (HD / 2), cell, 0);
+      }
+      // On an error the copies in flight land before this CTA may leave.
+      if (!ok || read_error(err) != 0) {
+        runs_drain(q_full, 0);
+        for (int x = max(0, u - C::NST); x < u; ++x) runs_drain(&full[x % C::NST], (x / C::NST) & 1);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 0 && rank == 1) {
+    // ---------------- arrivals of the odd CTA, passed on to the issuer
+    bool ok = mbar_wait(q_full, 0, err, PF_DEV_TIMEOUT_MMA);
+    ok = __all_sync(0xffffffffu, ok);
+    if (ok && lane == 0) mbar_arrive_cluster(map_to_rank(smem_u32(q_full), 0));
+    for (int u = 0; u < n_seq && ok; ++u) {
+      const int s = u % C::NST;
+      ok = mbar_wait(&full[s], (u / C::NST) & 1, err, PF_DEV_TIMEOUT_MMA);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      if (!seq_is_k(u)) clear_tail(u);
+      if (lane == 0) mbar_arrive_cluster(map_to_rank(smem_u32(&full[s]), 0));
+    }
+    __syncwarp();
+  } else if (warp == 0) {
+    // ---------------- MMA issue for the pair: the warp runs the loop in
+    // step, one elected lane issues
+    const bool leader = elect_one();
+    constexpr uint32_t id_qk = idesc_f16_f32(256, RCH, false);
+    constexpr uint32_t id_pv = idesc_f16_f32(256, HD, true);
+    const uint64_t qd0 = sdesc_sw128(smem_u32(smem));
+    bool ok = mbar_wait<true>(q_full, 0, err, PF_DEV_TIMEOUT_MMA);
+    ok = __all_sync(0xffffffffu, ok);
+    bool issued = false;
+    for (int u = 0; u < n_seq && ok; ++u) {
+      const int s = u % C::NST, j = seq_chunk(u);
+      const int b = C::NSB == 2 ? j & 1 : 0;
+      const uint32_t st = smem_u32(smem + C::OFF_ST + s * C::STAGE);
+      const bool is_k = seq_is_k(u);
+      ok = mbar_wait<true>(&full[s], (u / C::NST) & 1, err, PF_DEV_TIMEOUT_MMA);
+      if (ok && !is_k)
+        ok = mbar_wait<true>(&p_full[b], (C::NSB == 2 ? j >> 1 : j) & 1, err, PF_DEV_TIMEOUT_MMA);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      if (!is_k) clear_tail(u);
+      tc_fence_after();
+      if (leader) {
+        if (is_k) {
+          // S(j): P(j - NSB), which lay in this buffer, was read by an MMA issued before
+          const uint64_t kd0 = sdesc_sw128(st);
+#pragma unroll
+          for (int kk = 0; kk < HD / 16; ++kk) {
+            const int bx = kk >> 2, w = kk & 3;  // 64-dim box, 16-dim step within it
+            tc_mma_f16_pair(tmem + C::TMEM_S + b * RCH, qd0 + ((bx * (128 * 128) + w * 32) >> 4),
+                            kd0 + ((bx * (64 * 128) + w * 32) >> 4), id_qk, kk > 0 ? 1u : 0u);
+          }
+          tc_commit_pair(map_to_rank(smem_u32(&s_full[b]), 0));
+          tc_commit_pair(map_to_rank(smem_u32(&s_full[b]), 1));
+        } else {
+          const uint64_t vd0 = HD == 256 ? sdesc_sw128_lbo_sbo(st, RCH * 128, 1024) : sdesc_sw64_mn(st);
+          constexpr int KSTEP = 16 * (HD == 256 ? 128 : 64);  // bytes of 16 keys
+#pragma unroll
+          for (int kk = 0; kk < RCH / 16; ++kk)
+            tc_mma_f16_ts_pair(tmem + C::TMEM_O, tmem + C::TMEM_S + b * RCH + kk * 8, vd0 + ((kk * KSTEP) >> 4), id_pv,
+                               (j > 0 || kk > 0) ? 1u : 0u);
+          tc_commit_pair(map_to_rank(smem_u32(&pv_done[j & 1]), 0));
+          tc_commit_pair(map_to_rank(smem_u32(&pv_done[j & 1]), 1));
+        }
+        tc_commit_pair(map_to_rank(smem_u32(&empty[s]), 0));
+        tc_commit_pair(map_to_rank(smem_u32(&empty[s]), 1));
+      }
+      __syncwarp();
+      issued = true;
+    }
+    if (!ok && issued && leader) {
+      // the MMAs already issued finish before TMEM is freed
+      tc_commit_pair(map_to_rank(smem_u32(drain), 0));
+      runs_drain(drain, 0);
+    }
+    __syncwarp();
+  } else if ((warp & 3) < row_warps(rank)) {
+    // ---------------- rows (warps 2..5: TMEM lane quarter warp % 4)
+    const int qw = warp & 3;
+    const int R = RC + 32 * qw + lane;
+    const int t = R >> sh.log_g, head = (kvh << sh.log_g) + (R & ((1 << sh.log_g) - 1));
+    const bool row = R < total_rows;
+    const int pos = row ? pos0 + t : -1;
+    const uint64_t* row_mask = TREE && row ? mask + static_cast<size_t>(row0 + t) * words : nullptr;
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * qw) << 16);
+    constexpr bool KEEP = HD == 256;  // registers hold a chunk's scores (hd 64: they are read twice)
+    const uint64_t c2 = pack_f32x2(cexp, cexp);
+    float m = -INFINITY, l = 0.f;
+    bool ok = true;
+    for (int j = 0; j < n && ok; ++j) {
+      const int b = C::NSB == 2 ? j & 1 : 0;
+      const int key0 = (ch_first + j) * RCH;
+      const uint32_t ts = lanes + C::TMEM_S + b * RCH;
+      if (lane == 0) ok = mbar_wait<true>(&s_full[b], (C::NSB == 2 ? j >> 1 : j) & 1, err, PF_DEV_TIMEOUT_EPILOGUE);
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      if (!ok) break;
+      tc_fence_after();
+      // the row's view of the chunk, skipped where every row of the warp sees all of it
+      const bool all = TREE ? key0 + RCH <= pos0 : __all_sync(0xffffffffu, pos >= key0 + RCH - 1);
+      uint32_t bits[4];
+      if (!all) {
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          if (TREE) {
+            bits[w] = row ? tree_bits(row_mask, words, pos0, n_rows, key0 + 32 * w) : 0u;
+          } else {
+            const int nv = pos - key0 - 32 * w + 1;
+            bits[w] = nv >= 32 ? 0xffffffffu : nv <= 0 ? 0u : (1u << nv) - 1u;
+          }
+        }
+      }
+      uint32_t x[KEEP ? 4 : 2][32];
+      float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+      for (int h = 0; h < 4; h += 2) {
+        uint32_t(&x0)[32] = x[KEEP ? h : 0];
+        uint32_t(&x1)[32] = x[KEEP ? h + 1 : 1];
+        tmem_ld32(ts + 32 * h, x0);
+        tmem_ld32(ts + 32 * h + 32, x1);
+        tmem_ld_wait32(x0);
+        tmem_ld_wait32(x1);
+        if (!all) {
+          mask_scores(x0, bits[h]);
+          mask_scores(x1, bits[h + 1]);
+        }
+        max_scores(x0, mx);
+        max_scores(x1, mx);
+      }
+      const float mj = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+      // The reference moves only when this chunk's maximum passes it by more
+      // than 2^8 (or on the row's first visible keys); until then P is taken
+      // against the old one (p <= 2^8, well inside fp16) and O needs no touch.
+      const bool grow = mj != -INFINITY && (m == -INFINITY || (mj - m) * cexp > 8.f);
+      const float mn = grow ? mj : m;
+      const bool resc = grow && m != -INFINITY;
+      const float scale = resc ? ex2_approx((m - mn) * cexp) : 1.f;
+      const float nmc = mn == -INFINITY ? 0.f : -mn * cexp;
+      const uint64_t nmc2 = pack_f32x2(nmc, nmc);
+      uint64_t ls[4] = {0ull, 0ull, 0ull, 0ull};
+#pragma unroll
+      for (int h = 0; h < 4; h += 2) {
+        uint32_t(&x0)[32] = x[KEEP ? h : 0];
+        uint32_t(&x1)[32] = x[KEEP ? h + 1 : 1];
+        if (!KEEP) {
+          tmem_ld32(ts + 32 * h, x0);
+          tmem_ld32(ts + 32 * h + 32, x1);
+          tmem_ld_wait32(x0);
+          tmem_ld_wait32(x1);
+          if (!all) {
+            mask_scores(x0, bits[h]);
+            mask_scores(x1, bits[h + 1]);
+          }
+        }
+        uint32_t pw[32];  // 64 fp16 probabilities
+        exp_scores(x0, c2, nmc2, pw, ls);
+        exp_scores(x1, c2, nmc2, pw + 16, ls);
+        tmem_st32(ts + 16 * h, pw);  // over scores that have been read
+      }
+      const float2 l01 = unpack_f32x2(add_f32x2(add_f32x2(ls[0], ls[1]), add_f32x2(ls[2], ls[3])));
+      l = __fmaf_rn(l, scale, l01.x + l01.y);
+      m = mn;
+      tmem_st_wait();
+      // O *= scale once P V(j-1) has landed, only in the warps where a row
+      // moved its reference.  (S(j) was issued after P V(j-2), so each of the
+      // two barriers has at most the awaited phase outstanding.)
+      if (j >= 1 && __any_sync(0xffffffffu, resc)) {
+        if (lane == 0) ok = mbar_wait<true>(&pv_done[(j - 1) & 1], ((j - 1) >> 1) & 1, err, PF_DEV_TIMEOUT_EPILOGUE);
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll 1
+        for (int c = 0; c < HD / 32; ++c) {
+          uint32_t y[32];
+          tmem_ld32(lanes + C::TMEM_O + 32 * c, y);
+          tmem_ld_wait32(y);
+#pragma unroll
+          for (int q = 0; q < 32; ++q) y[q] = __float_as_uint(__uint_as_float(y[q]) * scale);
+          tmem_st32(lanes + C::TMEM_O + 32 * c, y);
+        }
+        tmem_st_wait();
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(map_to_rank(smem_u32(&p_full[b]), 0));
+    }
+    if (ok) {
+      if (lane == 0) ok = mbar_wait<true>(&pv_done[(n - 1) & 1], ((n - 1) >> 1) & 1, err, PF_DEV_TIMEOUT_EPILOGUE);
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+    }
+    if (ok) {
+      // Every MMA of the pair and every copy is done.  Each 32 x 32 block of O
+      // goes through a warp-private buffer in the idle ring, so that global
+      // stores cover whole row segments.
+      tc_fence_after();
+      // groups with keys of this row; 0: nothing to write
+      const int n_g = !row ? 0 : TREE ? rt.groups[run] : (pos / RCH) / sh.gc + 1;
+      const int kind = grp >= n_g ? 0 : n_g == 1 ? 1 : 2;  // 1: output row, 2: group state
+      const float inv = kind != 1 ? 1.f : l == 0.f ? 0.f : __frcp_rn(l);  // a row that sees nothing: zeros
+      const size_t own = kind == 1 ? (static_cast<size_t>(row0 + t) * sh.Hq + head) * HD
+                                   : (static_cast<size_t>(idx) * sh.slot_rows + (R - R0)) * runs_state_stride(HD);
+      const int rs = lane >> 3, pc = lane & 7;
+      size_t dst[8];
+      int dk[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        dk[i] = __shfl_sync(0xffffffffu, kind, 4 * i + rs);
+        dst[i] = __shfl_sync(0xffffffffu, static_cast<unsigned long long>(own), 4 * i + rs);
+      }
+      uint8_t* stg = smem + C::OFF_ST + qw * 4096;
+#pragma unroll 1
+      for (int c = 0; c < HD / 32; ++c) {
+        uint32_t y[32];
+        tmem_ld32(lanes + C::TMEM_O + 32 * c, y);
+        tmem_ld_wait32(y);
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+          *reinterpret_cast<float4*>(stg + lane * 128 + ((q ^ (lane & 7)) << 4)) =
+              make_float4(__uint_as_float(y[4 * q]) * inv, __uint_as_float(y[4 * q + 1]) * inv,
+                          __uint_as_float(y[4 * q + 2]) * inv, __uint_as_float(y[4 * q + 3]) * inv);
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int rr = 4 * i + rs;
+          if (dk[i] == 0) continue;
+          const float4 v = *reinterpret_cast<const float4*>(stg + rr * 128 + ((pc ^ (rr & 7)) << 4));
+          if (dk[i] == 1) {
+            const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x, v.y), hi = __floats2bfloat162_rn(v.z, v.w);
+            *reinterpret_cast<uint2*>(out + dst[i] + 32 * c + 4 * pc) =
+                make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+          } else {
+            *reinterpret_cast<float4*>(part + dst[i] + 32 * c + 4 * pc) = v;
+          }
+        }
+        __syncwarp();
+      }
+      if (kind == 2) *reinterpret_cast<float2*>(part + own + HD) = make_float2(m, l);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  // neither CTA leaves (or frees TMEM) while the pair's MMAs may still use it
+  cluster_sync_all();
+  if (warp == 0) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, C::TMEM_COLS);
+  }
+}
+
+// Rows with several groups: m = max m_g, w_g = 2^((m_g - m) c), out =
+// (sum w_g o_g) / (sum w_g l_g), sums in group order.  A warp per row R of a
+// row block, lane owning HD/32 consecutive dims; bound by the states' bytes
+// (L2: they were just written).
+template <int HD, bool TREE>
+__global__ void __launch_bounds__(256) attn_runs_merge_kernel(const __grid_constant__ RunTable rt, const RunsShape sh,
+                                                              const float* __restrict__ part,
+                                                              __nv_bfloat16* __restrict__ out) {
   constexpr int PER = HD / 32;
+  constexpr float c = attn_c<HD>();
   pdl_launch();
   pdl_wait();
   const int lane = threadIdx.x & 31;
-  const int64_t pair = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-  const int t = static_cast<int>(pair / Hq), h = static_cast<int>(pair % Hq);
-  if (t >= total) return;
-  int r = 0;
-  while (r + 1 < rt.n_runs && rt.row0[r + 1] <= t) ++r;
-  const int i = t - rt.row0[r], n = rt.n[r], pos0 = rt.pos0[r];
-  const int kvh = h / (Hq / Hkv);
-  float qf[PER], o[PER];
-  for (int d = 0; d < PER; ++d) {
-    qf[d] = __half2float(q[(static_cast<size_t>(t) * Hq + h) * HD + lane * PER + d]) * attn_c<HD>();
-    o[d] = 0.f;
+  const int kvh = blockIdx.y;
+  // blockIdx.x: (row block of any run) x (8-row slice); a run's blocks start
+  // at item0 / groups blocks of its own items
+  const int slices = sh.slot_rows / 8;
+  int blk = static_cast<int>(blockIdx.x) / slices;
+  const int R_in = (static_cast<int>(blockIdx.x) % slices) * 8 + (threadIdx.x >> 5);
+  int run = 0, nb = 0;
+  for (;; ++run) {
+    nb = ((rt.n[run] << sh.log_g) + RROWS - 1) / RROWS;
+    if (blk < nb || run == rt.n_runs - 1) break;
+    blk -= nb;
   }
-  float m = -INFINITY, l = 0.f;
-  const int keys = TREE ? pos0 + n : pos0 + i + 1;
-  for (int j = 0; j < keys; ++j) {
-    if (TREE && j >= pos0) {
-      const int d = j - pos0;
-      if (!(mask[static_cast<size_t>(t) * words + d / 64] >> (d % 64) & 1)) continue;
+  const int R = blk * RROWS + R_in;
+  if (R >= rt.n[run] << sh.log_g) return;
+  const int t = R >> sh.log_g;
+  const int n_g = TREE ? rt.groups[run] : ((rt.pos0[run] + t) / RCH) / sh.gc + 1;
+  if (n_g < 2) return;
+  // group g's slot of this block
+  const size_t step = static_cast<size_t>(nb) * sh.Hkv * sh.slot_rows * runs_state_stride(HD);
+  const float* base =
+      part + ((static_cast<size_t>(rt.item0[run] + (nb - 1 - blk)) * sh.Hkv + kvh) * sh.slot_rows + R_in) *
+                 runs_state_stride(HD);
+  float m = -INFINITY;
+  for (int g = lane; g < n_g; g += 32) m = fmaxf(m, base[g * step + HD]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  float acc[PER];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) acc[i] = 0.f;
+  float l = 0.f;
+  for (int g0 = 0; g0 < n_g; g0 += 4) {  // four groups' loads in flight
+    float o[4][PER];
+    float2 ml[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int g = min(g0 + k, n_g - 1);
+      const float* p = base + g * step;
+      ml[k] = *reinterpret_cast<const float2*>(p + HD);
+      if constexpr (PER >= 4) {
+#pragma unroll
+        for (int i = 0; i < PER; i += 4) {
+          const float4 v = *reinterpret_cast<const float4*>(p + lane * PER + i);
+          o[k][i] = v.x, o[k][i + 1] = v.y, o[k][i + 2] = v.z, o[k][i + 3] = v.w;
+        }
+      } else {
+        const float2 v = *reinterpret_cast<const float2*>(p + lane * PER);
+        o[k][0] = v.x, o[k][1] = v.y;
+      }
     }
-    const size_t row = (static_cast<size_t>(rt.cell0[r] + j) * Hkv + kvh) * HD + lane * PER;
-    float s = 0.f;
-    for (int d = 0; d < PER; ++d) s = __fmaf_rn(qf[d], __half2float(k[row + d]), s);
-    for (int x = 16; x > 0; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-    const float mn = fmaxf(m, s);
-    const float a = m == -INFINITY ? 0.f : ex2_approx(m - mn);
-    const float p = mn == -INFINITY ? 0.f : ex2_approx(s - mn);
-    l = l * a + p;
-    for (int d = 0; d < PER; ++d) o[d] = o[d] * a + p * __half2float(v[row + d]);
-    m = mn;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (g0 + k >= n_g || ml[k].x == -INFINITY) continue;
+      const float w = ex2_approx((ml[k].x - m) * c);
+      l = __fmaf_rn(w, ml[k].y, l);
+#pragma unroll
+      for (int i = 0; i < PER; ++i) acc[i] = __fmaf_rn(w, o[k][i], acc[i]);
+    }
   }
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  for (int d = 0; d < PER; ++d)
-    out[(static_cast<size_t>(t) * Hq + h) * HD + lane * PER + d] = __float2bfloat16(o[d] * inv);
+  const float inv = l == 0.f ? 0.f : __frcp_rn(l);
+  __nv_bfloat16* d = out + (static_cast<size_t>(rt.row0[run] + t) * sh.Hq + (kvh << sh.log_g) +
+                            (R & ((1 << sh.log_g) - 1))) * HD + lane * PER;
+#pragma unroll
+  for (int i = 0; i < PER; i += 2)
+    *reinterpret_cast<__nv_bfloat162*>(d + i) = __floats2bfloat162_rn(acc[i] * inv, acc[i + 1] * inv);
+}
+
+// ---------------------------------------------------------------------------
+// host: the cut of a call into work items
+
+struct RunsPlan {
+  RunTable rt;
+  RunsShape sh;
+  int blocks = 0;      // row blocks of all runs
+  bool split = false;  // some run has several groups
+  int64_t state_bytes = 0;
+};
+
+static int sm_count() {
+  static const int n = [] {
+    int dev = 0, v = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+      cudaGetLastError();
+      return 152;
+    }
+    return v > 0 ? v : 152;
+  }();
+  return n;
+}
+
+// The chunks per group: as many groups as shorten the call, by a count of
+// chunk times.  An item costs its chunks and `fixed` chunk times (prologue,
+// Q, output); the call ends no earlier than its longest item and its total
+// work over the pairs that fit at once, and splitting adds the states'
+// traffic and the merge launch (`fixed` again).  State slots are bounded by
+// four per resident pair.
+static void make_plan(RunsPlan& p, const pfop_attn_run* runs, int n_runs, int Hq, int Hkv, int hd, bool tree) {
+  const int G = Hq / Hkv;
+  int order[RUNS_MAX], row0[RUNS_MAX], cnt = 0, row = 0;
+  for (int r = 0; r < n_runs; ++r) {
+    if (runs[r].n_rows > 0) {
+      order[cnt++] = r;
+      row0[r] = row;
+    }
+    row += runs[r].n_rows;
+  }
+  // runs with the most keys first: their blocks are the longest items
+  std::stable_sort(order, order + cnt, [&](int a, int b) {
+    return runs[a].pos0 + runs[a].n_rows > runs[b].pos0 + runs[b].n_rows;
+  });
+  const int units = sm_count() / 2 * (hd == 256 ? RunsCfg<256>::OCC : RunsCfg<64>::OCC);
+  const int fixed = hd == 256 ? 3 : 4;
+  int max_ch = 0, max_rows = 0;
+  double work = 0;  // chunks over all row blocks
+  p.blocks = 0;
+  for (int i = 0; i < cnt; ++i) {
+    const pfop_attn_run& r = runs[order[i]];
+    const int nb = (r.n_rows * G + RROWS - 1) / RROWS, ch = (r.pos0 + r.n_rows + RCH - 1) / RCH;
+    max_ch = std::max(max_ch, ch);
+    max_rows = std::max(max_rows, std::min(RROWS, r.n_rows * G));
+    p.blocks += nb;
+    work += tree ? double(nb) * ch : nb * (r.pos0 + 0.5 * (r.n_rows + RROWS / G)) / RCH + 0.5 * nb;
+  }
+  auto items_of = [&](int gc) {
+    int64_t n = 0;
+    for (int i = 0; i < cnt; ++i) {
+      const pfop_attn_run& r = runs[order[i]];
+      n += int64_t((r.n_rows * G + RROWS - 1) / RROWS) * (((r.pos0 + r.n_rows + RCH - 1) / RCH + gc - 1) / gc);
+    }
+    return n;
+  };
+  int best_gc = max_ch;
+  double best = 1e30;
+  for (int gc = max_ch, s = 1; gc >= 1;) {
+    const int64_t items = items_of(gc);
+    if (gc < max_ch && items * Hkv > 4 * int64_t(units)) break;
+    const double live = std::max<double>(p.blocks, tree ? double(items) : work / gc + 0.5 * p.blocks);
+    const double t = std::max(double(gc + fixed), (work + fixed * live) * Hkv / units) + (gc < max_ch ? fixed : 0);
+    if (t < best) best = t, best_gc = gc;
+    // the next smaller group that makes another number of groups
+    int next = gc;
+    while (next >= gc && s <= max_ch) next = (max_ch + s) / (s + 1), ++s;
+    if (next >= gc) break;
+    gc = next;
+  }
+  p.sh.Hq = Hq;
+  p.sh.Hkv = Hkv;
+  p.sh.log_g = 0;
+  while ((1 << p.sh.log_g) < G) ++p.sh.log_g;
+  p.sh.gc = best_gc;
+  p.sh.slot_rows = (max_rows + 31) / 32 * 32;
+  p.split = false;
+  int items = 0;
+  p.rt.n_runs = cnt;
+  for (int i = 0; i < cnt; ++i) {
+    const pfop_attn_run& r = runs[order[i]];
+    const int nb = (r.n_rows * G + RROWS - 1) / RROWS, ch = (r.pos0 + r.n_rows + RCH - 1) / RCH;
+    p.rt.row0[i] = row0[order[i]];
+    p.rt.n[i] = r.n_rows;
+    p.rt.pos0[i] = r.pos0;
+    p.rt.cell0[i] = r.cell0;
+    p.rt.item0[i] = items;
+    p.rt.groups[i] = (ch + best_gc - 1) / best_gc;
+    if (p.rt.groups[i] > 1) p.split = true;
+    items += nb * p.rt.groups[i];
+  }
+  p.sh.items = items;
+  p.state_bytes =
+      p.split ? int64_t(items) * Hkv * p.sh.slot_rows * runs_state_stride(hd) * int64_t(sizeof(float)) : 0;
+}
+
+template <int HD, bool TREE>
+static cudaError_t launch_runs(const RunsPlan& p, const __half* q, const __half* k, const __half* v, int64_t n_cells,
+                               int total, const uint64_t* mask, int words, __nv_bfloat16* out, float* part, int* err,
+                               cudaStream_t s) {
+  using C = RunsCfg<HD>;
+  cudaError_t e = smem_opt_in<attn_runs_kernel<HD, TREE>>(C::SMEM);
+  if (e != cudaSuccess) return e;
+  const int Hq = p.sh.Hq, Hkv = p.sh.Hkv, G = Hq / Hkv;
+  // Q as [64-dim box][row][head][64 dims], K as [64-dim box][cell][64 dims],
+  // V as [box][cell][dims of one box]: hd/2 dims a CTA, in 64-dim boxes
+  // (128-byte swizzle) at hd 256, one 32-dim box (64-byte swizzle) at hd 64
+  CUtensorMap tq, tk, tv;
+  std::string why;
+  {
+    const uint64_t dims[4] = {64, static_cast<uint64_t>(Hq), static_cast<uint64_t>(total), HD / 64};
+    const uint64_t st[3] = {HD * 2, static_cast<uint64_t>(Hq) * HD * 2, 128};
+    const uint32_t box[4] = {64, static_cast<uint32_t>(G), static_cast<uint32_t>(128 / G), HD / 64};
+    if (!encode_fp16_sw128(&tq, q, 4, dims, st, box, &why)) return cudaErrorInvalidValue;
+  }
+  {
+    const uint64_t dims[3] = {static_cast<uint64_t>(Hkv) * HD, static_cast<uint64_t>(n_cells), HD / 64};
+    const uint64_t st[2] = {static_cast<uint64_t>(Hkv) * HD * 2, 128};
+    const uint32_t box[3] = {64, 64, HD / 64};
+    if (!encode_fp16_sw128(&tk, k, 3, dims, st, box, &why)) return cudaErrorInvalidValue;
+    const uint32_t vbox[3] = {HD == 256 ? 64u : 32u, RCH, HD == 256 ? 2u : 1u};
+    if (!(HD == 256 ? encode_fp16_sw128(&tv, v, 3, dims, st, vbox, &why)
+                    : encode_fp16_sw64(&tv, v, 3, dims, st, vbox, &why)))
+      return cudaErrorInvalidValue;
+  }
+  e = launch_k(attn_runs_kernel<HD, TREE>, dim3(2u * p.sh.items * Hkv), dim3(C::THREADS), C::SMEM, s, 2, tq, tk, tv,
+               p.rt, p.sh, mask, words, out, part, err);
+  if (e != cudaSuccess || !p.split) return e;
+  return launch_k(attn_runs_merge_kernel<HD, TREE>, dim3(p.blocks * (p.sh.slot_rows / 8), Hkv), dim3(256), 0, s, 1,
+                  p.rt, p.sh, static_cast<const float*>(part), out);
 }
 
 }  // namespace pf
@@ -118,27 +834,17 @@ int run_attention(bool tree, const void* q, const void* k, const void* v, int64_
     return fail(PF_E_ARG, "q, k, v and out must be 16-byte aligned");
   if (tree && (reinterpret_cast<uintptr_t>(mask) & 7)) return fail(PF_E_ARG, "mask must be 8-byte aligned");
   if (reinterpret_cast<uintptr_t>(work) & 255) return fail(PF_E_ARG, "the scratch must be 256-byte aligned");
-  if (work_bytes < WORK_HEADER) return fail(PF_E_ARG, "the scratch is smaller than these runs need");
-  RunTable rt;
-  int row = 0;
-  for (int r = 0; r < n_runs; ++r) {
-    if (runs[r].n_rows > 0) {
-      const int i = rt.n_runs++;
-      rt.row0[i] = row;
-      rt.n[i] = runs[r].n_rows;
-      rt.pos0[i] = runs[r].pos0;
-      rt.cell0[i] = runs[r].cell0;
-    }
-    row += runs[r].n_rows;
-  }
-  const dim3 grid(static_cast<unsigned>((total * Hq + 7) / 8));
-  auto go = [&](auto kernel) {
-    return launch_k(kernel, grid, dim3(256), 0, s, 1, rt, static_cast<const __half*>(q), static_cast<const __half*>(k),
-                    static_cast<const __half*>(v), Hq, Hkv, mask, words, static_cast<int>(total),
-                    static_cast<__nv_bfloat16*>(out));
+  RunsPlan p;
+  make_plan(p, runs, n_runs, Hq, Hkv, hd, tree);
+  if (work_bytes < WORK_HEADER + p.state_bytes) return fail(PF_E_ARG, "the scratch is smaller than these runs need");
+  int* err = static_cast<int*>(work);
+  float* part = reinterpret_cast<float*>(static_cast<uint8_t*>(work) + WORK_HEADER);
+  auto go = [&](auto launch) {
+    return launch(p, static_cast<const __half*>(q), static_cast<const __half*>(k), static_cast<const __half*>(v),
+                  n_cells, static_cast<int>(total), mask, words, static_cast<__nv_bfloat16*>(out), part, err, s);
   };
-  const cudaError_t e = hd == 256 ? (tree ? go(attn_runs_kernel<256, true>) : go(attn_runs_kernel<256, false>))
-                                  : (tree ? go(attn_runs_kernel<64, true>) : go(attn_runs_kernel<64, false>));
+  const cudaError_t e = hd == 256 ? (tree ? go(launch_runs<256, true>) : go(launch_runs<256, false>))
+                                  : (tree ? go(launch_runs<64, true>) : go(launch_runs<64, false>));
   if (e != cudaSuccess) return fail(PF_E_CUDA, std::string("attention launch: ") + cudaGetErrorString(e));
   return PF_OK;
 }
@@ -164,7 +870,12 @@ extern "C" int64_t pfop_attention_work_bytes(int32_t Hq, int32_t Hkv, int32_t hd
                                              int32_t n_runs) {
   int64_t total = 0;
   const int rc = check_runs(Hq, Hkv, hd, runs, n_runs, -1, &total);
-  return rc != PF_OK ? rc : WORK_HEADER;
+  if (rc != PF_OK) return rc;
+  if (total == 0) return WORK_HEADER;
+  RunsPlan a, b;
+  make_plan(a, runs, n_runs, Hq, Hkv, hd, false);
+  make_plan(b, runs, n_runs, Hq, Hkv, hd, true);
+  return WORK_HEADER + std::max(a.state_bytes, b.state_bytes);
 }
 
 extern "C" int pfop_attention_status(void* work_dev, void* stream) {

@@ -27,8 +27,9 @@ static PFN_encodeTiled_t get_encode_fn(std::string* err) {
   return fn;
 }
 
-bool encode_fp16_sw128(CUtensorMap* map, const void* base, int rank, const uint64_t* dims,
-                       const uint64_t* strides_bytes, const uint32_t* box, std::string* err) {
+static bool encode_fp16(CUtensorMap* map, const void* base, int rank, const uint64_t* dims,
+                        const uint64_t* strides_bytes, const uint32_t* box, CUtensorMapSwizzle swizzle,
+                        std::string* err) {
   PFN_encodeTiled_t enc = get_encode_fn(err);
   if (!enc) return false;
   cuuint64_t d[5], st[4];
@@ -40,13 +41,23 @@ bool encode_fp16_sw128(CUtensorMap* map, const void* base, int rank, const uint6
     if (i + 1 < rank) st[i] = strides_bytes[i];
   }
   CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, static_cast<cuuint32_t>(rank), const_cast<void*>(base), d, st,
-                   b, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   b, es, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) {
     if (err) *err = "cuTensorMapEncodeTiled failed (" + std::to_string((int)r) + ")";
     return false;
   }
   return true;
+}
+
+bool encode_fp16_sw128(CUtensorMap* map, const void* base, int rank, const uint64_t* dims,
+                       const uint64_t* strides_bytes, const uint32_t* box, std::string* err) {
+  return encode_fp16(map, base, rank, dims, strides_bytes, box, CU_TENSOR_MAP_SWIZZLE_128B, err);
+}
+
+bool encode_fp16_sw64(CUtensorMap* map, const void* base, int rank, const uint64_t* dims,
+                      const uint64_t* strides_bytes, const uint32_t* box, std::string* err) {
+  return encode_fp16(map, base, rank, dims, strides_bytes, box, CU_TENSOR_MAP_SWIZZLE_64B, err);
 }
 
 static bool encode_2d_bf16(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer, uint32_t box_inner,

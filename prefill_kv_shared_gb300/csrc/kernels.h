@@ -81,6 +81,9 @@ bool make_act_map(ActMat& a, std::string* err);
 // fp16 tensor map with the 128-byte swizzle (rank 2..5; strides of dims 1..)
 bool encode_fp16_sw128(CUtensorMap* map, const void* base, int rank, const uint64_t* dims,
                        const uint64_t* strides_bytes, const uint32_t* box, std::string* err);
+// the same with the 64-byte swizzle (boxes of 32 elements along dim 0)
+bool encode_fp16_sw64(CUtensorMap* map, const void* base, int rank, const uint64_t* dims,
+                      const uint64_t* strides_bytes, const uint32_t* box, std::string* err);
 bool make_weight_map(WeightMat& w, std::string* err);
 
 // k-splits (cluster size) for a weight shape, chosen from the shape and the
