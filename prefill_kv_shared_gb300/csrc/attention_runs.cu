@@ -20,15 +20,17 @@
 // chunks in flight beside Q at hd 256.
 //
 // Roles of a CTA: warp 1 copies Q and the K/V halves by TMA (one ring of
-// stages, in the order in which the MMAs use them); warp 0 of the even CTA
-// issues the MMAs of the pair, warp 0 of the odd CTA passes its ring's
-// arrivals on to it; warps 2..5 own the CTA's 128 rows (thread = TMEM lane =
+// stages, in the order in which the MMAs use them; the copies of both CTAs
+// complete on the even CTA's barriers); warp 0 of the even CTA issues the
+// MMAs of the pair; the others own the CTA's 128 rows (thread = TMEM lane =
 // row): softmax, P (fp16, over the columns of S that it came from), the
-// rescale of O, the output.  With hd 256 there are two S buffers, so S of
-// the next chunk is formed while P of this one is; with hd 64 there is one,
-// and two CTAs on an SM keep its tensor cores and exponentials busy.  All
-// waits are bounded (PF_WAIT_CYCLES): one that gives up flags the scratch's
-// error word and the pair unwinds.
+// rescale of O, the output.  Two S buffers let S of the next chunk be formed
+// while P of this one is.  At hd 256 one warpgroup (warps 2..5) keeps up
+// with the MMAs; at hd 64, where a chunk has a quarter of the MMA work for
+// the same exponentials, two warpgroups take one half of every chunk's keys
+// each, with their own m, l and O (TMEM has room for two), and join them at
+// the end.  All waits are bounded (PF_WAIT_CYCLES): one that gives up flags
+// the scratch's error word and the pair unwinds.
 #include "../../include/prefill_ops.h"
 #include "attn.cuh"
 #include "common.cuh"
@@ -64,16 +66,17 @@ struct RunsCfg {
   static constexpr int Q_BYTES = 128 * HD * 2;  // [64-dim box][128 rows][128 B]
   static constexpr int STAGE = 64 * HD * 2;     // half a chunk: K [box][64 keys][128 B], V [box][128 keys][hd/2 dims]
   static constexpr int NST = HD == 256 ? 5 : 8;
-  static constexpr int NSB = HD == 256 ? 2 : 1;  // S buffers
-  static constexpr int OCC = HD == 256 ? 1 : 2;  // CTAs per SM
+  static constexpr int NH = HD == 256 ? 1 : 2;  // parts of a chunk's keys, a warpgroup each
+  static constexpr int KPT = RCH / NH;          // keys per thread and chunk
   static constexpr int OFF_ST = Q_BYTES;
   static constexpr int OFF_BAR = OFF_ST + NST * STAGE;
-  static constexpr int SMEM = OFF_BAR + 256 + 1024;  // + barriers, + alignment slack
-  static constexpr int TMEM_S = 0;
-  static constexpr int TMEM_O = NSB * RCH;
-  static constexpr int TMEM_COLS = TMEM_O + HD <= 256 ? 256 : 512;
-  static_assert(TMEM_O + HD <= TMEM_COLS && TMEM_COLS * OCC <= 512, "TMEM");
-  static constexpr int THREADS = 192;
+  static constexpr int OFF_ML = OFF_BAR + 256;        // (m, l) of each part's rows
+  static constexpr int SMEM = OFF_ML + (NH > 1 ? NH * 128 * 8 : 0) + 1024;  // + alignment slack
+  static constexpr int TMEM_S = 0;          // two S buffers
+  static constexpr int TMEM_O = 2 * RCH;    // one O per part
+  static constexpr int TMEM_COLS = 512;
+  static_assert(TMEM_O + NH * HD <= TMEM_COLS, "TMEM");
+  static constexpr int THREADS = 64 + 128 * NH;
   static_assert(SMEM <= 232448, "shared memory");
 };
 
@@ -101,6 +104,33 @@ __device__ __forceinline__ void tc_mma_f16_ts_pair(uint32_t d_tmem, uint32_t a_t
       "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
       "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
+}
+
+// TMA copies of a pair: into this CTA's shared memory, completing on the
+// barrier at a shared::cluster address (here always the even CTA's)
+__device__ __forceinline__ void tma_load_3d_pair(void* smem_dst, const CUtensorMap* map, uint32_t bar, int c0, int c1,
+                                                 int c2) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.cta_group::2 "
+      "[%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(smem_dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_4d_pair(void* smem_dst, const CUtensorMap* map, uint32_t bar, int c0, int c1,
+                                                 int c2, int c3) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes.cta_group::2 "
+      "[%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(smem_u32(smem_dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+      : "memory");
+}
+
+// Arrive on a barrier of the pair without ordering other memory: what is
+// handed over lies in TMEM and is ordered by the tcgen05 fences around the
+// arrive and the wait.  (A release at cluster scope waits for all of the
+// thread's outstanding accesses: it was the kernel's first stall.)
+__device__ __forceinline__ void mbar_arrive_pair_relaxed(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
 // two fp32 operations in one instruction
@@ -193,7 +223,7 @@ __device__ __forceinline__ void exp_scores(const uint32_t (&x)[32], uint64_t c2,
 }
 
 template <int HD, bool TREE>
-__global__ void __launch_bounds__(RunsCfg<HD>::THREADS, RunsCfg<HD>::OCC)
+__global__ void __launch_bounds__(RunsCfg<HD>::THREADS, 1)
     attn_runs_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                      const __grid_constant__ CUtensorMap tmV, const __grid_constant__ RunTable rt, const RunsShape sh,
                      const uint64_t* __restrict__ mask, int words, __nv_bfloat16* __restrict__ out,
@@ -205,15 +235,16 @@ __global__ void __launch_bounds__(RunsCfg<HD>::THREADS, RunsCfg<HD>::OCC)
   // descriptor addresses both): same kernel, same alignment rounding.
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
-  uint64_t* q_full = bars;
-  uint64_t* full = bars + 1;     // NST: a stage has landed (in the even CTA: in both CTAs)
-  uint64_t* empty = bars + 9;    // NST: the MMAs have read it
-  uint64_t* s_full = bars + 17;  // NSB
-  uint64_t* p_full = bars + 19;  // NSB, the even CTA's counts the warps of both
-  uint64_t* pv_done = bars + 21;  // 2, by chunk parity
-  uint64_t* drain = bars + 23;    // error path only
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 24);
-  static_assert(C::NST <= 8 && C::NSB <= 2, "barrier layout");
+  uint64_t* q_full = bars;        // in the even CTA: Q of both has landed
+  uint64_t* full = bars + 1;      // NST, in the even CTA: a stage has landed in both
+  uint64_t* empty = bars + 9;     // NST: the MMAs have read it
+  uint64_t* s_full = bars + 17;   // by S buffer (chunk parity)
+  uint64_t* p_full = bars + 19;   // [part][S buffer], the even CTA's count the warps of both
+  uint64_t* pv_done = bars + 23;  // by chunk parity
+  uint64_t* tail = bars + 25;     // odd CTA: V of the last chunk has landed; even CTA: it is cleared there
+  uint64_t* drain = bars + 26;    // error path only
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 27);
+  static_assert(C::NST <= 8 && C::NH <= 2, "barrier layout");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = static_cast<int>(cluster_ctarank());
@@ -243,18 +274,17 @@ __global__ void __launch_bounds__(RunsCfg<HD>::THREADS, RunsCfg<HD>::OCC)
   auto row_warps = [&](int r) { return min(4, max(0, (total_rows - R0 - r * 128 + 31) >> 5)); };
 
   if (threadIdx.x == 0) {
-    const uint32_t both = rank == 0 ? 2 : 1;  // the odd CTA's arrival is passed on
-    mbar_init(q_full, both);
+    mbar_init(q_full, 1);
     for (int b = 0; b < C::NST; ++b) {
-      mbar_init(&full[b], both);
+      mbar_init(&full[b], 1);
       mbar_init(&empty[b], 1);
     }
-    for (int b = 0; b < C::NSB; ++b) {
+    for (int b = 0; b < 2; ++b) {
       mbar_init(&s_full[b], 1);
-      mbar_init(&p_full[b], row_warps(0) + row_warps(1));
+      mbar_init(&pv_done[b], 1);
     }
-    mbar_init(&pv_done[0], 1);
-    mbar_init(&pv_done[1], 1);
+    for (int b = 0; b < 2 * C::NH; ++b) mbar_init(&p_full[b], row_warps(0) + row_warps(1));
+    mbar_init(tail, 1);
     mbar_init(drain, 1);
     fence_mbar_init();
   }
@@ -271,23 +301,20 @@ __global__ void __launch_bounds__(RunsCfg<HD>::THREADS, RunsCfg<HD>::OCC)
   const uint32_t tmem = *tmem_slot;
   pdl_wait();
 
-  // K(i) and V(i) in the order of their use: with two S buffers S(i+1) is
-  // formed before P(i) V(i)
+  // K(i) and V(i) in the order of their use: S(i+1) is formed before P(i) V(i)
   const int n_seq = 2 * n;
-  auto seq_is_k = [&](int u) { return C::NSB == 2 ? (u == 0 || (u < n_seq - 1 && (u & 1))) : !(u & 1); };
-  auto seq_chunk = [&](int u) {
-    if (C::NSB == 2) return u == 0 ? 0 : u == n_seq - 1 ? n - 1 : (u & 1) ? (u + 1) / 2 : u / 2 - 1;
-    return u / 2;
-  };
-  // zero the V rows of keys past the run in a landed stage: P is 0 there,
-  // but what lies in those cells may be an infinity or NaN
-  auto clear_tail = [&](int u) {
-    const int left = run_keys - (ch_first + seq_chunk(u)) * RCH;
-    if (left >= RCH) return;
+  auto seq_is_k = [&](int u) { return u == 0 || (u < n_seq - 1 && (u & 1)); };
+  auto seq_chunk = [&](int u) { return u == 0 ? 0 : u == n_seq - 1 ? n - 1 : (u & 1) ? (u + 1) / 2 : u / 2 - 1; };
+  // The V rows of keys past the run (only in the run's last chunk) are
+  // cleared in shared memory before the MMAs read them: P is 0 there, but
+  // what lies in those cells may be an infinity or NaN.
+  const int tail_keys = run_keys - (ch_first + n - 1) * RCH;  // of the item's last chunk
+  const bool has_tail = tail_keys < RCH;
+  auto clear_tail = [&]() {
     constexpr int VB = HD == 256 ? 128 : 64;  // bytes of a key's row in a box
-    uint8_t* v = smem + C::OFF_ST + (u % C::NST) * C::STAGE;
+    uint8_t* v = smem + C::OFF_ST + ((n_seq - 1) % C::NST) * C::STAGE;
     for (int box = 0; box < C::STAGE / (RCH * VB); ++box)
-      for (int o = left * VB + lane * 16; o < RCH * VB; o += 512)
+      for (int o = tail_keys * VB + lane * 16; o < RCH * VB; o += 512)
         *reinterpret_cast<uint4*>(v + box * RCH * VB + o) = make_uint4(0u, 0u, 0u, 0u);
     fence_proxy_async_smem();
     __syncwarp();
@@ -296,41 +323,48 @@ __global__ void __launch_bounds__(RunsCfg<HD>::THREADS, RunsCfg<HD>::OCC)
   if (warp == 1) {
     // ---------------- TMA producer (each CTA its own rows and halves)
     if (lane == 0) {
-      mbar_arrive_expect_tx(q_full, C::Q_BYTES);
-      tma_load_4d(smem, &tmQ, q_full, 0, kvh << sh.log_g, row0 + (RC >> sh.log_g), 0);
+      if (rank == 0) mbar_arrive_expect_tx(q_full, 2 * C::Q_BYTES);
+      tma_load_4d_pair(smem, &tmQ, map_to_rank(smem_u32(q_full), 0), 0, kvh << sh.log_g, row0 + (RC >> sh.log_g), 0);
       bool ok = true;
       int u = 0;
       for (; u < n_seq && ok; ++u) {
         const int s = u % C::NST;
-        if (u >= C::NST) ok = mbar_wait<true>(&empty[s], ((u - C::NST) / C::NST) & 1, err, PF_DEV_TIMEOUT_PRODUCER);
+        if (u >= C::NST) ok = mbar_wait(&empty[s], ((u - C::NST) / C::NST) & 1, err, PF_DEV_TIMEOUT_PRODUCER);
         if (!ok) break;
         uint8_t* dst = smem + C::OFF_ST + s * C::STAGE;
         const int cell = rt.cell0[run] + (ch_first + seq_chunk(u)) * RCH;
-        mbar_arrive_expect_tx(&full[s], C::STAGE);
-        if (seq_is_k(u))
-          tma_load_3d(dst, &tmK, &full[s], kvh * HD, cell + rank * 64, 0);
-        else
-          tma_load_3d(dst, &tmV, &full[s], kvh * HD + rank * (HD / 2), cell, 0);
+        const bool last = has_tail && u == n_seq - 1;
+        const uint32_t bar = map_to_rank(smem_u32(&full[s]), 0);
+        if (rank == 0) mbar_arrive_expect_tx(&full[s], last ? C::STAGE : 2 * C::STAGE);
+        if (seq_is_k(u)) {
+          tma_load_3d_pair(dst, &tmK, bar, kvh * HD, cell + rank * 64, 0);
+        } else if (last && rank == 1) {
+          mbar_arrive_expect_tx(tail, C::STAGE);
+          tma_load_3d(dst, &tmV, tail, kvh * HD + HD / 2, cell, 0);
+        } else {
+          tma_load_3d_pair(dst, &tmV, bar, kvh * HD + rank * (HD / 2), cell, 0);
+        }
       }
-      // On an error the copies in flight land before this CTA may leave.
+      // On an error the copies in flight land before the pair may leave (the
+      // even CTA's barriers count those of both).
       if (!ok || read_error(err) != 0) {
-        runs_drain(q_full, 0);
-        for (int x = max(0, u - C::NST); x < u; ++x) runs_drain(&full[x % C::NST], (x / C::NST) & 1);
+        if (rank == 0) {
+          runs_drain(q_full, 0);
+          for (int x = max(0, u - C::NST); x < u; ++x) runs_drain(&full[x % C::NST], (x / C::NST) & 1);
+        } else if (has_tail && u == n_seq) {
+          runs_drain(tail, 0);
+        }
       }
     }
     __syncwarp();
   } else if (warp == 0 && rank == 1) {
-    // ---------------- arrivals of the odd CTA, passed on to the issuer
-    bool ok = mbar_wait(q_full, 0, err, PF_DEV_TIMEOUT_MMA);
-    ok = __all_sync(0xffffffffu, ok);
-    if (ok && lane == 0) mbar_arrive_cluster(map_to_rank(smem_u32(q_full), 0));
-    for (int u = 0; u < n_seq && ok; ++u) {
-      const int s = u % C::NST;
-      ok = mbar_wait(&full[s], (u / C::NST) & 1, err, PF_DEV_TIMEOUT_MMA);
+    if (has_tail) {
+      bool ok = mbar_wait(tail, 0, err, PF_DEV_TIMEOUT_MMA);
       ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
-      if (!seq_is_k(u)) clear_tail(u);
-      if (lane == 0) mbar_arrive_cluster(map_to_rank(smem_u32(&full[s]), 0));
+      if (ok) {
+        clear_tail();
+        if (lane == 0) mbar_arrive_cluster(map_to_rank(smem_u32(tail), 0));
+      }
     }
     __syncwarp();
   } else if (warp == 0) {
@@ -340,24 +374,20 @@ __global__ void __launch_bounds__(RunsCfg<HD>::THREADS, RunsCfg<HD>::OCC)
     constexpr uint32_t id_qk = idesc_f16_f32(256, RCH, false);
     constexpr uint32_t id_pv = idesc_f16_f32(256, HD, true);
     const uint64_t qd0 = sdesc_sw128(smem_u32(smem));
-    bool ok = mbar_wait<true>(q_full, 0, err, PF_DEV_TIMEOUT_MMA);
+    bool ok = mbar_wait_spin(q_full, 0, err, PF_DEV_TIMEOUT_MMA);
     ok = __all_sync(0xffffffffu, ok);
     bool issued = false;
     for (int u = 0; u < n_seq && ok; ++u) {
       const int s = u % C::NST, j = seq_chunk(u);
-      const int b = C::NSB == 2 ? j & 1 : 0;
+      const int b = j & 1;
       const uint32_t st = smem_u32(smem + C::OFF_ST + s * C::STAGE);
-      const bool is_k = seq_is_k(u);
-      ok = mbar_wait<true>(&full[s], (u / C::NST) & 1, err, PF_DEV_TIMEOUT_MMA);
-      if (ok && !is_k)
-        ok = mbar_wait<true>(&p_full[b], (C::NSB == 2 ? j >> 1 : j) & 1, err, PF_DEV_TIMEOUT_MMA);
+      ok = mbar_wait_spin(&full[s], (u / C::NST) & 1, err, PF_DEV_TIMEOUT_MMA);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
-      if (!is_k) clear_tail(u);
-      tc_fence_after();
-      if (leader) {
-        if (is_k) {
-          // S(j): P(j - NSB), which lay in this buffer, was read by an MMA issued before
+      if (seq_is_k(u)) {
+        // S(j): P(j-2), which lay in this buffer, was read by MMAs issued before
+        tc_fence_after();
+        if (leader) {
           const uint64_t kd0 = sdesc_sw128(st);
 #pragma unroll
           for (int kk = 0; kk < HD / 16; ++kk) {
@@ -367,16 +397,34 @@ __global__ void __launch_bounds__(RunsCfg<HD>::THREADS, RunsCfg<HD>::OCC)
           }
           tc_commit_pair(map_to_rank(smem_u32(&s_full[b]), 0));
           tc_commit_pair(map_to_rank(smem_u32(&s_full[b]), 1));
-        } else {
-          const uint64_t vd0 = HD == 256 ? sdesc_sw128_lbo_sbo(st, RCH * 128, 1024) : sdesc_sw64_mn(st);
-          constexpr int KSTEP = 16 * (HD == 256 ? 128 : 64);  // bytes of 16 keys
-#pragma unroll
-          for (int kk = 0; kk < RCH / 16; ++kk)
-            tc_mma_f16_ts_pair(tmem + C::TMEM_O, tmem + C::TMEM_S + b * RCH + kk * 8, vd0 + ((kk * KSTEP) >> 4), id_pv,
-                               (j > 0 || kk > 0) ? 1u : 0u);
-          tc_commit_pair(map_to_rank(smem_u32(&pv_done[j & 1]), 0));
-          tc_commit_pair(map_to_rank(smem_u32(&pv_done[j & 1]), 1));
         }
+      } else {
+        if (has_tail && u == n_seq - 1) {
+          ok = mbar_wait<true>(tail, 0, err, PF_DEV_TIMEOUT_MMA);
+          clear_tail();
+        }
+        const uint64_t vd0 = HD == 256 ? sdesc_sw128_lbo_sbo(st, RCH * 128, 1024) : sdesc_sw64_mn(st);
+        constexpr int KSTEP = 16 * (HD == 256 ? 128 : 64);  // bytes of 16 keys
+#pragma unroll
+        for (int h = 0; h < C::NH; ++h) {
+          if (ok) ok = mbar_wait_spin(&p_full[2 * h + b], (j >> 1) & 1, err, PF_DEV_TIMEOUT_MMA);
+          ok = __all_sync(0xffffffffu, ok);
+          tc_fence_after();
+          if (ok && leader) {
+#pragma unroll
+            for (int kk = 0; kk < C::KPT / 16; ++kk)
+              tc_mma_f16_ts_pair(tmem + C::TMEM_O + h * HD, tmem + C::TMEM_S + b * RCH + h * C::KPT + kk * 8,
+                                 vd0 + (((h * (C::KPT / 16) + kk) * KSTEP) >> 4), id_pv, (j > 0 || kk > 0) ? 1u : 0u);
+          }
+          __syncwarp();
+        }
+        if (!ok) break;
+        if (leader) {
+          tc_commit_pair(map_to_rank(smem_u32(&pv_done[b]), 0));
+          tc_commit_pair(map_to_rank(smem_u32(&pv_done[b]), 1));
+        }
+      }
+      if (leader) {
         tc_commit_pair(map_to_rank(smem_u32(&empty[s]), 0));
         tc_commit_pair(map_to_rank(smem_u32(&empty[s]), 1));
       }
@@ -390,57 +438,49 @@ __global__ void __launch_bounds__(RunsCfg<HD>::THREADS, RunsCfg<HD>::OCC)
     }
     __syncwarp();
   } else if ((warp & 3) < row_warps(rank)) {
-    // ---------------- rows (warps 2..5: TMEM lane quarter warp % 4)
-    const int qw = warp & 3;
+    // ---------------- rows (warps 2..: TMEM lane quarter warp % 4, part h of each chunk)
+    const int qw = warp & 3, h = (warp - 2) >> 2;
     const int R = RC + 32 * qw + lane;
     const int t = R >> sh.log_g, head = (kvh << sh.log_g) + (R & ((1 << sh.log_g) - 1));
     const bool row = R < total_rows;
     const int pos = row ? pos0 + t : -1;
     const uint64_t* row_mask = TREE && row ? mask + static_cast<size_t>(row0 + t) * words : nullptr;
     const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * qw) << 16);
-    constexpr bool KEEP = HD == 256;  // registers hold a chunk's scores (hd 64: they are read twice)
+    constexpr int NB = C::KPT / 32;
     const uint64_t c2 = pack_f32x2(cexp, cexp);
     float m = -INFINITY, l = 0.f;
     bool ok = true;
     for (int j = 0; j < n && ok; ++j) {
-      const int b = C::NSB == 2 ? j & 1 : 0;
-      const int key0 = (ch_first + j) * RCH;
-      const uint32_t ts = lanes + C::TMEM_S + b * RCH;
-      if (lane == 0) ok = mbar_wait<true>(&s_full[b], (C::NSB == 2 ? j >> 1 : j) & 1, err, PF_DEV_TIMEOUT_EPILOGUE);
+      const int b = j & 1;
+      const int key0 = (ch_first + j) * RCH + h * C::KPT;
+      const uint32_t ts = lanes + C::TMEM_S + b * RCH + h * C::KPT;
+      if (lane == 0) ok = mbar_wait_spin(&s_full[b], (j >> 1) & 1, err, PF_DEV_TIMEOUT_EPILOGUE);
       ok = __shfl_sync(0xffffffffu, ok, 0);
       if (!ok) break;
       tc_fence_after();
-      // the row's view of the chunk, skipped where every row of the warp sees all of it
-      const bool all = TREE ? key0 + RCH <= pos0 : __all_sync(0xffffffffu, pos >= key0 + RCH - 1);
-      uint32_t bits[4];
+      uint32_t x[NB][32];
+#pragma unroll
+      for (int w = 0; w < NB; ++w) tmem_ld32(ts + 32 * w, x[w]);
+      // the row's view of its keys, skipped where every row of the warp sees all of them
+      const bool all = TREE ? key0 + C::KPT <= pos0 : __all_sync(0xffffffffu, pos >= key0 + C::KPT - 1);
+#pragma unroll
+      for (int w = 0; w < NB; ++w) tmem_ld_wait32(x[w]);
       if (!all) {
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
+        for (int w = 0; w < NB; ++w) {
+          uint32_t bits;
           if (TREE) {
-            bits[w] = row ? tree_bits(row_mask, words, pos0, n_rows, key0 + 32 * w) : 0u;
+            bits = row ? tree_bits(row_mask, words, pos0, n_rows, key0 + 32 * w) : 0u;
           } else {
             const int nv = pos - key0 - 32 * w + 1;
-            bits[w] = nv >= 32 ? 0xffffffffu : nv <= 0 ? 0u : (1u << nv) - 1u;
+            bits = nv >= 32 ? 0xffffffffu : nv <= 0 ? 0u : (1u << nv) - 1u;
           }
+          mask_scores(x[w], bits);
         }
       }
-      uint32_t x[KEEP ? 4 : 2][32];
       float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-      for (int h = 0; h < 4; h += 2) {
-        uint32_t(&x0)[32] = x[KEEP ? h : 0];
-        uint32_t(&x1)[32] = x[KEEP ? h + 1 : 1];
-        tmem_ld32(ts + 32 * h, x0);
-        tmem_ld32(ts + 32 * h + 32, x1);
-        tmem_ld_wait32(x0);
-        tmem_ld_wait32(x1);
-        if (!all) {
-          mask_scores(x0, bits[h]);
-          mask_scores(x1, bits[h + 1]);
-        }
-        max_scores(x0, mx);
-        max_scores(x1, mx);
-      }
+      for (int w = 0; w < NB; ++w) max_scores(x[w], mx);
       const float mj = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
       // The reference moves only when this chunk's maximum passes it by more
       // than 2^8 (or on the row's first visible keys); until then P is taken
@@ -453,23 +493,11 @@ __global__ void __launch_bounds__(RunsCfg<HD>::THREADS, RunsCfg<HD>::OCC)
       const uint64_t nmc2 = pack_f32x2(nmc, nmc);
       uint64_t ls[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll
-      for (int h = 0; h < 4; h += 2) {
-        uint32_t(&x0)[32] = x[KEEP ? h : 0];
-        uint32_t(&x1)[32] = x[KEEP ? h + 1 : 1];
-        if (!KEEP) {
-          tmem_ld32(ts + 32 * h, x0);
-          tmem_ld32(ts + 32 * h + 32, x1);
-          tmem_ld_wait32(x0);
-          tmem_ld_wait32(x1);
-          if (!all) {
-            mask_scores(x0, bits[h]);
-            mask_scores(x1, bits[h + 1]);
-          }
-        }
+      for (int w = 0; w < NB; w += 2) {
         uint32_t pw[32];  // 64 fp16 probabilities
-        exp_scores(x0, c2, nmc2, pw, ls);
-        exp_scores(x1, c2, nmc2, pw + 16, ls);
-        tmem_st32(ts + 16 * h, pw);  // over scores that have been read
+        exp_scores(x[w], c2, nmc2, pw, ls);
+        exp_scores(x[w + 1], c2, nmc2, pw + 16, ls);
+        tmem_st32(ts + 16 * w, pw);  // over scores that have been read
       }
       const float2 l01 = unpack_f32x2(add_f32x2(add_f32x2(ls[0], ls[1]), add_f32x2(ls[2], ls[3])));
       l = __fmaf_rn(l, scale, l01.x + l01.y);
@@ -479,28 +507,41 @@ __global__ void __launch_bounds__(RunsCfg<HD>::THREADS, RunsCfg<HD>::OCC)
       // moved its reference.  (S(j) was issued after P V(j-2), so each of the
       // two barriers has at most the awaited phase outstanding.)
       if (j >= 1 && __any_sync(0xffffffffu, resc)) {
-        if (lane == 0) ok = mbar_wait<true>(&pv_done[(j - 1) & 1], ((j - 1) >> 1) & 1, err, PF_DEV_TIMEOUT_EPILOGUE);
+        if (lane == 0) ok = mbar_wait(&pv_done[(j - 1) & 1], ((j - 1) >> 1) & 1, err, PF_DEV_TIMEOUT_EPILOGUE);
         ok = __shfl_sync(0xffffffffu, ok, 0);
         if (!ok) break;
         tc_fence_after();
 #pragma unroll 1
         for (int c = 0; c < HD / 32; ++c) {
           uint32_t y[32];
-          tmem_ld32(lanes + C::TMEM_O + 32 * c, y);
+          tmem_ld32(lanes + C::TMEM_O + h * HD + 32 * c, y);
           tmem_ld_wait32(y);
 #pragma unroll
           for (int q = 0; q < 32; ++q) y[q] = __float_as_uint(__uint_as_float(y[q]) * scale);
-          tmem_st32(lanes + C::TMEM_O + 32 * c, y);
+          tmem_st32(lanes + C::TMEM_O + h * HD + 32 * c, y);
         }
         tmem_st_wait();
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(map_to_rank(smem_u32(&p_full[b]), 0));
+      if (lane == 0) mbar_arrive_pair_relaxed(map_to_rank(smem_u32(&p_full[2 * h + b]), 0));
     }
     if (ok) {
-      if (lane == 0) ok = mbar_wait<true>(&pv_done[(n - 1) & 1], ((n - 1) >> 1) & 1, err, PF_DEV_TIMEOUT_EPILOGUE);
+      if (lane == 0) ok = mbar_wait_spin(&pv_done[(n - 1) & 1], ((n - 1) >> 1) & 1, err, PF_DEV_TIMEOUT_EPILOGUE);
       ok = __shfl_sync(0xffffffffu, ok, 0);
+    }
+    // the parts' weights: w_h = 2^((m_h - m) c); each of a row's two warps
+    // writes half of the dims
+    float w0 = 1.f, w1 = 0.f;
+    if constexpr (C::NH > 1) {
+      float2* ml = reinterpret_cast<float2*>(smem + C::OFF_ML);
+      ml[h * 128 + 32 * qw + lane] = make_float2(ok ? m : __int_as_float(0x7fc00000), l);
+      asm volatile("bar.sync %0, 64;" ::"r"(1 + qw) : "memory");
+      const float2 a = ml[32 * qw + lane], c = ml[128 + 32 * qw + lane];
+      m = fmaxf(a.x, c.x);
+      w0 = a.x == -INFINITY ? 0.f : ex2_approx((a.x - m) * cexp);
+      w1 = c.x == -INFINITY ? 0.f : ex2_approx((c.x - m) * cexp);
+      l = w0 * a.y + w1 * c.y;
     }
     if (ok) {
       // Every MMA of the pair and every copy is done.  Each 32 x 32 block of O
@@ -511,6 +552,8 @@ __global__ void __launch_bounds__(RunsCfg<HD>::THREADS, RunsCfg<HD>::OCC)
       const int n_g = !row ? 0 : TREE ? rt.groups[run] : (pos / RCH) / sh.gc + 1;
       const int kind = grp >= n_g ? 0 : n_g == 1 ? 1 : 2;  // 1: output row, 2: group state
       const float inv = kind != 1 ? 1.f : l == 0.f ? 0.f : __frcp_rn(l);  // a row that sees nothing: zeros
+      w0 *= inv;
+      w1 *= inv;
       const size_t own = kind == 1 ? (static_cast<size_t>(row0 + t) * sh.Hq + head) * HD
                                    : (static_cast<size_t>(idx) * sh.slot_rows + (R - R0)) * runs_state_stride(HD);
       const int rs = lane >> 3, pc = lane & 7;
@@ -521,17 +564,27 @@ __global__ void __launch_bounds__(RunsCfg<HD>::THREADS, RunsCfg<HD>::OCC)
         dk[i] = __shfl_sync(0xffffffffu, kind, 4 * i + rs);
         dst[i] = __shfl_sync(0xffffffffu, static_cast<unsigned long long>(own), 4 * i + rs);
       }
-      uint8_t* stg = smem + C::OFF_ST + qw * 4096;
+      uint8_t* stg = smem + C::OFF_ST + (h * 4 + qw) * 4096;
 #pragma unroll 1
-      for (int c = 0; c < HD / 32; ++c) {
+      for (int c = h * (HD / 32 / C::NH); c < (h + 1) * (HD / 32 / C::NH); ++c) {
         uint32_t y[32];
         tmem_ld32(lanes + C::TMEM_O + 32 * c, y);
         tmem_ld_wait32(y);
+        if constexpr (C::NH > 1) {
+          uint32_t z[32];
+          tmem_ld32(lanes + C::TMEM_O + HD + 32 * c, z);
+          tmem_ld_wait32(z);
+#pragma unroll
+          for (int q = 0; q < 32; ++q)
+            y[q] = __float_as_uint(__fmaf_rn(w0, __uint_as_float(y[q]), w1 * __uint_as_float(z[q])));
+        } else {
+#pragma unroll
+          for (int q = 0; q < 32; ++q) y[q] = __float_as_uint(w0 * __uint_as_float(y[q]));
+        }
 #pragma unroll
         for (int q = 0; q < 8; ++q)
-          *reinterpret_cast<float4*>(stg + lane * 128 + ((q ^ (lane & 7)) << 4)) =
-              make_float4(__uint_as_float(y[4 * q]) * inv, __uint_as_float(y[4 * q + 1]) * inv,
-                          __uint_as_float(y[4 * q + 2]) * inv, __uint_as_float(y[4 * q + 3]) * inv);
+          *reinterpret_cast<uint4*>(stg + lane * 128 + ((q ^ (lane & 7)) << 4)) =
+              make_uint4(y[4 * q], y[4 * q + 1], y[4 * q + 2], y[4 * q + 3]);
         __syncwarp();
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -548,7 +601,7 @@ __global__ void __launch_bounds__(RunsCfg<HD>::THREADS, RunsCfg<HD>::OCC)
         }
         __syncwarp();
       }
-      if (kind == 2) *reinterpret_cast<float2*>(part + own + HD) = make_float2(m, l);
+      if (kind == 2 && h == 0) *reinterpret_cast<float2*>(part + own + HD) = make_float2(m, l);
     }
   }
   tc_fence_before();
@@ -684,7 +737,7 @@ static void make_plan(RunsPlan& p, const pfop_attn_run* runs, int n_runs, int Hq
   std::stable_sort(order, order + cnt, [&](int a, int b) {
     return runs[a].pos0 + runs[a].n_rows > runs[b].pos0 + runs[b].n_rows;
   });
-  const int units = sm_count() / 2 * (hd == 256 ? RunsCfg<256>::OCC : RunsCfg<64>::OCC);
+  const int units = sm_count() / 2;
   const int fixed = hd == 256 ? 3 : 4;
   int max_ch = 0, max_rows = 0;
   double work = 0;  // chunks over all row blocks
