@@ -241,7 +241,8 @@ typedef struct pfop_attn_run {
    one may not run at once).
    PF_E_ARG: hd other than 64 or 256; n_head not a multiple of n_head_kv
    with a group size dividing 16; more than 128 runs or 2^20 rows; a run
-   past n_cells; q, k, v, out not 16-byte aligned; a scratch too small. */
+   past n_cells; q, k, v not 16-byte or out not 32-byte aligned; a scratch too
+   small. */
 int pfop_attention_packed(const void* q_dev, const void* k_dev, const void* v_dev, int64_t n_cells, int32_t Hq,
                           int32_t Hkv, int32_t hd, const pfop_attn_run* runs, int32_t n_runs, void* out_dev,
                           void* work_dev, int64_t work_bytes, void* stream);

@@ -4,14 +4,19 @@
 //
 // MMA rows are (row, head-in-group) pairs of a run: row R = t*G + g is the
 // run's row t and query head kvh*G + g, so the G heads of a KV head share its
-// K/V.  A pair of CTAs (a 2-CTA cluster, tcgen05 .cta_group::2) takes 256
-// rows of one run and KV head and a group of gc consecutive 128-key chunks
-// of the run's positions, and runs one online softmax over the group:
+// K/V.  256 consecutive rows of a run and KV head are an item.  A pair of CTAs
+// (a 2-CTA cluster, tcgen05 .cta_group::2) works through segments, a segment
+// being an item and a range of its 128-key chunks, with one online softmax:
 //     S = Q K^T, m' = max(m, max_k s_k), p_k = 2^((s_k - m') c),
 //     l' = l 2^((m - m') c) + sum_k p_k, O' = O 2^((m - m') c) + fp16(P) V
-// with c = log2(e)/sqrt(hd), S, O, m, l in fp32.  A row whose keys lie in one
-// group writes O/l; otherwise each group leaves (O, m, l) in the scratch and
-// attn_runs_merge_kernel joins them in group order.
+// with c = log2(e)/sqrt(hd), S, O, m, l in fp32.  A segment that holds all
+// chunks of its item writes O/l; otherwise (O, m, l) goes to the scratch and
+// attn_runs_merge_kernel joins the item's segments in order.
+//
+// The cut: either a pair per item, or all items laid end to end (each
+// weighing its chunks and a fixed cost) and every resident pair given the
+// same share of that line, so that long and short sequences, many rows and
+// few, load the SMs evenly (make_plan).
 //
 // Why pairs: 128 rows against a chunk need 64 bytes of K/V per SM clock at
 // the full tensor rate, more than L2 delivers to all SMs at once; 256 rows
@@ -45,43 +50,48 @@ constexpr int RUNS_MAX = 128;
 constexpr int RCH = 128;    // keys of a chunk
 constexpr int RROWS = 256;  // MMA rows of a pair
 
-// the call's runs, passed in the kernel's parameters
+// the call's runs, passed in the kernel's parameters; a run's items are its
+// row blocks, last (longest) first, once per KV head
 struct RunTable {
   int n_runs = 0;
   int row0[RUNS_MAX];  // first packed row
   int n[RUNS_MAX], pos0[RUNS_MAX], cell0[RUNS_MAX];
-  int item0[RUNS_MAX];  // first work item; a run has (row blocks) x (groups) of them
-  int groups[RUNS_MAX];
+  int item0[RUNS_MAX + 1];  // items before the run
+  int w0[RUNS_MAX + 1];     // their weight
 };
 
 struct RunsShape {
   int Hq, Hkv, log_g;  // G = 1 << log_g query heads per KV head
-  int gc;              // chunks per group
-  int slot_rows;       // rows of a state slot in the scratch
-  int items;           // work items per KV head
+  int per;             // weight of a pair's share; 0: a pair per item
+  int pairs;
+  int slot_rows;  // rows of a state slot in the scratch
 };
+
+// weight of an item besides its chunks: its Q copy, first scores and output,
+// in chunk times
+constexpr int ITEM_FIXED = 2;
 
 template <int HD>
 struct RunsCfg {
   static constexpr int Q_BYTES = 128 * HD * 2;  // [64-dim box][128 rows][128 B]
   static constexpr int STAGE = 64 * HD * 2;     // half a chunk: K [box][64 keys][128 B], V [box][128 keys][hd/2 dims]
-  static constexpr int NST = HD == 256 ? 5 : 8;
+  static constexpr int NST = HD == 256 ? 5 : 16;
   static constexpr int NH = HD == 256 ? 1 : 2;  // parts of a chunk's keys, a warpgroup each
   static constexpr int KPT = RCH / NH;          // keys per thread and chunk
   static constexpr int OFF_ST = Q_BYTES;
   static constexpr int OFF_BAR = OFF_ST + NST * STAGE;
-  static constexpr int OFF_ML = OFF_BAR + 256;        // (m, l) of each part's rows
+  static constexpr int OFF_ML = OFF_BAR + 512;        // (m, l) of each part's rows
   static constexpr int SMEM = OFF_ML + (NH > 1 ? NH * 128 * 8 : 0) + 1024;  // + alignment slack
   static constexpr int TMEM_S = 0;          // two S buffers
   static constexpr int TMEM_O = 2 * RCH;    // one O per part
   static constexpr int TMEM_COLS = 512;
   static_assert(TMEM_O + NH * HD <= TMEM_COLS, "TMEM");
-  static constexpr int THREADS = 64 + 128 * NH;
+  static constexpr int THREADS = 128 + 128 * NH;
   static_assert(SMEM <= 232448, "shared memory");
 };
 
-// floats of one row's state: o[HD], m, l, 2 pad
-__host__ __device__ constexpr int runs_state_stride(int hd) { return hd + 4; }
+// floats of one row's state: o[HD], m, l, 6 pad (32-byte rows)
+__host__ __device__ constexpr int runs_state_stride(int hd) { return hd + 8; }
 
 // 64-byte-swizzled MN-major operand descriptor: rows (K) of 64 bytes, 8-row
 // groups of 512 bytes, one 32-element atom along MN
@@ -133,6 +143,13 @@ __device__ __forceinline__ void mbar_arrive_pair_relaxed(uint32_t cluster_addr) 
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
+// a whole 32-byte sector from one thread
+__device__ __forceinline__ void st_global_v8(void* p, const uint32_t* r) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]),
+               "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+
 // two fp32 operations in one instruction
 __device__ __forceinline__ uint64_t pack_f32x2(float a, float b) {
   uint64_t d;
@@ -164,18 +181,145 @@ __device__ __forceinline__ void runs_drain(uint64_t* bar, uint32_t parity) {
   }
 }
 
-// The run of work item (or row) `it`: the last one whose first is not above it.
-__device__ __forceinline__ int find_run(const int* first, int n_runs, int it) {
-  int lo = 0, hi = n_runs - 1;
+// the last entry of first[0 .. n-1] not above x
+__host__ __device__ __forceinline__ int find_last(const int* first, int n, int x) {
+  int lo = 0, hi = n - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
-    if (first[mid] <= it)
+    if (first[mid] <= x)
       lo = mid;
     else
       hi = mid - 1;
   }
   return lo;
 }
+
+// A run's row blocks and their chunks.  Block i (counted from the run's
+// end) has block b = nb-1-i of 256 >> log_g rows; causal, it needs the
+// chunks up to its last row.
+template <bool TREE>
+struct RunBlocks {
+  int n, pos0, bs_log, nb, last;  // last: chunks of the whole run
+  __host__ __device__ RunBlocks(int n_rows, int p0, int log_g)
+      : n(n_rows), pos0(p0), bs_log(8 - log_g), nb((n_rows + (1 << bs_log) - 1) >> bs_log),
+        last(static_cast<int>((static_cast<unsigned>(p0) + n_rows + RCH - 1) / RCH)) {}
+  // sum over x' < x of floor(x' / (128 / bs)); modulo 2^32 (differences of it are exact)
+  __host__ __device__ unsigned floors(unsigned x) const {
+    const int sl = 7 - bs_log;
+    const unsigned k = x >> sl;
+    const unsigned tri = k & 1 ? k * ((k - 1) >> 1) : (k >> 1) * (k - 1);
+    return (tri << sl) + k * (x - (k << sl));
+  }
+  // chunks of blocks 0 .. B-1 from the run's start, none of them the last
+  __host__ __device__ int from_start(int B) const {
+    const unsigned c = static_cast<unsigned>(pos0) + (1u << bs_log) + RCH - 1;
+    if (bs_log == 8) return static_cast<int>(B * (c / RCH) + static_cast<unsigned>(B) * (B - 1));
+    return static_cast<int>(floors((c >> bs_log) + B) - floors(c >> bs_log));
+  }
+  __host__ __device__ int chunks(int i) const {
+    if (TREE || i == 0) return last;
+    return static_cast<int>((static_cast<unsigned>(pos0) + (static_cast<unsigned>(nb - i) << bs_log) + RCH - 1) / RCH);
+  }
+  // weight of items 0 .. i-1
+  __host__ __device__ int weight(int i) const {
+    if (TREE || i == 0) return i * (last + ITEM_FIXED);
+    return i * ITEM_FIXED + last + from_start(nb - 1) - from_start(nb - i);
+  }
+};
+
+// an item: run, KV head, row block and its place on the line of weights
+template <bool TREE>
+struct ItemAt {
+  int run, kvh, i, w;  // w: weight of all items before
+  // by its number
+  __host__ __device__ static ItemAt number(const RunTable& rt, const RunsShape& sh, int idx) {
+    ItemAt a;
+    a.run = find_last(rt.item0, rt.n_runs, idx);
+    const RunBlocks<TREE> rb(rt.n[a.run], rt.pos0[a.run], sh.log_g);
+    const int loc = idx - rt.item0[a.run];
+    a.kvh = loc / rb.nb;
+    a.i = loc % rb.nb;
+    a.w = rt.w0[a.run] + a.kvh * rb.weight(rb.nb) + rb.weight(a.i);
+    return a;
+  }
+  // the one whose weight covers x
+  __host__ __device__ static ItemAt weight(const RunTable& rt, const RunsShape& sh, int x) {
+    ItemAt a;
+    a.run = find_last(rt.w0, rt.n_runs, x);
+    const RunBlocks<TREE> rb(rt.n[a.run], rt.pos0[a.run], sh.log_g);
+    const int head = rb.weight(rb.nb);
+    int rem = x - rt.w0[a.run];
+    a.kvh = rem / head;
+    rem -= a.kvh * head;
+    int lo = 0, hi = rb.nb - 1;
+    if (TREE) {
+      lo = rem / (rb.last + ITEM_FIXED);
+    } else {
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (rb.weight(mid) <= rem)
+          lo = mid;
+        else
+          hi = mid - 1;
+      }
+    }
+    a.i = lo;
+    a.w = x - rem + rb.weight(lo);
+    return a;
+  }
+};
+
+// The segments of a pair, in order.  A pair's share is a range of the line of
+// weights; the chunk k of an item lies at w + ITEM_FIXED + k.
+template <bool TREE>
+struct Segments {
+  const RunTable& rt;
+  const RunsShape& sh;
+  ItemAt<TREE> at;
+  int pair, lo, hi;
+  bool left;
+  // the segment
+  int run, kvh, R0, ch0, n;
+  int slot;  // state slot, -1: the item's only segment
+  __host__ __device__ Segments(const RunTable& t, const RunsShape& s, int p) : rt(t), sh(s), pair(p), left(true) {
+    if (sh.per == 0) {
+      at = ItemAt<TREE>::number(rt, sh, pair);
+      lo = at.w;
+      hi = at.w + 1;  // not used
+    } else {
+      lo = pair * sh.per;
+      hi = lo + sh.per < rt.w0[rt.n_runs] ? lo + sh.per : rt.w0[rt.n_runs];
+      left = lo < hi;
+      if (left) at = ItemAt<TREE>::weight(rt, sh, lo);
+    }
+  }
+  __host__ __device__ bool next() {
+    while (left) {
+      const RunBlocks<TREE> rb(rt.n[at.run], rt.pos0[at.run], sh.log_g);
+      const int ch = rb.chunks(at.i), w = at.w + ITEM_FIXED;
+      const int k0 = sh.per == 0 || lo < w ? 0 : lo - w, k1 = sh.per == 0 || hi - w > ch ? ch : hi - w;
+      run = at.run;
+      kvh = at.kvh;
+      R0 = (rb.nb - 1 - at.i) * RROWS;
+      ch0 = k0;
+      n = k1 - k0;
+      slot = k0 > 0 ? 2 * pair : k1 < ch ? 2 * pair + 1 : -1;
+      // on to the next item
+      at.w = w + ch;
+      if (sh.per == 0 || at.w >= hi) {
+        left = false;
+      } else if (++at.i == rb.nb) {
+        at.i = 0;
+        if (++at.kvh == sh.Hkv) {
+          at.kvh = 0;
+          ++at.run;
+        }
+      }
+      if (n > 0) return true;
+    }
+    return false;
+  }
+};
 
 // bits of the keys kk .. kk+31 (positions) that the row sees: the context
 // [0, pos0), then its mask's bits for the drafted tokens [0, n)
@@ -235,136 +379,150 @@ __global__ void __launch_bounds__(RunsCfg<HD>::THREADS, 1)
   // descriptor addresses both): same kernel, same alignment rounding.
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
-  uint64_t* q_full = bars;        // in the even CTA: Q of both has landed
-  uint64_t* full = bars + 1;      // NST, in the even CTA: a stage has landed in both
-  uint64_t* empty = bars + 9;     // NST: the MMAs have read it
-  uint64_t* s_full = bars + 17;   // by S buffer (chunk parity)
-  uint64_t* p_full = bars + 19;   // [part][S buffer], the even CTA's count the warps of both
-  uint64_t* pv_done = bars + 23;  // by chunk parity
-  uint64_t* tail = bars + 25;     // odd CTA: V of the last chunk has landed; even CTA: it is cleared there
-  uint64_t* drain = bars + 26;    // error path only
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 27);
-  static_assert(C::NST <= 8 && C::NH <= 2, "barrier layout");
+  uint64_t* full = bars;            // NST, in the even CTA: a stage has landed in both; in the odd CTA: a
+                                    // V to be cleared has landed there
+  uint64_t* empty = bars + C::NST;  // NST: the MMAs that read the stage are done (its S or P V too)
+  uint64_t* cleared = bars + 2 * C::NST;  // NST, in the even CTA: the odd CTA's V is cleared
+  uint64_t* q_full = bars + 3 * C::NST;   // in the even CTA: Q of both has landed
+  uint64_t* p_full = q_full + 1;          // by S buffer (chunk parity), in the even CTA: the row warps of both
+  uint64_t* o_free = q_full + 3;          // in the even CTA: the row warps of both have read O
+  uint64_t* q_empty = q_full + 4;         // the segment's last S is formed
+  uint64_t* drain = q_full + 5;           // error path only
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(q_full + 6);
+  static_assert((3 * C::NST + 7) * 8 <= 512 && C::NH <= 2, "barrier layout");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = static_cast<int>(cluster_ctarank());
   pdl_launch();
 
-  // ---- the pair's work item
-  const int idx = static_cast<int>(blockIdx.x >> 1);
-  const int kvh = idx % sh.Hkv, it = idx / sh.Hkv;
-  const int run = find_run(rt.item0, rt.n_runs, it);
-  const int n_rows = rt.n[run], pos0 = rt.pos0[run], row0 = rt.row0[run];
-  const int total_rows = n_rows << sh.log_g;
-  const int nb = (total_rows + RROWS - 1) / RROWS;
-  const int local = it - rt.item0[run];
-  const int grp = local / nb;
-  const int R0 = (nb - 1 - local % nb) * RROWS;  // blocks with the most keys first
-  const int t_last = min(n_rows - 1, (R0 + RROWS - 1) >> sh.log_g);
-  const int keys = TREE ? pos0 + n_rows : pos0 + t_last + 1;
-  const int ch_first = grp * sh.gc;
-  const int n = min((keys + RCH - 1) / RCH, ch_first + sh.gc) - ch_first;  // chunks
-  if (n <= 0) {  // no keys of this group reach the block's rows
-    pdl_wait();
-    return;
-  }
-  const int run_keys = pos0 + n_rows;
-  const int RC = R0 + rank * 128;  // this CTA's first row
-  // warps of rows, here and in the other CTA
-  auto row_warps = [&](int r) { return min(4, max(0, (total_rows - R0 - r * 128 + 31) >> 5)); };
-
   if (threadIdx.x == 0) {
-    mbar_init(q_full, 1);
     for (int b = 0; b < C::NST; ++b) {
       mbar_init(&full[b], 1);
       mbar_init(&empty[b], 1);
+      mbar_init(&cleared[b], 1);
     }
-    for (int b = 0; b < 2; ++b) {
-      mbar_init(&s_full[b], 1);
-      mbar_init(&pv_done[b], 1);
-    }
-    for (int b = 0; b < 2 * C::NH; ++b) mbar_init(&p_full[b], row_warps(0) + row_warps(1));
-    mbar_init(tail, 1);
+    mbar_init(q_full, 1);
+    mbar_init(q_empty, 1);
+    for (int b = 0; b < 2; ++b) mbar_init(&p_full[b], 8 * C::NH);
+    mbar_init(o_free, 8 * C::NH);
     mbar_init(drain, 1);
     fence_mbar_init();
   }
   if (warp == 1 && lane == 0) {
-    prefetch_tensormap(&tmQ);
     prefetch_tensormap(&tmK);
     prefetch_tensormap(&tmV);
   }
+  if (warp == 2 && lane == 0) prefetch_tensormap(&tmQ);
   if (warp == 0) tmem_alloc_pair(tmem_slot, C::TMEM_COLS);
   tc_fence_before();
   __syncthreads();
   cluster_sync_all();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  Segments<TREE> sg(rt, sh, static_cast<int>(blockIdx.x >> 1));
   pdl_wait();
 
-  // K(i) and V(i) in the order of their use: S(i+1) is formed before P(i) V(i)
-  const int n_seq = 2 * n;
-  auto seq_is_k = [&](int u) { return u == 0 || (u < n_seq - 1 && (u & 1)); };
-  auto seq_chunk = [&](int u) { return u == 0 ? 0 : u == n_seq - 1 ? n - 1 : (u & 1) ? (u + 1) / 2 : u / 2 - 1; };
+  // Counters that run on over the pair's segments, the same in every role:
+  // ring fills (fill f uses stage f % NST, in its use number f / NST), chunks
+  // (chunk j uses S buffer j & 1) and segments.  A segment's fills: K(0),
+  // K(1), V(0), K(2), V(1), .., V(n-1), so that S(j+1) is formed before P(j)
+  // V(j).  The MMAs of a fill arrive on its stage's `empty`, which serves all
+  // who wait for them in order: the K/V producer, and the row warps for S and
+  // for P V.  (A wait by parity must not come a phase early or late.  Not
+  // early: MMAs finish in order, and a row warp that waits for a fill has
+  // seen one at most three fills before it.  Not late: the stage's next use
+  // is over only after a later P, for which the waiting warp is needed.)
+  auto k_fill = [](int jl) { return jl == 0 ? 0 : 2 * jl - 1; };
+  auto v_fill = [](int jl, int n) { return jl == n - 1 ? 2 * n - 1 : 2 * jl + 2; };
+  auto fill_is_k = [&](int u) { return u == 0 || (u < 2 * sg.n - 1 && (u & 1)); };
+  auto fill_chunk = [&](int u) {
+    return u == 0 ? 0 : u == 2 * sg.n - 1 ? sg.n - 1 : (u & 1) ? (u + 1) / 2 : u / 2 - 1;
+  };
   // The V rows of keys past the run (only in the run's last chunk) are
   // cleared in shared memory before the MMAs read them: P is 0 there, but
-  // what lies in those cells may be an infinity or NaN.
-  const int tail_keys = run_keys - (ch_first + n - 1) * RCH;  // of the item's last chunk
-  const bool has_tail = tail_keys < RCH;
-  auto clear_tail = [&]() {
+  // what lies in those cells may be an infinity or NaN.  In the odd CTA that
+  // copy completes on the stage's own barrier and its clearing on `cleared`;
+  // a bit per stage holds the parity of the next such fill.
+  auto tail_keys = [&]() { return rt.pos0[sg.run] + rt.n[sg.run] - (sg.ch0 + sg.n - 1) * RCH; };
+  auto clear_tail = [&](uint32_t fill) {
     constexpr int VB = HD == 256 ? 128 : 64;  // bytes of a key's row in a box
-    uint8_t* v = smem + C::OFF_ST + ((n_seq - 1) % C::NST) * C::STAGE;
+    uint8_t* v = smem + C::OFF_ST + (fill % C::NST) * C::STAGE;
     for (int box = 0; box < C::STAGE / (RCH * VB); ++box)
-      for (int o = tail_keys * VB + lane * 16; o < RCH * VB; o += 512)
+      for (int o = tail_keys() * VB + lane * 16; o < RCH * VB; o += 512)
         *reinterpret_cast<uint4*>(v + box * RCH * VB + o) = make_uint4(0u, 0u, 0u, 0u);
     fence_proxy_async_smem();
     __syncwarp();
   };
 
   if (warp == 1) {
-    // ---------------- TMA producer (each CTA its own rows and halves)
+    // ---------------- K/V producer (each CTA its own halves)
     if (lane == 0) {
-      if (rank == 0) mbar_arrive_expect_tx(q_full, 2 * C::Q_BYTES);
-      tma_load_4d_pair(smem, &tmQ, map_to_rank(smem_u32(q_full), 0), 0, kvh << sh.log_g, row0 + (RC >> sh.log_g), 0);
       bool ok = true;
-      int u = 0;
-      for (; u < n_seq && ok; ++u) {
-        const int s = u % C::NST;
-        if (u >= C::NST) ok = mbar_wait(&empty[s], ((u - C::NST) / C::NST) & 1, err, PF_DEV_TIMEOUT_PRODUCER);
-        if (!ok) break;
-        uint8_t* dst = smem + C::OFF_ST + s * C::STAGE;
-        const int cell = rt.cell0[run] + (ch_first + seq_chunk(u)) * RCH;
-        const bool last = has_tail && u == n_seq - 1;
-        const uint32_t bar = map_to_rank(smem_u32(&full[s]), 0);
-        if (rank == 0) mbar_arrive_expect_tx(&full[s], last ? C::STAGE : 2 * C::STAGE);
-        if (seq_is_k(u)) {
-          tma_load_3d_pair(dst, &tmK, bar, kvh * HD, cell + rank * 64, 0);
-        } else if (last && rank == 1) {
-          mbar_arrive_expect_tx(tail, C::STAGE);
-          tma_load_3d(dst, &tmV, tail, kvh * HD + HD / 2, cell, 0);
-        } else {
-          tma_load_3d_pair(dst, &tmV, bar, kvh * HD + rank * (HD / 2), cell, 0);
+      uint32_t f = 0, tails = 0;
+      while (ok && sg.next()) {
+        const bool has_tail = tail_keys() < RCH;
+        for (int u = 0; u < 2 * sg.n; ++u, ++f) {
+          const int s = f % C::NST;
+          if (f >= C::NST) ok = mbar_wait(&empty[s], (f / C::NST + 1) & 1, err, PF_DEV_TIMEOUT_PRODUCER);
+          if (!ok) break;
+          uint8_t* dst = smem + C::OFF_ST + s * C::STAGE;
+          const int cell = rt.cell0[sg.run] + (sg.ch0 + fill_chunk(u)) * RCH;
+          const bool last = has_tail && u == 2 * sg.n - 1;
+          const uint32_t bar = map_to_rank(smem_u32(&full[s]), 0);
+          if (rank == 0) mbar_arrive_expect_tx(&full[s], last ? C::STAGE : 2 * C::STAGE);
+          if (fill_is_k(u)) {
+            tma_load_3d_pair(dst, &tmK, bar, sg.kvh * HD, cell + rank * 64, 0);
+          } else if (last && rank == 1) {
+            mbar_arrive_expect_tx(&full[s], C::STAGE);
+            tma_load_3d(dst, &tmV, &full[s], sg.kvh * HD + HD / 2, cell, 0);
+            tails ^= 1u << s;
+          } else {
+            tma_load_3d_pair(dst, &tmV, bar, sg.kvh * HD + rank * (HD / 2), cell, 0);
+          }
         }
       }
       // On an error the copies in flight land before the pair may leave (the
       // even CTA's barriers count those of both).
       if (!ok || read_error(err) != 0) {
         if (rank == 0) {
-          runs_drain(q_full, 0);
-          for (int x = max(0, u - C::NST); x < u; ++x) runs_drain(&full[x % C::NST], (x / C::NST) & 1);
-        } else if (has_tail && u == n_seq) {
-          runs_drain(tail, 0);
+          for (uint32_t x = f > C::NST ? f - C::NST : 0; x < f; ++x) runs_drain(&full[x % C::NST], (x / C::NST) & 1);
+        } else {
+          // a stage that never held such a copy is in phase 0, whose waiting
+          // for parity 1 ends at once
+          for (int x = 0; x < C::NST; ++x) runs_drain(&full[x], (tails >> x & 1u) ^ 1u);
         }
       }
     }
     __syncwarp();
-  } else if (warp == 0 && rank == 1) {
-    if (has_tail) {
-      bool ok = mbar_wait(tail, 0, err, PF_DEV_TIMEOUT_MMA);
-      ok = __all_sync(0xffffffffu, ok);
-      if (ok) {
-        clear_tail();
-        if (lane == 0) mbar_arrive_cluster(map_to_rank(smem_u32(tail), 0));
+  } else if (warp == 2) {
+    // ---------------- Q producer
+    if (lane == 0) {
+      bool ok = true;
+      uint32_t seg = 0;
+      for (; ok && sg.next(); ++seg) {
+        if (seg > 0) ok = mbar_wait(q_empty, (seg - 1) & 1, err, PF_DEV_TIMEOUT_PRODUCER);
+        if (!ok) break;
+        if (rank == 0) mbar_arrive_expect_tx(q_full, 2 * C::Q_BYTES);
+        tma_load_4d_pair(smem, &tmQ, map_to_rank(smem_u32(q_full), 0), 0, sg.kvh << sh.log_g,
+                         rt.row0[sg.run] + ((sg.R0 + rank * 128) >> sh.log_g), 0);
       }
+      if ((!ok || read_error(err) != 0) && rank == 0 && seg > 0) runs_drain(q_full, (seg - 1) & 1);
+    }
+    __syncwarp();
+  } else if (warp == 0 && rank == 1) {
+    // ---------------- the odd CTA's half of the run's last V
+    bool ok = true;
+    uint32_t f = 0, tails = 0;
+    while (ok && sg.next()) {
+      f += 2 * sg.n;
+      if (tail_keys() >= RCH) continue;
+      const int s = (f - 1) % C::NST;
+      ok = mbar_wait(&full[s], tails >> s & 1u, err, PF_DEV_TIMEOUT_MMA);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      tails ^= 1u << s;
+      clear_tail(f - 1);
+      if (lane == 0) mbar_arrive_cluster(map_to_rank(smem_u32(&cleared[s]), 0));
     }
     __syncwarp();
   } else if (warp == 0) {
@@ -374,62 +532,70 @@ __global__ void __launch_bounds__(RunsCfg<HD>::THREADS, 1)
     constexpr uint32_t id_qk = idesc_f16_f32(256, RCH, false);
     constexpr uint32_t id_pv = idesc_f16_f32(256, HD, true);
     const uint64_t qd0 = sdesc_sw128(smem_u32(smem));
-    bool ok = mbar_wait_spin(q_full, 0, err, PF_DEV_TIMEOUT_MMA);
-    ok = __all_sync(0xffffffffu, ok);
-    bool issued = false;
-    for (int u = 0; u < n_seq && ok; ++u) {
-      const int s = u % C::NST, j = seq_chunk(u);
-      const int b = j & 1;
-      const uint32_t st = smem_u32(smem + C::OFF_ST + s * C::STAGE);
-      ok = mbar_wait_spin(&full[s], (u / C::NST) & 1, err, PF_DEV_TIMEOUT_MMA);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
-      if (seq_is_k(u)) {
-        // S(j): P(j-2), which lay in this buffer, was read by MMAs issued before
-        tc_fence_after();
-        if (leader) {
-          const uint64_t kd0 = sdesc_sw128(st);
+    const uint32_t ring = smem_u32(smem + C::OFF_ST);
+    const uint32_t empty0 = map_to_rank(smem_u32(empty), 0), empty1 = map_to_rank(smem_u32(empty), 1);
+    bool ok = true, issued = false;
+    uint32_t f0 = 0, j0 = 0, seg = 0, tails = 0;
+    // every lane waits; only the elected lane's success lets MMAs go
+    auto issue_s = [&](int jl) {
+      const uint32_t f = f0 + k_fill(jl), s = f % C::NST;
+      // S(j): P(j-2), which lay in this buffer, was read by MMAs issued before
+      ok = ok && mbar_wait_spin(&full[s], (f / C::NST) & 1, err, PF_DEV_TIMEOUT_MMA);
+      tc_fence_after();
+      if (leader && ok) {
+        const uint64_t kd0 = sdesc_sw128(ring + s * C::STAGE);
+        const uint32_t d = tmem + C::TMEM_S + ((j0 + jl) & 1) * RCH;
 #pragma unroll
-          for (int kk = 0; kk < HD / 16; ++kk) {
-            const int bx = kk >> 2, w = kk & 3;  // 64-dim box, 16-dim step within it
-            tc_mma_f16_pair(tmem + C::TMEM_S + b * RCH, qd0 + ((bx * (128 * 128) + w * 32) >> 4),
-                            kd0 + ((bx * (64 * 128) + w * 32) >> 4), id_qk, kk > 0 ? 1u : 0u);
-          }
-          tc_commit_pair(map_to_rank(smem_u32(&s_full[b]), 0));
-          tc_commit_pair(map_to_rank(smem_u32(&s_full[b]), 1));
+        for (int kk = 0; kk < HD / 16; ++kk) {
+          const int bx = kk >> 2, w = kk & 3;  // 64-dim box, 16-dim step within it
+          tc_mma_f16_pair(d, qd0 + ((bx * (128 * 128) + w * 32) >> 4), kd0 + ((bx * (64 * 128) + w * 32) >> 4), id_qk,
+                          kk > 0 ? 1u : 0u);
         }
-      } else {
-        if (has_tail && u == n_seq - 1) {
-          ok = mbar_wait<true>(tail, 0, err, PF_DEV_TIMEOUT_MMA);
-          clear_tail();
+        tc_commit_pair(empty0 + s * 8);
+        tc_commit_pair(empty1 + s * 8);
+        if (jl == sg.n - 1) {
+          tc_commit_pair(map_to_rank(smem_u32(q_empty), 0));
+          tc_commit_pair(map_to_rank(smem_u32(q_empty), 1));
         }
-        const uint64_t vd0 = HD == 256 ? sdesc_sw128_lbo_sbo(st, RCH * 128, 1024) : sdesc_sw64_mn(st);
-        constexpr int KSTEP = 16 * (HD == 256 ? 128 : 64);  // bytes of 16 keys
-#pragma unroll
-        for (int h = 0; h < C::NH; ++h) {
-          if (ok) ok = mbar_wait_spin(&p_full[2 * h + b], (j >> 1) & 1, err, PF_DEV_TIMEOUT_MMA);
-          ok = __all_sync(0xffffffffu, ok);
-          tc_fence_after();
-          if (ok && leader) {
-#pragma unroll
-            for (int kk = 0; kk < C::KPT / 16; ++kk)
-              tc_mma_f16_ts_pair(tmem + C::TMEM_O + h * HD, tmem + C::TMEM_S + b * RCH + h * C::KPT + kk * 8,
-                                 vd0 + (((h * (C::KPT / 16) + kk) * KSTEP) >> 4), id_pv, (j > 0 || kk > 0) ? 1u : 0u);
-          }
-          __syncwarp();
-        }
-        if (!ok) break;
-        if (leader) {
-          tc_commit_pair(map_to_rank(smem_u32(&pv_done[b]), 0));
-          tc_commit_pair(map_to_rank(smem_u32(&pv_done[b]), 1));
-        }
-      }
-      if (leader) {
-        tc_commit_pair(map_to_rank(smem_u32(&empty[s]), 0));
-        tc_commit_pair(map_to_rank(smem_u32(&empty[s]), 1));
+        issued = true;
       }
       __syncwarp();
-      issued = true;
+    };
+    for (; sg.next(); j0 += sg.n, f0 += 2 * sg.n, ++seg) {
+      const bool has_tail = tail_keys() < RCH;
+      ok = ok && mbar_wait_spin(q_full, seg & 1, err, PF_DEV_TIMEOUT_MMA);
+      issue_s(0);
+      for (int jl = 0; jl < sg.n; ++jl) {
+        if (jl + 1 < sg.n) issue_s(jl + 1);
+        const uint32_t f = f0 + v_fill(jl, sg.n), s = f % C::NST, j = j0 + jl;
+        ok = ok && mbar_wait_spin(&full[s], (f / C::NST) & 1, err, PF_DEV_TIMEOUT_MMA);
+        if (has_tail && jl == sg.n - 1) {
+          ok = ok && mbar_wait<true>(&cleared[s], tails >> s & 1u, err, PF_DEV_TIMEOUT_MMA);
+          tails ^= 1u << s;
+          if (!__all_sync(0xffffffffu, ok)) break;
+          clear_tail(f);
+        }
+        // the last segment's O is read out before this one's replaces it
+        if (jl == 0 && seg > 0) ok = ok && mbar_wait(o_free, (seg - 1) & 1, err, PF_DEV_TIMEOUT_MMA);
+        ok = ok && mbar_wait_spin(&p_full[j & 1], (j >> 1) & 1, err, PF_DEV_TIMEOUT_MMA);
+        tc_fence_after();
+        if (leader && ok) {
+          const uint32_t st = ring + s * C::STAGE;
+          const uint64_t vd0 = HD == 256 ? sdesc_sw128_lbo_sbo(st, RCH * 128, 1024) : sdesc_sw64_mn(st);
+          constexpr int KSTEP = 16 * (HD == 256 ? 128 : 64);  // bytes of 16 keys
+          const uint32_t a = tmem + C::TMEM_S + (j & 1) * RCH;
+#pragma unroll
+          for (int h = 0; h < C::NH; ++h)
+#pragma unroll
+            for (int kk = 0; kk < C::KPT / 16; ++kk)
+              tc_mma_f16_ts_pair(tmem + C::TMEM_O + h * HD, a + h * C::KPT + kk * 8,
+                                 vd0 + (((h * (C::KPT / 16) + kk) * KSTEP) >> 4), id_pv, (jl > 0 || kk > 0) ? 1u : 0u);
+          tc_commit_pair(empty0 + s * 8);
+          tc_commit_pair(empty1 + s * 8);
+        }
+        if (!__all_sync(0xffffffffu, ok)) break;
+      }
+      if (!__all_sync(0xffffffffu, ok)) break;
     }
     if (!ok && issued && leader) {
       // the MMAs already issued finish before TMEM is freed
@@ -437,171 +603,168 @@ __global__ void __launch_bounds__(RunsCfg<HD>::THREADS, 1)
       runs_drain(drain, 0);
     }
     __syncwarp();
-  } else if ((warp & 3) < row_warps(rank)) {
-    // ---------------- rows (warps 2..: TMEM lane quarter warp % 4, part h of each chunk)
-    const int qw = warp & 3, h = (warp - 2) >> 2;
-    const int R = RC + 32 * qw + lane;
-    const int t = R >> sh.log_g, head = (kvh << sh.log_g) + (R & ((1 << sh.log_g) - 1));
-    const bool row = R < total_rows;
-    const int pos = row ? pos0 + t : -1;
-    const uint64_t* row_mask = TREE && row ? mask + static_cast<size_t>(row0 + t) * words : nullptr;
+  } else if (warp >= 4) {
+    // ---------------- rows (warps 4..: TMEM lane quarter warp % 4, part h of each chunk)
+    const int qw = warp & 3, h = (warp - 4) >> 2;
     const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * qw) << 16);
     constexpr int NB = C::KPT / 32;
     const uint64_t c2 = pack_f32x2(cexp, cexp);
-    float m = -INFINITY, l = 0.f;
+    const uint32_t o_free_at = map_to_rank(smem_u32(o_free), 0);
+    const uint32_t p_full_at = map_to_rank(smem_u32(p_full), 0);
     bool ok = true;
-    for (int j = 0; j < n && ok; ++j) {
-      const int b = j & 1;
-      const int key0 = (ch_first + j) * RCH + h * C::KPT;
-      const uint32_t ts = lanes + C::TMEM_S + b * RCH + h * C::KPT;
-      if (lane == 0) ok = mbar_wait_spin(&s_full[b], (j >> 1) & 1, err, PF_DEV_TIMEOUT_EPILOGUE);
+    uint32_t j0 = 0, f0 = 0;
+    // the MMAs of fill f are done
+    auto done = [&](uint32_t f) {
+      if (lane == 0) ok = mbar_wait_spin(&empty[f % C::NST], (f / C::NST) & 1, err, PF_DEV_TIMEOUT_EPILOGUE);
       ok = __shfl_sync(0xffffffffu, ok, 0);
+      return ok;
+    };
+    for (; ok && sg.next(); j0 += sg.n, f0 += 2 * sg.n) {
+      const int n_rows = rt.n[sg.run], pos0 = rt.pos0[sg.run], row0 = rt.row0[sg.run];
+      const int total_rows = n_rows << sh.log_g;
+      const int Rw = sg.R0 + rank * 128 + 32 * qw;  // the warp's first row
+      const bool active = Rw < total_rows;          // warps without rows only keep step
+      const int R = Rw + lane;
+      const int t = R >> sh.log_g, head = (sg.kvh << sh.log_g) + (R & ((1 << sh.log_g) - 1));
+      const bool row = R < total_rows;
+      const int pos = row ? pos0 + t : -1;
+      const uint64_t* row_mask = TREE && row ? mask + static_cast<size_t>(row0 + t) * words : nullptr;
+      float m = -INFINITY, l = 0.f;
+      for (int jl = 0; jl < sg.n; ++jl) {
+        const int b = (j0 + jl) & 1;
+        if (!done(f0 + k_fill(jl))) break;
+        if (active) {
+          const int key0 = (sg.ch0 + jl) * RCH + h * C::KPT;
+          const uint32_t ts = lanes + C::TMEM_S + b * RCH + h * C::KPT;
+          tc_fence_after();
+          uint32_t x[NB][32];
+#pragma unroll
+          for (int w = 0; w < NB; ++w) tmem_ld32(ts + 32 * w, x[w]);
+          // the row's view of its keys, skipped where every row of the warp sees all of them
+          const bool all = TREE ? key0 + C::KPT <= pos0 : __all_sync(0xffffffffu, pos >= key0 + C::KPT - 1);
+#pragma unroll
+          for (int w = 0; w < NB; ++w) tmem_ld_wait32(x[w]);
+          if (!all) {
+#pragma unroll
+            for (int w = 0; w < NB; ++w) {
+              uint32_t bits;
+              if (TREE) {
+                bits = row ? tree_bits(row_mask, words, pos0, n_rows, key0 + 32 * w) : 0u;
+              } else {
+                const int nv = pos - key0 - 32 * w + 1;
+                bits = nv >= 32 ? 0xffffffffu : nv <= 0 ? 0u : (1u << nv) - 1u;
+              }
+              mask_scores(x[w], bits);
+            }
+          }
+          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int w = 0; w < NB; ++w) max_scores(x[w], mx);
+          const float mj = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+          // The reference moves only when this chunk's maximum passes it by
+          // more than 2^8 (or on the row's first visible keys); until then P is
+          // taken against the old one (p <= 2^8, well inside fp16) and O needs
+          // no touch.
+          const bool grow = mj != -INFINITY && (m == -INFINITY || (mj - m) * cexp > 8.f);
+          const float mn = grow ? mj : m;
+          const bool resc = grow && m != -INFINITY;
+          const float scale = resc ? ex2_approx((m - mn) * cexp) : 1.f;
+          const float nmc = mn == -INFINITY ? 0.f : -mn * cexp;
+          const uint64_t nmc2 = pack_f32x2(nmc, nmc);
+          uint64_t ls[4] = {0ull, 0ull, 0ull, 0ull};
+#pragma unroll
+          for (int w = 0; w < NB; w += 2) {
+            uint32_t pw[32];  // 64 fp16 probabilities
+            exp_scores(x[w], c2, nmc2, pw, ls);
+            exp_scores(x[w + 1], c2, nmc2, pw + 16, ls);
+            tmem_st32(ts + 16 * w, pw);  // over scores that have been read
+          }
+          const float2 l01 = unpack_f32x2(add_f32x2(add_f32x2(ls[0], ls[1]), add_f32x2(ls[2], ls[3])));
+          l = __fmaf_rn(l, scale, l01.x + l01.y);
+          m = mn;
+          tmem_st_wait();
+          // O *= scale once P V(j-1) has landed, only in the warps where a row
+          // moved its reference
+          if (jl >= 1 && __any_sync(0xffffffffu, resc)) {
+            if (!done(f0 + v_fill(jl - 1, sg.n))) break;
+            tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < HD / 32; ++c) {
+              uint32_t y[32];
+              tmem_ld32(lanes + C::TMEM_O + h * HD + 32 * c, y);
+              tmem_ld_wait32(y);
+#pragma unroll
+              for (int q = 0; q < 32; ++q) y[q] = __float_as_uint(__uint_as_float(y[q]) * scale);
+              tmem_st32(lanes + C::TMEM_O + h * HD + 32 * c, y);
+            }
+            tmem_st_wait();
+          }
+          tc_fence_before();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive_pair_relaxed(p_full_at + b * 8);
+      }
+      if (ok) done(f0 + v_fill(sg.n - 1, sg.n));
+      // the parts' weights: w_h = 2^((m_h - m) c); each of a row's two warps
+      // writes half of the dims
+      float w0 = 1.f, w1 = 0.f;
+      if constexpr (C::NH > 1) {
+        float2* ml = reinterpret_cast<float2*>(smem + C::OFF_ML);
+        ml[h * 128 + 32 * qw + lane] = make_float2(m, ok ? l : -1.f);  // -1: this warp gave up (l is a sum of p >= 0)
+        asm volatile("bar.sync %0, 64;" ::"r"(1 + qw) : "memory");
+        const float2 a = ml[32 * qw + lane], c = ml[128 + 32 * qw + lane];
+        ok = __all_sync(0xffffffffu, a.y != -1.f && c.y != -1.f);
+        m = fmaxf(a.x, c.x);
+        w0 = a.x == -INFINITY ? 0.f : ex2_approx((a.x - m) * cexp);
+        w1 = c.x == -INFINITY ? 0.f : ex2_approx((c.x - m) * cexp);
+        l = w0 * a.y + w1 * c.y;
+      }
       if (!ok) break;
-      tc_fence_after();
-      uint32_t x[NB][32];
-#pragma unroll
-      for (int w = 0; w < NB; ++w) tmem_ld32(ts + 32 * w, x[w]);
-      // the row's view of its keys, skipped where every row of the warp sees all of them
-      const bool all = TREE ? key0 + C::KPT <= pos0 : __all_sync(0xffffffffu, pos >= key0 + C::KPT - 1);
-#pragma unroll
-      for (int w = 0; w < NB; ++w) tmem_ld_wait32(x[w]);
-      if (!all) {
-#pragma unroll
-        for (int w = 0; w < NB; ++w) {
-          uint32_t bits;
-          if (TREE) {
-            bits = row ? tree_bits(row_mask, words, pos0, n_rows, key0 + 32 * w) : 0u;
-          } else {
-            const int nv = pos - key0 - 32 * w + 1;
-            bits = nv >= 32 ? 0xffffffffu : nv <= 0 ? 0u : (1u << nv) - 1u;
-          }
-          mask_scores(x[w], bits);
-        }
-      }
-      float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-      for (int w = 0; w < NB; ++w) max_scores(x[w], mx);
-      const float mj = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-      // The reference moves only when this chunk's maximum passes it by more
-      // than 2^8 (or on the row's first visible keys); until then P is taken
-      // against the old one (p <= 2^8, well inside fp16) and O needs no touch.
-      const bool grow = mj != -INFINITY && (m == -INFINITY || (mj - m) * cexp > 8.f);
-      const float mn = grow ? mj : m;
-      const bool resc = grow && m != -INFINITY;
-      const float scale = resc ? ex2_approx((m - mn) * cexp) : 1.f;
-      const float nmc = mn == -INFINITY ? 0.f : -mn * cexp;
-      const uint64_t nmc2 = pack_f32x2(nmc, nmc);
-      uint64_t ls[4] = {0ull, 0ull, 0ull, 0ull};
-#pragma unroll
-      for (int w = 0; w < NB; w += 2) {
-        uint32_t pw[32];  // 64 fp16 probabilities
-        exp_scores(x[w], c2, nmc2, pw, ls);
-        exp_scores(x[w + 1], c2, nmc2, pw + 16, ls);
-        tmem_st32(ts + 16 * w, pw);  // over scores that have been read
-      }
-      const float2 l01 = unpack_f32x2(add_f32x2(add_f32x2(ls[0], ls[1]), add_f32x2(ls[2], ls[3])));
-      l = __fmaf_rn(l, scale, l01.x + l01.y);
-      m = mn;
-      tmem_st_wait();
-      // O *= scale once P V(j-1) has landed, only in the warps where a row
-      // moved its reference.  (S(j) was issued after P V(j-2), so each of the
-      // two barriers has at most the awaited phase outstanding.)
-      if (j >= 1 && __any_sync(0xffffffffu, resc)) {
-        if (lane == 0) ok = mbar_wait(&pv_done[(j - 1) & 1], ((j - 1) >> 1) & 1, err, PF_DEV_TIMEOUT_EPILOGUE);
-        ok = __shfl_sync(0xffffffffu, ok, 0);
-        if (!ok) break;
+      if (active) {
+        // a thread writes its row, 32-byte sectors at a time
         tc_fence_after();
+        const bool whole = sg.slot < 0;
+        const float inv = !whole ? 1.f : l == 0.f ? 0.f : __frcp_rn(l);  // a row that sees nothing: zeros
+        w0 *= inv;
+        w1 *= inv;
+        const size_t own = whole ? (static_cast<size_t>(row0 + t) * sh.Hq + head) * HD
+                                 : (static_cast<size_t>(sg.slot) * sh.slot_rows + (R - sg.R0)) * runs_state_stride(HD);
 #pragma unroll 1
-        for (int c = 0; c < HD / 32; ++c) {
+        for (int c = h * (HD / 32 / C::NH); c < (h + 1) * (HD / 32 / C::NH); ++c) {
           uint32_t y[32];
-          tmem_ld32(lanes + C::TMEM_O + h * HD + 32 * c, y);
+          tmem_ld32(lanes + C::TMEM_O + 32 * c, y);
           tmem_ld_wait32(y);
+          if constexpr (C::NH > 1) {
+            uint32_t z[32];
+            tmem_ld32(lanes + C::TMEM_O + HD + 32 * c, z);
+            tmem_ld_wait32(z);
 #pragma unroll
-          for (int q = 0; q < 32; ++q) y[q] = __float_as_uint(__uint_as_float(y[q]) * scale);
-          tmem_st32(lanes + C::TMEM_O + h * HD + 32 * c, y);
-        }
-        tmem_st_wait();
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_pair_relaxed(map_to_rank(smem_u32(&p_full[2 * h + b]), 0));
-    }
-    if (ok) {
-      if (lane == 0) ok = mbar_wait_spin(&pv_done[(n - 1) & 1], ((n - 1) >> 1) & 1, err, PF_DEV_TIMEOUT_EPILOGUE);
-      ok = __shfl_sync(0xffffffffu, ok, 0);
-    }
-    // the parts' weights: w_h = 2^((m_h - m) c); each of a row's two warps
-    // writes half of the dims
-    float w0 = 1.f, w1 = 0.f;
-    if constexpr (C::NH > 1) {
-      float2* ml = reinterpret_cast<float2*>(smem + C::OFF_ML);
-      ml[h * 128 + 32 * qw + lane] = make_float2(ok ? m : __int_as_float(0x7fc00000), l);
-      asm volatile("bar.sync %0, 64;" ::"r"(1 + qw) : "memory");
-      const float2 a = ml[32 * qw + lane], c = ml[128 + 32 * qw + lane];
-      m = fmaxf(a.x, c.x);
-      w0 = a.x == -INFINITY ? 0.f : ex2_approx((a.x - m) * cexp);
-      w1 = c.x == -INFINITY ? 0.f : ex2_approx((c.x - m) * cexp);
-      l = w0 * a.y + w1 * c.y;
-    }
-    if (ok) {
-      // Every MMA of the pair and every copy is done.  Each 32 x 32 block of O
-      // goes through a warp-private buffer in the idle ring, so that global
-      // stores cover whole row segments.
-      tc_fence_after();
-      // groups with keys of this row; 0: nothing to write
-      const int n_g = !row ? 0 : TREE ? rt.groups[run] : (pos / RCH) / sh.gc + 1;
-      const int kind = grp >= n_g ? 0 : n_g == 1 ? 1 : 2;  // 1: output row, 2: group state
-      const float inv = kind != 1 ? 1.f : l == 0.f ? 0.f : __frcp_rn(l);  // a row that sees nothing: zeros
-      w0 *= inv;
-      w1 *= inv;
-      const size_t own = kind == 1 ? (static_cast<size_t>(row0 + t) * sh.Hq + head) * HD
-                                   : (static_cast<size_t>(idx) * sh.slot_rows + (R - R0)) * runs_state_stride(HD);
-      const int rs = lane >> 3, pc = lane & 7;
-      size_t dst[8];
-      int dk[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        dk[i] = __shfl_sync(0xffffffffu, kind, 4 * i + rs);
-        dst[i] = __shfl_sync(0xffffffffu, static_cast<unsigned long long>(own), 4 * i + rs);
-      }
-      uint8_t* stg = smem + C::OFF_ST + (h * 4 + qw) * 4096;
-#pragma unroll 1
-      for (int c = h * (HD / 32 / C::NH); c < (h + 1) * (HD / 32 / C::NH); ++c) {
-        uint32_t y[32];
-        tmem_ld32(lanes + C::TMEM_O + 32 * c, y);
-        tmem_ld_wait32(y);
-        if constexpr (C::NH > 1) {
-          uint32_t z[32];
-          tmem_ld32(lanes + C::TMEM_O + HD + 32 * c, z);
-          tmem_ld_wait32(z);
-#pragma unroll
-          for (int q = 0; q < 32; ++q)
-            y[q] = __float_as_uint(__fmaf_rn(w0, __uint_as_float(y[q]), w1 * __uint_as_float(z[q])));
-        } else {
-#pragma unroll
-          for (int q = 0; q < 32; ++q) y[q] = __float_as_uint(w0 * __uint_as_float(y[q]));
-        }
-#pragma unroll
-        for (int q = 0; q < 8; ++q)
-          *reinterpret_cast<uint4*>(stg + lane * 128 + ((q ^ (lane & 7)) << 4)) =
-              make_uint4(y[4 * q], y[4 * q + 1], y[4 * q + 2], y[4 * q + 3]);
-        __syncwarp();
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int rr = 4 * i + rs;
-          if (dk[i] == 0) continue;
-          const float4 v = *reinterpret_cast<const float4*>(stg + rr * 128 + ((pc ^ (rr & 7)) << 4));
-          if (dk[i] == 1) {
-            const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x, v.y), hi = __floats2bfloat162_rn(v.z, v.w);
-            *reinterpret_cast<uint2*>(out + dst[i] + 32 * c + 4 * pc) =
-                make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+            for (int q = 0; q < 32; ++q)
+              y[q] = __float_as_uint(__fmaf_rn(w0, __uint_as_float(y[q]), w1 * __uint_as_float(z[q])));
           } else {
-            *reinterpret_cast<float4*>(part + dst[i] + 32 * c + 4 * pc) = v;
+#pragma unroll
+            for (int q = 0; q < 32; ++q) y[q] = __float_as_uint(w0 * __uint_as_float(y[q]));
           }
+          if (row && whole) {
+            uint32_t hb[16];
+#pragma unroll
+            for (int q = 0; q < 16; ++q) {
+              const __nv_bfloat162 v = __floats2bfloat162_rn(__uint_as_float(y[2 * q]), __uint_as_float(y[2 * q + 1]));
+              hb[q] = *reinterpret_cast<const uint32_t*>(&v);
+            }
+            st_global_v8(out + own + 32 * c, hb);
+            st_global_v8(out + own + 32 * c + 16, hb + 8);
+          } else if (row) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) st_global_v8(part + own + 32 * c + 8 * q, y + 8 * q);
+          }
+          __syncwarp();
         }
-        __syncwarp();
+        if (!whole && row && h == 0) *reinterpret_cast<float2*>(part + own + HD) = make_float2(m, l);
+        tc_fence_before();
       }
-      if (kind == 2 && h == 0) *reinterpret_cast<float2*>(part + own + HD) = make_float2(m, l);
+      __syncwarp();
+      if (lane == 0) mbar_arrive_pair_relaxed(o_free_at);
     }
   }
   tc_fence_before();
@@ -614,79 +777,102 @@ __global__ void __launch_bounds__(RunsCfg<HD>::THREADS, 1)
   }
 }
 
-// Rows with several groups: m = max m_g, w_g = 2^((m_g - m) c), out =
-// (sum w_g o_g) / (sum w_g l_g), sums in group order.  A warp per row R of a
-// row block, lane owning HD/32 consecutive dims; bound by the states' bytes
-// (L2: they were just written).
+// Items cut over several pairs: m = max m_p, w_p = 2^((m_p - m) c), out =
+// (sum w_p o_p) / (sum w_p l_p) over the item's pairs.  `wpr` warps take a row
+// (its pairs dealt out among them, then their sums joined in warp order),
+// lane owning HD/32 consecutive dims; bound by the latency of reading the
+// states from L2, so a row of many pairs wants many warps.  blockIdx.x
+// counts items, or, where there are fewer of them, the boundaries between
+// pairs (an item is taken at its first).
 template <int HD, bool TREE>
 __global__ void __launch_bounds__(256) attn_runs_merge_kernel(const __grid_constant__ RunTable rt, const RunsShape sh,
-                                                              const float* __restrict__ part,
+                                                              int by_item, int wpr, const float* __restrict__ part,
                                                               __nv_bfloat16* __restrict__ out) {
   constexpr int PER = HD / 32;
   constexpr float c = attn_c<HD>();
+  constexpr int ST = runs_state_stride(HD);
+  __shared__ float joined[8][HD + 4];
   pdl_launch();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const ItemAt<TREE> at = by_item ? ItemAt<TREE>::number(rt, sh, static_cast<int>(blockIdx.x))
+                                  : ItemAt<TREE>::weight(rt, sh, (static_cast<int>(blockIdx.x) + 1) * sh.per);
+  const RunBlocks<TREE> rb(rt.n[at.run], rt.pos0[at.run], sh.log_g);
+  const int w = at.w + ITEM_FIXED;
+  const int p0 = w / sh.per, p1 = (w + rb.chunks(at.i) - 1) / sh.per;
+  const int R0 = (rb.nb - 1 - at.i) * RROWS;
+  const int R_in = static_cast<int>(blockIdx.y) * (8 / wpr) + warp / wpr;
+  const int sub = warp % wpr;
+  const int rows = min(RROWS, (rt.n[at.run] << sh.log_g) - R0);
   pdl_wait();
-  const int lane = threadIdx.x & 31;
-  const int kvh = blockIdx.y;
-  // blockIdx.x: (row block of any run) x (8-row slice); a run's blocks start
-  // at item0 / groups blocks of its own items
-  const int slices = sh.slot_rows / 8;
-  int blk = static_cast<int>(blockIdx.x) / slices;
-  const int R_in = (static_cast<int>(blockIdx.x) % slices) * 8 + (threadIdx.x >> 5);
-  int run = 0, nb = 0;
-  for (;; ++run) {
-    nb = ((rt.n[run] << sh.log_g) + RROWS - 1) / RROWS;
-    if (blk < nb || run == rt.n_runs - 1) break;
-    blk -= nb;
-  }
-  const int R = blk * RROWS + R_in;
-  if (R >= rt.n[run] << sh.log_g) return;
-  const int t = R >> sh.log_g;
-  const int n_g = TREE ? rt.groups[run] : ((rt.pos0[run] + t) / RCH) / sh.gc + 1;
-  if (n_g < 2) return;
-  // group g's slot of this block
-  const size_t step = static_cast<size_t>(nb) * sh.Hkv * sh.slot_rows * runs_state_stride(HD);
-  const float* base =
-      part + ((static_cast<size_t>(rt.item0[run] + (nb - 1 - blk)) * sh.Hkv + kvh) * sh.slot_rows + R_in) *
-                 runs_state_stride(HD);
-  float m = -INFINITY;
-  for (int g = lane; g < n_g; g += 32) m = fmaxf(m, base[g * step + HD]);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  // uniform over the block: the item has one segment, or is another boundary's
+  if (p0 == p1 || (!by_item && static_cast<int>(blockIdx.x) != p0)) return;
+  const bool live = R_in < rows;
+  // pair p's state of the row: the first pair's slot is its second
+  auto state = [&](int p) {
+    return part + (static_cast<size_t>(p == p0 ? 2 * p + 1 : 2 * p) * sh.slot_rows + R_in) * ST;
+  };
+  float m = -INFINITY, l = 0.f;
   float acc[PER];
 #pragma unroll
   for (int i = 0; i < PER; ++i) acc[i] = 0.f;
-  float l = 0.f;
-  for (int g0 = 0; g0 < n_g; g0 += 4) {  // four groups' loads in flight
-    float o[4][PER];
-    float2 ml[4];
+  if (live) {
+    for (int p = p0 + sub + lane * wpr; p <= p1; p += 32 * wpr) m = fmaxf(m, state(p)[HD]);
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int g = min(g0 + k, n_g - 1);
-      const float* p = base + g * step;
-      ml[k] = *reinterpret_cast<const float2*>(p + HD);
-      if constexpr (PER >= 4) {
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    for (int q = p0 + sub; q <= p1; q += 4 * wpr) {  // four states' loads in flight
+      float o[4][PER];
+      float2 ml[4];
 #pragma unroll
-        for (int i = 0; i < PER; i += 4) {
-          const float4 v = *reinterpret_cast<const float4*>(p + lane * PER + i);
-          o[k][i] = v.x, o[k][i + 1] = v.y, o[k][i + 2] = v.z, o[k][i + 3] = v.w;
+      for (int k = 0; k < 4; ++k) {
+        const float* s = state(min(q + k * wpr, p1));
+        ml[k] = *reinterpret_cast<const float2*>(s + HD);
+        if constexpr (PER >= 4) {
+#pragma unroll
+          for (int i = 0; i < PER; i += 4) {
+            const float4 v = *reinterpret_cast<const float4*>(s + lane * PER + i);
+            o[k][i] = v.x, o[k][i + 1] = v.y, o[k][i + 2] = v.z, o[k][i + 3] = v.w;
+          }
+        } else {
+          const float2 v = *reinterpret_cast<const float2*>(s + lane * PER);
+          o[k][0] = v.x, o[k][1] = v.y;
         }
-      } else {
-        const float2 v = *reinterpret_cast<const float2*>(p + lane * PER);
-        o[k][0] = v.x, o[k][1] = v.y;
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (q + k * wpr > p1 || ml[k].x == -INFINITY) continue;
+        const float wt = ex2_approx((ml[k].x - m) * c);
+        l = __fmaf_rn(wt, ml[k].y, l);
+#pragma unroll
+        for (int i = 0; i < PER; ++i) acc[i] = __fmaf_rn(wt, o[k][i], acc[i]);
       }
     }
+  }
+  if (wpr > 1) {
+    float* mine = joined[warp];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      if (g0 + k >= n_g || ml[k].x == -INFINITY) continue;
-      const float w = ex2_approx((ml[k].x - m) * c);
-      l = __fmaf_rn(w, ml[k].y, l);
+    for (int i = 0; i < PER; ++i) mine[lane * PER + i] = acc[i];
+    if (lane == 0) mine[HD] = m, mine[HD + 1] = l;
+    __syncthreads();
+    if (sub != 0) return;
+    float mm = m;
+    for (int k = 1; k < wpr; ++k) mm = fmaxf(mm, joined[warp + k][HD]);
+    const float w_own = m == -INFINITY ? 0.f : ex2_approx((m - mm) * c);
+    l *= w_own;
 #pragma unroll
-      for (int i = 0; i < PER; ++i) acc[i] = __fmaf_rn(w, o[k][i], acc[i]);
+    for (int i = 0; i < PER; ++i) acc[i] *= w_own;
+    for (int k = 1; k < wpr; ++k) {
+      const float* s = joined[warp + k];
+      if (s[HD] == -INFINITY) continue;
+      const float wt = ex2_approx((s[HD] - mm) * c);
+      l = __fmaf_rn(wt, s[HD + 1], l);
+#pragma unroll
+      for (int i = 0; i < PER; ++i) acc[i] = __fmaf_rn(wt, s[lane * PER + i], acc[i]);
     }
   }
+  if (!live) return;
   const float inv = l == 0.f ? 0.f : __frcp_rn(l);
-  __nv_bfloat16* d = out + (static_cast<size_t>(rt.row0[run] + t) * sh.Hq + (kvh << sh.log_g) +
+  const int R = R0 + R_in;
+  __nv_bfloat16* d = out + (static_cast<size_t>(rt.row0[at.run] + (R >> sh.log_g)) * sh.Hq + (at.kvh << sh.log_g) +
                             (R & ((1 << sh.log_g) - 1))) * HD + lane * PER;
 #pragma unroll
   for (int i = 0; i < PER; i += 2)
@@ -699,8 +885,7 @@ __global__ void __launch_bounds__(256) attn_runs_merge_kernel(const __grid_const
 struct RunsPlan {
   RunTable rt;
   RunsShape sh;
-  int blocks = 0;      // row blocks of all runs
-  bool split = false;  // some run has several groups
+  int items = 0;
   int64_t state_bytes = 0;
 };
 
@@ -717,85 +902,59 @@ static int sm_count() {
   return n;
 }
 
-// The chunks per group: as many groups as shorten the call, by a count of
-// chunk times.  An item costs its chunks and `fixed` chunk times (prologue,
-// Q, output); the call ends no earlier than its longest item and its total
-// work over the pairs that fit at once, and splitting adds the states'
-// traffic and the merge launch (`fixed` again).  State slots are bounded by
-// four per resident pair.
-static void make_plan(RunsPlan& p, const pfop_attn_run* runs, int n_runs, int Hq, int Hkv, int hd, bool tree) {
-  const int G = Hq / Hkv;
-  int order[RUNS_MAX], row0[RUNS_MAX], cnt = 0, row = 0;
-  for (int r = 0; r < n_runs; ++r) {
-    if (runs[r].n_rows > 0) {
-      order[cnt++] = r;
-      row0[r] = row;
-    }
-    row += runs[r].n_rows;
-  }
-  // runs with the most keys first: their blocks are the longest items
-  std::stable_sort(order, order + cnt, [&](int a, int b) {
-    return runs[a].pos0 + runs[a].n_rows > runs[b].pos0 + runs[b].n_rows;
-  });
-  const int units = sm_count() / 2;
-  const int fixed = hd == 256 ? 3 : 4;
-  int max_ch = 0, max_rows = 0;
-  double work = 0;  // chunks over all row blocks
-  p.blocks = 0;
-  for (int i = 0; i < cnt; ++i) {
-    const pfop_attn_run& r = runs[order[i]];
-    const int nb = (r.n_rows * G + RROWS - 1) / RROWS, ch = (r.pos0 + r.n_rows + RCH - 1) / RCH;
-    max_ch = std::max(max_ch, ch);
-    max_rows = std::max(max_rows, std::min(RROWS, r.n_rows * G));
-    p.blocks += nb;
-    work += tree ? double(nb) * ch : nb * (r.pos0 + 0.5 * (r.n_rows + RROWS / G)) / RCH + 0.5 * nb;
-  }
-  auto items_of = [&](int gc) {
-    int64_t n = 0;
-    for (int i = 0; i < cnt; ++i) {
-      const pfop_attn_run& r = runs[order[i]];
-      n += int64_t((r.n_rows * G + RROWS - 1) / RROWS) * (((r.pos0 + r.n_rows + RCH - 1) / RCH + gc - 1) / gc);
-    }
-    return n;
-  };
-  int best_gc = max_ch;
-  double best = 1e30;
-  for (int gc = max_ch, s = 1; gc >= 1;) {
-    const int64_t items = items_of(gc);
-    if (gc < max_ch && items * Hkv > 4 * int64_t(units)) break;
-    const double live = std::max<double>(p.blocks, tree ? double(items) : work / gc + 0.5 * p.blocks);
-    const double t = std::max(double(gc + fixed), (work + fixed * live) * Hkv / units) + (gc < max_ch ? fixed : 0);
-    if (t < best) best = t, best_gc = gc;
-    // the next smaller group that makes another number of groups
-    int next = gc;
-    while (next >= gc && s <= max_ch) next = (max_ch + s) / (s + 1), ++s;
-    if (next >= gc) break;
-    gc = next;
-  }
+// Which cut: a pair per item where the items fit the GPU at once and the
+// longest takes no longer than an even share would with the states' traffic
+// and the merge launch (MERGE_COST chunk times); else even shares over the
+// resident pairs, but none below MIN_SHARE.  False: more work than the line
+// of weights can count.
+constexpr int MERGE_COST = 4;
+constexpr int MIN_SHARE = ITEM_FIXED + 2;
+
+template <bool TREE>
+static bool make_plan(RunsPlan& p, const pfop_attn_run* runs, int n_runs, int Hq, int Hkv, int hd) {
   p.sh.Hq = Hq;
   p.sh.Hkv = Hkv;
   p.sh.log_g = 0;
-  while ((1 << p.sh.log_g) < G) ++p.sh.log_g;
-  p.sh.gc = best_gc;
-  p.sh.slot_rows = (max_rows + 31) / 32 * 32;
-  p.split = false;
-  int items = 0;
-  p.rt.n_runs = cnt;
-  for (int i = 0; i < cnt; ++i) {
-    const pfop_attn_run& r = runs[order[i]];
-    const int nb = (r.n_rows * G + RROWS - 1) / RROWS, ch = (r.pos0 + r.n_rows + RCH - 1) / RCH;
-    p.rt.row0[i] = row0[order[i]];
-    p.rt.n[i] = r.n_rows;
-    p.rt.pos0[i] = r.pos0;
-    p.rt.cell0[i] = r.cell0;
-    p.rt.item0[i] = items;
-    p.rt.groups[i] = (ch + best_gc - 1) / best_gc;
-    if (p.rt.groups[i] > 1) p.split = true;
-    items += nb * p.rt.groups[i];
+  while ((1 << p.sh.log_g) < Hq / Hkv) ++p.sh.log_g;
+  int row = 0, n = 0, longest = 0, max_rows = 0;
+  int64_t items = 0, weight = 0;
+  for (int r = 0; r < n_runs; ++r) {
+    if (runs[r].n_rows > 0) {
+      const RunBlocks<TREE> rb(runs[r].n_rows, runs[r].pos0, p.sh.log_g);
+      // an upper bound first: the weights below are 32-bit
+      if (weight + int64_t(rb.nb) * Hkv * (int64_t(rb.last) + ITEM_FIXED) >= (int64_t(1) << 30)) return false;
+      p.rt.row0[n] = row;
+      p.rt.n[n] = runs[r].n_rows;
+      p.rt.pos0[n] = runs[r].pos0;
+      p.rt.cell0[n] = runs[r].cell0;
+      p.rt.item0[n] = static_cast<int>(items);
+      p.rt.w0[n] = static_cast<int>(weight);
+      ++n;
+      items += int64_t(rb.nb) * Hkv;
+      weight += int64_t(rb.weight(rb.nb)) * Hkv;
+      longest = std::max(longest, rb.last);
+      max_rows = std::max(max_rows, std::min(RROWS, runs[r].n_rows << p.sh.log_g));
+    }
+    row += runs[r].n_rows;
   }
-  p.sh.items = items;
-  p.state_bytes =
-      p.split ? int64_t(items) * Hkv * p.sh.slot_rows * runs_state_stride(hd) * int64_t(sizeof(float)) : 0;
+  p.rt.n_runs = n;
+  p.rt.item0[n] = static_cast<int>(items);
+  p.rt.w0[n] = static_cast<int>(weight);
+  p.items = static_cast<int>(items);
+  p.sh.slot_rows = (max_rows + 31) / 32 * 32;
+  const int units = std::max(1, sm_count() / 2);
+  const int share = std::max<int>(MIN_SHARE, static_cast<int>((weight + units - 1) / units));
+  if (items <= units && longest + ITEM_FIXED <= share + MERGE_COST) {
+    p.sh.per = 0;
+    p.sh.pairs = p.items;
+    p.state_bytes = 0;
+  } else {
+    p.sh.per = share;
+    p.sh.pairs = static_cast<int>((weight + share - 1) / share);
+    p.state_bytes =
+        int64_t(2) * p.sh.pairs * p.sh.slot_rows * runs_state_stride(hd) * static_cast<int64_t>(sizeof(float));
+  }
+  return true;
 }
 
 template <int HD, bool TREE>
@@ -827,11 +986,16 @@ static cudaError_t launch_runs(const RunsPlan& p, const __half* q, const __half*
                     : encode_fp16_sw64(&tv, v, 3, dims, st, vbox, &why)))
       return cudaErrorInvalidValue;
   }
-  e = launch_k(attn_runs_kernel<HD, TREE>, dim3(2u * p.sh.items * Hkv), dim3(C::THREADS), C::SMEM, s, 2, tq, tk, tv,
-               p.rt, p.sh, mask, words, out, part, err);
-  if (e != cudaSuccess || !p.split) return e;
-  return launch_k(attn_runs_merge_kernel<HD, TREE>, dim3(p.blocks * (p.sh.slot_rows / 8), Hkv), dim3(256), 0, s, 1,
-                  p.rt, p.sh, static_cast<const float*>(part), out);
+  e = launch_k(attn_runs_kernel<HD, TREE>, dim3(2u * p.sh.pairs), dim3(C::THREADS), C::SMEM, s, 2, tq, tk, tv, p.rt,
+               p.sh, mask, words, out, part, err);
+  if (e != cudaSuccess || p.sh.per == 0 || p.sh.pairs == 1) return e;
+  // warps per row: an item lies in about pairs / items + 1 pairs
+  const int by_item = p.items < p.sh.pairs - 1 ? 1 : 0;
+  const int spread = p.sh.pairs / std::max(1, p.items) + 1;
+  const int wpr = spread <= 4 ? 1 : spread <= 8 ? 2 : spread <= 16 ? 4 : 8;
+  return launch_k(attn_runs_merge_kernel<HD, TREE>,
+                  dim3(by_item ? p.items : p.sh.pairs - 1, p.sh.slot_rows / (8 / wpr)), dim3(256), 0, s, 1, p.rt, p.sh,
+                  by_item, wpr, static_cast<const float*>(part), out);
 }
 
 }  // namespace pf
@@ -882,13 +1046,14 @@ int run_attention(bool tree, const void* q, const void* k, const void* v, int64_
   }
   if (total == 0) return PF_OK;
   if (!q || !k || !v || !out || !work || (tree && !mask)) return fail(PF_E_ARG, "null buffer");
-  if ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v) |
-       reinterpret_cast<uintptr_t>(out)) & 15)
-    return fail(PF_E_ARG, "q, k, v and out must be 16-byte aligned");
+  if (((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v)) & 15) ||
+      (reinterpret_cast<uintptr_t>(out) & 31))
+    return fail(PF_E_ARG, "q, k and v must be 16-byte aligned, out 32-byte aligned");
   if (tree && (reinterpret_cast<uintptr_t>(mask) & 7)) return fail(PF_E_ARG, "mask must be 8-byte aligned");
   if (reinterpret_cast<uintptr_t>(work) & 255) return fail(PF_E_ARG, "the scratch must be 256-byte aligned");
   RunsPlan p;
-  make_plan(p, runs, n_runs, Hq, Hkv, hd, tree);
+  if (!(tree ? make_plan<true>(p, runs, n_runs, Hq, Hkv, hd) : make_plan<false>(p, runs, n_runs, Hq, Hkv, hd)))
+    return fail(PF_E_ARG, "more work than one call takes (2^30 chunks of 256 rows by 128 keys)");
   if (work_bytes < WORK_HEADER + p.state_bytes) return fail(PF_E_ARG, "the scratch is smaller than these runs need");
   int* err = static_cast<int*>(work);
   float* part = reinterpret_cast<float*>(static_cast<uint8_t*>(work) + WORK_HEADER);
@@ -926,8 +1091,8 @@ extern "C" int64_t pfop_attention_work_bytes(int32_t Hq, int32_t Hkv, int32_t hd
   if (rc != PF_OK) return rc;
   if (total == 0) return WORK_HEADER;
   RunsPlan a, b;
-  make_plan(a, runs, n_runs, Hq, Hkv, hd, false);
-  make_plan(b, runs, n_runs, Hq, Hkv, hd, true);
+  if (!make_plan<false>(a, runs, n_runs, Hq, Hkv, hd) || !make_plan<true>(b, runs, n_runs, Hq, Hkv, hd))
+    return fail(PF_E_ARG, "more work than one call takes (2^30 chunks of 256 rows by 128 keys)");
   return WORK_HEADER + std::max(a.state_bytes, b.state_bytes);
 }
 

@@ -76,7 +76,7 @@ def test_mask_words(lib, words, rows):
 def test_buffers(lib):
     one = [(4, 0, 0)]
     for name in ("q", "k", "v", "out"):
-        for bad in (None, 0x10008):
+        for bad in (None, 0x10008) + ((0x10010,) if name == "out" else ()):
             assert _packed(lib, one, **{name: bad}) == PF_E_ARG, name
     assert _packed(lib, one, work=None) == PF_E_ARG
     assert _packed(lib, one, work=WORK + 16) == PF_E_ARG
