@@ -29,13 +29,15 @@
 // complete on the even CTA's barriers); warp 0 of the even CTA issues the
 // MMAs of the pair; the others own the CTA's 128 rows (thread = TMEM lane =
 // row): softmax, P (fp16, over the columns of S that it came from), the
-// rescale of O, the output.  Two S buffers let S of the next chunk be formed
-// while P of this one is.  At hd 256 one warpgroup (warps 2..5) keeps up
-// with the MMAs; at hd 64, where a chunk has a quarter of the MMA work for
-// the same exponentials, two warpgroups take one half of every chunk's keys
-// each, with their own m, l and O (TMEM has room for two), and join them at
-// the end.  All waits are bounded (PF_WAIT_CYCLES): one that gives up flags
-// the scratch's error word and the pair unwinds.
+// rescale of O, the output.  At hd 256 one warpgroup keeps up with the MMAs
+// (2048 clocks a chunk against about 1600) and two S buffers let S of the
+// next chunk be formed while P of this one is.  At hd 64 a chunk has a
+// quarter of the MMA work for the same exponentials: two warpgroups take the
+// chunks in turn, each with its own m, l and O (joined at the segment's
+// end), so that one's exponentials run while the other loads, looks for the
+// maximum or hands over, and three S buffers keep both supplied.  All waits
+// are bounded (PF_WAIT_CYCLES): one that gives up flags the scratch's error
+// word and the pair unwinds.
 #include "../../include/prefill_ops.h"
 #include "attn.cuh"
 #include "common.cuh"
@@ -76,17 +78,21 @@ struct RunsCfg {
   static constexpr int Q_BYTES = 128 * HD * 2;  // [64-dim box][128 rows][128 B]
   static constexpr int STAGE = 64 * HD * 2;     // half a chunk: K [box][64 keys][128 B], V [box][128 keys][hd/2 dims]
   static constexpr int NST = HD == 256 ? 5 : 16;
-  static constexpr int NH = HD == 256 ? 1 : 2;  // parts of a chunk's keys, a warpgroup each
-  static constexpr int KPT = RCH / NH;          // keys per thread and chunk
+  static constexpr int NG = HD == 256 ? 1 : 2;  // row warpgroups, taking chunks in turn
+  static constexpr int NSB = NG + 1;            // S buffers
+  static constexpr int LA = NSB - 1;            // chunks that S is formed ahead of P V
   static constexpr int OFF_ST = Q_BYTES;
   static constexpr int OFF_BAR = OFF_ST + NST * STAGE;
-  static constexpr int OFF_ML = OFF_BAR + 512;        // (m, l) of each part's rows
-  static constexpr int SMEM = OFF_ML + (NH > 1 ? NH * 128 * 8 : 0) + 1024;  // + alignment slack
-  static constexpr int TMEM_S = 0;          // two S buffers
-  static constexpr int TMEM_O = 2 * RCH;    // one O per part
+  static constexpr int OFF_ML = OFF_BAR + 512;        // (m, l) of each warpgroup's rows
+  static constexpr int SMEM = OFF_ML + (NG > 1 ? NG * 128 * 8 : 0) + 1024;  // + alignment slack
+  static constexpr int TMEM_S = 0;
+  static constexpr int TMEM_O = NSB * RCH;  // an O per warpgroup
   static constexpr int TMEM_COLS = 512;
-  static_assert(TMEM_O + NH * HD <= TMEM_COLS, "TMEM");
-  static constexpr int THREADS = 128 + 128 * NH;
+  static_assert(TMEM_O + NG * HD <= TMEM_COLS, "TMEM");
+  static constexpr int THREADS = 128 + 128 * NG;
+  // Registers (setmaxnreg, hd 64): a row thread holds its 128 scores.
+  // 128 * 88 + 256 * 208 of the 384 * 168 that the block is launched with.
+  static constexpr int LEAN_REGS = 88, ROW_REGS = 208;
   static_assert(SMEM <= 232448, "shared memory");
 };
 
@@ -384,12 +390,12 @@ __global__ void __launch_bounds__(RunsCfg<HD>::THREADS, 1)
   uint64_t* empty = bars + C::NST;  // NST: the MMAs that read the stage are done (its S or P V too)
   uint64_t* cleared = bars + 2 * C::NST;  // NST, in the even CTA: the odd CTA's V is cleared
   uint64_t* q_full = bars + 3 * C::NST;   // in the even CTA: Q of both has landed
-  uint64_t* p_full = q_full + 1;          // by S buffer (chunk parity), in the even CTA: the row warps of both
-  uint64_t* o_free = q_full + 3;          // in the even CTA: the row warps of both have read O
-  uint64_t* q_empty = q_full + 4;         // the segment's last S is formed
-  uint64_t* drain = q_full + 5;           // error path only
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(q_full + 6);
-  static_assert((3 * C::NST + 7) * 8 <= 512 && C::NH <= 2, "barrier layout");
+  uint64_t* q_empty = q_full + 1;         // the segment's last S is formed
+  uint64_t* o_free = q_full + 2;          // in the even CTA: the row warps of both have read O
+  uint64_t* drain = q_full + 3;           // error path only
+  uint64_t* p_full = q_full + 4;          // by S buffer, in the even CTA: a warpgroup of both CTAs
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(p_full + C::NSB);
+  static_assert((3 * C::NST + 5 + C::NSB) * 8 <= 512 && C::NG <= 2, "barrier layout");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = static_cast<int>(cluster_ctarank());
@@ -403,8 +409,8 @@ __global__ void __launch_bounds__(RunsCfg<HD>::THREADS, 1)
     }
     mbar_init(q_full, 1);
     mbar_init(q_empty, 1);
-    for (int b = 0; b < 2; ++b) mbar_init(&p_full[b], 8 * C::NH);
-    mbar_init(o_free, 8 * C::NH);
+    for (int b = 0; b < C::NSB; ++b) mbar_init(&p_full[b], 8);
+    mbar_init(o_free, 8 * C::NG);
     mbar_init(drain, 1);
     fence_mbar_init();
   }
@@ -424,20 +430,17 @@ __global__ void __launch_bounds__(RunsCfg<HD>::THREADS, 1)
 
   // Counters that run on over the pair's segments, the same in every role:
   // ring fills (fill f uses stage f % NST, in its use number f / NST), chunks
-  // (chunk j uses S buffer j & 1) and segments.  A segment's fills: K(0),
-  // K(1), V(0), K(2), V(1), .., V(n-1), so that S(j+1) is formed before P(j)
-  // V(j).  The MMAs of a fill arrive on its stage's `empty`, which serves all
-  // who wait for them in order: the K/V producer, and the row warps for S and
-  // for P V.  (A wait by parity must not come a phase early or late.  Not
-  // early: MMAs finish in order, and a row warp that waits for a fill has
-  // seen one at most three fills before it.  Not late: the stage's next use
-  // is over only after a later P, for which the waiting warp is needed.)
-  auto k_fill = [](int jl) { return jl == 0 ? 0 : 2 * jl - 1; };
-  auto v_fill = [](int jl, int n) { return jl == n - 1 ? 2 * n - 1 : 2 * jl + 2; };
-  auto fill_is_k = [&](int u) { return u == 0 || (u < 2 * sg.n - 1 && (u & 1)); };
-  auto fill_chunk = [&](int u) {
-    return u == 0 ? 0 : u == 2 * sg.n - 1 ? sg.n - 1 : (u & 1) ? (u + 1) / 2 : u / 2 - 1;
-  };
+  // (chunk j uses S buffer j % NSB and warpgroup j % NG) and segments.  A
+  // segment's fills: K(0) .. K(LA-1), then K(LA), V(0), K(LA+1), V(1), ..,
+  // V(n-1), so that S(j+LA) is formed before P(j) V(j).  The MMAs of a fill
+  // arrive on its stage's `empty`, which serves all who wait for them in
+  // order: the K/V producer, and the row warps for S and for P V.  (A wait by
+  // parity must not come a phase early or late.  Not early: MMAs finish in
+  // order, and a row warp that waits for a fill has seen one less than NST
+  // before it.  Not late: the stage's next use is over only after a later P
+  // V, for which the waiting warp's P or its o_free is needed.)
+  auto k_fill = [](int jl) { return jl < C::LA ? jl : 2 * jl - C::LA; };
+  auto v_fill = [](int jl, int n) { return jl + C::LA < n ? 2 * jl + C::LA + 1 : n + jl; };
   // The V rows of keys past the run (only in the run's last chunk) are
   // cleared in shared memory before the MMAs read them: P is 0 there, but
   // what lies in those cells may be an infinity or NaN.  In the odd CTA that
@@ -454,160 +457,13 @@ __global__ void __launch_bounds__(RunsCfg<HD>::THREADS, 1)
     __syncwarp();
   };
 
-  if (warp == 1) {
-    // ---------------- K/V producer (each CTA its own halves)
-    if (lane == 0) {
-      bool ok = true;
-      uint32_t f = 0, tails = 0;
-      while (ok && sg.next()) {
-        const bool has_tail = tail_keys() < RCH;
-        for (int u = 0; u < 2 * sg.n; ++u, ++f) {
-          const int s = f % C::NST;
-          if (f >= C::NST) ok = mbar_wait(&empty[s], (f / C::NST + 1) & 1, err, PF_DEV_TIMEOUT_PRODUCER);
-          if (!ok) break;
-          uint8_t* dst = smem + C::OFF_ST + s * C::STAGE;
-          const int cell = rt.cell0[sg.run] + (sg.ch0 + fill_chunk(u)) * RCH;
-          const bool last = has_tail && u == 2 * sg.n - 1;
-          const uint32_t bar = map_to_rank(smem_u32(&full[s]), 0);
-          if (rank == 0) mbar_arrive_expect_tx(&full[s], last ? C::STAGE : 2 * C::STAGE);
-          if (fill_is_k(u)) {
-            tma_load_3d_pair(dst, &tmK, bar, sg.kvh * HD, cell + rank * 64, 0);
-          } else if (last && rank == 1) {
-            mbar_arrive_expect_tx(&full[s], C::STAGE);
-            tma_load_3d(dst, &tmV, &full[s], sg.kvh * HD + HD / 2, cell, 0);
-            tails ^= 1u << s;
-          } else {
-            tma_load_3d_pair(dst, &tmV, bar, sg.kvh * HD + rank * (HD / 2), cell, 0);
-          }
-        }
-      }
-      // On an error the copies in flight land before the pair may leave (the
-      // even CTA's barriers count those of both).
-      if (!ok || read_error(err) != 0) {
-        if (rank == 0) {
-          for (uint32_t x = f > C::NST ? f - C::NST : 0; x < f; ++x) runs_drain(&full[x % C::NST], (x / C::NST) & 1);
-        } else {
-          // a stage that never held such a copy is in phase 0, whose waiting
-          // for parity 1 ends at once
-          for (int x = 0; x < C::NST; ++x) runs_drain(&full[x], (tails >> x & 1u) ^ 1u);
-        }
-      }
-    }
-    __syncwarp();
-  } else if (warp == 2) {
-    // ---------------- Q producer
-    if (lane == 0) {
-      bool ok = true;
-      uint32_t seg = 0;
-      for (; ok && sg.next(); ++seg) {
-        if (seg > 0) ok = mbar_wait(q_empty, (seg - 1) & 1, err, PF_DEV_TIMEOUT_PRODUCER);
-        if (!ok) break;
-        if (rank == 0) mbar_arrive_expect_tx(q_full, 2 * C::Q_BYTES);
-        tma_load_4d_pair(smem, &tmQ, map_to_rank(smem_u32(q_full), 0), 0, sg.kvh << sh.log_g,
-                         rt.row0[sg.run] + ((sg.R0 + rank * 128) >> sh.log_g), 0);
-      }
-      if ((!ok || read_error(err) != 0) && rank == 0 && seg > 0) runs_drain(q_full, (seg - 1) & 1);
-    }
-    __syncwarp();
-  } else if (warp == 0 && rank == 1) {
-    // ---------------- the odd CTA's half of the run's last V
-    bool ok = true;
-    uint32_t f = 0, tails = 0;
-    while (ok && sg.next()) {
-      f += 2 * sg.n;
-      if (tail_keys() >= RCH) continue;
-      const int s = (f - 1) % C::NST;
-      ok = mbar_wait(&full[s], tails >> s & 1u, err, PF_DEV_TIMEOUT_MMA);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
-      tails ^= 1u << s;
-      clear_tail(f - 1);
-      if (lane == 0) mbar_arrive_cluster(map_to_rank(smem_u32(&cleared[s]), 0));
-    }
-    __syncwarp();
-  } else if (warp == 0) {
-    // ---------------- MMA issue for the pair: the warp runs the loop in
-    // step, one elected lane issues
-    const bool leader = elect_one();
-    constexpr uint32_t id_qk = idesc_f16_f32(256, RCH, false);
-    constexpr uint32_t id_pv = idesc_f16_f32(256, HD, true);
-    const uint64_t qd0 = sdesc_sw128(smem_u32(smem));
-    const uint32_t ring = smem_u32(smem + C::OFF_ST);
-    const uint32_t empty0 = map_to_rank(smem_u32(empty), 0), empty1 = map_to_rank(smem_u32(empty), 1);
-    bool ok = true, issued = false;
-    uint32_t f0 = 0, j0 = 0, seg = 0, tails = 0;
-    // every lane waits; only the elected lane's success lets MMAs go
-    auto issue_s = [&](int jl) {
-      const uint32_t f = f0 + k_fill(jl), s = f % C::NST;
-      // S(j): P(j-2), which lay in this buffer, was read by MMAs issued before
-      ok = ok && mbar_wait_spin(&full[s], (f / C::NST) & 1, err, PF_DEV_TIMEOUT_MMA);
-      tc_fence_after();
-      if (leader && ok) {
-        const uint64_t kd0 = sdesc_sw128(ring + s * C::STAGE);
-        const uint32_t d = tmem + C::TMEM_S + ((j0 + jl) & 1) * RCH;
-#pragma unroll
-        for (int kk = 0; kk < HD / 16; ++kk) {
-          const int bx = kk >> 2, w = kk & 3;  // 64-dim box, 16-dim step within it
-          tc_mma_f16_pair(d, qd0 + ((bx * (128 * 128) + w * 32) >> 4), kd0 + ((bx * (64 * 128) + w * 32) >> 4), id_qk,
-                          kk > 0 ? 1u : 0u);
-        }
-        tc_commit_pair(empty0 + s * 8);
-        tc_commit_pair(empty1 + s * 8);
-        if (jl == sg.n - 1) {
-          tc_commit_pair(map_to_rank(smem_u32(q_empty), 0));
-          tc_commit_pair(map_to_rank(smem_u32(q_empty), 1));
-        }
-        issued = true;
-      }
-      __syncwarp();
-    };
-    for (; sg.next(); j0 += sg.n, f0 += 2 * sg.n, ++seg) {
-      const bool has_tail = tail_keys() < RCH;
-      ok = ok && mbar_wait_spin(q_full, seg & 1, err, PF_DEV_TIMEOUT_MMA);
-      issue_s(0);
-      for (int jl = 0; jl < sg.n; ++jl) {
-        if (jl + 1 < sg.n) issue_s(jl + 1);
-        const uint32_t f = f0 + v_fill(jl, sg.n), s = f % C::NST, j = j0 + jl;
-        ok = ok && mbar_wait_spin(&full[s], (f / C::NST) & 1, err, PF_DEV_TIMEOUT_MMA);
-        if (has_tail && jl == sg.n - 1) {
-          ok = ok && mbar_wait<true>(&cleared[s], tails >> s & 1u, err, PF_DEV_TIMEOUT_MMA);
-          tails ^= 1u << s;
-          if (!__all_sync(0xffffffffu, ok)) break;
-          clear_tail(f);
-        }
-        // the last segment's O is read out before this one's replaces it
-        if (jl == 0 && seg > 0) ok = ok && mbar_wait(o_free, (seg - 1) & 1, err, PF_DEV_TIMEOUT_MMA);
-        ok = ok && mbar_wait_spin(&p_full[j & 1], (j >> 1) & 1, err, PF_DEV_TIMEOUT_MMA);
-        tc_fence_after();
-        if (leader && ok) {
-          const uint32_t st = ring + s * C::STAGE;
-          const uint64_t vd0 = HD == 256 ? sdesc_sw128_lbo_sbo(st, RCH * 128, 1024) : sdesc_sw64_mn(st);
-          constexpr int KSTEP = 16 * (HD == 256 ? 128 : 64);  // bytes of 16 keys
-          const uint32_t a = tmem + C::TMEM_S + (j & 1) * RCH;
-#pragma unroll
-          for (int h = 0; h < C::NH; ++h)
-#pragma unroll
-            for (int kk = 0; kk < C::KPT / 16; ++kk)
-              tc_mma_f16_ts_pair(tmem + C::TMEM_O + h * HD, a + h * C::KPT + kk * 8,
-                                 vd0 + (((h * (C::KPT / 16) + kk) * KSTEP) >> 4), id_pv, (jl > 0 || kk > 0) ? 1u : 0u);
-          tc_commit_pair(empty0 + s * 8);
-          tc_commit_pair(empty1 + s * 8);
-        }
-        if (!__all_sync(0xffffffffu, ok)) break;
-      }
-      if (!__all_sync(0xffffffffu, ok)) break;
-    }
-    if (!ok && issued && leader) {
-      // the MMAs already issued finish before TMEM is freed
-      tc_commit_pair(map_to_rank(smem_u32(drain), 0));
-      runs_drain(drain, 0);
-    }
-    __syncwarp();
-  } else if (warp >= 4) {
-    // ---------------- rows (warps 4..: TMEM lane quarter warp % 4, part h of each chunk)
+  if (warp >= 4) {
+    if constexpr (C::NG > 1) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::ROW_REGS));
+    // ---------------- rows (warps 4..: TMEM lane quarter warp % 4, warpgroup h)
     const int qw = warp & 3, h = (warp - 4) >> 2;
     const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * qw) << 16);
-    constexpr int NB = C::KPT / 32;
+    const uint32_t o_at = lanes + C::TMEM_O + h * HD;
+    constexpr int NB = RCH / 32;
     const uint64_t c2 = pack_f32x2(cexp, cexp);
     const uint32_t o_free_at = map_to_rank(smem_u32(o_free), 0);
     const uint32_t p_full_at = map_to_rank(smem_u32(p_full), 0);
@@ -615,8 +471,8 @@ __global__ void __launch_bounds__(RunsCfg<HD>::THREADS, 1)
     uint32_t j0 = 0, f0 = 0;
     // the MMAs of fill f are done
     auto done = [&](uint32_t f) {
-      if (lane == 0) ok = mbar_wait_spin(&empty[f % C::NST], (f / C::NST) & 1, err, PF_DEV_TIMEOUT_EPILOGUE);
-      ok = __shfl_sync(0xffffffffu, ok, 0);
+      ok = mbar_wait_spin(&empty[f % C::NST], (f / C::NST) & 1, err, PF_DEV_TIMEOUT_EPILOGUE);
+      ok = __all_sync(0xffffffffu, ok);
       return ok;
     };
     for (; ok && sg.next(); j0 += sg.n, f0 += 2 * sg.n) {
@@ -630,18 +486,19 @@ __global__ void __launch_bounds__(RunsCfg<HD>::THREADS, 1)
       const int pos = row ? pos0 + t : -1;
       const uint64_t* row_mask = TREE && row ? mask + static_cast<size_t>(row0 + t) * words : nullptr;
       float m = -INFINITY, l = 0.f;
-      for (int jl = 0; jl < sg.n; ++jl) {
-        const int b = (j0 + jl) & 1;
+      const int first = C::NG == 1 ? 0 : static_cast<int>((j0 + h) & 1);  // of the warpgroup's chunks
+      for (int jl = first; jl < sg.n; jl += C::NG) {
+        const int b = (j0 + jl) % C::NSB;
         if (!done(f0 + k_fill(jl))) break;
         if (active) {
-          const int key0 = (sg.ch0 + jl) * RCH + h * C::KPT;
-          const uint32_t ts = lanes + C::TMEM_S + b * RCH + h * C::KPT;
+          const int key0 = (sg.ch0 + jl) * RCH;
+          const uint32_t ts = lanes + C::TMEM_S + b * RCH;
           tc_fence_after();
           uint32_t x[NB][32];
 #pragma unroll
           for (int w = 0; w < NB; ++w) tmem_ld32(ts + 32 * w, x[w]);
           // the row's view of its keys, skipped where every row of the warp sees all of them
-          const bool all = TREE ? key0 + C::KPT <= pos0 : __all_sync(0xffffffffu, pos >= key0 + C::KPT - 1);
+          const bool all = TREE ? key0 + RCH <= pos0 : __all_sync(0xffffffffu, pos >= key0 + RCH - 1);
 #pragma unroll
           for (int w = 0; w < NB; ++w) tmem_ld_wait32(x[w]);
           if (!all) {
@@ -683,19 +540,19 @@ __global__ void __launch_bounds__(RunsCfg<HD>::THREADS, 1)
           l = __fmaf_rn(l, scale, l01.x + l01.y);
           m = mn;
           tmem_st_wait();
-          // O *= scale once P V(j-1) has landed, only in the warps where a row
+          // O *= scale once the last P V of it has landed, only in the warps where a row
           // moved its reference
-          if (jl >= 1 && __any_sync(0xffffffffu, resc)) {
-            if (!done(f0 + v_fill(jl - 1, sg.n))) break;
+          if (jl >= C::NG && __any_sync(0xffffffffu, resc)) {
+            if (!done(f0 + v_fill(jl - C::NG, sg.n))) break;
             tc_fence_after();
 #pragma unroll 1
             for (int c = 0; c < HD / 32; ++c) {
               uint32_t y[32];
-              tmem_ld32(lanes + C::TMEM_O + h * HD + 32 * c, y);
+              tmem_ld32(o_at + 32 * c, y);
               tmem_ld_wait32(y);
 #pragma unroll
               for (int q = 0; q < 32; ++q) y[q] = __float_as_uint(__uint_as_float(y[q]) * scale);
-              tmem_st32(lanes + C::TMEM_O + h * HD + 32 * c, y);
+              tmem_st32(o_at + 32 * c, y);
             }
             tmem_st_wait();
           }
@@ -705,10 +562,10 @@ __global__ void __launch_bounds__(RunsCfg<HD>::THREADS, 1)
         if (lane == 0) mbar_arrive_pair_relaxed(p_full_at + b * 8);
       }
       if (ok) done(f0 + v_fill(sg.n - 1, sg.n));
-      // the parts' weights: w_h = 2^((m_h - m) c); each of a row's two warps
-      // writes half of the dims
+      // the warpgroups' weights: w_h = 2^((m_h - m) c); each of a row's two
+      // warps writes half of the dims
       float w0 = 1.f, w1 = 0.f;
-      if constexpr (C::NH > 1) {
+      if constexpr (C::NG > 1) {
         float2* ml = reinterpret_cast<float2*>(smem + C::OFF_ML);
         ml[h * 128 + 32 * qw + lane] = make_float2(m, ok ? l : -1.f);  // -1: this warp gave up (l is a sum of p >= 0)
         asm volatile("bar.sync %0, 64;" ::"r"(1 + qw) : "memory");
@@ -730,20 +587,27 @@ __global__ void __launch_bounds__(RunsCfg<HD>::THREADS, 1)
         const size_t own = whole ? (static_cast<size_t>(row0 + t) * sh.Hq + head) * HD
                                  : (static_cast<size_t>(sg.slot) * sh.slot_rows + (R - sg.R0)) * runs_state_stride(HD);
 #pragma unroll 1
-        for (int c = h * (HD / 32 / C::NH); c < (h + 1) * (HD / 32 / C::NH); ++c) {
+        for (int c = h * (HD / 32 / C::NG); c < (h + 1) * (HD / 32 / C::NG); ++c) {
           uint32_t y[32];
-          tmem_ld32(lanes + C::TMEM_O + 32 * c, y);
-          tmem_ld_wait32(y);
-          if constexpr (C::NH > 1) {
-            uint32_t z[32];
-            tmem_ld32(lanes + C::TMEM_O + HD + 32 * c, z);
-            tmem_ld_wait32(z);
-#pragma unroll
-            for (int q = 0; q < 32; ++q)
-              y[q] = __float_as_uint(__fmaf_rn(w0, __uint_as_float(y[q]), w1 * __uint_as_float(z[q])));
-          } else {
+          if (C::NG == 1 || sg.n > 1) {
+            tmem_ld32(lanes + C::TMEM_O + 32 * c, y);
+            tmem_ld_wait32(y);
 #pragma unroll
             for (int q = 0; q < 32; ++q) y[q] = __float_as_uint(w0 * __uint_as_float(y[q]));
+            if constexpr (C::NG > 1) {
+              uint32_t z[32];
+              tmem_ld32(lanes + C::TMEM_O + HD + 32 * c, z);
+              tmem_ld_wait32(z);
+#pragma unroll
+              for (int q = 0; q < 32; ++q)
+                y[q] = __float_as_uint(__fmaf_rn(w1, __uint_as_float(z[q]), __uint_as_float(y[q])));
+            }
+          } else {  // one chunk: the other warpgroup's O holds nothing
+            const int g = static_cast<int>(j0 & 1);
+            tmem_ld32(lanes + C::TMEM_O + g * HD + 32 * c, y);
+            tmem_ld_wait32(y);
+#pragma unroll
+            for (int q = 0; q < 32; ++q) y[q] = __float_as_uint((g ? w1 : w0) * __uint_as_float(y[q]));
           }
           if (row && whole) {
             uint32_t hb[16];
@@ -765,6 +629,160 @@ __global__ void __launch_bounds__(RunsCfg<HD>::THREADS, 1)
       }
       __syncwarp();
       if (lane == 0) mbar_arrive_pair_relaxed(o_free_at);
+    }
+  } else {
+    if constexpr (C::NG > 1) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::LEAN_REGS));
+    if (warp == 1) {
+      // ---------------- K/V producer (each CTA its own halves)
+      if (lane == 0) {
+        bool ok = true;
+        uint32_t f = 0, tails = 0;
+        while (ok && sg.next()) {
+          const bool has_tail = tail_keys() < RCH;
+          auto load = [&](bool is_k, int jl) {
+            const int s = f % C::NST;
+            if (f >= C::NST) ok = ok && mbar_wait(&empty[s], (f / C::NST + 1) & 1, err, PF_DEV_TIMEOUT_PRODUCER);
+            if (!ok) return;
+            uint8_t* dst = smem + C::OFF_ST + s * C::STAGE;
+            const int cell = rt.cell0[sg.run] + (sg.ch0 + jl) * RCH;
+            const bool last = !is_k && has_tail && jl == sg.n - 1;
+            const uint32_t bar = map_to_rank(smem_u32(&full[s]), 0);
+            if (rank == 0) mbar_arrive_expect_tx(&full[s], last ? C::STAGE : 2 * C::STAGE);
+            if (is_k) {
+              tma_load_3d_pair(dst, &tmK, bar, sg.kvh * HD, cell + rank * 64, 0);
+            } else if (last && rank == 1) {
+              mbar_arrive_expect_tx(&full[s], C::STAGE);
+              tma_load_3d(dst, &tmV, &full[s], sg.kvh * HD + HD / 2, cell, 0);
+              tails ^= 1u << s;
+            } else {
+              tma_load_3d_pair(dst, &tmV, bar, sg.kvh * HD + rank * (HD / 2), cell, 0);
+            }
+            ++f;
+          };
+          for (int jl = -C::LA; jl < sg.n && ok; ++jl) {
+            if (jl + C::LA < sg.n) load(true, jl + C::LA);
+            if (jl >= 0) load(false, jl);
+          }
+        }
+        // On an error the copies in flight land before the pair may leave (the
+        // even CTA's barriers count those of both).
+        if (!ok || read_error(err) != 0) {
+          if (rank == 0) {
+            for (uint32_t x = f > C::NST ? f - C::NST : 0; x < f; ++x) runs_drain(&full[x % C::NST], (x / C::NST) & 1);
+          } else {
+            // a stage that never held such a copy is in phase 0, whose waiting
+            // for parity 1 ends at once
+            for (int x = 0; x < C::NST; ++x) runs_drain(&full[x], (tails >> x & 1u) ^ 1u);
+          }
+        }
+      }
+      __syncwarp();
+    } else if (warp == 2) {
+      // ---------------- Q producer
+      if (lane == 0) {
+        bool ok = true;
+        uint32_t seg = 0;
+        for (; ok && sg.next(); ++seg) {
+          if (seg > 0) ok = mbar_wait(q_empty, (seg - 1) & 1, err, PF_DEV_TIMEOUT_PRODUCER);
+          if (!ok) break;
+          if (rank == 0) mbar_arrive_expect_tx(q_full, 2 * C::Q_BYTES);
+          tma_load_4d_pair(smem, &tmQ, map_to_rank(smem_u32(q_full), 0), 0, sg.kvh << sh.log_g,
+                           rt.row0[sg.run] + ((sg.R0 + rank * 128) >> sh.log_g), 0);
+        }
+        if ((!ok || read_error(err) != 0) && rank == 0 && seg > 0) runs_drain(q_full, (seg - 1) & 1);
+      }
+      __syncwarp();
+    } else if (warp == 0 && rank == 1) {
+      // ---------------- the odd CTA's half of the run's last V
+      bool ok = true;
+      uint32_t f = 0, tails = 0;
+      while (ok && sg.next()) {
+        f += 2 * sg.n;
+        if (tail_keys() >= RCH) continue;
+        const int s = (f - 1) % C::NST;
+        ok = mbar_wait(&full[s], tails >> s & 1u, err, PF_DEV_TIMEOUT_MMA);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tails ^= 1u << s;
+        clear_tail(f - 1);
+        if (lane == 0) mbar_arrive_cluster(map_to_rank(smem_u32(&cleared[s]), 0));
+      }
+      __syncwarp();
+    } else if (warp == 0) {
+      // ---------------- MMA issue for the pair: the warp runs the loop in
+      // step, one elected lane issues
+      const bool leader = elect_one();
+      constexpr uint32_t id_qk = idesc_f16_f32(256, RCH, false);
+      constexpr uint32_t id_pv = idesc_f16_f32(256, HD, true);
+      const uint64_t qd0 = sdesc_sw128(smem_u32(smem));
+      const uint32_t ring = smem_u32(smem + C::OFF_ST);
+      const uint32_t empty0 = map_to_rank(smem_u32(empty), 0), empty1 = map_to_rank(smem_u32(empty), 1);
+      bool ok = true, issued = false;
+      uint32_t f0 = 0, j0 = 0, seg = 0, tails = 0;
+      // every lane waits; only the elected lane's success lets MMAs go
+      auto issue_s = [&](int jl) {
+        const uint32_t f = f0 + k_fill(jl), s = f % C::NST;
+        // P(j - NSB), which lay in this buffer, was read by MMAs issued before
+        ok = ok && mbar_wait_spin(&full[s], (f / C::NST) & 1, err, PF_DEV_TIMEOUT_MMA);
+        tc_fence_after();
+        if (leader && ok) {
+          const uint64_t kd0 = sdesc_sw128(ring + s * C::STAGE);
+          const uint32_t d = tmem + C::TMEM_S + ((j0 + jl) % C::NSB) * RCH;
+#pragma unroll
+          for (int kk = 0; kk < HD / 16; ++kk) {
+            const int bx = kk >> 2, w = kk & 3;  // 64-dim box, 16-dim step within it
+            tc_mma_f16_pair(d, qd0 + ((bx * (128 * 128) + w * 32) >> 4), kd0 + ((bx * (64 * 128) + w * 32) >> 4), id_qk,
+                            kk > 0 ? 1u : 0u);
+          }
+          tc_commit_pair(empty0 + s * 8);
+          tc_commit_pair(empty1 + s * 8);
+          if (jl == sg.n - 1) {
+            tc_commit_pair(map_to_rank(smem_u32(q_empty), 0));
+            tc_commit_pair(map_to_rank(smem_u32(q_empty), 1));
+          }
+          issued = true;
+        }
+        __syncwarp();
+      };
+      for (; sg.next(); j0 += sg.n, f0 += 2 * sg.n, ++seg) {
+        const bool has_tail = tail_keys() < RCH;
+        ok = ok && mbar_wait_spin(q_full, seg & 1, err, PF_DEV_TIMEOUT_MMA);
+        for (int jl = 0; jl < C::LA && jl < sg.n; ++jl) issue_s(jl);
+        for (int jl = 0; jl < sg.n; ++jl) {
+          if (jl + C::LA < sg.n) issue_s(jl + C::LA);
+          const uint32_t f = f0 + v_fill(jl, sg.n), s = f % C::NST, j = j0 + jl;
+          ok = ok && mbar_wait_spin(&full[s], (f / C::NST) & 1, err, PF_DEV_TIMEOUT_MMA);
+          if (has_tail && jl == sg.n - 1) {
+            ok = ok && mbar_wait<true>(&cleared[s], tails >> s & 1u, err, PF_DEV_TIMEOUT_MMA);
+            tails ^= 1u << s;
+            if (!__all_sync(0xffffffffu, ok)) break;
+            clear_tail(f);
+          }
+          // the last segment's O is read out before this one's replaces it
+          if (jl == 0 && seg > 0) ok = ok && mbar_wait(o_free, (seg - 1) & 1, err, PF_DEV_TIMEOUT_MMA);
+          ok = ok && mbar_wait_spin(&p_full[j % C::NSB], (j / C::NSB) & 1, err, PF_DEV_TIMEOUT_MMA);
+          tc_fence_after();
+          if (leader && ok) {
+            const uint32_t st = ring + s * C::STAGE;
+            const uint64_t vd0 = HD == 256 ? sdesc_sw128_lbo_sbo(st, RCH * 128, 1024) : sdesc_sw64_mn(st);
+            constexpr int KSTEP = 16 * (HD == 256 ? 128 : 64);  // bytes of 16 keys
+            const uint32_t a = tmem + C::TMEM_S + (j % C::NSB) * RCH, d = tmem + C::TMEM_O + (j % C::NG) * HD;
+#pragma unroll
+            for (int kk = 0; kk < RCH / 16; ++kk)
+              tc_mma_f16_ts_pair(d, a + kk * 8, vd0 + ((kk * KSTEP) >> 4), id_pv, (jl >= C::NG || kk > 0) ? 1u : 0u);
+            tc_commit_pair(empty0 + s * 8);
+            tc_commit_pair(empty1 + s * 8);
+          }
+          if (!__all_sync(0xffffffffu, ok)) break;
+        }
+        if (!__all_sync(0xffffffffu, ok)) break;
+      }
+      if (!ok && issued && leader) {
+        // the MMAs already issued finish before TMEM is freed
+        tc_commit_pair(map_to_rank(smem_u32(drain), 0));
+        runs_drain(drain, 0);
+      }
+      __syncwarp();
     }
   }
   tc_fence_before();
