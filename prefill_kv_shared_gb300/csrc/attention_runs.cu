@@ -24,10 +24,13 @@
 // every V chunk (hd/2 dims), need 32, and the halves leave room for 2.5
 // chunks in flight beside Q at hd 256.
 //
-// Roles of a CTA: warp 1 copies Q and the K/V halves by TMA (one ring of
+// Roles of a CTA: warp 1 copies the K/V halves by TMA (one ring of
 // stages, in the order in which the MMAs use them; the copies of both CTAs
-// complete on the even CTA's barriers); warp 0 of the even CTA issues the
-// MMAs of the pair; the others own the CTA's 128 rows (thread = TMEM lane =
+// complete on the even CTA's barriers), warp 2 Q; warp 0 of the even CTA
+// issues the pair's MMAs, at hd 64 with warp 3 for O += P V (waiting and
+// issuing for both took one warp about 1400 clocks a chunk, twice the MMAs of
+// a chunk at hd 64; at hd 256 one warp is better, since S(j+2) then needs no
+// wait for P(j) V(j)); warps 4 and up own the CTA's 128 rows (thread = TMEM lane =
 // row): softmax, P (fp16, over the columns of S that it came from), the
 // rescale of O, the output.  At hd 256 one warpgroup keeps up with the MMAs
 // (2048 clocks a chunk against about 1600) and two S buffers let S of the
@@ -66,6 +69,7 @@ struct RunsShape {
   int Hq, Hkv, log_g;  // G = 1 << log_g query heads per KV head
   int per;             // weight of a pair's share; 0: a pair per item
   int pairs;
+  int desc_by_item;  // the merge kernel's table has an entry per item, not per pair (the smaller of the two)
   int slot_rows;  // rows of a state slot in the scratch
 };
 
@@ -377,7 +381,7 @@ __global__ void __launch_bounds__(RunsCfg<HD>::THREADS, 1)
     attn_runs_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                      const __grid_constant__ CUtensorMap tmV, const __grid_constant__ RunTable rt, const RunsShape sh,
                      const uint64_t* __restrict__ mask, int words, __nv_bfloat16* __restrict__ out,
-                     float* __restrict__ part, int* err) {
+                     float* __restrict__ part, int* __restrict__ desc, int* err) {
   using C = RunsCfg<HD>;
   constexpr float cexp = attn_c<HD>();
   extern __shared__ uint8_t smem_raw[];
@@ -392,10 +396,10 @@ __global__ void __launch_bounds__(RunsCfg<HD>::THREADS, 1)
   uint64_t* q_full = bars + 3 * C::NST;   // in the even CTA: Q of both has landed
   uint64_t* q_empty = q_full + 1;         // the segment's last S is formed
   uint64_t* o_free = q_full + 2;          // in the even CTA: the row warps of both have read O
-  uint64_t* drain = q_full + 3;           // error path only
-  uint64_t* p_full = q_full + 4;          // by S buffer, in the even CTA: a warpgroup of both CTAs
+  uint64_t* drain = q_full + 3;           // 2, error path only
+  uint64_t* p_full = q_full + 5;          // by S buffer, in the even CTA: a warpgroup of both CTAs
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(p_full + C::NSB);
-  static_assert((3 * C::NST + 5 + C::NSB) * 8 <= 512 && C::NG <= 2, "barrier layout");
+  static_assert((3 * C::NST + 6 + C::NSB) * 8 <= 512 && C::NG <= 2, "barrier layout");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = static_cast<int>(cluster_ctarank());
@@ -411,7 +415,8 @@ __global__ void __launch_bounds__(RunsCfg<HD>::THREADS, 1)
     mbar_init(q_empty, 1);
     for (int b = 0; b < C::NSB; ++b) mbar_init(&p_full[b], 8);
     mbar_init(o_free, 8 * C::NG);
-    mbar_init(drain, 1);
+    mbar_init(&drain[0], 1);
+    mbar_init(&drain[1], 1);
     fence_mbar_init();
   }
   if (warp == 1 && lane == 0) {
@@ -434,11 +439,13 @@ __global__ void __launch_bounds__(RunsCfg<HD>::THREADS, 1)
   // segment's fills: K(0) .. K(LA-1), then K(LA), V(0), K(LA+1), V(1), ..,
   // V(n-1), so that S(j+LA) is formed before P(j) V(j).  The MMAs of a fill
   // arrive on its stage's `empty`, which serves all who wait for them in
-  // order: the K/V producer, and the row warps for S and for P V.  (A wait by
-  // parity must not come a phase early or late.  Not early: MMAs finish in
-  // order, and a row warp that waits for a fill has seen one less than NST
-  // before it.  Not late: the stage's next use is over only after a later P
-  // V, for which the waiting warp's P or its o_free is needed.)
+  // order: the K/V producer, the row warps for S and for P V, and the S
+  // issuer for P V.  (A wait by parity must not come a phase early or late.
+  // Not early: who waits for a fill knows that the copies of fewer than NST
+  // fills before it were issued and that S and P V up to NSB chunks back are
+  // done, so the stage's last use is over.  Not late: the stage's next use is
+  // over only after a later P V, which needs the waiting warp's P, its S or
+  // its o_free.)
   auto k_fill = [](int jl) { return jl < C::LA ? jl : 2 * jl - C::LA; };
   auto v_fill = [](int jl, int n) { return jl + C::LA < n ? 2 * jl + C::LA + 1 : n + jl; };
   // The V rows of keys past the run (only in the run's last chunk) are
@@ -563,7 +570,7 @@ __global__ void __launch_bounds__(RunsCfg<HD>::THREADS, 1)
       }
       if (ok) done(f0 + v_fill(sg.n - 1, sg.n));
       // the warpgroups' weights: w_h = 2^((m_h - m) c); each of a row's two
-      // warps writes half of the dims
+      // warps writes half of the 64 dims
       float w0 = 1.f, w1 = 0.f;
       if constexpr (C::NG > 1) {
         float2* ml = reinterpret_cast<float2*>(smem + C::OFF_ML);
@@ -586,29 +593,7 @@ __global__ void __launch_bounds__(RunsCfg<HD>::THREADS, 1)
         w1 *= inv;
         const size_t own = whole ? (static_cast<size_t>(row0 + t) * sh.Hq + head) * HD
                                  : (static_cast<size_t>(sg.slot) * sh.slot_rows + (R - sg.R0)) * runs_state_stride(HD);
-#pragma unroll 1
-        for (int c = h * (HD / 32 / C::NG); c < (h + 1) * (HD / 32 / C::NG); ++c) {
-          uint32_t y[32];
-          if (C::NG == 1 || sg.n > 1) {
-            tmem_ld32(lanes + C::TMEM_O + 32 * c, y);
-            tmem_ld_wait32(y);
-#pragma unroll
-            for (int q = 0; q < 32; ++q) y[q] = __float_as_uint(w0 * __uint_as_float(y[q]));
-            if constexpr (C::NG > 1) {
-              uint32_t z[32];
-              tmem_ld32(lanes + C::TMEM_O + HD + 32 * c, z);
-              tmem_ld_wait32(z);
-#pragma unroll
-              for (int q = 0; q < 32; ++q)
-                y[q] = __float_as_uint(__fmaf_rn(w1, __uint_as_float(z[q]), __uint_as_float(y[q])));
-            }
-          } else {  // one chunk: the other warpgroup's O holds nothing
-            const int g = static_cast<int>(j0 & 1);
-            tmem_ld32(lanes + C::TMEM_O + g * HD + 32 * c, y);
-            tmem_ld_wait32(y);
-#pragma unroll
-            for (int q = 0; q < 32; ++q) y[q] = __float_as_uint((g ? w1 : w0) * __uint_as_float(y[q]));
-          }
+        auto store = [&](int c, const uint32_t (&y)[32]) {
           if (row && whole) {
             uint32_t hb[16];
 #pragma unroll
@@ -623,6 +608,37 @@ __global__ void __launch_bounds__(RunsCfg<HD>::THREADS, 1)
             for (int q = 0; q < 4; ++q) st_global_v8(part + own + 32 * c + 8 * q, y + 8 * q);
           }
           __syncwarp();
+        };
+        // two loads of 32 columns in flight
+        uint32_t y[32], z[32];
+        if constexpr (C::NG == 1) {
+#pragma unroll 1
+          for (int c = 0; c < HD / 32; c += 2) {
+            tmem_ld32(lanes + C::TMEM_O + 32 * c, y);
+            tmem_ld32(lanes + C::TMEM_O + 32 * c + 32, z);
+            tmem_ld_wait32(y);
+            tmem_ld_wait32(z);
+#pragma unroll
+            for (int q = 0; q < 32; ++q) {
+              y[q] = __float_as_uint(w0 * __uint_as_float(y[q]));
+              z[q] = __float_as_uint(w0 * __uint_as_float(z[q]));
+            }
+            store(c, y);
+            store(c + 1, z);
+          }
+        } else {
+          // columns h * 32 .. + 31 of both O; after one chunk the other
+          // warpgroup's holds nothing
+          const int own_g = static_cast<int>(j0 & 1), other = sg.n > 1 ? own_g ^ 1 : own_g;
+          const float wa = own_g ? w1 : w0, wb = sg.n > 1 ? (own_g ? w0 : w1) : 0.f;
+          tmem_ld32(lanes + C::TMEM_O + own_g * HD + 32 * h, y);
+          tmem_ld32(lanes + C::TMEM_O + other * HD + 32 * h, z);
+          tmem_ld_wait32(y);
+          tmem_ld_wait32(z);
+#pragma unroll
+          for (int q = 0; q < 32; ++q)
+            y[q] = __float_as_uint(__fmaf_rn(wa, __uint_as_float(y[q]), wb * __uint_as_float(z[q])));
+          store(h, y);
         }
         if (!whole && row && h == 0) *reinterpret_cast<float2*>(part + own + HD) = make_float2(m, l);
         tc_fence_before();
@@ -708,31 +724,61 @@ __global__ void __launch_bounds__(RunsCfg<HD>::THREADS, 1)
         if (lane == 0) mbar_arrive_cluster(map_to_rank(smem_u32(&cleared[s]), 0));
       }
       __syncwarp();
-    } else if (warp == 0) {
-      // ---------------- MMA issue for the pair: the warp runs the loop in
-      // step, one elected lane issues
+    } else if (rank == 1) {
+      // ---------------- warp 3: what the merge kernel has to know of this pair
+      if (lane == 0 && sh.per != 0) {
+        int4* d = reinterpret_cast<int4*>(desc);
+        const int pair = static_cast<int>(blockIdx.x >> 1);
+        if (!sh.desc_by_item) d[2 * pair] = make_int4(0, 0, 0, 0);
+        while (sg.next()) {
+          if (sg.ch0 > 0 || (sg.slot < 0 && !sh.desc_by_item)) continue;
+          // the item's first segment: its pairs (0: it is whole), rows, first packed row, KV head; first row
+          const RunBlocks<TREE> rb(rt.n[sg.run], rt.pos0[sg.run], sh.log_g);
+          const int i = rb.nb - 1 - sg.R0 / RROWS;
+          const int left = rb.chunks(i) - sg.n;  // chunks in the pairs after this one
+          const int at = sh.desc_by_item ? rt.item0[sg.run] + sg.kvh * rb.nb + i : pair;
+          d[2 * at] = make_int4(left ? 1 + (left + sh.per - 1) / sh.per : 0,
+                                min(RROWS, (rt.n[sg.run] << sh.log_g) - sg.R0), rt.row0[sg.run], sg.kvh);
+          d[2 * at + 1] = make_int4(sg.R0, pair, 0, 0);
+        }
+      }
+      __syncwarp();
+    } else {
+      // ---------------- MMA issue for the pair: a warp runs its loop in step,
+      // one elected lane issues.  Every lane waits; only the elected lane's
+      // success lets MMAs go.
       const bool leader = elect_one();
-      constexpr uint32_t id_qk = idesc_f16_f32(256, RCH, false);
-      constexpr uint32_t id_pv = idesc_f16_f32(256, HD, true);
-      const uint64_t qd0 = sdesc_sw128(smem_u32(smem));
       const uint32_t ring = smem_u32(smem + C::OFF_ST);
       const uint32_t empty0 = map_to_rank(smem_u32(empty), 0), empty1 = map_to_rank(smem_u32(empty), 1);
       bool ok = true, issued = false;
       uint32_t f0 = 0, j0 = 0, seg = 0, tails = 0;
-      // every lane waits; only the elected lane's success lets MMAs go
+      constexpr bool TWO = C::NG > 1;  // S and P V have a warp each
+      constexpr uint32_t id_qk = idesc_f16_f32(256, RCH, false);
+      constexpr uint32_t id_pv = idesc_f16_f32(256, HD, true);
+      const uint64_t qd0 = sdesc_sw128(smem_u32(smem));
+      uint32_t v_of[C::NSB];  // fills of V of the last NSB chunks, oldest first
+#pragma unroll
+      for (int i = 0; i < C::NSB; ++i) v_of[i] = 0;
+      // S(j) = Q K^T
       auto issue_s = [&](int jl) {
-        const uint32_t f = f0 + k_fill(jl), s = f % C::NST;
-        // P(j - NSB), which lay in this buffer, was read by MMAs issued before
+        const uint32_t f = f0 + k_fill(jl), s = f % C::NST, j = j0 + jl, b = j % C::NSB;
         ok = ok && mbar_wait_spin(&full[s], (f / C::NST) & 1, err, PF_DEV_TIMEOUT_MMA);
-        tc_fence_after();
+        if (TWO) {
+          // the buffer's last P has been used (one warp: by MMAs issued before)
+          if (j >= C::NSB)
+            ok = ok && mbar_wait_spin(&empty[v_of[0] % C::NST], (v_of[0] / C::NST) & 1, err, PF_DEV_TIMEOUT_MMA);
+          tc_fence_after();
+#pragma unroll
+          for (int i = 0; i + 1 < C::NSB; ++i) v_of[i] = v_of[i + 1];
+          v_of[C::NSB - 1] = f0 + v_fill(jl, sg.n);
+        }
         if (leader && ok) {
           const uint64_t kd0 = sdesc_sw128(ring + s * C::STAGE);
-          const uint32_t d = tmem + C::TMEM_S + ((j0 + jl) % C::NSB) * RCH;
 #pragma unroll
           for (int kk = 0; kk < HD / 16; ++kk) {
             const int bx = kk >> 2, w = kk & 3;  // 64-dim box, 16-dim step within it
-            tc_mma_f16_pair(d, qd0 + ((bx * (128 * 128) + w * 32) >> 4), kd0 + ((bx * (64 * 128) + w * 32) >> 4), id_qk,
-                            kk > 0 ? 1u : 0u);
+            tc_mma_f16_pair(tmem + C::TMEM_S + b * RCH, qd0 + ((bx * (128 * 128) + w * 32) >> 4),
+                            kd0 + ((bx * (64 * 128) + w * 32) >> 4), id_qk, kk > 0 ? 1u : 0u);
           }
           tc_commit_pair(empty0 + s * 8);
           tc_commit_pair(empty1 + s * 8);
@@ -744,43 +790,54 @@ __global__ void __launch_bounds__(RunsCfg<HD>::THREADS, 1)
         }
         __syncwarp();
       };
-      for (; sg.next(); j0 += sg.n, f0 += 2 * sg.n, ++seg) {
-        const bool has_tail = tail_keys() < RCH;
-        ok = ok && mbar_wait_spin(q_full, seg & 1, err, PF_DEV_TIMEOUT_MMA);
-        for (int jl = 0; jl < C::LA && jl < sg.n; ++jl) issue_s(jl);
-        for (int jl = 0; jl < sg.n; ++jl) {
-          if (jl + C::LA < sg.n) issue_s(jl + C::LA);
-          const uint32_t f = f0 + v_fill(jl, sg.n), s = f % C::NST, j = j0 + jl;
-          ok = ok && mbar_wait_spin(&full[s], (f / C::NST) & 1, err, PF_DEV_TIMEOUT_MMA);
-          if (has_tail && jl == sg.n - 1) {
-            ok = ok && mbar_wait<true>(&cleared[s], tails >> s & 1u, err, PF_DEV_TIMEOUT_MMA);
-            tails ^= 1u << s;
-            if (!__all_sync(0xffffffffu, ok)) break;
-            clear_tail(f);
-          }
-          // the last segment's O is read out before this one's replaces it
-          if (jl == 0 && seg > 0) ok = ok && mbar_wait(o_free, (seg - 1) & 1, err, PF_DEV_TIMEOUT_MMA);
-          ok = ok && mbar_wait_spin(&p_full[j % C::NSB], (j / C::NSB) & 1, err, PF_DEV_TIMEOUT_MMA);
-          tc_fence_after();
-          if (leader && ok) {
-            const uint32_t st = ring + s * C::STAGE;
-            const uint64_t vd0 = HD == 256 ? sdesc_sw128_lbo_sbo(st, RCH * 128, 1024) : sdesc_sw64_mn(st);
-            constexpr int KSTEP = 16 * (HD == 256 ? 128 : 64);  // bytes of 16 keys
-            const uint32_t a = tmem + C::TMEM_S + (j % C::NSB) * RCH, d = tmem + C::TMEM_O + (j % C::NG) * HD;
-#pragma unroll
-            for (int kk = 0; kk < RCH / 16; ++kk)
-              tc_mma_f16_ts_pair(d, a + kk * 8, vd0 + ((kk * KSTEP) >> 4), id_pv, (jl >= C::NG || kk > 0) ? 1u : 0u);
-            tc_commit_pair(empty0 + s * 8);
-            tc_commit_pair(empty1 + s * 8);
-          }
-          if (!__all_sync(0xffffffffu, ok)) break;
+      // O += P(j) V(j)
+      auto issue_pv = [&](int jl) {
+        const uint32_t f = f0 + v_fill(jl, sg.n), s = f % C::NST, j = j0 + jl, b = j % C::NSB;
+        ok = ok && mbar_wait_spin(&full[s], (f / C::NST) & 1, err, PF_DEV_TIMEOUT_MMA);
+        if (jl == sg.n - 1 && tail_keys() < RCH) {
+          ok = ok && mbar_wait<true>(&cleared[s], tails >> s & 1u, err, PF_DEV_TIMEOUT_MMA);
+          tails ^= 1u << s;
+          ok = __all_sync(0xffffffffu, ok);
+          if (ok) clear_tail(f);
         }
+        // the last segment's O is read out before this one's replaces it
+        if (jl == 0 && seg > 0) ok = ok && mbar_wait(o_free, (seg - 1) & 1, err, PF_DEV_TIMEOUT_MMA);
+        ok = ok && mbar_wait_spin(&p_full[b], (j / C::NSB) & 1, err, PF_DEV_TIMEOUT_MMA);
+        tc_fence_after();
+        if (leader && ok) {
+          const uint32_t st = ring + s * C::STAGE;
+          const uint64_t vd0 = HD == 256 ? sdesc_sw128_lbo_sbo(st, RCH * 128, 1024) : sdesc_sw64_mn(st);
+          constexpr int KSTEP = 16 * (HD == 256 ? 128 : 64);  // bytes of 16 keys
+          const uint32_t a = tmem + C::TMEM_S + b * RCH, d = tmem + C::TMEM_O + (j % C::NG) * HD;
+#pragma unroll
+          for (int kk = 0; kk < RCH / 16; ++kk)
+            tc_mma_f16_ts_pair(d, a + kk * 8, vd0 + ((kk * KSTEP) >> 4), id_pv, (jl >= C::NG || kk > 0) ? 1u : 0u);
+          tc_commit_pair(empty0 + s * 8);
+          tc_commit_pair(empty1 + s * 8);
+          issued = true;
+        }
+      };
+      for (; (TWO || warp == 0) && sg.next(); j0 += sg.n, f0 += 2 * sg.n, ++seg) {
+        if (warp == 0) {
+          ok = ok && mbar_wait_spin(q_full, seg & 1, err, PF_DEV_TIMEOUT_MMA);
+          for (int jl = 0; jl < (TWO ? sg.n : C::LA) && jl < sg.n; ++jl) {
+            issue_s(jl);
+            if (!__all_sync(0xffffffffu, ok)) break;
+          }
+        }
+        if (!TWO || warp == 3)
+          for (int jl = 0; jl < sg.n; ++jl) {
+            if (!TWO && jl + C::LA < sg.n) issue_s(jl + C::LA);
+            issue_pv(jl);
+            if (!__all_sync(0xffffffffu, ok)) break;
+          }
         if (!__all_sync(0xffffffffu, ok)) break;
       }
       if (!ok && issued && leader) {
         // the MMAs already issued finish before TMEM is freed
-        tc_commit_pair(map_to_rank(smem_u32(drain), 0));
-        runs_drain(drain, 0);
+        uint64_t* bar = &drain[warp == 0 ? 0 : 1];
+        tc_commit_pair(map_to_rank(smem_u32(bar), 0));
+        runs_drain(bar, 0);
       }
       __syncwarp();
     }
@@ -796,73 +853,71 @@ __global__ void __launch_bounds__(RunsCfg<HD>::THREADS, 1)
 }
 
 // Items cut over several pairs: m = max m_p, w_p = 2^((m_p - m) c), out =
-// (sum w_p o_p) / (sum w_p l_p) over the item's pairs.  `wpr` warps take a row
-// (its pairs dealt out among them, then their sums joined in warp order),
-// lane owning HD/32 consecutive dims; bound by the latency of reading the
-// states from L2, so a row of many pairs wants many warps.  blockIdx.x
-// counts items, or, where there are fewer of them, the boundaries between
-// pairs (an item is taken at its first).
-template <int HD, bool TREE>
-__global__ void __launch_bounds__(256) attn_runs_merge_kernel(const __grid_constant__ RunTable rt, const RunsShape sh,
-                                                              int by_item, int wpr, const float* __restrict__ part,
-                                                              __nv_bfloat16* __restrict__ out) {
+// (sum w_p o_p) / (sum w_p l_p) over the item's pairs p, p+1, .. in order.
+// blockIdx.x counts items, or pairs with the item that starts in a pair's last
+// segment (desc: 8 ints each).  `wpr` warps take a row (its pairs dealt out among them,
+// their sums joined in warp order), lane owning HD/32 consecutive dims.
+// Bound by the latency of reading the states from L2: four are in flight,
+// and a row of many pairs wants many warps.
+template <int HD>
+__global__ void __launch_bounds__(256) attn_runs_merge_kernel(const RunsShape sh, int wpr, const int* desc,
+                                                              const float* part, __nv_bfloat16* out) {
   constexpr int PER = HD / 32;
   constexpr float c = attn_c<HD>();
   constexpr int ST = runs_state_stride(HD);
   __shared__ float joined[8][HD + 4];
-  pdl_launch();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const ItemAt<TREE> at = by_item ? ItemAt<TREE>::number(rt, sh, static_cast<int>(blockIdx.x))
-                                  : ItemAt<TREE>::weight(rt, sh, (static_cast<int>(blockIdx.x) + 1) * sh.per);
-  const RunBlocks<TREE> rb(rt.n[at.run], rt.pos0[at.run], sh.log_g);
-  const int w = at.w + ITEM_FIXED;
-  const int p0 = w / sh.per, p1 = (w + rb.chunks(at.i) - 1) / sh.per;
-  const int R0 = (rb.nb - 1 - at.i) * RROWS;
   const int R_in = static_cast<int>(blockIdx.y) * (8 / wpr) + warp / wpr;
   const int sub = warp % wpr;
-  const int rows = min(RROWS, (rt.n[at.run] << sh.log_g) - R0);
+  pdl_launch();
   pdl_wait();
-  // uniform over the block: the item has one segment, or is another boundary's
-  if (p0 == p1 || (!by_item && static_cast<int>(blockIdx.x) != p0)) return;
-  const bool live = R_in < rows;
-  // pair p's state of the row: the first pair's slot is its second
-  auto state = [&](int p) {
-    return part + (static_cast<size_t>(p == p0 ? 2 * p + 1 : 2 * p) * sh.slot_rows + R_in) * ST;
-  };
+  const int4 d = __ldcg(reinterpret_cast<const int4*>(desc) + 2 * blockIdx.x);  // pairs, rows, first packed row, KV head
+  const int2 e = __ldcg(reinterpret_cast<const int2*>(desc) + 4 * blockIdx.x + 2);
+  const int R0 = e.x, p0 = e.y;
+  const int np = d.x;
+  // uniform over the block: nothing to join, or none of the rows are the block's
+  if (np == 0 || static_cast<int>(blockIdx.y) * (8 / wpr) >= d.y) return;
+  const bool live = R_in < d.y;
   float m = -INFINITY, l = 0.f;
   float acc[PER];
 #pragma unroll
   for (int i = 0; i < PER; ++i) acc[i] = 0.f;
-  if (live) {
-    for (int p = p0 + sub + lane * wpr; p <= p1; p += 32 * wpr) m = fmaxf(m, state(p)[HD]);
+  for (int q = sub; q < np && live; q += 4 * wpr) {
+    float o[4][PER];
+    float2 ml[4];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    for (int q = p0 + sub; q <= p1; q += 4 * wpr) {  // four states' loads in flight
-      float o[4][PER];
-      float2 ml[4];
+    for (int k = 0; k < 4; ++k) {
+      const int p = min(q + k * wpr, np - 1);
+      // the first pair's slot is its second
+      const float* s = part + (static_cast<size_t>(p == 0 ? 2 * p0 + 1 : 2 * (p0 + p)) * sh.slot_rows + R_in) * ST;
+      ml[k] = __ldcg(reinterpret_cast<const float2*>(s + HD));
+      if (q + k * wpr >= np) ml[k].x = -INFINITY;
+      if constexpr (PER >= 4) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float* s = state(min(q + k * wpr, p1));
-        ml[k] = *reinterpret_cast<const float2*>(s + HD);
-        if constexpr (PER >= 4) {
-#pragma unroll
-          for (int i = 0; i < PER; i += 4) {
-            const float4 v = *reinterpret_cast<const float4*>(s + lane * PER + i);
-            o[k][i] = v.x, o[k][i + 1] = v.y, o[k][i + 2] = v.z, o[k][i + 3] = v.w;
-          }
-        } else {
-          const float2 v = *reinterpret_cast<const float2*>(s + lane * PER);
-          o[k][0] = v.x, o[k][1] = v.y;
+        for (int i = 0; i < PER; i += 4) {
+          const float4 v = __ldcg(reinterpret_cast<const float4*>(s + lane * PER + i));
+          o[k][i] = v.x, o[k][i + 1] = v.y, o[k][i + 2] = v.z, o[k][i + 3] = v.w;
         }
+      } else {
+        const float2 v = __ldcg(reinterpret_cast<const float2*>(s + lane * PER));
+        o[k][0] = v.x, o[k][1] = v.y;
       }
+    }
+    const float mn = fmaxf(fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x)), m);
+    if (mn != m) {
+      const float w = m == -INFINITY ? 0.f : ex2_approx((m - mn) * c);
+      l *= w;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        if (q + k * wpr > p1 || ml[k].x == -INFINITY) continue;
-        const float wt = ex2_approx((ml[k].x - m) * c);
-        l = __fmaf_rn(wt, ml[k].y, l);
+      for (int i = 0; i < PER; ++i) acc[i] *= w;
+      m = mn;
+    }
 #pragma unroll
-        for (int i = 0; i < PER; ++i) acc[i] = __fmaf_rn(wt, o[k][i], acc[i]);
-      }
+    for (int k = 0; k < 4; ++k) {
+      if (ml[k].x == -INFINITY) continue;
+      const float w = ex2_approx((ml[k].x - m) * c);
+      l = __fmaf_rn(w, ml[k].y, l);
+#pragma unroll
+      for (int i = 0; i < PER; ++i) acc[i] = __fmaf_rn(w, o[k][i], acc[i]);
     }
   }
   if (wpr > 1) {
@@ -881,20 +936,27 @@ __global__ void __launch_bounds__(256) attn_runs_merge_kernel(const __grid_const
     for (int k = 1; k < wpr; ++k) {
       const float* s = joined[warp + k];
       if (s[HD] == -INFINITY) continue;
-      const float wt = ex2_approx((s[HD] - mm) * c);
-      l = __fmaf_rn(wt, s[HD + 1], l);
+      const float w = ex2_approx((s[HD] - mm) * c);
+      l = __fmaf_rn(w, s[HD + 1], l);
 #pragma unroll
-      for (int i = 0; i < PER; ++i) acc[i] = __fmaf_rn(wt, s[lane * PER + i], acc[i]);
+      for (int i = 0; i < PER; ++i) acc[i] = __fmaf_rn(w, s[lane * PER + i], acc[i]);
     }
   }
   if (!live) return;
   const float inv = l == 0.f ? 0.f : __frcp_rn(l);
   const int R = R0 + R_in;
-  __nv_bfloat16* d = out + (static_cast<size_t>(rt.row0[at.run] + (R >> sh.log_g)) * sh.Hq + (at.kvh << sh.log_g) +
-                            (R & ((1 << sh.log_g) - 1))) * HD + lane * PER;
+  __nv_bfloat16* dst = out + (static_cast<size_t>(d.z + (R >> sh.log_g)) * sh.Hq + (d.w << sh.log_g) +
+                              (R & ((1 << sh.log_g) - 1))) * HD + lane * PER;
+  uint32_t hb[PER / 2];
 #pragma unroll
-  for (int i = 0; i < PER; i += 2)
-    *reinterpret_cast<__nv_bfloat162*>(d + i) = __floats2bfloat162_rn(acc[i] * inv, acc[i + 1] * inv);
+  for (int i = 0; i < PER; i += 2) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(acc[i] * inv, acc[i + 1] * inv);
+    hb[i / 2] = *reinterpret_cast<const uint32_t*>(&v);
+  }
+  if constexpr (PER == 8)
+    *reinterpret_cast<uint4*>(dst) = make_uint4(hb[0], hb[1], hb[2], hb[3]);
+  else
+    *reinterpret_cast<uint32_t*>(dst) = hb[0];
 }
 
 // ---------------------------------------------------------------------------
@@ -904,7 +966,8 @@ struct RunsPlan {
   RunTable rt;
   RunsShape sh;
   int items = 0;
-  int64_t state_bytes = 0;
+  int64_t desc_bytes = 0;   // the merge kernel's table, ahead of the states
+  int64_t state_bytes = 0;  // both
 };
 
 static int sm_count() {
@@ -963,22 +1026,24 @@ static bool make_plan(RunsPlan& p, const pfop_attn_run* runs, int n_runs, int Hq
   const int units = std::max(1, sm_count() / 2);
   const int share = std::max<int>(MIN_SHARE, static_cast<int>((weight + units - 1) / units));
   if (items <= units && longest + ITEM_FIXED <= share + MERGE_COST) {
-    p.sh.per = 0;
+    p.sh.per = p.sh.desc_by_item = 0;
     p.sh.pairs = p.items;
-    p.state_bytes = 0;
+    p.desc_bytes = p.state_bytes = 0;
   } else {
     p.sh.per = share;
     p.sh.pairs = static_cast<int>((weight + share - 1) / share);
+    p.sh.desc_by_item = p.items < p.sh.pairs ? 1 : 0;
+    p.desc_bytes = (int64_t(std::min(p.sh.pairs, p.items)) * 32 + 255) / 256 * 256;
     p.state_bytes =
-        int64_t(2) * p.sh.pairs * p.sh.slot_rows * runs_state_stride(hd) * static_cast<int64_t>(sizeof(float));
+        p.desc_bytes + int64_t(2) * p.sh.pairs * p.sh.slot_rows * runs_state_stride(hd) * static_cast<int64_t>(sizeof(float));
   }
   return true;
 }
 
 template <int HD, bool TREE>
 static cudaError_t launch_runs(const RunsPlan& p, const __half* q, const __half* k, const __half* v, int64_t n_cells,
-                               int total, const uint64_t* mask, int words, __nv_bfloat16* out, float* part, int* err,
-                               cudaStream_t s) {
+                               int total, const uint64_t* mask, int words, __nv_bfloat16* out, uint8_t* states,
+                               int* err, cudaStream_t s) {
   using C = RunsCfg<HD>;
   cudaError_t e = smem_opt_in<attn_runs_kernel<HD, TREE>>(C::SMEM);
   if (e != cudaSuccess) return e;
@@ -1004,16 +1069,16 @@ static cudaError_t launch_runs(const RunsPlan& p, const __half* q, const __half*
                     : encode_fp16_sw64(&tv, v, 3, dims, st, vbox, &why)))
       return cudaErrorInvalidValue;
   }
+  int* desc = reinterpret_cast<int*>(states);
+  float* part = reinterpret_cast<float*>(states + p.desc_bytes);
   e = launch_k(attn_runs_kernel<HD, TREE>, dim3(2u * p.sh.pairs), dim3(C::THREADS), C::SMEM, s, 2, tq, tk, tv, p.rt,
-               p.sh, mask, words, out, part, err);
+               p.sh, mask, words, out, part, desc, err);
   if (e != cudaSuccess || p.sh.per == 0 || p.sh.pairs == 1) return e;
   // warps per row: an item lies in about pairs / items + 1 pairs
-  const int by_item = p.items < p.sh.pairs - 1 ? 1 : 0;
   const int spread = p.sh.pairs / std::max(1, p.items) + 1;
   const int wpr = spread <= 4 ? 1 : spread <= 8 ? 2 : spread <= 16 ? 4 : 8;
-  return launch_k(attn_runs_merge_kernel<HD, TREE>,
-                  dim3(by_item ? p.items : p.sh.pairs - 1, p.sh.slot_rows / (8 / wpr)), dim3(256), 0, s, 1, p.rt, p.sh,
-                  by_item, wpr, static_cast<const float*>(part), out);
+  return launch_k(attn_runs_merge_kernel<HD>, dim3(std::min(p.sh.pairs, p.items), p.sh.slot_rows / (8 / wpr)), dim3(256), 0, s, 1,
+                  p.sh, wpr, static_cast<const int*>(desc), static_cast<const float*>(part), out);
 }
 
 }  // namespace pf
@@ -1074,10 +1139,10 @@ int run_attention(bool tree, const void* q, const void* k, const void* v, int64_
     return fail(PF_E_ARG, "more work than one call takes (2^30 chunks of 256 rows by 128 keys)");
   if (work_bytes < WORK_HEADER + p.state_bytes) return fail(PF_E_ARG, "the scratch is smaller than these runs need");
   int* err = static_cast<int*>(work);
-  float* part = reinterpret_cast<float*>(static_cast<uint8_t*>(work) + WORK_HEADER);
+  uint8_t* states = static_cast<uint8_t*>(work) + WORK_HEADER;
   auto go = [&](auto launch) {
     return launch(p, static_cast<const __half*>(q), static_cast<const __half*>(k), static_cast<const __half*>(v),
-                  n_cells, static_cast<int>(total), mask, words, static_cast<__nv_bfloat16*>(out), part, err, s);
+                  n_cells, static_cast<int>(total), mask, words, static_cast<__nv_bfloat16*>(out), states, err, s);
   };
   const cudaError_t e = hd == 256 ? (tree ? go(launch_runs<256, true>) : go(launch_runs<256, false>))
                                   : (tree ? go(launch_runs<64, true>) : go(launch_runs<64, false>));
