@@ -335,30 +335,43 @@ def repack_q4(w, bn: int):
 # several sequences in one call: attention and log probabilities
 
 
-def _on_device(t, what: str, dtype: str, shape, device) -> int:
-    """Address of a contiguous CUDA tensor on `device` of the given type and
-    shape (None in a shape: any size)."""
-    if str(t.dtype) != "torch." + dtype:
+_torch = None
+
+
+def _t():
+    """torch, imported at first use (the library itself does not need it)."""
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+    return _torch
+
+
+def _on_device(t, what: str, dtype, shape, index: int) -> int:
+    """Address of a contiguous tensor of the given type and shape on CUDA
+    device `index`."""
+    if t.dtype is dtype and t.shape == shape and t.get_device() == index and t.is_contiguous():
+        return t.data_ptr()
+    if t.dtype is not dtype:
         raise ValueError(f"{what}: element type must be {dtype}, got {t.dtype}")
-    if len(t.shape) != len(shape) or any(w is not None and w != n for w, n in zip(shape, t.shape)):
+    if t.shape != shape:
         raise ValueError(f"{what}: shape {tuple(t.shape)} does not fit {tuple(shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{what}: buffer must be contiguous")
-    if t.device != device:
-        raise ValueError(f"{what}: must be on {device}, is on {t.device}")
-    return t.data_ptr()
+    if t.get_device() != index:
+        raise ValueError(f"{what}: must be on CUDA device {index}, is on {t.device}")
+    raise ValueError(f"{what}: buffer must be contiguous")
 
 
-def _call_on(device, stream, fn, *args):
-    """fn(*args, stream) with `device` current; stream None: the device's
-    current torch stream (so the call is ordered with the torch work around
-    it)."""
-    import torch
-    if torch.cuda.current_device() != device.index:
-        with torch.cuda.device(device):
-            return _call_on(device, stream, fn, *args)
-    s = torch.cuda.current_stream(device).cuda_stream if stream is None else _stream(stream)
-    check_op(fn(*args, s))
+def _call_on(index: int, stream, fn, *args):
+    """fn(*args, stream) with CUDA device `index` current; stream None: the
+    device's current torch stream, so that the call is ordered with the torch
+    work around it."""
+    c = _t()._C
+    if c._cuda_getDevice() != index:
+        with _torch.cuda.device(index):
+            return _call_on(index, stream, fn, *args)
+    rc = fn(*args, c._cuda_getCurrentRawStream(index) if stream is None else _stream(stream))
+    if rc != PF_OK:
+        check_op(rc)
 
 
 class AttnRuns:
@@ -370,20 +383,19 @@ class AttnRuns:
     graphs recorded with the same AttnRuns may not run at once)."""
 
     def __init__(self, runs, n_head: int, n_head_kv: int, head_dim: int, device=None):
-        import torch
+        torch = _t()
         self._lib = load()
         self.shape = (n_head, n_head_kv, head_dim)
         runs = [(int(n), int(p), int(c)) for n, p, c in runs]
         self.n_runs = len(runs)
         self.n_rows = sum(r[0] for r in runs)
         self.runs = (AttnRun * max(1, len(runs)))(*[AttnRun(*r) for r in runs])
-        self.device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
-        with torch.cuda.device(self.device):
-            self.device = torch.device("cuda", torch.cuda.current_device())
+        with torch.cuda.device(device if device is not None else torch.cuda.current_device()):
+            self.device = torch.cuda.current_device()
             need = int(self._lib.pfop_attention_work_bytes(n_head, n_head_kv, head_dim, self.runs, self.n_runs))
             if need < 0:
                 check_op(need)
-            self.work = torch.empty(need, dtype=torch.uint8, device=self.device)
+            self.work = torch.empty(need, dtype=torch.uint8, device="cuda")
             self.work[:256].zero_()
         self.work_bytes = need
 
@@ -394,13 +406,12 @@ class AttnRuns:
 
     def _args(self, q, k, v, out):
         hq, hkv, hd = self.shape
-        if q.shape[0] < self.n_rows or out.shape[0] < self.n_rows:
+        f16, d, cells = _torch.float16, self.device, len(k)
+        if len(q) < self.n_rows or len(out) < self.n_rows:
             raise ValueError(f"q and out: the runs have {self.n_rows} rows")
-        d = self.device
-        return (_on_device(q, "q", "float16", (None, hq, hd), d), _on_device(k, "k", "float16", (None, hkv, hd), d),
-                _on_device(v, "v", "float16", (k.shape[0], hkv, hd), d), k.shape[0], hq, hkv, hd, self.runs,
-                self.n_runs), (_on_device(out, "out", "bfloat16", (None, hq, hd), d), self.work.data_ptr(),
-                               self.work_bytes)
+        return (_on_device(q, "q", f16, (len(q), hq, hd), d), _on_device(k, "k", f16, (cells, hkv, hd), d),
+                _on_device(v, "v", f16, (cells, hkv, hd), d), cells, hq, hkv, hd, self.runs, self.n_runs), \
+               (_on_device(out, "out", _torch.bfloat16, (len(out), hq, hd), d), self.work.data_ptr(), self.work_bytes)
 
 
 def attention_packed(q, k, v, runs: AttnRuns, out, stream=None):
@@ -416,11 +427,12 @@ def attention_tree(q, k, v, runs: AttnRuns, mask, out, stream=None):
     """Attention of drafted token trees (pfop_attention_tree): as
     attention_packed, with mask [T, words] int64, bit j % 64 of word j / 64
     set where the row sees drafted token j of its run."""
-    if len(mask.shape) != 2 or mask.shape[0] < runs.n_rows:
+    if mask.dim() != 2 or len(mask) < runs.n_rows:
         raise ValueError(f"mask: needs [{runs.n_rows}, words]")
     a, b = runs._args(q, k, v, out)
-    m = _on_device(mask, "mask", "int64", (None, None), runs.device)
-    _call_on(runs.device, stream, runs._lib.pfop_attention_tree, *a, m, mask.shape[1], *b)
+    words = mask.shape[1]
+    m = _on_device(mask, "mask", _torch.int64, (len(mask), words), runs.device)
+    _call_on(runs.device, stream, runs._lib.pfop_attention_tree, *a, m, words, *b)
 
 
 def logprobs(logits, tokens=None, logp=None, entropy=None, top_id=None, top_logp=None, stream=None):
@@ -430,27 +442,29 @@ def logprobs(logits, tokens=None, logp=None, entropy=None, top_id=None, top_logp
     top_id [rows, n] int32 with top_logp [rows, n] float32.  Outputs left
     None are skipped.  Enqueued on `stream` (None: the current torch
     stream)."""
-    if len(logits.shape) != 2 or (logits.shape[1] > 1 and logits.stride(1) != 1):
-        raise ValueError("logits: needs [rows, vocab] with dense rows")
-    kinds = {"torch.float32": PF_L_F32, "torch.bfloat16": PF_L_BF16}
-    if str(logits.dtype) not in kinds:
+    torch = _t()
+    if logits.dtype is torch.float32:
+        kind = PF_L_F32
+    elif logits.dtype is torch.bfloat16:
+        kind = PF_L_BF16
+    else:
         raise ValueError(f"logits: element type must be float32 or bfloat16, got {logits.dtype}")
+    if logits.dim() != 2 or (logits.shape[1] > 1 and logits.stride(1) != 1):
+        raise ValueError("logits: needs [rows, vocab] with dense rows")
     if (tokens is None) != (logp is None) or (top_id is None) != (top_logp is None):
         raise ValueError("tokens and logp, top_id and top_logp go together")
-    if not logits.is_cuda:
+    d = logits.get_device()
+    if d < 0:
         raise ValueError(f"logits: must be on a CUDA device, is on {logits.device}")
     rows, vocab = logits.shape
-    d = logits.device
-    n_top = 0 if top_id is None else top_id.shape[1]
-
-    def at(t, what, dtype, shape):
-        return None if t is None else _on_device(t, what, dtype, shape, d)
-
-    args = (kinds[str(logits.dtype)], logits.data_ptr(), logits.stride(0) if rows > 1 else vocab, rows, vocab,
-            at(tokens, "tokens", "int32", (rows,)), n_top, at(logp, "logp", "float32", (rows,)),
-            at(entropy, "entropy", "float32", (rows,)), at(top_id, "top_id", "int32", (rows, n_top)),
-            at(top_logp, "top_logp", "float32", (rows, n_top)))
-    _call_on(d, stream, load().pfop_logprobs, *args)
+    f32, i32, one = torch.float32, torch.int32, (rows,)
+    n_top = 0 if top_id is None else top_id.shape[-1]
+    _call_on(d, stream, load().pfop_logprobs, kind, logits.data_ptr(), logits.stride(0) if rows > 1 else vocab, rows,
+             vocab, None if tokens is None else _on_device(tokens, "tokens", i32, one, d), n_top,
+             None if logp is None else _on_device(logp, "logp", f32, one, d),
+             None if entropy is None else _on_device(entropy, "entropy", f32, one, d),
+             None if top_id is None else _on_device(top_id, "top_id", i32, (rows, n_top), d),
+             None if top_logp is None else _on_device(top_logp, "top_logp", f32, (rows, n_top), d))
 
 
 # ---------------------------------------------------------------------------

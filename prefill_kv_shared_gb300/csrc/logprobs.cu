@@ -11,15 +11,17 @@
 //
 // The alternatives need no second look at the whole row: the n-th largest of
 // the maxima of 32 groups of threads is not above the n-th largest value, so
-// only threads whose own maximum reaches it read their logits again (from
-// L2) and list those that do: a few dozen of a row as a rule, whose ranks
-// are then counted.  Where the list overflows (many equal values, as in a
-// row that is mostly masked) a radix select finds the n-th value and the
-// lowest ids at it.
+// only threads whose own maximum reaches it go over their logits again and
+// list those that do: a few dozen of a row as a rule, whose ranks are then
+// counted.  Where the list overflows (many equal values, as in a row that is
+// mostly masked) a radix select finds the n-th value and the lowest ids at it.
 //
-// Bound by the row's bytes from HBM for many rows, by latency for few: then
-// a cluster of up to 8 CTAs takes a row, a slice each, and rank 0 joins
-// their sums and lists through distributed shared memory.
+// A CTA takes a row, or a cluster of up to 8 a slice each (rank 0 joins their
+// sums and lists through distributed shared memory).  A slice of up to 64 KB
+// is brought into shared memory by one bulk copy, which keeps the HBM busy
+// with no registers held and makes the second look cheap; longer slices are
+// read through registers, and again from L2.  Bound by the row's bytes for
+// many rows, by latency for few.
 #include "../../include/prefill_ops.h"
 #include "common.cuh"
 #include "kernels.h"
@@ -28,15 +30,15 @@
 
 namespace pf {
 
-constexpr int LP_THREADS = 256;
+constexpr int LP_THREADS = 512;
 constexpr int LP_WARPS = LP_THREADS / 32;
 constexpr int LP_TOP_MAX = 32;
-constexpr int LP_GROUPS = LP_THREADS / 8;  // 32: one per lane
+constexpr int LP_GROUP = LP_THREADS / 32;  // threads of a group
 constexpr int LP_CAND = 512;               // listed candidates
 constexpr int LP_CLUSTER_MAX = 8;
-constexpr int LP_CTAS_PER_SM = 5;          // 48 registers a thread
+constexpr int LP_SMEM_SLICE = 65536;       // bytes of a slice held in shared memory
 constexpr float LP_LOG2E = 1.4426950408889634f, LP_LN2 = 0.6931471805599453f;
-static_assert(LP_GROUPS == 32 && LP_TOP_MAX <= LP_GROUPS, "a lane per group");
+static_assert(LP_TOP_MAX <= 32 && LP_GROUP <= 32, "a lane per group");
 
 struct LogprobArgs {
   const void* logits;
@@ -101,108 +103,188 @@ __device__ __forceinline__ unsigned long long lp_key(uint32_t order, int id) {
 // running maximum and sums
 struct LpSums {
   float m = -INFINITY, s = 0.f, h = 0.f;
-  __device__ __forceinline__ void raise(float to) {
-    if (to > m) {
-      if (m != -INFINITY) {
-        const float d = (to - m) * LP_LOG2E, w = lp_ex2(-d);
-        h = w * (h - d * s);
-        s *= w;
-        if (w == 0.f) s = h = s != s ? s : 0.f;  // d may be inf
-      }
-      m = to;
-    }
+  // the sums against a maximum `to` >= m
+  __device__ __forceinline__ void rebase(float to) {
+    const float d = (to - m) * LP_LOG2E, w = lp_ex2(-d);
+    // w 0 (nothing seen yet, or d infinite): a NaN stays, else nothing is left
+    const float z = s != s ? s : 0.f;
+    h = w == 0.f || m == -INFINITY ? z : w * (h - d * s);
+    s = w == 0.f || m == -INFINITY ? z : w * s;
+    m = to;
   }
-  __device__ __forceinline__ void join(float om, float os, float oh) {
-    LpSums o;
-    o.m = om, o.s = os, o.h = oh;
-    raise(om);
-    o.raise(m);
-    s += o.s;
-    h += o.h;
+  __device__ __forceinline__ void raise(float to) {
+    if (to > m) rebase(to);
+  }
+  // over the warp, the same in every lane
+  __device__ __forceinline__ void join() {
+    float to = m;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) to = fmaxf(to, __shfl_xor_sync(0xffffffffu, to, o));
+    rebase(to);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      s += __shfl_xor_sync(0xffffffffu, s, o);
+      h += __shfl_xor_sync(0xffffffffu, h, o);
+    }
   }
 };
 
-// A thread's logits of the slice x[0 .. n): vectors tid, tid + 256, .. of the
-// 16-byte aligned middle and one logit of each ragged end.  BATCH vectors
-// are in flight; body(values, first id of each vector, count) per batch.
-template <class T>
+__device__ __forceinline__ uint64_t lp_pack(float a, float b) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
+  return d;
+}
+__device__ __forceinline__ float2 lp_unpack(uint64_t v) {
+  float2 f;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
+  return f;
+}
+
+// A thread's logits of the slice x[0 .. n) (SM: in shared memory, else in
+// global): vectors tid, tid + LP_THREADS, .. of the 16-byte aligned middle
+// and one logit of each ragged end.
+template <class T, bool SM>
 struct LpSlice {
   static constexpr int VN = LpVec<T>::N;
+  static constexpr int BATCH = SM ? 2 : 4;  // vectors taken at once
   const T* x;
   int n, head, nvec;
-  __device__ LpSlice(const T* p, int len) : x(p), n(len) {
-    const int mis = static_cast<int>((reinterpret_cast<uintptr_t>(p) & 15) / sizeof(T));
+  __device__ LpSlice(const T* p, int len, int mis) : x(p), n(len) {
     head = min(len, mis ? VN - mis : 0);
     nvec = (len - head) / VN;
   }
-  // f(value, id in the slice) for this thread's logits, one at a time
+  __device__ __forceinline__ uint4 vec(int v) const {
+    const uint4* p = reinterpret_cast<const uint4*>(x + head) + v;
+    return SM ? *p : __ldcg(p);
+  }
+  // f(value, id in the slice) for this thread's logits of at least tau
+  template <class F>
+  __device__ __forceinline__ void from(float tau, F&& f) const {
+    const int t = threadIdx.x;
+    auto one = [&](float v, int i) {
+      if (v >= tau) f(v, i);
+    };
+    if (t < head) one(LpVec<T>::one(x + t), t);
+    for (int v = t; v < nvec; v += BATCH * LP_THREADS) {
+      uint4 r[BATCH];
+#pragma unroll
+      for (int b = 0; b < BATCH; ++b)
+        r[b] = vec(v + b * LP_THREADS < nvec ? v + b * LP_THREADS : v);
+#pragma unroll
+      for (int b = 0; b < BATCH; ++b) {
+        float e[VN];
+        LpVec<T>::get(r[b], e);
+        float mx = e[0];
+#pragma unroll
+        for (int i = 1; i < VN; ++i) mx = fmaxf(mx, e[i]);
+        if (mx >= tau && v + b * LP_THREADS < nvec) {
+#pragma unroll
+          for (int i = 0; i < VN; ++i) one(e[i], head + (v + b * LP_THREADS) * VN + i);
+        }
+      }
+    }
+    const int tail = head + nvec * VN;
+    if (t < n - tail) one(LpVec<T>::one(x + tail + t), tail + t);
+  }
+  // f(value, id in the slice) for all of them
   template <class F>
   __device__ __forceinline__ void each(F&& f) const {
     const int t = threadIdx.x;
     if (t < head) f(LpVec<T>::one(x + t), t);
-    for (int v = t; v < nvec; v += LP_THREADS) {
-      const int id = head + v * VN;
-      float e[VN];
-      LpVec<T>::get(__ldcg(reinterpret_cast<const uint4*>(x + id)), e);
+    int v = t;
+    for (; v < nvec; v += BATCH * LP_THREADS) {
+      uint4 r[BATCH];
 #pragma unroll
-      for (int i = 0; i < VN; ++i) f(e[i], id + i);
+      for (int b = 0; b < BATCH; ++b) r[b] = v + b * LP_THREADS < nvec ? vec(v + b * LP_THREADS) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int b = 0; b < BATCH; ++b) {
+        if (v + b * LP_THREADS >= nvec) break;
+        float e[VN];
+        LpVec<T>::get(r[b], e);
+#pragma unroll
+        for (int i = 0; i < VN; ++i) f(e[i], head + (v + b * LP_THREADS) * VN + i);
+      }
     }
     const int tail = head + nvec * VN;
     if (t < n - tail) f(LpVec<T>::one(x + tail + t), tail + t);
   }
-  __device__ __forceinline__ void sums(LpSums& a) const {
-    constexpr int BATCH = 4;
-    const int t = threadIdx.x;
-    auto add = [&](const float* e, int cnt) {
-      float mx = e[0];
+  template <int CNT>
+  static __device__ __forceinline__ void add(LpSums& a, const float* e) {
+    float mx = e[0];
 #pragma unroll
-      for (int i = 1; i < BATCH * VN; ++i)
-        if (i < cnt) mx = fmaxf(mx, e[i]);
-      a.raise(mx);
-      // x - m first: m log2 e alone may overflow
-      const float m = a.m == -INFINITY ? 0.f : a.m;
-      float s0 = 0.f, s1 = 0.f, h0 = 0.f, h1 = 0.f;
+    for (int i = 1; i < CNT; ++i) mx = fmaxf(mx, e[i]);
+    a.raise(mx);
+    // x - m first: m log2 e alone may overflow
+    const float m = a.m == -INFINITY ? 0.f : a.m;
+    if constexpr (CNT == 1) {
+      const float t = lp_max_nan((e[0] - m) * LP_LOG2E, -200.f), w = lp_ex2(t);
+      a.s += w;
+      a.h = __fmaf_rn(w, t, a.h);
+    } else {
+      // two logits an instruction
+      const uint64_t nm = lp_pack(-m, -m), c = lp_pack(LP_LOG2E, LP_LOG2E);
+      uint64_t s[2] = {0ull, 0ull}, h[2] = {0ull, 0ull};
 #pragma unroll
-      for (int i = 0; i < BATCH * VN; i += 2) {
-        if (i < cnt) {
-          const float t0 = lp_max_nan((e[i] - m) * LP_LOG2E, -200.f), e0 = lp_ex2(t0);
-          s0 += e0;
-          h0 = __fmaf_rn(e0, t0, h0);
-        }
-        if (i + 1 < cnt) {
-          const float t1 = lp_max_nan((e[i + 1] - m) * LP_LOG2E, -200.f), e1 = lp_ex2(t1);
-          s1 += e1;
-          h1 = __fmaf_rn(e1, t1, h1);
-        }
+      for (int i = 0; i < CNT; i += 2) {
+        uint64_t d = lp_pack(e[i], e[i + 1]);
+        asm("add.rn.f32x2 %0, %0, %1;" : "+l"(d) : "l"(nm));
+        asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(d) : "l"(c));
+        float2 t = lp_unpack(d);
+        t.x = lp_max_nan(t.x, -200.f);
+        t.y = lp_max_nan(t.y, -200.f);
+        const uint64_t w = lp_pack(lp_ex2(t.x), lp_ex2(t.y)), tt = lp_pack(t.x, t.y);
+        const int q = (i >> 1) & 1;
+        asm("add.rn.f32x2 %0, %0, %1;" : "+l"(s[q]) : "l"(w));
+        asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(h[q]) : "l"(w), "l"(tt));
       }
-      a.s += s0 + s1;
-      a.h += h0 + h1;
-    };
-    const uint4* xv = reinterpret_cast<const uint4*>(x + head);
+      const float2 s0 = lp_unpack(s[0]), s1 = lp_unpack(s[1]), h0 = lp_unpack(h[0]), h1 = lp_unpack(h[1]);
+      a.s += (s0.x + s0.y) + (s1.x + s1.y);
+      a.h += (h0.x + h0.y) + (h1.x + h1.y);
+    }
+  }
+  __device__ __forceinline__ void sums(LpSums& a) const {
+    const int t = threadIdx.x;
     int v = t;
-    for (; v + (BATCH - 1) * LP_THREADS < nvec; v += BATCH * LP_THREADS) {
+    if constexpr (SM) {
+      for (; v + (BATCH - 1) * LP_THREADS < nvec; v += BATCH * LP_THREADS) {
+        float e[BATCH * VN];
+#pragma unroll
+        for (int b = 0; b < BATCH; ++b) LpVec<T>::get(vec(v + b * LP_THREADS), e + b * VN);
+        add<BATCH * VN>(a, e);
+      }
+    } else if (v + (BATCH - 1) * LP_THREADS < nvec) {
+      // the next batch is on its way while this one is taken
       uint4 r[BATCH];
 #pragma unroll
-      for (int b = 0; b < BATCH; ++b) r[b] = __ldcg(xv + v + b * LP_THREADS);
-      float e[BATCH * VN];
+      for (int b = 0; b < BATCH; ++b) r[b] = vec(v + b * LP_THREADS);
+      for (;;) {
+        const int w = v + BATCH * LP_THREADS;
+        const bool more = w + (BATCH - 1) * LP_THREADS < nvec;
+        float e[BATCH * VN];
 #pragma unroll
-      for (int b = 0; b < BATCH; ++b) LpVec<T>::get(r[b], e + b * VN);
-      add(e, BATCH * VN);
+        for (int b = 0; b < BATCH; ++b) LpVec<T>::get(r[b], e + b * VN);
+        if (more) {
+#pragma unroll
+          for (int b = 0; b < BATCH; ++b) r[b] = vec(w + b * LP_THREADS);
+        }
+        add<BATCH * VN>(a, e);
+        v = w;
+        if (!more) break;
+      }
     }
     for (; v < nvec; v += LP_THREADS) {
-      float e[BATCH * VN];
-      LpVec<T>::get(__ldcg(xv + v), e);
-      add(e, VN);
+      float e[VN];
+      LpVec<T>::get(vec(v), e);
+      add<VN>(a, e);
     }
     const int tail = head + nvec * VN;
-    float e[BATCH * VN];
     if (t < head) {
-      e[0] = LpVec<T>::one(x + t);
-      add(e, 1);
+      const float e = LpVec<T>::one(x + t);
+      add<1>(a, &e);
     }
     if (t < n - tail) {
-      e[0] = LpVec<T>::one(x + tail + t);
-      add(e, 1);
+      const float e = LpVec<T>::one(x + tail + t);
+      add<1>(a, &e);
     }
   }
 };
@@ -213,9 +295,11 @@ struct LpShared {
   unsigned long long cand[LP_CAND];
   float4 sums[LP_CLUSTER_MAX];  // rank 0: m, s, h of each CTA
   float m[LP_WARPS], s[LP_WARPS], h[LP_WARPS];
-  float group[LP_GROUPS];
+  float group[32];
   int hist[256];
-  int count, prefix, left, found, warp_count[LP_WARPS];
+  float tau;
+  int count, prefix, left, warp_count[LP_WARPS];
+  uint64_t landed;  // barrier of the slice's copy
 };
 
 // The n best of sh.cand[0 .. cnt) (all different) into dst, in order: a
@@ -224,6 +308,7 @@ __device__ __forceinline__ void lp_rank(const unsigned long long* cand, int cnt,
   for (int i = threadIdx.x; i < cnt; i += LP_THREADS) {
     const unsigned long long k = cand[i];
     int r = 0;
+#pragma unroll 8
     for (int j = 0; j < cnt; ++j) r += cand[j] > k ? 1 : 0;
     if (r < n) dst[r] = k;
   }
@@ -232,8 +317,8 @@ __device__ __forceinline__ void lp_rank(const unsigned long long* cand, int cnt,
 // The n best of a slice with too many candidates for the list: the n-th
 // largest value by four passes over 8 bits of its order each, the larger
 // ones, and the lowest ids at that value.
-template <class T>
-__device__ __noinline__ void lp_select(const LpSlice<T>& sl, int id0, int n, LpShared& sh) {
+template <class T, bool SM>
+__device__ __noinline__ void lp_select(const LpSlice<T, SM>& sl, int id0, int n, LpShared& sh) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   uint32_t prefix = 0;
   int left = n;  // of the values with this prefix
@@ -303,59 +388,81 @@ __device__ __noinline__ void lp_select(const LpSlice<T>& sl, int id0, int n, LpS
   lp_rank(sh.cand, n, n, sh.top);
 }
 
-template <class T>
-__global__ void __launch_bounds__(LP_THREADS, LP_CTAS_PER_SM) logprobs_kernel(const LogprobArgs a, int cluster) {
+template <class T, bool SM>
+__global__ void __launch_bounds__(LP_THREADS, SM ? 3 : 2) logprobs_kernel(const LogprobArgs a, int cluster) {
   __shared__ LpShared sh;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int r = static_cast<int>(blockIdx.x) / cluster, rank = static_cast<int>(blockIdx.x) % cluster;
   const T* x = static_cast<const T*>(a.logits) + static_cast<int64_t>(r) * a.ld;
   const int id0 = rank * a.slice;
-  const LpSlice<T> sl(x + id0, min(a.vocab - id0, a.slice));
+  const int len = min(a.vocab - id0, a.slice);
+  const int mis = static_cast<int>((reinterpret_cast<uintptr_t>(x + id0) & 15) / sizeof(T));
+  extern __shared__ __align__(16) uint8_t lp_slice[];
+  // the copy keeps the logits' alignment
+  const LpSlice<T, SM> sl(SM ? reinterpret_cast<const T*>(lp_slice) + mis : x + id0, len, mis);
   pdl_launch();
   // no CTA writes into another before that one runs: arrive now, wait there
   if (cluster > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
-  if (tid == 0) sh.count = 0;
-  pdl_wait();
+  if (tid == 0) {
+    sh.count = 0;
+    if (SM) {
+      mbar_init(&sh.landed, 1);
+      fence_mbar_init();
+    }
+  }
+  bool landed = true;
+  if constexpr (SM) {
+    __syncthreads();
+    pdl_wait();
+    T* d = reinterpret_cast<T*>(lp_slice) + mis;
+    if (tid == 0) {
+      const uint32_t bytes = static_cast<uint32_t>(sl.nvec) * 16u;
+      mbar_arrive_expect_tx(&sh.landed, bytes);
+      if (bytes) bulk_load(d + sl.head, x + id0 + sl.head, bytes, &sh.landed);
+    }
+    const int tail = sl.head + sl.nvec * LpVec<T>::N;
+    if (tid < sl.head) d[tid] = x[id0 + tid];
+    if (tid < len - tail) d[tail + tid] = x[id0 + tail + tid];
+    // a copy that never lands (the bounded wait gives up) leaves the row marked
+    landed = mbar_wait(&sh.landed, 0, nullptr, PF_DEV_TIMEOUT_PRODUCER);
+    landed = __syncthreads_and(landed);
+  } else {
+    pdl_wait();
+  }
 
   LpSums q;
-  sl.sums(q);
+  if (landed) sl.sums(q);
   const float own = q.m;
-  // the block's sums
+  // the warp's sums, and the maxima of the 32 groups of threads
   {
-    float g = own;  // the group's maximum
+    float g = own;
 #pragma unroll
-    for (int o = 1; o < 8; o <<= 1) g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, o));
-    if ((lane & 7) == 0) sh.group[tid >> 3] = g;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      const float om = __shfl_xor_sync(0xffffffffu, q.m, o), os = __shfl_xor_sync(0xffffffffu, q.s, o),
-                  oh = __shfl_xor_sync(0xffffffffu, q.h, o);
-      q.join(om, os, oh);
-    }
+    for (int o = 1; o < LP_GROUP; o <<= 1) g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, o));
+    if (tid % LP_GROUP == 0) sh.group[tid / LP_GROUP] = g;
+    q.join();
     if (lane == 0) sh.m[warp] = q.m, sh.s[warp] = q.s, sh.h[warp] = q.h;
   }
   __syncthreads();
   const int n = a.n_top;
-  if (n > 0) {
-    // the n-th largest of the groups' maxima (every warp for itself)
-    const float g = sh.group[lane];
-    int rk = 0;
+  if (n > 0 && landed) {
+    if (warp == 0) {
+      // the n-th largest of the groups' maxima
+      const float g = sh.group[lane];
+      int rk = 0;
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
-      const float o = __shfl_sync(0xffffffffu, g, i);
-      rk += (o > g || (o == g && i < lane)) ? 1 : 0;
+      for (int i = 0; i < 32; ++i) {
+        const float o = __shfl_sync(0xffffffffu, g, i);
+        rk += (o > g || (o == g && i < lane)) ? 1 : 0;
+      }
+      if (rk == n - 1) sh.tau = g;
     }
-    const float tau = __shfl_sync(0xffffffffu, g, __ffs(__ballot_sync(0xffffffffu, rk == n - 1)) - 1);
-    if (own >= tau) {
-      const uint32_t ot = lp_order(tau);
-      sl.each([&](float v, int i) {
-        const uint32_t o = lp_order(v);
-        if (o >= ot) {
-          const int at = atomicAdd(&sh.count, 1);
-          if (at < LP_CAND) sh.cand[at] = lp_key(o, id0 + i);
-        }
+    __syncthreads();
+    const float tau = sh.tau;
+    if (own >= tau)
+      sl.from(tau, [&](float v, int i) {
+        const int at = atomicAdd(&sh.count, 1);
+        if (at < LP_CAND) sh.cand[at] = lp_key(lp_order(v), id0 + i);
       });
-    }
     __syncthreads();
     const int cnt = sh.count;
     if (cnt <= LP_CAND) {
@@ -364,54 +471,60 @@ __global__ void __launch_bounds__(LP_THREADS, LP_CTAS_PER_SM) logprobs_kernel(co
       __syncthreads();  // every thread has read the count
       lp_select(sl, id0, n, sh);
     }
+    __syncthreads();  // the list is complete
   }
+  // From here one warp a CTA: the CTA's sums (lane w: warp w's), then the
+  // cluster's
+  if (warp != 0 && cluster == 1) return;
   const unsigned long long* top = sh.top;
   LpSums z;
+  if (warp == 0) {
+    if (lane < LP_WARPS) z.m = sh.m[lane], z.s = sh.s[lane], z.h = sh.h[lane];
+    z.join();
+  }
   if (cluster > 1) {
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
     if (warp == 0) {
-      // the CTA's sums, to rank 0
-      LpSums b;
-      for (int w = 0; w < LP_WARPS; ++w) b.join(sh.m[w], sh.s[w], sh.h[w]);
       if (lane == 0) {
         const uint32_t at = map_to_rank(smem_u32(&sh.sums[rank]), 0);
-        asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(at), "f"(b.m), "f"(b.s), "f"(b.h), "f"(0.f)
+        asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(at), "f"(z.m), "f"(z.s), "f"(z.h), "f"(0.f)
                      : "memory");
       }
-    }
-    __syncthreads();  // the CTA's list is complete
-    if (tid < n) {
-      const uint32_t at = map_to_rank(smem_u32(&sh.all[rank * n + tid]), 0);
-      asm volatile("st.shared::cluster.b64 [%0], %1;" ::"r"(at), "l"(sh.top[tid]) : "memory");
+      if (lane < n) {
+        const uint32_t at = map_to_rank(smem_u32(&sh.all[rank * n + lane]), 0);
+        asm volatile("st.shared::cluster.b64 [%0], %1;" ::"r"(at), "l"(sh.top[lane]) : "memory");
+      }
     }
     cluster_sync_all();
     if (rank != 0) return;
-    for (int c = 0; c < cluster; ++c) z.join(sh.sums[c].x, sh.sums[c].y, sh.sums[c].z);
     if (n > 0) {
       lp_rank(sh.all, cluster * n, n, sh.cand);
       top = sh.cand;
+      __syncthreads();
     }
-  } else {
-    for (int w = 0; w < LP_WARPS; ++w) z.join(sh.m[w], sh.s[w], sh.h[w]);
+    if (warp != 0) return;
+    z = LpSums();
+    if (lane < cluster) z.m = sh.sums[lane].x, z.s = sh.sums[lane].y, z.h = sh.sums[lane].z;
+    z.join();
   }
-  __syncthreads();
   const bool ok = z.s >= 1.f && z.m < INFINITY;  // false for a NaN too: a NaN, +inf, or only -inf
   const float nan = __int_as_float(0x7fc00000), log_s = logf(z.s);
-  if (tid < n) {
-    const unsigned long long k = top[tid];
-    const int64_t at = static_cast<int64_t>(r) * n + tid;
+  if (lane < n) {
+    const unsigned long long k = top[lane];
+    const int64_t at = static_cast<int64_t>(r) * n + lane;
     a.top_id[at] = ok ? static_cast<int>(0xffffffffu - static_cast<uint32_t>(k)) : -1;
     a.top_logp[at] = ok ? lp_value(static_cast<uint32_t>(k >> 32)) - z.m - log_s : nan;
   }
-  if (tid == LP_THREADS - 1 && a.logp) {
+  if (lane == 0 && a.logp) {
     const int t = a.tok[r];
     a.logp[r] = ok && t >= 0 && t < a.vocab ? LpVec<T>::one(x + t) - z.m - log_s : nan;
   }
-  if (tid == LP_THREADS - 2 && a.entropy) a.entropy[r] = ok ? log_s - LP_LN2 * (z.h / z.s) : nan;
+  if (lane == 31 && a.entropy) a.entropy[r] = ok ? log_s - LP_LN2 * (z.h / z.s) : nan;
 }
 
-// CTAs per row: as many as the GPU holds at once, each with at least
-// LP_SLICE_MIN logits.
+// CTAs per row: enough that a slice fits shared memory, and for few rows as
+// many as leave a slice of LP_SLICE_MIN logits and still run at once (three
+// a SM with full slices).
 constexpr int LP_SLICE_MIN = 2048;
 
 template <class T>
@@ -420,11 +533,18 @@ static cudaError_t launch_logprobs(LogprobArgs a, int rows, cudaStream_t s) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
-  int cluster = LP_CLUSTER_MAX;
-  while (cluster > 1 && (static_cast<int64_t>(rows) * cluster > static_cast<int64_t>(LP_CTAS_PER_SM) * sms || a.vocab / cluster < LP_SLICE_MIN))
-    cluster /= 2;
+  int cluster = 1;
+  while (cluster < LP_CLUSTER_MAX && a.vocab / (2 * cluster) >= LP_SLICE_MIN &&
+         (static_cast<int64_t>(a.vocab) * sizeof(T) > static_cast<int64_t>(LP_SMEM_SLICE) * cluster ||
+          static_cast<int64_t>(rows) * 2 * cluster <= 3ll * sms))
+    cluster *= 2;
   a.slice = ((a.vocab + cluster - 1) / cluster + 7) / 8 * 8;
-  return launch_k(logprobs_kernel<T>, dim3(static_cast<unsigned>(rows) * cluster), dim3(LP_THREADS), 0, s, cluster, a,
+  const dim3 grid(static_cast<unsigned>(rows) * cluster);
+  const int64_t bytes = static_cast<int64_t>(a.slice) * sizeof(T);
+  if (bytes > LP_SMEM_SLICE) return launch_k(logprobs_kernel<T, false>, grid, dim3(LP_THREADS), 0, s, cluster, a, cluster);
+  e = smem_opt_in<logprobs_kernel<T, true>>(LP_SMEM_SLICE + 16);
+  if (e != cudaSuccess) return e;
+  return launch_k(logprobs_kernel<T, true>, grid, dim3(LP_THREADS), static_cast<size_t>(bytes) + 16, s, cluster, a,
                   cluster);
 }
 

@@ -370,7 +370,7 @@ def test_wrappers_refuse_what_does_not_fit():
         a.update(bad)
         with pytest.raises(ValueError):
             binding.attention_packed(a["q"], a["k"], a["v"], plan, a["out"])
-    for bad in (mask[:3], mask.int(), mask[:, 0], mask.cpu()):
+    for bad in (mask[:3], mask.int(), mask[:, 0], mask.cpu(), mask.repeat(1, 2)[:, :1]):
         with pytest.raises(ValueError):
             binding.attention_tree(q, k, v, plan, bad, out)
     with pytest.raises(binding.PrefillError):  # a run past the cache
