@@ -30,13 +30,14 @@
 
 namespace pf {
 
-constexpr int LP_THREADS = 512;
+constexpr int LP_THREADS = 256;
 constexpr int LP_WARPS = LP_THREADS / 32;
 constexpr int LP_TOP_MAX = 32;
 constexpr int LP_GROUP = LP_THREADS / 32;  // threads of a group
 constexpr int LP_CAND = 512;               // listed candidates
 constexpr int LP_CLUSTER_MAX = 8;
 constexpr int LP_SMEM_SLICE = 65536;       // bytes of a slice held in shared memory
+constexpr int LP_CTAS_PER_SM = 3;          // by 64 KB slices
 constexpr float LP_LOG2E = 1.4426950408889634f, LP_LN2 = 0.6931471805599453f;
 static_assert(LP_TOP_MAX <= 32 && LP_GROUP <= 32, "a lane per group");
 
@@ -146,7 +147,7 @@ __device__ __forceinline__ float2 lp_unpack(uint64_t v) {
 template <class T, bool SM>
 struct LpSlice {
   static constexpr int VN = LpVec<T>::N;
-  static constexpr int BATCH = SM ? 2 : 4;  // vectors taken at once
+  static constexpr int BATCH = 4;  // vectors taken at once
   const T* x;
   int n, head, nvec;
   __device__ LpSlice(const T* p, int len, int mis) : x(p), n(len) {
@@ -157,34 +158,28 @@ struct LpSlice {
     const uint4* p = reinterpret_cast<const uint4*>(x + head) + v;
     return SM ? *p : __ldcg(p);
   }
-  // f(value, id in the slice) for this thread's logits of at least tau
+  // f(value, id in the slice) for the logits of at least tau among those of
+  // thread t, its vectors dealt out over the warp
   template <class F>
-  __device__ __forceinline__ void from(float tau, F&& f) const {
-    const int t = threadIdx.x;
+  __device__ __forceinline__ void from(int t, float tau, F&& f) const {
+    const int lane = threadIdx.x & 31;
     auto one = [&](float v, int i) {
       if (v >= tau) f(v, i);
     };
-    if (t < head) one(LpVec<T>::one(x + t), t);
-    for (int v = t; v < nvec; v += BATCH * LP_THREADS) {
-      uint4 r[BATCH];
+    for (int v = t + lane * LP_THREADS; v < nvec; v += 32 * LP_THREADS) {
+      float e[VN];
+      LpVec<T>::get(vec(v), e);
+      float mx = e[0];
 #pragma unroll
-      for (int b = 0; b < BATCH; ++b)
-        r[b] = vec(v + b * LP_THREADS < nvec ? v + b * LP_THREADS : v);
+      for (int i = 1; i < VN; ++i) mx = fmaxf(mx, e[i]);
+      if (mx >= tau) {
 #pragma unroll
-      for (int b = 0; b < BATCH; ++b) {
-        float e[VN];
-        LpVec<T>::get(r[b], e);
-        float mx = e[0];
-#pragma unroll
-        for (int i = 1; i < VN; ++i) mx = fmaxf(mx, e[i]);
-        if (mx >= tau && v + b * LP_THREADS < nvec) {
-#pragma unroll
-          for (int i = 0; i < VN; ++i) one(e[i], head + (v + b * LP_THREADS) * VN + i);
-        }
+        for (int i = 0; i < VN; ++i) one(e[i], head + v * VN + i);
       }
     }
     const int tail = head + nvec * VN;
-    if (t < n - tail) one(LpVec<T>::one(x + tail + t), tail + t);
+    if (lane == 0 && t < head) one(LpVec<T>::one(x + t), t);
+    if (lane == 0 && t < n - tail) one(LpVec<T>::one(x + tail + t), tail + t);
   }
   // f(value, id in the slice) for all of them
   template <class F>
@@ -298,7 +293,8 @@ struct LpShared {
   float group[32];
   int hist[256];
   float tau;
-  int count, prefix, left, warp_count[LP_WARPS];
+  int queue[LP_THREADS];  // threads that reach tau
+  int queued, count, prefix, left, warp_count[LP_WARPS];
   uint64_t landed;  // barrier of the slice's copy
 };
 
@@ -389,7 +385,7 @@ __device__ __noinline__ void lp_select(const LpSlice<T, SM>& sl, int id0, int n,
 }
 
 template <class T, bool SM>
-__global__ void __launch_bounds__(LP_THREADS, SM ? 3 : 2) logprobs_kernel(const LogprobArgs a, int cluster) {
+__global__ void __launch_bounds__(LP_THREADS, SM ? LP_CTAS_PER_SM : 2) logprobs_kernel(const LogprobArgs a, int cluster) {
   __shared__ LpShared sh;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int r = static_cast<int>(blockIdx.x) / cluster, rank = static_cast<int>(blockIdx.x) % cluster;
@@ -404,7 +400,7 @@ __global__ void __launch_bounds__(LP_THREADS, SM ? 3 : 2) logprobs_kernel(const 
   // no CTA writes into another before that one runs: arrive now, wait there
   if (cluster > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
   if (tid == 0) {
-    sh.count = 0;
+    sh.count = sh.queued = 0;
     if (SM) {
       mbar_init(&sh.landed, 1);
       fence_mbar_init();
@@ -424,12 +420,19 @@ __global__ void __launch_bounds__(LP_THREADS, SM ? 3 : 2) logprobs_kernel(const 
     if (tid < sl.head) d[tid] = x[id0 + tid];
     if (tid < len - tail) d[tail + tid] = x[id0 + tail + tid];
     // a copy that never lands (the bounded wait gives up) leaves the row marked
-    landed = mbar_wait(&sh.landed, 0, nullptr, PF_DEV_TIMEOUT_PRODUCER);
+    if (warp == 0) landed = mbar_wait(&sh.landed, 0, nullptr, PF_DEV_TIMEOUT_PRODUCER);
     landed = __syncthreads_and(landed);
   } else {
     pdl_wait();
   }
 
+  // the asked token's logit, well before it is needed
+  int tok = -1;
+  float x_tok = 0.f;
+  if (tid == 0 && rank == 0 && a.logp) {
+    tok = a.tok[r];
+    if (tok >= 0 && tok < a.vocab) x_tok = LpVec<T>::one(x + tok);
+  }
   LpSums q;
   if (landed) sl.sums(q);
   const float own = q.m;
@@ -458,10 +461,12 @@ __global__ void __launch_bounds__(LP_THREADS, SM ? 3 : 2) logprobs_kernel(const 
     }
     __syncthreads();
     const float tau = sh.tau;
-    if (own >= tau)
-      sl.from(tau, [&](float v, int i) {
+    if (own >= tau) sh.queue[atomicAdd(&sh.queued, 1)] = tid;
+    __syncthreads();
+    for (int i = warp; i < sh.queued; i += LP_WARPS)
+      sl.from(sh.queue[i], tau, [&](float v, int at_id) {
         const int at = atomicAdd(&sh.count, 1);
-        if (at < LP_CAND) sh.cand[at] = lp_key(lp_order(v), id0 + i);
+        if (at < LP_CAND) sh.cand[at] = lp_key(lp_order(v), id0 + at_id);
       });
     __syncthreads();
     const int cnt = sh.count;
@@ -515,10 +520,7 @@ __global__ void __launch_bounds__(LP_THREADS, SM ? 3 : 2) logprobs_kernel(const 
     a.top_id[at] = ok ? static_cast<int>(0xffffffffu - static_cast<uint32_t>(k)) : -1;
     a.top_logp[at] = ok ? lp_value(static_cast<uint32_t>(k >> 32)) - z.m - log_s : nan;
   }
-  if (lane == 0 && a.logp) {
-    const int t = a.tok[r];
-    a.logp[r] = ok && t >= 0 && t < a.vocab ? LpVec<T>::one(x + t) - z.m - log_s : nan;
-  }
+  if (lane == 0 && a.logp) a.logp[r] = ok && tok >= 0 && tok < a.vocab ? x_tok - z.m - log_s : nan;
   if (lane == 31 && a.entropy) a.entropy[r] = ok ? log_s - LP_LN2 * (z.h / z.s) : nan;
 }
 
@@ -536,7 +538,7 @@ static cudaError_t launch_logprobs(LogprobArgs a, int rows, cudaStream_t s) {
   int cluster = 1;
   while (cluster < LP_CLUSTER_MAX && a.vocab / (2 * cluster) >= LP_SLICE_MIN &&
          (static_cast<int64_t>(a.vocab) * sizeof(T) > static_cast<int64_t>(LP_SMEM_SLICE) * cluster ||
-          static_cast<int64_t>(rows) * 2 * cluster <= 3ll * sms))
+          static_cast<int64_t>(rows) * 2 * cluster <= static_cast<int64_t>(LP_CTAS_PER_SM) * sms))
     cluster *= 2;
   a.slice = ((a.vocab + cluster - 1) / cluster + 7) / 8 * 8;
   const dim3 grid(static_cast<unsigned>(rows) * cluster);
