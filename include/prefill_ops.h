@@ -235,7 +235,7 @@ typedef struct pfop_attn_run {
    shapes of the call's runs, not on the other runs' values; a repeated call
    gives the same bits.
    work_dev: device scratch of the call, 256-byte aligned, work_bytes of it
-   at least pfop_attention_work_bytes of the runs; its first 256 bytes must
+   at least pfop_attention_work_bytes of the runs; its first 4096 bytes must
    be zero before its first call.  Calls that share a scratch must not
    overlap on the GPU (one stream, or events; two recorded graphs that share
    one may not run at once).
@@ -261,7 +261,7 @@ int pfop_attention_tree(const void* q_dev, const void* k_dev, const void* v_dev,
                         int32_t mask_words, void* out_dev, void* work_dev, int64_t work_bytes, void* stream);
 
 /* Scratch bytes that either call needs for these runs on the current device
-   (host only; without a device, as on a GB300), or PF_E_ARG. */
+   (host only; without a device, as on a GB300; at least 4096), or PF_E_ARG. */
 int64_t pfop_attention_work_bytes(int32_t Hq, int32_t Hkv, int32_t hd, const pfop_attn_run* runs, int32_t n_runs);
 
 /* Wait for `stream` and report whether a call using this scratch gave up a

@@ -396,7 +396,7 @@ class AttnRuns:
             if need < 0:
                 check_op(need)
             self.work = torch.empty(need, dtype=torch.uint8, device="cuda")
-            self.work[:256].zero_()
+            self.work[:4096].zero_()
         self.work_bytes = need
 
     def check(self, stream=None):

@@ -9,14 +9,20 @@
 // being an item and a range of its 128-key chunks, with one online softmax:
 //     S = Q K^T, m' = max(m, max_k s_k), p_k = 2^((s_k - m') c),
 //     l' = l 2^((m - m') c) + sum_k p_k, O' = O 2^((m - m') c) + fp16(P) V
-// with c = log2(e)/sqrt(hd), S, O, m, l in fp32.  A segment that holds all
-// chunks of its item writes O/l; otherwise (O, m, l) goes to the scratch and
-// attn_runs_merge_kernel joins the item's segments in order.
+// with c = log2(e)/sqrt(hd), S, O, m, l in fp32.
 //
 // The cut: either a pair per item, or all items laid end to end (each
 // weighing its chunks and a fixed cost) and every resident pair given the
 // same share of that line, so that long and short sequences, many rows and
-// few, load the SMs evenly (make_plan).
+// few, load the SMs evenly (make_plan).  A segment that holds all chunks of
+// its item writes O/l.  Of an item cut in two, the first part (in pair p)
+// leaves its state (O, m, l) in the scratch and the second (in pair p+1)
+// joins it with its own: a pair takes its segments from the line's end, so
+// the state is the first thing pair p makes and the last that pair p+1
+// needs, and pair p+1 waits only for a pair of a lower index, which never
+// waits before that.  (A merge kernel for these took 24 us of a 250 us call.)
+// Items cut in three or more leave all their states to
+// attn_runs_merge_kernel.
 //
 // Why pairs: 128 rows against a chunk need 64 bytes of K/V per SM clock at
 // the full tensor rate, more than L2 delivers to all SMs at once; 256 rows
@@ -100,8 +106,11 @@ struct RunsCfg {
   static_assert(SMEM <= 232448, "shared memory");
 };
 
-// floats of one row's state: o[HD], m, l, 6 pad (32-byte rows)
-__host__ __device__ constexpr int runs_state_stride(int hd) { return hd + 8; }
+// A state slot, per 32 rows (a warp's): o as [4 dims][row][4], so that lanes
+// that hold a row each access 512 contiguous bytes, then (m, l) per row.
+// (Rows stored one after another took a segment's end 2 us, a second part
+// 10 us: every lane in another line.)
+__host__ __device__ constexpr int runs_state_floats(int hd) { return 32 * hd + 64; }
 
 // 64-byte-swizzled MN-major operand descriptor: rows (K) of 64 bytes, 8-row
 // groups of 512 bytes, one 32-element atom along MN
@@ -188,6 +197,27 @@ __device__ __forceinline__ void runs_drain(uint64_t* bar, uint32_t parity) {
   const long long t0 = clock64();
   while (!mbar_try_wait(a, parity)) {
     if (clock64() - t0 > 400000000ll) return;
+  }
+}
+
+// Wait (bounded like the barriers' waits) until a flag in global memory has
+// counted to n, and make what was written before visible.
+__device__ __forceinline__ bool wait_flag(const int* flag, int n, int* err) {
+  long long t0 = 0;
+  for (uint32_t i = 1;; ++i) {
+    int v;
+    asm volatile("ld.acquire.gpu.global.b32 %0, [%1];" : "=r"(v) : "l"(flag) : "memory");
+    if (v >= n) return true;
+    if ((i & 255u) == 0u) {
+      const long long now = clock64();
+      if (t0 == 0) {
+        t0 = now;
+      } else if (now - t0 > PF_WAIT_CYCLES) {
+        set_error(err, PF_DEV_TIMEOUT_EPILOGUE);
+        return false;
+      }
+      if (read_error(err) != 0) return false;
+    }
   }
 }
 
@@ -279,8 +309,14 @@ struct ItemAt {
   }
 };
 
-// The segments of a pair, in order.  A pair's share is a range of the line of
-// weights; the chunk k of an item lies at w + ITEM_FIXED + k.
+// The segments of a pair, from the end of its share.  The share is a range of
+// the line of weights; the chunk k of an item lies at w + ITEM_FIXED + k.
+enum SegKind : int {
+  SEG_WHOLE = 0,  // all of its item
+  SEG_FIRST = 1,  // first of two: leaves its state to the next pair
+  SEG_SECOND = 2,  // second of two: joins the pair before's
+  SEG_PART = 3,   // of three or more
+};
 template <bool TREE>
 struct Segments {
   const RunTable& rt;
@@ -289,41 +325,51 @@ struct Segments {
   int pair, lo, hi;
   bool left;
   // the segment
-  int run, kvh, R0, ch0, n;
-  int slot;  // state slot, -1: the item's only segment
+  int run, kvh, R0, ch0, n, kind;
+  int slot;  // its state's slot: an item's first segment 2 pair + 1, others 2 pair
   __host__ __device__ Segments(const RunTable& t, const RunsShape& s, int p) : rt(t), sh(s), pair(p), left(true) {
     if (sh.per == 0) {
       at = ItemAt<TREE>::number(rt, sh, pair);
-      lo = at.w;
-      hi = at.w + 1;  // not used
+      lo = hi = 0;  // not used
     } else {
       lo = pair * sh.per;
       hi = lo + sh.per < rt.w0[rt.n_runs] ? lo + sh.per : rt.w0[rt.n_runs];
       left = lo < hi;
-      if (left) at = ItemAt<TREE>::weight(rt, sh, lo);
+      if (left) at = ItemAt<TREE>::weight(rt, sh, hi - 1);
     }
   }
   __host__ __device__ bool next() {
     while (left) {
       const RunBlocks<TREE> rb(rt.n[at.run], rt.pos0[at.run], sh.log_g);
       const int ch = rb.chunks(at.i), w = at.w + ITEM_FIXED;
-      const int k0 = sh.per == 0 || lo < w ? 0 : lo - w, k1 = sh.per == 0 || hi - w > ch ? ch : hi - w;
+      const bool all = sh.per == 0;
+      const int k0 = all || lo < w ? 0 : lo - w, k1 = all || hi - w > ch ? ch : hi - w;
       run = at.run;
       kvh = at.kvh;
       R0 = (rb.nb - 1 - at.i) * RROWS;
       ch0 = k0;
       n = k1 - k0;
-      slot = k0 > 0 ? 2 * pair : k1 < ch ? 2 * pair + 1 : -1;
-      // on to the next item
-      at.w = w + ch;
-      if (sh.per == 0 || at.w >= hi) {
+      slot = 2 * pair + (k0 == 0 ? 1 : 0);
+      kind = SEG_WHOLE;
+      if (n < ch) {
+        // the item's chunks outside lie before this share, behind it, or both
+        if (k0 == 0)
+          kind = ch - k1 <= sh.per ? SEG_FIRST : SEG_PART;
+        else
+          kind = k1 == ch && w >= lo - sh.per ? SEG_SECOND : SEG_PART;
+      }
+      // on to the item before
+      if (all || at.w <= lo) {
         left = false;
-      } else if (++at.i == rb.nb) {
-        at.i = 0;
-        if (++at.kvh == sh.Hkv) {
-          at.kvh = 0;
-          ++at.run;
+      } else {
+        if (--at.i < 0) {
+          if (--at.kvh < 0) {
+            at.kvh = sh.Hkv - 1;
+            --at.run;
+          }
+          at.i = RunBlocks<TREE>(rt.n[at.run], rt.pos0[at.run], sh.log_g).nb - 1;
         }
+        at.w -= ITEM_FIXED + RunBlocks<TREE>(rt.n[at.run], rt.pos0[at.run], sh.log_g).chunks(at.i);
       }
       if (n > 0) return true;
     }
@@ -381,7 +427,7 @@ __global__ void __launch_bounds__(RunsCfg<HD>::THREADS, 1)
     attn_runs_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                      const __grid_constant__ CUtensorMap tmV, const __grid_constant__ RunTable rt, const RunsShape sh,
                      const uint64_t* __restrict__ mask, int words, __nv_bfloat16* __restrict__ out,
-                     float* __restrict__ part, int* __restrict__ desc, int* err) {
+                     float* part, int* __restrict__ desc, int* err, int* flags) {
   using C = RunsCfg<HD>;
   constexpr float cexp = attn_c<HD>();
   extern __shared__ uint8_t smem_raw[];
@@ -425,12 +471,12 @@ __global__ void __launch_bounds__(RunsCfg<HD>::THREADS, 1)
   }
   if (warp == 2 && lane == 0) prefetch_tensormap(&tmQ);
   if (warp == 0) tmem_alloc_pair(tmem_slot, C::TMEM_COLS);
+  Segments<TREE> sg(rt, sh, static_cast<int>(blockIdx.x >> 1));
   tc_fence_before();
   __syncthreads();
   cluster_sync_all();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  Segments<TREE> sg(rt, sh, static_cast<int>(blockIdx.x >> 1));
   pdl_wait();
 
   // Counters that run on over the pair's segments, the same in every role:
@@ -587,25 +633,63 @@ __global__ void __launch_bounds__(RunsCfg<HD>::THREADS, 1)
       if (active) {
         // a thread writes its row, 32-byte sectors at a time
         tc_fence_after();
-        const bool whole = sg.slot < 0;
+        const bool whole = sg.kind == SEG_WHOLE || sg.kind == SEG_SECOND;
+        // the warp's rows in a state slot
+        auto state_at = [&](int slot) {
+          return (static_cast<size_t>(slot) * (sh.slot_rows / 32) + ((Rw - sg.R0) >> 5)) * runs_state_floats(HD);
+        };
+        // the first part's state of this row, and its weight
+        const float* other_part = nullptr;
+        float w_other = 0.f;
+        int* flag = nullptr;
+        if (sg.kind == SEG_SECOND) {
+          flag = flags + (sg.pair - 1) * 8 + rank * 4 + qw;
+          if (!wait_flag(flag, C::NG, err)) ok = false;
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          other_part = part + state_at(2 * sg.pair - 1);
+          const float2 ml = __ldcg(reinterpret_cast<const float2*>(other_part + 32 * HD) + lane);
+          const float mm = fmaxf(m, ml.x);
+          const float a = m == -INFINITY ? 0.f : ex2_approx((m - mm) * cexp);
+          w_other = ml.x == -INFINITY ? 0.f : ex2_approx((ml.x - mm) * cexp);
+          l = a * l + w_other * ml.y;
+          w0 *= a;
+          w1 *= a;
+        }
         const float inv = !whole ? 1.f : l == 0.f ? 0.f : __frcp_rn(l);  // a row that sees nothing: zeros
         w0 *= inv;
         w1 *= inv;
-        const size_t own = whole ? (static_cast<size_t>(row0 + t) * sh.Hq + head) * HD
-                                 : (static_cast<size_t>(sg.slot) * sh.slot_rows + (R - sg.R0)) * runs_state_stride(HD);
+        w_other *= inv;
+        __nv_bfloat16* own_out = out + (static_cast<size_t>(row0 + t) * sh.Hq + head) * HD;
+        float* own_state = part + state_at(sg.slot);
         auto store = [&](int c, const uint32_t (&y)[32]) {
           if (row && whole) {
             uint32_t hb[16];
+            float f[32];
+#pragma unroll
+            for (int q = 0; q < 32; ++q) f[q] = __uint_as_float(y[q]);
+            if (sg.kind == SEG_SECOND) {
+#pragma unroll
+              for (int q = 0; q < 8; ++q) {
+                const float4 o = __ldcg(reinterpret_cast<const float4*>(other_part) + (8 * c + q) * 32 + lane);
+                f[4 * q] = __fmaf_rn(w_other, o.x, f[4 * q]);
+                f[4 * q + 1] = __fmaf_rn(w_other, o.y, f[4 * q + 1]);
+                f[4 * q + 2] = __fmaf_rn(w_other, o.z, f[4 * q + 2]);
+                f[4 * q + 3] = __fmaf_rn(w_other, o.w, f[4 * q + 3]);
+              }
+            }
 #pragma unroll
             for (int q = 0; q < 16; ++q) {
-              const __nv_bfloat162 v = __floats2bfloat162_rn(__uint_as_float(y[2 * q]), __uint_as_float(y[2 * q + 1]));
+              const __nv_bfloat162 v = __floats2bfloat162_rn(f[2 * q], f[2 * q + 1]);
               hb[q] = *reinterpret_cast<const uint32_t*>(&v);
             }
-            st_global_v8(out + own + 32 * c, hb);
-            st_global_v8(out + own + 32 * c + 16, hb + 8);
-          } else if (row) {
+            st_global_v8(own_out + 32 * c, hb);
+            st_global_v8(own_out + 32 * c + 16, hb + 8);
+          } else if (!whole) {  // rows past the run's as well: their lanes' places are there
 #pragma unroll
-            for (int q = 0; q < 4; ++q) st_global_v8(part + own + 32 * c + 8 * q, y + 8 * q);
+            for (int q = 0; q < 8; ++q)
+              *(reinterpret_cast<uint4*>(own_state) + (8 * c + q) * 32 + lane) =
+                  make_uint4(y[4 * q], y[4 * q + 1], y[4 * q + 2], y[4 * q + 3]);
           }
           __syncwarp();
         };
@@ -640,7 +724,17 @@ __global__ void __launch_bounds__(RunsCfg<HD>::THREADS, 1)
             y[q] = __float_as_uint(__fmaf_rn(wa, __uint_as_float(y[q]), wb * __uint_as_float(z[q])));
           store(h, y);
         }
-        if (!whole && row && h == 0) *reinterpret_cast<float2*>(part + own + HD) = make_float2(m, l);
+        if (!whole && h == 0) reinterpret_cast<float2*>(own_state + 32 * HD)[lane] = make_float2(m, l);
+        __syncwarp();
+        if (lane == 0) {
+          // the warp's rows of the state are there; or read, and the flag as it was
+          if (sg.kind == SEG_FIRST) {
+            __threadfence();
+            atomicAdd(flags + sg.pair * 8 + rank * 4 + qw, 1);
+          } else if (sg.kind == SEG_SECOND && atomicAdd(flag, 1) == 2 * C::NG - 1) {
+            atomicExch(flag, 0);
+          }
+        }
         tc_fence_before();
       }
       __syncwarp();
@@ -731,13 +825,13 @@ __global__ void __launch_bounds__(RunsCfg<HD>::THREADS, 1)
         const int pair = static_cast<int>(blockIdx.x >> 1);
         if (!sh.desc_by_item) d[2 * pair] = make_int4(0, 0, 0, 0);
         while (sg.next()) {
-          if (sg.ch0 > 0 || (sg.slot < 0 && !sh.desc_by_item)) continue;
-          // the item's first segment: its pairs (0: it is whole), rows, first packed row, KV head; first row
+          if (sg.ch0 > 0 || (sg.kind != SEG_PART && !sh.desc_by_item)) continue;
+          // the item's first segment: its pairs (0: nothing to join), rows, first packed row, KV head; first row
           const RunBlocks<TREE> rb(rt.n[sg.run], rt.pos0[sg.run], sh.log_g);
           const int i = rb.nb - 1 - sg.R0 / RROWS;
           const int left = rb.chunks(i) - sg.n;  // chunks in the pairs after this one
           const int at = sh.desc_by_item ? rt.item0[sg.run] + sg.kvh * rb.nb + i : pair;
-          d[2 * at] = make_int4(left ? 1 + (left + sh.per - 1) / sh.per : 0,
+          d[2 * at] = make_int4(sg.kind == SEG_PART ? 1 + (left + sh.per - 1) / sh.per : 0,
                                 min(RROWS, (rt.n[sg.run] << sh.log_g) - sg.R0), rt.row0[sg.run], sg.kvh);
           d[2 * at + 1] = make_int4(sg.R0, pair, 0, 0);
         }
@@ -852,111 +946,93 @@ __global__ void __launch_bounds__(RunsCfg<HD>::THREADS, 1)
   }
 }
 
-// Items cut over several pairs: m = max m_p, w_p = 2^((m_p - m) c), out =
+// Items cut in three or more: m = max m_p, w_p = 2^((m_p - m) c), out =
 // (sum w_p o_p) / (sum w_p l_p) over the item's pairs p, p+1, .. in order.
-// blockIdx.x counts items, or pairs with the item that starts in a pair's last
-// segment (desc: 8 ints each).  `wpr` warps take a row (its pairs dealt out among them,
-// their sums joined in warp order), lane owning HD/32 consecutive dims.
-// Bound by the latency of reading the states from L2: four are in flight,
-// and a row of many pairs wants many warps.
+// blockIdx.x counts items, or pairs with the item that starts in a pair's
+// first segment (desc: 8 ints each); blockIdx.y 32-row groups; `ways` warps
+// take four dims of the group's rows (lane = row), the states dealt out among
+// them and their sums joined in warp order.  Bound by the latency of reading
+// the states from L2: eight are in flight, and many states want many warps.
 template <int HD>
-__global__ void __launch_bounds__(256) attn_runs_merge_kernel(const RunsShape sh, int wpr, const int* desc,
+__global__ void __launch_bounds__(256) attn_runs_merge_kernel(const RunsShape sh, int ways, const int* desc,
                                                               const float* part, __nv_bfloat16* out) {
-  constexpr int PER = HD / 32;
   constexpr float c = attn_c<HD>();
-  constexpr int ST = runs_state_stride(HD);
-  __shared__ float joined[8][HD + 4];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int R_in = static_cast<int>(blockIdx.y) * (8 / wpr) + warp / wpr;
-  const int sub = warp % wpr;
+  constexpr int FLY = 8;
+  __shared__ float4 sum[8][32];
+  __shared__ float2 sum_ml[8][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = warp % ways;
+  const int quad = static_cast<int>(blockIdx.z) * (8 / ways) + warp / ways;
   pdl_launch();
   pdl_wait();
   const int4 d = __ldcg(reinterpret_cast<const int4*>(desc) + 2 * blockIdx.x);  // pairs, rows, first packed row, KV head
   const int2 e = __ldcg(reinterpret_cast<const int2*>(desc) + 4 * blockIdx.x + 2);
-  const int R0 = e.x, p0 = e.y;
-  const int np = d.x;
-  // uniform over the block: nothing to join, or none of the rows are the block's
-  if (np == 0 || static_cast<int>(blockIdx.y) * (8 / wpr) >= d.y) return;
-  const bool live = R_in < d.y;
+  const int R0 = e.x, p0 = e.y, np = d.x;
+  const int R_in = static_cast<int>(blockIdx.y) * 32 + lane;
+  if (np == 0 || static_cast<int>(blockIdx.y) * 32 >= d.y) return;  // nothing to join, or none of the rows
   float m = -INFINITY, l = 0.f;
-  float acc[PER];
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int q = sub; q < np; q += FLY * ways) {
+    float4 o[FLY];
+    float2 ml[FLY];
 #pragma unroll
-  for (int i = 0; i < PER; ++i) acc[i] = 0.f;
-  for (int q = sub; q < np && live; q += 4 * wpr) {
-    float o[4][PER];
-    float2 ml[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int p = min(q + k * wpr, np - 1);
+    for (int k = 0; k < FLY; ++k) {
+      const int p = min(q + k * ways, np - 1);
       // the first pair's slot is its second
-      const float* s = part + (static_cast<size_t>(p == 0 ? 2 * p0 + 1 : 2 * (p0 + p)) * sh.slot_rows + R_in) * ST;
-      ml[k] = __ldcg(reinterpret_cast<const float2*>(s + HD));
-      if (q + k * wpr >= np) ml[k].x = -INFINITY;
-      if constexpr (PER >= 4) {
-#pragma unroll
-        for (int i = 0; i < PER; i += 4) {
-          const float4 v = __ldcg(reinterpret_cast<const float4*>(s + lane * PER + i));
-          o[k][i] = v.x, o[k][i + 1] = v.y, o[k][i + 2] = v.z, o[k][i + 3] = v.w;
-        }
-      } else {
-        const float2 v = __ldcg(reinterpret_cast<const float2*>(s + lane * PER));
-        o[k][0] = v.x, o[k][1] = v.y;
-      }
+      const float* s = part + (static_cast<size_t>(p == 0 ? 2 * p0 + 1 : 2 * (p0 + p)) * (sh.slot_rows / 32) + blockIdx.y) *
+                                  runs_state_floats(HD);
+      ml[k] = __ldcg(reinterpret_cast<const float2*>(s + 32 * HD) + lane);
+      o[k] = __ldcg(reinterpret_cast<const float4*>(s) + quad * 32 + lane);
+      if (q + k * ways >= np) ml[k].x = -INFINITY;
     }
-    const float mn = fmaxf(fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x)), m);
-    if (mn != m) {
-      const float w = m == -INFINITY ? 0.f : ex2_approx((m - mn) * c);
-      l *= w;
+    float mn = m;
 #pragma unroll
-      for (int i = 0; i < PER; ++i) acc[i] *= w;
-      m = mn;
-    }
+    for (int k = 0; k < FLY; ++k) mn = fmaxf(mn, ml[k].x);
+    if (mn == -INFINITY) continue;
+    const float w = m == -INFINITY ? 0.f : ex2_approx((m - mn) * c);
+    l *= w;
+    acc.x *= w, acc.y *= w, acc.z *= w, acc.w *= w;
+    m = mn;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
+    for (int k = 0; k < FLY; ++k) {
       if (ml[k].x == -INFINITY) continue;
-      const float w = ex2_approx((ml[k].x - m) * c);
-      l = __fmaf_rn(w, ml[k].y, l);
-#pragma unroll
-      for (int i = 0; i < PER; ++i) acc[i] = __fmaf_rn(w, o[k][i], acc[i]);
+      const float wk = ex2_approx((ml[k].x - m) * c);
+      l = __fmaf_rn(wk, ml[k].y, l);
+      acc.x = __fmaf_rn(wk, o[k].x, acc.x);
+      acc.y = __fmaf_rn(wk, o[k].y, acc.y);
+      acc.z = __fmaf_rn(wk, o[k].z, acc.z);
+      acc.w = __fmaf_rn(wk, o[k].w, acc.w);
     }
   }
-  if (wpr > 1) {
-    float* mine = joined[warp];
-#pragma unroll
-    for (int i = 0; i < PER; ++i) mine[lane * PER + i] = acc[i];
-    if (lane == 0) mine[HD] = m, mine[HD + 1] = l;
+  if (ways > 1) {
+    sum[warp][lane] = acc;
+    sum_ml[warp][lane] = make_float2(m, l);
     __syncthreads();
     if (sub != 0) return;
-    float mm = m;
-    for (int k = 1; k < wpr; ++k) mm = fmaxf(mm, joined[warp + k][HD]);
-    const float w_own = m == -INFINITY ? 0.f : ex2_approx((m - mm) * c);
-    l *= w_own;
-#pragma unroll
-    for (int i = 0; i < PER; ++i) acc[i] *= w_own;
-    for (int k = 1; k < wpr; ++k) {
-      const float* s = joined[warp + k];
-      if (s[HD] == -INFINITY) continue;
-      const float w = ex2_approx((s[HD] - mm) * c);
-      l = __fmaf_rn(w, s[HD + 1], l);
-#pragma unroll
-      for (int i = 0; i < PER; ++i) acc[i] = __fmaf_rn(w, s[lane * PER + i], acc[i]);
+    float mn = m;
+    for (int k = 1; k < ways; ++k) mn = fmaxf(mn, sum_ml[warp + k][lane].x);
+    const float w = m == -INFINITY ? 0.f : ex2_approx((m - mn) * c);
+    l *= w;
+    acc.x *= w, acc.y *= w, acc.z *= w, acc.w *= w;
+    for (int k = 1; k < ways; ++k) {
+      const float2 ml = sum_ml[warp + k][lane];
+      const float4 o = sum[warp + k][lane];
+      const float wk = ml.x == -INFINITY ? 0.f : ex2_approx((ml.x - mn) * c);
+      l = __fmaf_rn(wk, ml.y, l);
+      acc.x = __fmaf_rn(wk, o.x, acc.x);
+      acc.y = __fmaf_rn(wk, o.y, acc.y);
+      acc.z = __fmaf_rn(wk, o.z, acc.z);
+      acc.w = __fmaf_rn(wk, o.w, acc.w);
     }
   }
-  if (!live) return;
+  if (R_in >= d.y) return;
   const float inv = l == 0.f ? 0.f : __frcp_rn(l);
   const int R = R0 + R_in;
   __nv_bfloat16* dst = out + (static_cast<size_t>(d.z + (R >> sh.log_g)) * sh.Hq + (d.w << sh.log_g) +
-                              (R & ((1 << sh.log_g) - 1))) * HD + lane * PER;
-  uint32_t hb[PER / 2];
-#pragma unroll
-  for (int i = 0; i < PER; i += 2) {
-    const __nv_bfloat162 v = __floats2bfloat162_rn(acc[i] * inv, acc[i + 1] * inv);
-    hb[i / 2] = *reinterpret_cast<const uint32_t*>(&v);
-  }
-  if constexpr (PER == 8)
-    *reinterpret_cast<uint4*>(dst) = make_uint4(hb[0], hb[1], hb[2], hb[3]);
-  else
-    *reinterpret_cast<uint32_t*>(dst) = hb[0];
+                              (R & ((1 << sh.log_g) - 1))) * HD + 4 * quad;
+  const __nv_bfloat162 v0 = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
+  const __nv_bfloat162 v1 = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
+  *reinterpret_cast<uint2*>(dst) =
+      make_uint2(*reinterpret_cast<const uint32_t*>(&v0), *reinterpret_cast<const uint32_t*>(&v1));
 }
 
 // ---------------------------------------------------------------------------
@@ -968,6 +1044,7 @@ struct RunsPlan {
   int items = 0;
   int64_t desc_bytes = 0;   // the merge kernel's table, ahead of the states
   int64_t state_bytes = 0;  // both
+  bool merge = false;       // an item may be cut in three or more
 };
 
 static int sm_count() {
@@ -984,11 +1061,12 @@ static int sm_count() {
 }
 
 // Which cut: a pair per item where the items fit the GPU at once and the
-// longest takes no longer than an even share would with the states' traffic
-// and the merge launch (MERGE_COST chunk times); else even shares over the
-// resident pairs, but none below MIN_SHARE.  False: more work than the line
-// of weights can count.
-constexpr int MERGE_COST = 4;
+// longest takes no longer than an even share would with what joining costs
+// (JOIN_COST chunk times in the pairs, MERGE_COST with the merge kernel);
+// else even shares over the resident pairs, but none below MIN_SHARE.
+// False: more work than the line of weights can count.
+constexpr int JOIN_COST = 4, MERGE_COST = 6;
+constexpr int MAX_PAIRS = 120;  // flags of 8 words each in the scratch's header
 constexpr int MIN_SHARE = ITEM_FIXED + 2;
 
 template <bool TREE>
@@ -1023,19 +1101,21 @@ static bool make_plan(RunsPlan& p, const pfop_attn_run* runs, int n_runs, int Hq
   p.rt.w0[n] = static_cast<int>(weight);
   p.items = static_cast<int>(items);
   p.sh.slot_rows = (max_rows + 31) / 32 * 32;
-  const int units = std::max(1, sm_count() / 2);
+  const int units = std::min(MAX_PAIRS, std::max(1, sm_count() / 2));
   const int share = std::max<int>(MIN_SHARE, static_cast<int>((weight + units - 1) / units));
-  if (items <= units && longest + ITEM_FIXED <= share + MERGE_COST) {
+  if (items <= units && longest + ITEM_FIXED <= share + (longest > share + 1 ? MERGE_COST : JOIN_COST)) {
     p.sh.per = p.sh.desc_by_item = 0;
     p.sh.pairs = p.items;
     p.desc_bytes = p.state_bytes = 0;
+    p.merge = false;
   } else {
     p.sh.per = share;
     p.sh.pairs = static_cast<int>((weight + share - 1) / share);
+    p.merge = longest > share + 1;  // else no item covers a whole share
     p.sh.desc_by_item = p.items < p.sh.pairs ? 1 : 0;
     p.desc_bytes = (int64_t(std::min(p.sh.pairs, p.items)) * 32 + 255) / 256 * 256;
     p.state_bytes =
-        p.desc_bytes + int64_t(2) * p.sh.pairs * p.sh.slot_rows * runs_state_stride(hd) * static_cast<int64_t>(sizeof(float));
+        p.desc_bytes + int64_t(2) * p.sh.pairs * (p.sh.slot_rows / 32) * runs_state_floats(hd) * static_cast<int64_t>(sizeof(float));
   }
   return true;
 }
@@ -1043,7 +1123,7 @@ static bool make_plan(RunsPlan& p, const pfop_attn_run* runs, int n_runs, int Hq
 template <int HD, bool TREE>
 static cudaError_t launch_runs(const RunsPlan& p, const __half* q, const __half* k, const __half* v, int64_t n_cells,
                                int total, const uint64_t* mask, int words, __nv_bfloat16* out, uint8_t* states,
-                               int* err, cudaStream_t s) {
+                               int* err, int* flags, cudaStream_t s) {
   using C = RunsCfg<HD>;
   cudaError_t e = smem_opt_in<attn_runs_kernel<HD, TREE>>(C::SMEM);
   if (e != cudaSuccess) return e;
@@ -1072,13 +1152,14 @@ static cudaError_t launch_runs(const RunsPlan& p, const __half* q, const __half*
   int* desc = reinterpret_cast<int*>(states);
   float* part = reinterpret_cast<float*>(states + p.desc_bytes);
   e = launch_k(attn_runs_kernel<HD, TREE>, dim3(2u * p.sh.pairs), dim3(C::THREADS), C::SMEM, s, 2, tq, tk, tv, p.rt,
-               p.sh, mask, words, out, part, desc, err);
-  if (e != cudaSuccess || p.sh.per == 0 || p.sh.pairs == 1) return e;
-  // warps per row: an item lies in about pairs / items + 1 pairs
-  const int spread = p.sh.pairs / std::max(1, p.items) + 1;
-  const int wpr = spread <= 4 ? 1 : spread <= 8 ? 2 : spread <= 16 ? 4 : 8;
-  return launch_k(attn_runs_merge_kernel<HD>, dim3(std::min(p.sh.pairs, p.items), p.sh.slot_rows / (8 / wpr)), dim3(256), 0, s, 1,
-                  p.sh, wpr, static_cast<const int*>(desc), static_cast<const float*>(part), out);
+               p.sh, mask, words, out, part, desc, err, flags);
+  if (e != cudaSuccess || !p.merge) return e;
+  // an item lies in about pairs / items pairs: one round of loads each
+  const int spread = p.sh.pairs / p.items;
+  const int ways = spread <= 8 ? 1 : spread <= 16 ? 2 : spread <= 32 ? 4 : 8;
+  return launch_k(attn_runs_merge_kernel<HD>,
+                  dim3(std::min(p.sh.pairs, p.items), p.sh.slot_rows / 32, HD / 32 * ways), dim3(256), 0, s, 1, p.sh,
+                  ways, static_cast<const int*>(desc), static_cast<const float*>(part), out);
 }
 
 }  // namespace pf
@@ -1087,7 +1168,9 @@ namespace {
 
 using namespace pf;
 
-constexpr int64_t WORK_HEADER = 256;  // the error word, alone in its lines
+constexpr int64_t WORK_HEADER = 4096;  // the error word; from word FLAGS_AT the pairs' flags
+constexpr int FLAGS_AT = 64;
+static_assert((FLAGS_AT + 8 * MAX_PAIRS) * 4 <= WORK_HEADER, "scratch header");
 
 int fail(int code, const std::string& m) {
   set_op_error(m);
@@ -1142,7 +1225,7 @@ int run_attention(bool tree, const void* q, const void* k, const void* v, int64_
   uint8_t* states = static_cast<uint8_t*>(work) + WORK_HEADER;
   auto go = [&](auto launch) {
     return launch(p, static_cast<const __half*>(q), static_cast<const __half*>(k), static_cast<const __half*>(v),
-                  n_cells, static_cast<int>(total), mask, words, static_cast<__nv_bfloat16*>(out), states, err, s);
+                  n_cells, static_cast<int>(total), mask, words, static_cast<__nv_bfloat16*>(out), states, err, err + FLAGS_AT, s);
   };
   const cudaError_t e = hd == 256 ? (tree ? go(launch_runs<256, true>) : go(launch_runs<256, false>))
                                   : (tree ? go(launch_runs<64, true>) : go(launch_runs<64, false>));
@@ -1185,7 +1268,7 @@ extern "C" int pfop_attention_status(void* work_dev, void* stream) {
   int h = 0;
   cudaError_t e = cudaMemcpyAsync(&h, work_dev, 4, cudaMemcpyDeviceToHost, s);
   if (e == cudaSuccess) e = cudaStreamSynchronize(s);
-  if (e == cudaSuccess && h) e = cudaMemsetAsync(work_dev, 0, 4, s);
+  if (e == cudaSuccess && h) e = cudaMemsetAsync(work_dev, 0, WORK_HEADER, s);  // flags of a call that gave up too
   if (e != cudaSuccess) return fail(PF_E_CUDA, std::string("attention status: ") + cudaGetErrorString(e));
   if (h) return fail(PF_E_DEVICE_TIMEOUT, "attention gave up a bounded wait, code " + std::to_string(h));
   return PF_OK;

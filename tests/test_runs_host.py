@@ -92,11 +92,11 @@ def test_scratch_sizes(lib, heads, runs):
     where states have to be kept, one below the header always."""
     arr, n = _runs(*runs)
     need = lib.pfop_attention_work_bytes(*heads, arr, n)
-    assert 256 <= need < 1 << 30
-    assert lib.pfop_attention_work_bytes(*heads, arr, 0) == 256
-    assert _packed(lib, runs, cells=1 << 20, heads=heads, nbytes=255) == PF_E_ARG
+    assert 4096 <= need < 1 << 30
+    assert lib.pfop_attention_work_bytes(*heads, arr, 0) == 4096
+    assert _packed(lib, runs, cells=1 << 20, heads=heads, nbytes=4095) == PF_E_ARG
     if runs[0][0] <= 256:
-        assert _tree(lib, runs, cells=1 << 20, heads=heads, words=4, nbytes=255) == PF_E_ARG
+        assert _tree(lib, runs, cells=1 << 20, heads=heads, words=4, nbytes=4095) == PF_E_ARG
 
 
 def _logprobs(lib, ltype=0, logits=Q, ld=100, rows=2, vocab=100, tok=K, n_top=0, logp=V, ent=OUT, tid=None, tlp=None):
