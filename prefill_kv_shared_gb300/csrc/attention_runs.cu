@@ -21,8 +21,8 @@
 // the state is the first thing pair p makes and the last that pair p+1
 // needs, and pair p+1 waits only for a pair of a lower index, which never
 // waits before that.  (A merge kernel for these took 24 us of a 250 us call.)
-// Items cut in three or more leave all their states to
-// attn_runs_merge_kernel.
+// Where an item may be cut in three or more, all cut items leave their states
+// to attn_runs_merge_kernel.
 //
 // Why pairs: 128 rows against a chunk need 64 bytes of K/V per SM clock at
 // the full tensor rate, more than L2 delivers to all SMs at once; 256 rows
@@ -75,6 +75,7 @@ struct RunsShape {
   int Hq, Hkv, log_g;  // G = 1 << log_g query heads per KV head
   int per;             // weight of a pair's share; 0: a pair per item
   int pairs;
+  int merge;  // an item may be cut in three or more: the merge kernel joins all that are cut
   int desc_by_item;  // the merge kernel's table has an entry per item, not per pair (the smaller of the two)
   int slot_rows;  // rows of a state slot in the scratch
 };
@@ -315,7 +316,7 @@ enum SegKind : int {
   SEG_WHOLE = 0,  // all of its item
   SEG_FIRST = 1,  // first of two: leaves its state to the next pair
   SEG_SECOND = 2,  // second of two: joins the pair before's
-  SEG_PART = 3,   // of three or more
+  SEG_PART = 3,   // the merge kernel joins it
 };
 template <bool TREE>
 struct Segments {
@@ -353,7 +354,9 @@ struct Segments {
       kind = SEG_WHOLE;
       if (n < ch) {
         // the item's chunks outside lie before this share, behind it, or both
-        if (k0 == 0)
+        if (sh.merge)
+          kind = SEG_PART;
+        else if (k0 == 0)
           kind = ch - k1 <= sh.per ? SEG_FIRST : SEG_PART;
         else
           kind = k1 == ch && w >= lo - sh.per ? SEG_SECOND : SEG_PART;
@@ -946,7 +949,7 @@ __global__ void __launch_bounds__(RunsCfg<HD>::THREADS, 1)
   }
 }
 
-// Items cut in three or more: m = max m_p, w_p = 2^((m_p - m) c), out =
+// Cut items: m = max m_p, w_p = 2^((m_p - m) c), out =
 // (sum w_p o_p) / (sum w_p l_p) over the item's pairs p, p+1, .. in order.
 // blockIdx.x counts items, or pairs with the item that starts in a pair's
 // first segment (desc: 8 ints each); blockIdx.y 32-row groups; `ways` warps
@@ -1044,7 +1047,6 @@ struct RunsPlan {
   int items = 0;
   int64_t desc_bytes = 0;   // the merge kernel's table, ahead of the states
   int64_t state_bytes = 0;  // both
-  bool merge = false;       // an item may be cut in three or more
 };
 
 static int sm_count() {
@@ -1107,11 +1109,11 @@ static bool make_plan(RunsPlan& p, const pfop_attn_run* runs, int n_runs, int Hq
     p.sh.per = p.sh.desc_by_item = 0;
     p.sh.pairs = p.items;
     p.desc_bytes = p.state_bytes = 0;
-    p.merge = false;
+    p.sh.merge = 0;
   } else {
     p.sh.per = share;
     p.sh.pairs = static_cast<int>((weight + share - 1) / share);
-    p.merge = longest > share + 1;  // else no item covers a whole share
+    p.sh.merge = longest > share + 1 ? 1 : 0;  // else no item covers a whole share
     p.sh.desc_by_item = p.items < p.sh.pairs ? 1 : 0;
     p.desc_bytes = (int64_t(std::min(p.sh.pairs, p.items)) * 32 + 255) / 256 * 256;
     p.state_bytes =
@@ -1153,7 +1155,7 @@ static cudaError_t launch_runs(const RunsPlan& p, const __half* q, const __half*
   float* part = reinterpret_cast<float*>(states + p.desc_bytes);
   e = launch_k(attn_runs_kernel<HD, TREE>, dim3(2u * p.sh.pairs), dim3(C::THREADS), C::SMEM, s, 2, tq, tk, tv, p.rt,
                p.sh, mask, words, out, part, desc, err, flags);
-  if (e != cudaSuccess || !p.merge) return e;
+  if (e != cudaSuccess || !p.sh.merge) return e;
   // an item lies in about pairs / items pairs: one round of loads each
   const int spread = p.sh.pairs / p.items;
   const int ways = spread <= 8 ? 1 : spread <= 16 ? 2 : spread <= 32 ? 4 : 8;
