@@ -531,7 +531,7 @@ __global__ void __launch_bounds__(RunsCfg<HD>::THREADS, 1)
       ok = __all_sync(0xffffffffu, ok);
       return ok;
     };
-    for (; ok && sg.next(); j0 += sg.n, f0 += 2 * sg.n) {
+    for (bool more = sg.next(); ok && more;) {
       const int n_rows = rt.n[sg.run], pos0 = rt.pos0[sg.run], row0 = rt.row0[sg.run];
       const int total_rows = n_rows << sh.log_g;
       const int Rw = sg.R0 + rank * 128 + 32 * qw;  // the warp's first row
@@ -617,7 +617,10 @@ __global__ void __launch_bounds__(RunsCfg<HD>::THREADS, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive_pair_relaxed(p_full_at + b * 8);
       }
-      if (ok) done(f0 + v_fill(sg.n - 1, sg.n));
+      // the next segment is looked up while the last P V is formed
+      const int n = sg.n, R0 = sg.R0, kind = sg.kind, slot = sg.slot;
+      more = sg.next();
+      if (ok) done(f0 + v_fill(n - 1, n));
       // the warpgroups' weights: w_h = 2^((m_h - m) c); each of a row's two
       // warps writes half of the 64 dims
       float w0 = 1.f, w1 = 0.f;
@@ -636,16 +639,16 @@ __global__ void __launch_bounds__(RunsCfg<HD>::THREADS, 1)
       if (active) {
         // a thread writes its row, 32-byte sectors at a time
         tc_fence_after();
-        const bool whole = sg.kind == SEG_WHOLE || sg.kind == SEG_SECOND;
+        const bool whole = kind == SEG_WHOLE || kind == SEG_SECOND;
         // the warp's rows in a state slot
         auto state_at = [&](int slot) {
-          return (static_cast<size_t>(slot) * (sh.slot_rows / 32) + ((Rw - sg.R0) >> 5)) * runs_state_floats(HD);
+          return (static_cast<size_t>(slot) * (sh.slot_rows / 32) + ((Rw - R0) >> 5)) * runs_state_floats(HD);
         };
         // the first part's state of this row, and its weight
         const float* other_part = nullptr;
         float w_other = 0.f;
         int* flag = nullptr;
-        if (sg.kind == SEG_SECOND) {
+        if (kind == SEG_SECOND) {
           flag = flags + (sg.pair - 1) * 8 + rank * 4 + qw;
           if (!wait_flag(flag, C::NG, err)) ok = false;
           ok = __all_sync(0xffffffffu, ok);
@@ -664,14 +667,14 @@ __global__ void __launch_bounds__(RunsCfg<HD>::THREADS, 1)
         w1 *= inv;
         w_other *= inv;
         __nv_bfloat16* own_out = out + (static_cast<size_t>(row0 + t) * sh.Hq + head) * HD;
-        float* own_state = part + state_at(sg.slot);
+        float* own_state = part + state_at(slot);
         auto store = [&](int c, const uint32_t (&y)[32]) {
           if (row && whole) {
             uint32_t hb[16];
             float f[32];
 #pragma unroll
             for (int q = 0; q < 32; ++q) f[q] = __uint_as_float(y[q]);
-            if (sg.kind == SEG_SECOND) {
+            if (kind == SEG_SECOND) {
 #pragma unroll
               for (int q = 0; q < 8; ++q) {
                 const float4 o = __ldcg(reinterpret_cast<const float4*>(other_part) + (8 * c + q) * 32 + lane);
@@ -716,8 +719,8 @@ __global__ void __launch_bounds__(RunsCfg<HD>::THREADS, 1)
         } else {
           // columns h * 32 .. + 31 of both O; after one chunk the other
           // warpgroup's holds nothing
-          const int own_g = static_cast<int>(j0 & 1), other = sg.n > 1 ? own_g ^ 1 : own_g;
-          const float wa = own_g ? w1 : w0, wb = sg.n > 1 ? (own_g ? w0 : w1) : 0.f;
+          const int own_g = static_cast<int>(j0 & 1), other = n > 1 ? own_g ^ 1 : own_g;
+          const float wa = own_g ? w1 : w0, wb = n > 1 ? (own_g ? w0 : w1) : 0.f;
           tmem_ld32(lanes + C::TMEM_O + own_g * HD + 32 * h, y);
           tmem_ld32(lanes + C::TMEM_O + other * HD + 32 * h, z);
           tmem_ld_wait32(y);
@@ -731,10 +734,10 @@ __global__ void __launch_bounds__(RunsCfg<HD>::THREADS, 1)
         __syncwarp();
         if (lane == 0) {
           // the warp's rows of the state are there; or read, and the flag as it was
-          if (sg.kind == SEG_FIRST) {
+          if (kind == SEG_FIRST) {
             __threadfence();
             atomicAdd(flags + sg.pair * 8 + rank * 4 + qw, 1);
-          } else if (sg.kind == SEG_SECOND && atomicAdd(flag, 1) == 2 * C::NG - 1) {
+          } else if (kind == SEG_SECOND && atomicAdd(flag, 1) == 2 * C::NG - 1) {
             atomicExch(flag, 0);
           }
         }
@@ -742,6 +745,8 @@ __global__ void __launch_bounds__(RunsCfg<HD>::THREADS, 1)
       }
       __syncwarp();
       if (lane == 0) mbar_arrive_pair_relaxed(o_free_at);
+      j0 += n;
+      f0 += 2 * n;
     }
   } else {
     if constexpr (C::NG > 1) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::LEAN_REGS));
