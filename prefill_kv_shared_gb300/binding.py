@@ -406,12 +406,26 @@ class AttnRuns:
 
     def _args(self, q, k, v, out):
         hq, hkv, hd = self.shape
-        f16, d, cells = _torch.float16, self.device, len(k)
+        rows, cells, d = len(q), len(k), self.device
+        f16, kv = _torch.float16, (cells, hkv, hd)
+        if not (q.dtype is f16 and k.dtype is f16 and v.dtype is f16 and out.dtype is _torch.bfloat16
+                and q.shape == (rows, hq, hd) and k.shape == kv and v.shape == kv and out.shape[1:] == (hq, hd)
+                and q.get_device() == d and k.get_device() == d and v.get_device() == d and out.get_device() == d
+                and q.is_contiguous() and k.is_contiguous() and v.is_contiguous() and out.is_contiguous()
+                and rows >= self.n_rows and len(out) >= self.n_rows):
+            self._refuse(q, k, v, out)
+        return (q.data_ptr(), k.data_ptr(), v.data_ptr(), cells, hq, hkv, hd, self.runs, self.n_runs), \
+               (out.data_ptr(), self.work.data_ptr(), self.work_bytes)
+
+    def _refuse(self, q, k, v, out):
+        """Say which buffer does not fit."""
+        hq, hkv, hd = self.shape
         if len(q) < self.n_rows or len(out) < self.n_rows:
             raise ValueError(f"q and out: the runs have {self.n_rows} rows")
-        return (_on_device(q, "q", f16, (len(q), hq, hd), d), _on_device(k, "k", f16, (cells, hkv, hd), d),
-                _on_device(v, "v", f16, (cells, hkv, hd), d), cells, hq, hkv, hd, self.runs, self.n_runs), \
-               (_on_device(out, "out", _torch.bfloat16, (len(out), hq, hd), d), self.work.data_ptr(), self.work_bytes)
+        _on_device(q, "q", _torch.float16, (len(q), hq, hd), self.device)
+        _on_device(k, "k", _torch.float16, (len(k), hkv, hd), self.device)
+        _on_device(v, "v", _torch.float16, (len(k), hkv, hd), self.device)
+        _on_device(out, "out", _torch.bfloat16, (len(out), hq, hd), self.device)
 
 
 def attention_packed(q, k, v, runs: AttnRuns, out, stream=None):

@@ -101,6 +101,13 @@ struct RunsCfg {
   static constexpr int TMEM_COLS = 512;
   static_assert(TMEM_O + NG * HD <= TMEM_COLS, "TMEM");
   static constexpr int THREADS = 128 + 128 * NG;
+  // Row (in the pair's 256) of row i of CTA `rank`.  At hd 64 the CTAs take
+  // 32-row groups in turn, so that an item of few rows loads the exponential
+  // units of both SMs.
+  static constexpr int Q_ROWS = HD == 256 ? 128 : 32;  // rows of a copy of Q
+  static __device__ __forceinline__ int row_of(int rank, int i) {
+    return HD == 256 ? rank * 128 + i : ((i >> 5) * 2 + rank) * 32 + (i & 31);
+  }
   // Registers (setmaxnreg, hd 64): a row thread holds its 128 scores.
   // 128 * 88 + 256 * 208 of the 384 * 168 that the block is launched with.
   static constexpr int LEAN_REGS = 88, ROW_REGS = 208;
@@ -534,7 +541,7 @@ __global__ void __launch_bounds__(RunsCfg<HD>::THREADS, 1)
     for (bool more = sg.next(); ok && more;) {
       const int n_rows = rt.n[sg.run], pos0 = rt.pos0[sg.run], row0 = rt.row0[sg.run];
       const int total_rows = n_rows << sh.log_g;
-      const int Rw = sg.R0 + rank * 128 + 32 * qw;  // the warp's first row
+      const int Rw = sg.R0 + C::row_of(rank, 32 * qw);  // the warp's first row
       const bool active = Rw < total_rows;          // warps without rows only keep step
       const int R = Rw + lane;
       const int t = R >> sh.log_g, head = (sg.kvh << sh.log_g) + (R & ((1 << sh.log_g) - 1));
@@ -804,8 +811,11 @@ __global__ void __launch_bounds__(RunsCfg<HD>::THREADS, 1)
           if (seg > 0) ok = mbar_wait(q_empty, (seg - 1) & 1, err, PF_DEV_TIMEOUT_PRODUCER);
           if (!ok) break;
           if (rank == 0) mbar_arrive_expect_tx(q_full, 2 * C::Q_BYTES);
-          tma_load_4d_pair(smem, &tmQ, map_to_rank(smem_u32(q_full), 0), 0, sg.kvh << sh.log_g,
-                           rt.row0[sg.run] + ((sg.R0 + rank * 128) >> sh.log_g), 0);
+          // the CTA's rows in one copy, or 32 by 32
+#pragma unroll
+          for (int i = 0; i < 128 / C::Q_ROWS; ++i)
+            tma_load_4d_pair(smem + i * C::Q_ROWS * 128, &tmQ, map_to_rank(smem_u32(q_full), 0), 0, sg.kvh << sh.log_g,
+                             rt.row0[sg.run] + ((sg.R0 + C::row_of(rank, i * C::Q_ROWS)) >> sh.log_g), 0);
         }
         if ((!ok || read_error(err) != 0) && rank == 0 && seg > 0) runs_drain(q_full, (seg - 1) & 1);
       }
@@ -1143,7 +1153,7 @@ static cudaError_t launch_runs(const RunsPlan& p, const __half* q, const __half*
   {
     const uint64_t dims[4] = {64, static_cast<uint64_t>(Hq), static_cast<uint64_t>(total), HD / 64};
     const uint64_t st[3] = {HD * 2, static_cast<uint64_t>(Hq) * HD * 2, 128};
-    const uint32_t box[4] = {64, static_cast<uint32_t>(G), static_cast<uint32_t>(128 / G), HD / 64};
+    const uint32_t box[4] = {64, static_cast<uint32_t>(G), static_cast<uint32_t>(C::Q_ROWS / G), HD / 64};
     if (!encode_fp16_sw128(&tq, q, 4, dims, st, box, &why)) return cudaErrorInvalidValue;
   }
   {
