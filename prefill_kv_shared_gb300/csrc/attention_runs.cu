@@ -88,6 +88,7 @@ template <int HD>
 struct RunsCfg {
   static constexpr int Q_BYTES = 128 * HD * 2;  // [64-dim box][128 rows][128 B]
   static constexpr int STAGE = 64 * HD * 2;     // half a chunk: K [box][64 keys][128 B], V [box][128 keys][hd/2 dims]
+  static constexpr int V_BOXES = HD == 256 ? 2 : 1;  // of a V half
   static constexpr int NST = HD == 256 ? 5 : 16;
   static constexpr int NG = HD == 256 ? 1 : 2;  // row warpgroups, taking chunks in turn
   static constexpr int NSB = NG + 1;            // S buffers
@@ -758,67 +759,76 @@ __global__ void __launch_bounds__(RunsCfg<HD>::THREADS, 1)
   } else {
     if constexpr (C::NG > 1) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::LEAN_REGS));
     if (warp == 1) {
-      // ---------------- K/V producer (each CTA its own halves)
-      if (lane == 0) {
-        bool ok = true;
-        uint32_t f = 0, tails = 0;
-        while (ok && sg.next()) {
-          const bool has_tail = tail_keys() < RCH;
-          auto load = [&](bool is_k, int jl) {
-            const int s = f % C::NST;
-            if (f >= C::NST) ok = ok && mbar_wait(&empty[s], (f / C::NST + 1) & 1, err, PF_DEV_TIMEOUT_PRODUCER);
-            if (!ok) return;
-            uint8_t* dst = smem + C::OFF_ST + s * C::STAGE;
-            const int cell = rt.cell0[sg.run] + (sg.ch0 + jl) * RCH;
-            const bool last = !is_k && has_tail && jl == sg.n - 1;
-            const uint32_t bar = map_to_rank(smem_u32(&full[s]), 0);
+      // ---------------- K/V producer (each CTA its own halves).  A stage comes
+      // as one copy per 64-dim box, a lane each: copies of one thread are
+      // served one after another, those of several overlap.
+      bool ok = true;
+      uint32_t f = 0, tails = 0;
+      while (ok && sg.next()) {
+        const bool has_tail = tail_keys() < RCH;
+        auto load = [&](bool is_k, int jl) {
+          const int s = f % C::NST;
+          if (f >= C::NST) ok = mbar_wait(&empty[s], (f / C::NST + 1) & 1, err, PF_DEV_TIMEOUT_PRODUCER);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) return;
+          uint8_t* dst = smem + C::OFF_ST + s * C::STAGE;
+          const int cell = rt.cell0[sg.run] + (sg.ch0 + jl) * RCH;
+          const bool last = !is_k && has_tail && jl == sg.n - 1;
+          const uint32_t bar = map_to_rank(smem_u32(&full[s]), 0);
+          if (lane == 0) {
             if (rank == 0) mbar_arrive_expect_tx(&full[s], last ? C::STAGE : 2 * C::STAGE);
-            if (is_k) {
-              tma_load_3d_pair(dst, &tmK, bar, sg.kvh * HD, cell + rank * 64, 0);
-            } else if (last && rank == 1) {
-              mbar_arrive_expect_tx(&full[s], C::STAGE);
-              tma_load_3d(dst, &tmV, &full[s], sg.kvh * HD + HD / 2, cell, 0);
-              tails ^= 1u << s;
-            } else {
-              tma_load_3d_pair(dst, &tmV, bar, sg.kvh * HD + rank * (HD / 2), cell, 0);
-            }
-            ++f;
-          };
-          for (int jl = -C::LA; jl < sg.n && ok; ++jl) {
-            if (jl + C::LA < sg.n) load(true, jl + C::LA);
-            if (jl >= 0) load(false, jl);
+            if (rank == 1 && last) mbar_arrive_expect_tx(&full[s], C::STAGE);
           }
+          __syncwarp();
+          if (is_k) {
+            if (lane < HD / 64)
+              tma_load_3d_pair(dst + lane * (64 * 128), &tmK, bar, sg.kvh * HD, cell + rank * 64, lane);
+          } else if (lane < C::V_BOXES) {
+            const int c0 = sg.kvh * HD + rank * (HD / 2);
+            if (last && rank == 1)
+              tma_load_3d(dst + lane * (C::STAGE / C::V_BOXES), &tmV, &full[s], c0, cell, lane);
+            else
+              tma_load_3d_pair(dst + lane * (C::STAGE / C::V_BOXES), &tmV, bar, c0, cell, lane);
+          }
+          if (last) tails ^= 1u << s;
+          ++f;
+        };
+        for (int jl = -C::LA; jl < sg.n && ok; ++jl) {
+          if (jl + C::LA < sg.n) load(true, jl + C::LA);
+          if (jl >= 0 && ok) load(false, jl);
         }
-        // On an error the copies in flight land before the pair may leave (the
-        // even CTA's barriers count those of both).
-        if (!ok || read_error(err) != 0) {
-          if (rank == 0) {
-            for (uint32_t x = f > C::NST ? f - C::NST : 0; x < f; ++x) runs_drain(&full[x % C::NST], (x / C::NST) & 1);
-          } else {
-            // a stage that never held such a copy is in phase 0, whose waiting
-            // for parity 1 ends at once
-            for (int x = 0; x < C::NST; ++x) runs_drain(&full[x], (tails >> x & 1u) ^ 1u);
-          }
+      }
+      // On an error the copies in flight land before the pair may leave (the
+      // even CTA's barriers count those of both).
+      if (lane == 0 && (!ok || read_error(err) != 0)) {
+        if (rank == 0) {
+          for (uint32_t x = f > C::NST ? f - C::NST : 0; x < f; ++x) runs_drain(&full[x % C::NST], (x / C::NST) & 1);
+        } else {
+          // a stage that never held such a copy is in phase 0, whose waiting
+          // for parity 1 ends at once
+          for (int x = 0; x < C::NST; ++x) runs_drain(&full[x], (tails >> x & 1u) ^ 1u);
         }
       }
       __syncwarp();
     } else if (warp == 2) {
-      // ---------------- Q producer
-      if (lane == 0) {
-        bool ok = true;
-        uint32_t seg = 0;
-        for (; ok && sg.next(); ++seg) {
-          if (seg > 0) ok = mbar_wait(q_empty, (seg - 1) & 1, err, PF_DEV_TIMEOUT_PRODUCER);
-          if (!ok) break;
-          if (rank == 0) mbar_arrive_expect_tx(q_full, 2 * C::Q_BYTES);
-          // the CTA's rows in one copy, or 32 by 32
-#pragma unroll
-          for (int i = 0; i < 128 / C::Q_ROWS; ++i)
-            tma_load_4d_pair(smem + i * C::Q_ROWS * 128, &tmQ, map_to_rank(smem_u32(q_full), 0), 0, sg.kvh << sh.log_g,
-                             rt.row0[sg.run] + ((sg.R0 + C::row_of(rank, i * C::Q_ROWS)) >> sh.log_g), 0);
+      // ---------------- Q producer: a copy per 64-dim box, or per 32 rows
+      bool ok = true;
+      uint32_t seg = 0;
+      for (; ok && sg.next(); ++seg) {
+        if (seg > 0) ok = mbar_wait(q_empty, (seg - 1) & 1, err, PF_DEV_TIMEOUT_PRODUCER);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        if (lane == 0 && rank == 0) mbar_arrive_expect_tx(q_full, 2 * C::Q_BYTES);
+        __syncwarp();
+        constexpr int GROUPS = 128 / C::Q_ROWS;
+        if (lane < GROUPS * (HD / 64)) {
+          const int box = lane / GROUPS, g = lane % GROUPS;
+          tma_load_4d_pair(smem + box * (128 * 128) + g * C::Q_ROWS * 128, &tmQ, map_to_rank(smem_u32(q_full), 0), 0,
+                           sg.kvh << sh.log_g,
+                           rt.row0[sg.run] + ((sg.R0 + C::row_of(rank, g * C::Q_ROWS)) >> sh.log_g), box);
         }
-        if ((!ok || read_error(err) != 0) && rank == 0 && seg > 0) runs_drain(q_full, (seg - 1) & 1);
       }
+      if (lane == 0 && (!ok || read_error(err) != 0) && rank == 0 && seg > 0) runs_drain(q_full, (seg - 1) & 1);
       __syncwarp();
     } else if (warp == 0 && rank == 1) {
       // ---------------- the odd CTA's half of the run's last V
@@ -1153,15 +1163,15 @@ static cudaError_t launch_runs(const RunsPlan& p, const __half* q, const __half*
   {
     const uint64_t dims[4] = {64, static_cast<uint64_t>(Hq), static_cast<uint64_t>(total), HD / 64};
     const uint64_t st[3] = {HD * 2, static_cast<uint64_t>(Hq) * HD * 2, 128};
-    const uint32_t box[4] = {64, static_cast<uint32_t>(G), static_cast<uint32_t>(C::Q_ROWS / G), HD / 64};
+    const uint32_t box[4] = {64, static_cast<uint32_t>(G), static_cast<uint32_t>(C::Q_ROWS / G), 1};
     if (!encode_fp16_sw128(&tq, q, 4, dims, st, box, &why)) return cudaErrorInvalidValue;
   }
   {
     const uint64_t dims[3] = {static_cast<uint64_t>(Hkv) * HD, static_cast<uint64_t>(n_cells), HD / 64};
     const uint64_t st[2] = {static_cast<uint64_t>(Hkv) * HD * 2, 128};
-    const uint32_t box[3] = {64, 64, HD / 64};
+    const uint32_t box[3] = {64, 64, 1};
     if (!encode_fp16_sw128(&tk, k, 3, dims, st, box, &why)) return cudaErrorInvalidValue;
-    const uint32_t vbox[3] = {HD == 256 ? 64u : 32u, RCH, HD == 256 ? 2u : 1u};
+    const uint32_t vbox[3] = {HD == 256 ? 64u : 32u, RCH, 1};
     if (!(HD == 256 ? encode_fp16_sw128(&tv, v, 3, dims, st, vbox, &why)
                     : encode_fp16_sw64(&tv, v, 3, dims, st, vbox, &why)))
       return cudaErrorInvalidValue;
