@@ -378,9 +378,11 @@ class AttnRuns:
     """The runs of an attention_packed / attention_tree call and the call's
     scratch: runs = [(n_rows, pos0, cell0), ...] (see pfop_attn_run), for
     n_head / n_head_kv heads of head_dim.  Kept by a program for as many
-    calls as have these runs; calls that use one AttnRuns share its scratch,
-    so they must not overlap on the GPU (one stream, or events between them;
-    graphs recorded with the same AttnRuns may not run at once)."""
+    calls as have these runs, and until the last of them is done; calls that
+    use one AttnRuns share its scratch, so they must not overlap on the GPU
+    (one stream, or events between them; graphs recorded with the same
+    AttnRuns may not run at once).  Made outside a recording it may be used on
+    any stream; made within one it belongs to that graph."""
 
     def __init__(self, runs, n_head: int, n_head_kv: int, head_dim: int, device=None):
         torch = _t()
@@ -397,14 +399,17 @@ class AttnRuns:
                 check_op(need)
             self.work = torch.empty(need, dtype=torch.uint8, device="cuda")
             self.work[:4096].zero_()
-        self.work_bytes = need
+            if not torch.cuda.is_current_stream_capturing():
+                torch.cuda.current_stream().synchronize()  # a call may come on any stream
+        self.work_at, self.work_bytes = self.work.data_ptr(), need
 
     def check(self, stream=None):
         """Wait for the stream (None: the current one) and raise if a call
         gave up a bounded wait."""
-        _call_on(self.device, stream, self._lib.pfop_attention_status, self.work.data_ptr())
+        _call_on(self.device, stream, self._lib.pfop_attention_status, self.work_at)
 
-    def _args(self, q, k, v, out):
+    def _fit(self, q, k, v, out):
+        """The number of cells; raises where a buffer does not fit."""
         hq, hkv, hd = self.shape
         rows, cells, d = len(q), len(k), self.device
         f16, kv = _torch.float16, (cells, hkv, hd)
@@ -414,8 +419,7 @@ class AttnRuns:
                 and q.is_contiguous() and k.is_contiguous() and v.is_contiguous() and out.is_contiguous()
                 and rows >= self.n_rows and len(out) >= self.n_rows):
             self._refuse(q, k, v, out)
-        return (q.data_ptr(), k.data_ptr(), v.data_ptr(), cells, hq, hkv, hd, self.runs, self.n_runs), \
-               (out.data_ptr(), self.work.data_ptr(), self.work_bytes)
+        return cells
 
     def _refuse(self, q, k, v, out):
         """Say which buffer does not fit."""
@@ -433,8 +437,9 @@ def attention_packed(q, k, v, runs: AttnRuns, out, stream=None):
     q [T, n_head, head_dim] and k, v [n_cells, n_head_kv, head_dim] float16,
     out [T, n_head, head_dim] bfloat16, all on the runs' device.  Enqueued on
     `stream` (None: the current torch stream)."""
-    a, b = runs._args(q, k, v, out)
-    _call_on(runs.device, stream, runs._lib.pfop_attention_packed, *a, *b)
+    cells = runs._fit(q, k, v, out)
+    _call_on(runs.device, stream, runs._lib.pfop_attention_packed, q.data_ptr(), k.data_ptr(), v.data_ptr(), cells,
+             *runs.shape, runs.runs, runs.n_runs, out.data_ptr(), runs.work_at, runs.work_bytes)
 
 
 def attention_tree(q, k, v, runs: AttnRuns, mask, out, stream=None):
@@ -443,10 +448,11 @@ def attention_tree(q, k, v, runs: AttnRuns, mask, out, stream=None):
     set where the row sees drafted token j of its run."""
     if mask.dim() != 2 or len(mask) < runs.n_rows:
         raise ValueError(f"mask: needs [{runs.n_rows}, words]")
-    a, b = runs._args(q, k, v, out)
+    cells = runs._fit(q, k, v, out)
     words = mask.shape[1]
     m = _on_device(mask, "mask", _torch.int64, (len(mask), words), runs.device)
-    _call_on(runs.device, stream, runs._lib.pfop_attention_tree, *a, m, words, *b)
+    _call_on(runs.device, stream, runs._lib.pfop_attention_tree, q.data_ptr(), k.data_ptr(), v.data_ptr(), cells,
+             *runs.shape, runs.runs, runs.n_runs, m, words, out.data_ptr(), runs.work_at, runs.work_bytes)
 
 
 def logprobs(logits, tokens=None, logp=None, entropy=None, top_id=None, top_logp=None, stream=None):

@@ -358,6 +358,49 @@ def test_two_streams_at_once():
         _check(heads, runs, q, k, v, out)
 
 
+@pytest.mark.parametrize("heads", [(8, 1, 256), (32, 4, 64)])
+def test_runs_made_on_one_stream_used_on_another(heads):
+    """A scratch that is made behind long work of one stream, in memory that
+    held other values, is ready for a call on another stream."""
+    runs, cells = _layout([40, 300, 7], [2500, 100, 9000])
+    q, k, v, out = _inputs(heads, runs, cells, 59)
+    marked = torch.full((64 << 20,), 255, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    del marked  # the next allocations get its memory
+    torch.cuda._sleep(20_000_000)
+    plan = binding.AttnRuns(runs, *heads)
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        binding.attention_packed(q, k, v, plan, out)
+    plan.check(side)
+    _check(heads, runs, q, k, v, out)
+
+
+@pytest.mark.parametrize("heads", [(8, 1, 256), (32, 4, 64)])
+def test_one_scratch_for_changing_runs(heads):
+    """Calls one after another in one scratch, their items whole, cut in two
+    and cut in many."""
+    sizes = [([3, 3], [10, 20]), ([70, 90, 33, 200], [1500, 800, 3000, 0]), ([20], [20000]),
+             ([64, 1, 128], [600, 6000, 0])]
+    jobs = []
+    for i, (rows, past) in enumerate(sizes):
+        runs, cells = _layout(rows, past)
+        q, k, v, out = _inputs(heads, runs, cells, 61 + i)
+        mask_np = _random_tree(runs, 4, i)
+        jobs.append((runs, q, k, v, out, out.clone(), binding.AttnRuns(runs, *heads), mask_np,
+                     torch.from_numpy(mask_np.view(np.int64)).cuda()))
+    big = max((j[6] for j in jobs), key=lambda p: p.work_bytes)
+    for _ in range(3):
+        for runs, q, k, v, out, out2, plan, _, mask in jobs:
+            plan.work, plan.work_at, plan.work_bytes = big.work, big.work_at, big.work_bytes
+            binding.attention_packed(q, k, v, plan, out)
+            binding.attention_tree(q, k, v, plan, mask, out2)
+    big.check()
+    for runs, q, k, v, out, out2, _, mask_np, _ in jobs:
+        _check(heads, runs, q, k, v, out)
+        _check(heads, runs, q, k, v, out2, mask_np)
+
+
 def test_wrappers_refuse_what_does_not_fit():
     heads = (8, 2, 64)
     runs = [(4, 10, 0)]
