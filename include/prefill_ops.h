@@ -230,7 +230,8 @@ typedef struct pfop_attn_run {
    (rows from T on are not touched).  Row i of a run sees its sequence's
    positions 0 .. pos0 + i.  Cells of no run's positions 0 .. pos0 + n_rows
    - 1 are never used, whatever they hold; the runs' own cells must hold
-   finite values.  Probabilities are rounded to fp16 before P V, sums and
+   finite values (an infinity or NaN in V reaches the rows of its run that do
+   not see it too, but no other run's).  Probabilities are rounded to fp16 before P V, sums and
    states are fp32.  A row's bits depend on its position, its keys and the
    shapes of the call's runs, not on the other runs' values; a repeated call
    gives the same bits.
@@ -265,8 +266,9 @@ int pfop_attention_tree(const void* q_dev, const void* k_dev, const void* v_dev,
 int64_t pfop_attention_work_bytes(int32_t Hq, int32_t Hkv, int32_t hd, const pfop_attn_run* runs, int32_t n_runs);
 
 /* Wait for `stream` and report whether a call using this scratch gave up a
-   bounded wait (PF_E_DEVICE_TIMEOUT: its results are invalid); clears the
-   report. */
+   bounded wait (PF_E_DEVICE_TIMEOUT: the results of that call and of those
+   after it are invalid).  Then it makes the scratch as good as new; until it
+   is called the scratch must not be used for further results. */
 int pfop_attention_status(void* work_dev, void* stream);
 
 /* Log probabilities over a vocabulary, for every row of logits [rows][ld]

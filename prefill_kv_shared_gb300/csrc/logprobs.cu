@@ -419,7 +419,7 @@ __global__ void __launch_bounds__(LP_THREADS, SM ? LP_CTAS_PER_SM : 2) logprobs_
     const int tail = sl.head + sl.nvec * LpVec<T>::N;
     if (tid < sl.head) d[tid] = x[id0 + tid];
     if (tid < len - tail) d[tail + tid] = x[id0 + tail + tid];
-    // a copy that never lands (the bounded wait gives up) leaves the row marked
+    // a copy that never lands (the bounded wait gives up) makes the row one without a distribution
     if (warp == 0) landed = mbar_wait(&sh.landed, 0, nullptr, PF_DEV_TIMEOUT_PRODUCER);
     landed = __syncthreads_and(landed);
   } else {
@@ -434,7 +434,10 @@ __global__ void __launch_bounds__(LP_THREADS, SM ? LP_CTAS_PER_SM : 2) logprobs_
     if (tok >= 0 && tok < a.vocab) x_tok = LpVec<T>::one(x + tok);
   }
   LpSums q;
-  if (landed) sl.sums(q);
+  if (landed)
+    sl.sums(q);
+  else
+    q.s = __int_as_float(0x7fc00000);
   const float own = q.m;
   // the warp's sums, and the maxima of the 32 groups of threads
   {
