@@ -5,23 +5,31 @@
 // vocabulary: log p[v] = (x[v] - m) - log s and entropy = log s - ln 2 h / s.
 // One pass over the row: a thread keeps its own m, s, h (when m moves by d:
 // s <- 2^-d s, h <- 2^-d (h - d s)), joined over the block and the cluster.
-// t is held at -200 or above, so that a masked logit (-inf, or the type's
-// lowest value) adds 2^t t = 0 and not 0 * inf; a NaN stays a NaN and marks
-// the row as one without a distribution.
+// A masked logit (-inf, or the type's lowest value) has to add 2^t t = 0 and
+// not 0 * inf: once a thread has met one it holds t at -200 or above.  A NaN
+// stays a NaN and marks the row as one without a distribution.
 //
 // The alternatives need no second look at the whole row: the n-th largest of
 // the maxima of 32 groups of threads is not above the n-th largest value, so
-// only threads whose own maximum reaches it go over their logits again and
-// list those that do: a few dozen of a row as a rule, whose ranks are then
-// counted.  Where the list overflows (many equal values, as in a row that is
+// only what reaches it is listed, a few dozen logits as a rule, whose ranks
+// are then counted.  A thread keeps where its largest step of 16 logits began
+// and the next largest step's maximum: mostly that one step is all that has
+// to be read again.  (Reading all of such a thread's logits again took 127 us
+// instead of 109 for 3000 rows of 50257 fp32 logits, which have left L2 by
+// then.)  Where the list overflows (many equal values, as in a row that is
 // mostly masked) a radix select finds the n-th value and the lowest ids at it.
 //
 // A CTA takes a row, or a cluster of up to 8 a slice each (rank 0 joins their
-// sums and lists through distributed shared memory).  A slice of up to 64 KB
-// is brought into shared memory by one bulk copy, which keeps the HBM busy
-// with no registers held and makes the second look cheap; longer slices are
-// read through registers, and again from L2.  Bound by the row's bytes for
-// many rows, by latency for few.
+// sums and lists through distributed shared memory).  The logits come in bulk
+// copies of 2 KB, two on their way for every warp: no registers are held and
+// no warp waits for another until the row's end.  (Whole 64 KB slices in
+// shared memory, three to an SM, left too few rows in flight: 512 rows of
+// 32768 fp32 logits 21.7 us, now 14.4.)
+//
+// Bound by the row's bytes for many rows, and by what a CTA does once a row
+// (launch, first copy, joins, ranks: about 4 us), by latency for few.  32768
+// logits, 5 or 8 alternatives: 1 row fp32 4.5 us; 512 rows fp32 14.4 us, 4.7
+// TB/s; 4096 rows bf16 56 us, 4.8 TB/s (59 with three in ten masked).
 #include "../../include/prefill_ops.h"
 #include "common.cuh"
 #include "kernels.h"
@@ -30,21 +38,21 @@
 
 namespace pf {
 
-constexpr int LP_THREADS = 256;
-constexpr int LP_WARPS = LP_THREADS / 32;
 constexpr int LP_TOP_MAX = 32;
-constexpr int LP_GROUP = LP_THREADS / 32;  // threads of a group
-constexpr int LP_CAND = 512;               // listed candidates
+constexpr int LP_CAND = 256;  // listed candidates
 constexpr int LP_CLUSTER_MAX = 8;
-constexpr int LP_SMEM_SLICE = 65536;       // bytes of a slice held in shared memory
-constexpr int LP_CTAS_PER_SM = 3;          // by 64 KB slices
+constexpr int LP_CHUNK_VECS = 128;  // 16-byte vectors of a warp's copy
+constexpr int LP_STAGES = 2;        // copies a warp has on their way
+// W: warps of a CTA
+constexpr int lp_ring_bytes(int w) { return w * LP_STAGES * LP_CHUNK_VECS * 16; }
+constexpr int lp_ctas_per_sm(int w) { return 32 / w; }
 constexpr float LP_LOG2E = 1.4426950408889634f, LP_LN2 = 0.6931471805599453f;
-static_assert(LP_TOP_MAX <= 32 && LP_GROUP <= 32, "a lane per group");
+static_assert(LP_TOP_MAX <= 32 && LP_CLUSTER_MAX * LP_TOP_MAX <= LP_CAND, "a lane per alternative, a list for a cluster's");
 
 struct LogprobArgs {
   const void* logits;
   int64_t ld;
-  int vocab, slice;  // slice: logits per CTA of a cluster, a multiple of 8
+  int rows, vocab, slice;  // slice: logits per CTA of a cluster, a multiple of 8
   const int* tok;
   int n_top;
   float *logp, *entropy;
@@ -101,6 +109,22 @@ __device__ __forceinline__ unsigned long long lp_key(uint32_t order, int id) {
   return (static_cast<unsigned long long>(order) << 32) | (0xffffffffu - static_cast<uint32_t>(id));
 }
 
+__device__ __forceinline__ uint64_t lp_pack(float a, float b) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
+  return d;
+}
+__device__ __forceinline__ float2 lp_unpack(uint64_t v) {
+  float2 f;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
+  return f;
+}
+__device__ __forceinline__ float lp_max3(float a, float b, float c) {
+  float y;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
+
 // running maximum and sums
 struct LpSums {
   float m = -INFINITY, s = 0.f, h = 0.f;
@@ -113,8 +137,45 @@ struct LpSums {
     s = w == 0.f || m == -INFINITY ? z : w * s;
     m = to;
   }
-  __device__ __forceinline__ void raise(float to) {
-    if (to > m) rebase(to);
+  // one more logit
+  __device__ __forceinline__ void take(float x) {
+    if (x > m) rebase(x);
+    // x - m first: m log2 e alone may overflow
+    const float t = lp_max_nan((x - (m == -INFINITY ? 0.f : m)) * LP_LOG2E, -200.f), w = lp_ex2(t);
+    s += w;
+    h = __fmaf_rn(w, t, h);
+  }
+  // CNT more, none above m.  HOLD false: without holding t at -200, a fifth
+  // of the work of the ALU pipe; where h then comes out as a NaN (2^t t =
+  // 0 * -inf) they are not added and the answer is false.
+  template <int CNT, bool HOLD>
+  __device__ __forceinline__ bool add(const float* e) {
+    const float at = m == -INFINITY ? 0.f : m;
+    // two logits an instruction
+    const uint64_t nm = lp_pack(-at, -at), c = lp_pack(LP_LOG2E, LP_LOG2E);
+    uint64_t s2[2] = {0ull, 0ull}, h2[2] = {0ull, 0ull};
+#pragma unroll
+    for (int i = 0; i < CNT; i += 2) {
+      uint64_t d = lp_pack(e[i], e[i + 1]);
+      asm("add.rn.f32x2 %0, %0, %1;" : "+l"(d) : "l"(nm));
+      asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(d) : "l"(c));
+      float2 t = lp_unpack(d);
+      if (HOLD) {
+        t.x = lp_max_nan(t.x, -200.f);
+        t.y = lp_max_nan(t.y, -200.f);
+        d = lp_pack(t.x, t.y);
+      }
+      const uint64_t w = lp_pack(lp_ex2(t.x), lp_ex2(t.y));
+      const int q = (i >> 1) & 1;
+      asm("add.rn.f32x2 %0, %0, %1;" : "+l"(s2[q]) : "l"(w));
+      asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(h2[q]) : "l"(w), "l"(d));
+    }
+    const float2 s0 = lp_unpack(s2[0]), s1 = lp_unpack(s2[1]), h0 = lp_unpack(h2[0]), h1 = lp_unpack(h2[1]);
+    const float ho = (h0.x + h0.y) + (h1.x + h1.y);
+    if (!HOLD && ho != ho) return false;
+    s += (s0.x + s0.y) + (s1.x + s1.y);
+    h += ho;
+    return true;
   }
   // over the warp, the same in every lane
   __device__ __forceinline__ void join() {
@@ -130,178 +191,194 @@ struct LpSums {
   }
 };
 
-__device__ __forceinline__ uint64_t lp_pack(float a, float b) {
-  uint64_t d;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
-  return d;
-}
-__device__ __forceinline__ float2 lp_unpack(uint64_t v) {
-  float2 f;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
-  return f;
-}
-
-// A thread's logits of the slice x[0 .. n) (SM: in shared memory, else in
-// global): vectors tid, tid + LP_THREADS, .. of the 16-byte aligned middle
-// and one logit of each ragged end.
-template <class T, bool SM>
+// A CTA's logits x[0 .. n): one a thread at each ragged end, and between them
+// 16-byte aligned vectors, LP_CHUNK bytes of them at a time to a warp, the
+// warps in turn.
+template <class T, int W>
 struct LpSlice {
   static constexpr int VN = LpVec<T>::N;
-  static constexpr int BATCH = 4;  // vectors taken at once
+  static constexpr int TAKE = 16 / VN;  // vectors of a step: 16 logits
   const T* x;
   int n, head, nvec;
-  __device__ LpSlice(const T* p, int len, int mis) : x(p), n(len) {
+  __device__ LpSlice(const T* p, int len) : x(p), n(len) {
+    const int mis = static_cast<int>((reinterpret_cast<uintptr_t>(p) & 15) / sizeof(T));
     head = min(len, mis ? VN - mis : 0);
     nvec = (len - head) / VN;
   }
-  __device__ __forceinline__ uint4 vec(int v) const {
-    const uint4* p = reinterpret_cast<const uint4*>(x + head) + v;
-    return SM ? *p : __ldcg(p);
-  }
-  // f(value, id in the slice) for the logits of at least tau among those of
-  // thread t, its vectors dealt out over the warp
+  __device__ __forceinline__ const uint4* vecs() const { return reinterpret_cast<const uint4*>(x + head); }
+  __device__ __forceinline__ int chunks() const { return (nvec + LP_CHUNK_VECS - 1) / LP_CHUNK_VECS; }
+  // f(value, id in the slice) for the logits of vector v that are at least tau
   template <class F>
-  __device__ __forceinline__ void from(int t, float tau, F&& f) const {
-    const int lane = threadIdx.x & 31;
+  __device__ __forceinline__ void look(int v, float tau, F&& f) const {
+    if (v >= nvec) return;
+    float e[VN];
+    LpVec<T>::get(__ldcg(vecs() + v), e);
+    float mx = e[0];
+#pragma unroll
+    for (int i = 1; i < VN; ++i) mx = fmaxf(mx, e[i]);
+    if (mx < tau) return;
+#pragma unroll
+    for (int i = 0; i < VN; ++i)
+      if (e[i] >= tau) f(e[i], head + v * VN + i);
+  }
+  // The logits of at least tau: of the steps that begin at vectors
+  // few[0 .. n_few), and all of the threads many[0 .. n_many)'s
+  template <class F>
+  __device__ __forceinline__ void from(const int* few, int n_few, const int* many, int n_many, float tau, F&& f) const {
+    constexpr int PER = LP_CHUNK_VECS / 32;  // a thread's vectors of a chunk
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int steps = n_few * TAKE;
+    // vectors dealt out over the CTA, then those of a thread over a warp
+    const int per_thread = PER * ((chunks() + W - 1) / W);
+    int i = threadIdx.x, q = warp, k = lane;
+#pragma unroll 1
+    for (;;) {  // (one copy of the code: what is run once a row costs its fetching)
+      int v;
+      if (i < steps) {
+        v = few[i / TAKE] + 32 * (i % TAKE);
+        i += (32 * W);
+      } else if (q < n_many) {
+        const int t = many[q];
+        v = k < per_thread ? ((t >> 5) + W * (k / PER)) * LP_CHUNK_VECS + (k % PER) * 32 + (t & 31) : nvec;
+        k += 32;
+        if (k >= per_thread) k = lane, q += W;
+      } else {
+        break;
+      }
+      look(v, tau, f);
+    }
+    const int t = threadIdx.x, tail = head + nvec * VN;
     auto one = [&](float v, int i) {
       if (v >= tau) f(v, i);
     };
-    for (int v = t + lane * LP_THREADS; v < nvec; v += 32 * LP_THREADS) {
-      float e[VN];
-      LpVec<T>::get(vec(v), e);
-      float mx = e[0];
-#pragma unroll
-      for (int i = 1; i < VN; ++i) mx = fmaxf(mx, e[i]);
-      if (mx >= tau) {
-#pragma unroll
-        for (int i = 0; i < VN; ++i) one(e[i], head + v * VN + i);
-      }
-    }
-    const int tail = head + nvec * VN;
-    if (lane == 0 && t < head) one(LpVec<T>::one(x + t), t);
-    if (lane == 0 && t < n - tail) one(LpVec<T>::one(x + tail + t), tail + t);
+    if (t < head) one(LpVec<T>::one(x + t), t);
+    if (t < n - tail) one(LpVec<T>::one(x + tail + t), tail + t);
   }
   // f(value, id in the slice) for all of them
   template <class F>
   __device__ __forceinline__ void each(F&& f) const {
+    constexpr int BATCH = 4;  // vectors in flight
     const int t = threadIdx.x;
     if (t < head) f(LpVec<T>::one(x + t), t);
-    int v = t;
-    for (; v < nvec; v += BATCH * LP_THREADS) {
+    for (int v = t; v < nvec; v += BATCH * (32 * W)) {
       uint4 r[BATCH];
 #pragma unroll
-      for (int b = 0; b < BATCH; ++b) r[b] = v + b * LP_THREADS < nvec ? vec(v + b * LP_THREADS) : make_uint4(0, 0, 0, 0);
+      for (int b = 0; b < BATCH; ++b)
+        r[b] = v + b * (32 * W) < nvec ? __ldcg(vecs() + v + b * (32 * W)) : make_uint4(0, 0, 0, 0);
 #pragma unroll
       for (int b = 0; b < BATCH; ++b) {
-        if (v + b * LP_THREADS >= nvec) break;
+        if (v + b * (32 * W) >= nvec) break;
         float e[VN];
         LpVec<T>::get(r[b], e);
 #pragma unroll
-        for (int i = 0; i < VN; ++i) f(e[i], head + (v + b * LP_THREADS) * VN + i);
+        for (int i = 0; i < VN; ++i) f(e[i], head + (v + b * (32 * W)) * VN + i);
       }
     }
     const int tail = head + nvec * VN;
     if (t < n - tail) f(LpVec<T>::one(x + tail + t), tail + t);
   }
-  template <int CNT>
-  static __device__ __forceinline__ void add(LpSums& a, const float* e) {
-    float mx = e[0];
-#pragma unroll
-    for (int i = 1; i < CNT; ++i) mx = fmaxf(mx, e[i]);
-    a.raise(mx);
-    // x - m first: m log2 e alone may overflow
-    const float m = a.m == -INFINITY ? 0.f : a.m;
-    if constexpr (CNT == 1) {
-      const float t = lp_max_nan((e[0] - m) * LP_LOG2E, -200.f), w = lp_ex2(t);
-      a.s += w;
-      a.h = __fmaf_rn(w, t, a.h);
-    } else {
-      // two logits an instruction
-      const uint64_t nm = lp_pack(-m, -m), c = lp_pack(LP_LOG2E, LP_LOG2E);
-      uint64_t s[2] = {0ull, 0ull}, h[2] = {0ull, 0ull};
-#pragma unroll
-      for (int i = 0; i < CNT; i += 2) {
-        uint64_t d = lp_pack(e[i], e[i + 1]);
-        asm("add.rn.f32x2 %0, %0, %1;" : "+l"(d) : "l"(nm));
-        asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(d) : "l"(c));
-        float2 t = lp_unpack(d);
-        t.x = lp_max_nan(t.x, -200.f);
-        t.y = lp_max_nan(t.y, -200.f);
-        const uint64_t w = lp_pack(lp_ex2(t.x), lp_ex2(t.y)), tt = lp_pack(t.x, t.y);
-        const int q = (i >> 1) & 1;
-        asm("add.rn.f32x2 %0, %0, %1;" : "+l"(s[q]) : "l"(w));
-        asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(h[q]) : "l"(w), "l"(tt));
-      }
-      const float2 s0 = lp_unpack(s[0]), s1 = lp_unpack(s[1]), h0 = lp_unpack(h[0]), h1 = lp_unpack(h[1]);
-      a.s += (s0.x + s0.y) + (s1.x + s1.y);
-      a.h += (h0.x + h0.y) + (h1.x + h1.y);
-    }
-  }
-  __device__ __forceinline__ void sums(LpSums& a) const {
-    const int t = threadIdx.x;
-    int v = t;
-    if constexpr (SM) {
-      for (; v + (BATCH - 1) * LP_THREADS < nvec; v += BATCH * LP_THREADS) {
-        float e[BATCH * VN];
-#pragma unroll
-        for (int b = 0; b < BATCH; ++b) LpVec<T>::get(vec(v + b * LP_THREADS), e + b * VN);
-        add<BATCH * VN>(a, e);
-      }
-    } else if (v + (BATCH - 1) * LP_THREADS < nvec) {
-      // the next batch is on its way while this one is taken
-      uint4 r[BATCH];
-#pragma unroll
-      for (int b = 0; b < BATCH; ++b) r[b] = vec(v + b * LP_THREADS);
-      for (;;) {
-        const int w = v + BATCH * LP_THREADS;
-        const bool more = w + (BATCH - 1) * LP_THREADS < nvec;
-        float e[BATCH * VN];
-#pragma unroll
-        for (int b = 0; b < BATCH; ++b) LpVec<T>::get(r[b], e + b * VN);
-        if (more) {
-#pragma unroll
-          for (int b = 0; b < BATCH; ++b) r[b] = vec(w + b * LP_THREADS);
-        }
-        add<BATCH * VN>(a, e);
-        v = w;
-        if (!more) break;
-      }
-    }
-    for (; v < nvec; v += LP_THREADS) {
-      float e[VN];
-      LpVec<T>::get(vec(v), e);
-      add<VN>(a, e);
-    }
+  // Sums of the thread's logits.  The warp's chunks pass through its LP_STAGES
+  // places of shared memory, a barrier each; lane 0 keeps the copies of the
+  // next ones on their way.  best: first vector of the step with the largest
+  // logit (nvec: none); no other step has one above m2.  False: a copy did
+  // not land in time.
+  __device__ __forceinline__ bool sums(LpSums& a, int& best, float& m2, uint4* ring, uint64_t* landed) const {
+    const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
+    const int cnt = warp < chunks() ? (chunks() - warp + W - 1) / W : 0;
     const int tail = head + nvec * VN;
-    if (t < head) {
-      const float e = LpVec<T>::one(x + t);
-      add<1>(a, &e);
+    auto copy = [&](int i) {
+      const int v0 = (warp + i * W) * LP_CHUNK_VECS;
+      const uint32_t bytes = static_cast<uint32_t>(min(LP_CHUNK_VECS, nvec - v0)) * 16u;
+      uint64_t* bar = landed + i % LP_STAGES;
+      mbar_arrive_expect_tx(bar, bytes);
+      bulk_load(ring + i % LP_STAGES * LP_CHUNK_VECS, vecs() + v0, bytes, bar);
+    };
+    if (lane == 0)
+      for (int i = 0; i < LP_STAGES && i < cnt; ++i) copy(i);
+    bool low = false;  // a logit far below the others, or a NaN, has been met
+    if (t < head) a.take(LpVec<T>::one(x + t));
+    if (t < n - tail) a.take(LpVec<T>::one(x + tail + t));
+    auto wait = [&](int i) {
+      const bool in = mbar_wait(landed + i % LP_STAGES, i / LP_STAGES & 1, nullptr, PF_DEV_TIMEOUT_PRODUCER);
+      return __all_sync(0xffffffffu, in) != 0;
+    };
+#pragma unroll 1
+    for (int i = 0; i < cnt; ++i) {
+      if (!wait(i)) {
+        for (int j = i + 1; j < min(i + LP_STAGES, cnt); ++j) wait(j);  // copies on their way
+        return false;
+      }
+      const int v0 = (warp + i * W) * LP_CHUNK_VECS;
+      const uint4* c = ring + i % LP_STAGES * LP_CHUNK_VECS + lane;
+      auto raise = [&](float mx, int v) {
+        if (mx > a.m) {
+          m2 = a.m;
+          a.rebase(mx);
+          best = v;
+        } else {
+          m2 = fmaxf(m2, mx);
+        }
+      };
+      if (v0 + LP_CHUNK_VECS <= nvec) {
+        static_assert(LP_CHUNK_VECS % (32 * TAKE) == 0, "a chunk is a number of whole steps");
+#pragma unroll 1
+        for (int b = 0; b < LP_CHUNK_VECS / 32; b += TAKE) {
+          float e[16];
+#pragma unroll
+          for (int k = 0; k < TAKE; ++k) LpVec<T>::get(c[32 * (b + k)], e + k * VN);
+          float mx = fmaxf(e[0], e[1]);
+#pragma unroll
+          for (int k = 2; k < 16; k += 2) mx = lp_max3(mx, e[k], e[k + 1]);
+          raise(mx, v0 + 32 * b + lane);
+          if (low || !a.template add<16, false>(e)) {
+            low = true;
+            a.template add<16, true>(e);
+          }
+        }
+      } else {
+#pragma unroll 1
+        for (int b = 0; v0 + 32 * b + lane < nvec; ++b) {
+          float e[VN];
+          LpVec<T>::get(c[32 * b], e);
+          float mx = fmaxf(e[0], e[1]);
+#pragma unroll
+          for (int k = 2; k < VN; k += 2) mx = lp_max3(mx, e[k], e[k + 1]);
+          raise(mx, v0 + 32 * (b - b % TAKE) + lane);
+          a.template add<VN, true>(e);
+        }
+      }
+      __syncwarp();  // the place has been read
+      if (lane == 0 && i + LP_STAGES < cnt) copy(i + LP_STAGES);
     }
-    if (t < n - tail) {
-      const float e = LpVec<T>::one(x + tail + t);
-      add<1>(a, &e);
-    }
+    return true;
   }
 };
 
+template <int W>
 struct LpShared {
-  unsigned long long top[LP_TOP_MAX];                   // the CTA's best, in order
-  unsigned long long all[LP_CLUSTER_MAX * LP_TOP_MAX];  // rank 0: the cluster's
-  unsigned long long cand[LP_CAND];
-  float4 sums[LP_CLUSTER_MAX];  // rank 0: m, s, h of each CTA
-  float m[LP_WARPS], s[LP_WARPS], h[LP_WARPS];
+  unsigned long long top[LP_TOP_MAX];  // the CTA's best, in order
+  union {
+    unsigned long long cand[LP_CAND];
+    int hist[256];
+  };
+  float m[W], s[W], h[W];
   float group[32];
-  int hist[256];
   float tau;
-  int queue[LP_THREADS];  // threads that reach tau
-  int queued, count, prefix, left, warp_count[LP_WARPS];
-  uint64_t landed;  // barrier of the slice's copy
+  int queue[(32 * W)];  // steps that reach tau from its start, threads from its end
+  int n_few, n_many, count, prefix, left, warp_count[W];
+  uint64_t landed[W * LP_STAGES];  // barriers of the copies
+};
+// rank 0 of a cluster: what the CTAs bring, behind the ring
+struct LpCluster {
+  unsigned long long top[LP_CLUSTER_MAX * LP_TOP_MAX];
+  float4 sums[LP_CLUSTER_MAX];  // m, s, h
 };
 
 // The n best of sh.cand[0 .. cnt) (all different) into dst, in order: a
 // candidate's rank is the number of larger ones.
+template <int W>
 __device__ __forceinline__ void lp_rank(const unsigned long long* cand, int cnt, int n, unsigned long long* dst) {
-  for (int i = threadIdx.x; i < cnt; i += LP_THREADS) {
+  for (int i = threadIdx.x; i < cnt; i += (32 * W)) {
     const unsigned long long k = cand[i];
     int r = 0;
 #pragma unroll 8
@@ -313,13 +390,13 @@ __device__ __forceinline__ void lp_rank(const unsigned long long* cand, int cnt,
 // The n best of a slice with too many candidates for the list: the n-th
 // largest value by four passes over 8 bits of its order each, the larger
 // ones, and the lowest ids at that value.
-template <class T, bool SM>
-__device__ __noinline__ void lp_select(const LpSlice<T, SM>& sl, int id0, int n, LpShared& sh) {
+template <class T, int W>
+__device__ __noinline__ void lp_select(const LpSlice<T, W>& sl, int id0, int n, LpShared<W>& sh) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   uint32_t prefix = 0;
   int left = n;  // of the values with this prefix
   for (int shift = 24; shift >= 0; shift -= 8) {
-    for (int i = tid; i < 256; i += LP_THREADS) sh.hist[i] = 0;
+    for (int i = tid; i < 256; i += (32 * W)) sh.hist[i] = 0;
     __syncthreads();
     sl.each([&](float v, int) {
       const uint32_t o = lp_order(v);
@@ -365,14 +442,14 @@ __device__ __noinline__ void lp_select(const LpSlice<T, SM>& sl, int id0, int n,
   __syncthreads();
   const int larger = sh.count;  // n - left
   int found = 0;
-  for (int base = 0; base < sl.n && found < left; base += LP_THREADS) {
+  for (int base = 0; base < sl.n && found < left; base += (32 * W)) {
     const int i = base + tid;
     const bool eq = i < sl.n && lp_order(LpVec<T>::one(sl.x + i)) == prefix;
     const unsigned b = __ballot_sync(0xffffffffu, eq);
     if (lane == 0) sh.warp_count[warp] = __popc(b);
     __syncthreads();
     int at = found, total = found;
-    for (int w = 0; w < LP_WARPS; ++w) {
+    for (int w = 0; w < W; ++w) {
       if (w < warp) at += sh.warp_count[w];
       total += sh.warp_count[w];
     }
@@ -381,50 +458,29 @@ __device__ __noinline__ void lp_select(const LpSlice<T, SM>& sl, int id0, int n,
     found = total;
     __syncthreads();
   }
-  lp_rank(sh.cand, n, n, sh.top);
+  lp_rank<W>(sh.cand, n, n, sh.top);
 }
 
-template <class T, bool SM>
-__global__ void __launch_bounds__(LP_THREADS, SM ? LP_CTAS_PER_SM : 2) logprobs_kernel(const LogprobArgs a, int cluster) {
-  __shared__ LpShared sh;
+template <class T, int W>
+__global__ void __launch_bounds__(32 * W, lp_ctas_per_sm(W)) logprobs_kernel(const LogprobArgs a, int cluster) {
+  __shared__ LpShared<W> sh;
+  extern __shared__ __align__(16) uint4 lp_ring[];
+  LpCluster& all = *reinterpret_cast<LpCluster*>(lp_ring + lp_ring_bytes(W) / 16);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int r = static_cast<int>(blockIdx.x) / cluster, rank = static_cast<int>(blockIdx.x) % cluster;
   const T* x = static_cast<const T*>(a.logits) + static_cast<int64_t>(r) * a.ld;
   const int id0 = rank * a.slice;
-  const int len = min(a.vocab - id0, a.slice);
-  const int mis = static_cast<int>((reinterpret_cast<uintptr_t>(x + id0) & 15) / sizeof(T));
-  extern __shared__ __align__(16) uint8_t lp_slice[];
-  // the copy keeps the logits' alignment
-  const LpSlice<T, SM> sl(SM ? reinterpret_cast<const T*>(lp_slice) + mis : x + id0, len, mis);
-  pdl_launch();
+  const LpSlice<T, W> sl(x + id0, min(a.vocab - id0, a.slice));
   // no CTA writes into another before that one runs: arrive now, wait there
   if (cluster > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
-  if (tid == 0) {
-    sh.count = sh.queued = 0;
-    if (SM) {
-      mbar_init(&sh.landed, 1);
-      fence_mbar_init();
-    }
+  if (tid == 0) sh.count = sh.n_few = sh.n_many = 0;
+  uint64_t* landed = &sh.landed[warp * LP_STAGES];
+  if (lane == 0) {
+    for (int i = 0; i < LP_STAGES; ++i) mbar_init(&landed[i], 1);
+    fence_mbar_init();
   }
-  bool landed = true;
-  if constexpr (SM) {
-    __syncthreads();
-    pdl_wait();
-    T* d = reinterpret_cast<T*>(lp_slice) + mis;
-    if (tid == 0) {
-      const uint32_t bytes = static_cast<uint32_t>(sl.nvec) * 16u;
-      mbar_arrive_expect_tx(&sh.landed, bytes);
-      if (bytes) bulk_load(d + sl.head, x + id0 + sl.head, bytes, &sh.landed);
-    }
-    const int tail = sl.head + sl.nvec * LpVec<T>::N;
-    if (tid < sl.head) d[tid] = x[id0 + tid];
-    if (tid < len - tail) d[tail + tid] = x[id0 + tail + tid];
-    // a copy that never lands (the bounded wait gives up) makes the row one without a distribution
-    if (warp == 0) landed = mbar_wait(&sh.landed, 0, nullptr, PF_DEV_TIMEOUT_PRODUCER);
-    landed = __syncthreads_and(landed);
-  } else {
-    pdl_wait();
-  }
+  __syncwarp();
+  pdl_wait();
 
   // the asked token's logit, well before it is needed
   int tok = -1;
@@ -434,23 +490,26 @@ __global__ void __launch_bounds__(LP_THREADS, SM ? LP_CTAS_PER_SM : 2) logprobs_
     if (tok >= 0 && tok < a.vocab) x_tok = LpVec<T>::one(x + tok);
   }
   LpSums q;
-  if (landed)
-    sl.sums(q);
-  else
-    q.s = __int_as_float(0x7fc00000);
+  int best = sl.nvec;
+  float m2 = -INFINITY;
+  // a copy that never lands makes the row one without a distribution
+  if (!sl.sums(q, best, m2, lp_ring + warp * (LP_STAGES * LP_CHUNK_VECS), landed)) q.s = __int_as_float(0x7fc00000);
+  // (earlier, the next call's CTAs would fill the SMs unevenly: 512 rows 15.4 us, not 14.6)
+  pdl_launch();
   const float own = q.m;
+  constexpr int GROUP = W;  // threads of a group
   // the warp's sums, and the maxima of the 32 groups of threads
   {
     float g = own;
 #pragma unroll
-    for (int o = 1; o < LP_GROUP; o <<= 1) g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, o));
-    if (tid % LP_GROUP == 0) sh.group[tid / LP_GROUP] = g;
+    for (int o = 1; o < GROUP; o <<= 1) g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, o));
+    if (tid % GROUP == 0) sh.group[tid / GROUP] = g;
     q.join();
     if (lane == 0) sh.m[warp] = q.m, sh.s[warp] = q.s, sh.h[warp] = q.h;
   }
   __syncthreads();
   const int n = a.n_top;
-  if (n > 0 && landed) {
+  if (n > 0) {
     if (warp == 0) {
       // the n-th largest of the groups' maxima
       const float g = sh.group[lane];
@@ -464,17 +523,23 @@ __global__ void __launch_bounds__(LP_THREADS, SM ? LP_CTAS_PER_SM : 2) logprobs_
     }
     __syncthreads();
     const float tau = sh.tau;
-    if (own >= tau) sh.queue[atomicAdd(&sh.queued, 1)] = tid;
+    if (own >= tau) {
+      // (both lists fit: a thread is in one)
+      if (m2 < tau)
+        sh.queue[atomicAdd(&sh.n_few, 1)] = best;
+      else
+        sh.queue[(32 * W) - 1 - atomicAdd(&sh.n_many, 1)] = tid;
+    }
     __syncthreads();
-    for (int i = warp; i < sh.queued; i += LP_WARPS)
-      sl.from(sh.queue[i], tau, [&](float v, int at_id) {
-        const int at = atomicAdd(&sh.count, 1);
-        if (at < LP_CAND) sh.cand[at] = lp_key(lp_order(v), id0 + at_id);
-      });
+    const int n_many = sh.n_many;
+    sl.from(sh.queue, sh.n_few, sh.queue + (32 * W) - n_many, n_many, tau, [&](float v, int at_id) {
+      const int at = atomicAdd(&sh.count, 1);
+      if (at < LP_CAND) sh.cand[at] = lp_key(lp_order(v), id0 + at_id);
+    });
     __syncthreads();
     const int cnt = sh.count;
     if (cnt <= LP_CAND) {
-      lp_rank(sh.cand, cnt, n, sh.top);
+      lp_rank<W>(sh.cand, cnt, n, sh.top);
     } else {
       __syncthreads();  // every thread has read the count
       lp_select(sl, id0, n, sh);
@@ -487,32 +552,32 @@ __global__ void __launch_bounds__(LP_THREADS, SM ? LP_CTAS_PER_SM : 2) logprobs_
   const unsigned long long* top = sh.top;
   LpSums z;
   if (warp == 0) {
-    if (lane < LP_WARPS) z.m = sh.m[lane], z.s = sh.s[lane], z.h = sh.h[lane];
+    if (lane < W) z.m = sh.m[lane], z.s = sh.s[lane], z.h = sh.h[lane];
     z.join();
   }
   if (cluster > 1) {
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
     if (warp == 0) {
       if (lane == 0) {
-        const uint32_t at = map_to_rank(smem_u32(&sh.sums[rank]), 0);
+        const uint32_t at = map_to_rank(smem_u32(&all.sums[rank]), 0);
         asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(at), "f"(z.m), "f"(z.s), "f"(z.h), "f"(0.f)
                      : "memory");
       }
       if (lane < n) {
-        const uint32_t at = map_to_rank(smem_u32(&sh.all[rank * n + lane]), 0);
+        const uint32_t at = map_to_rank(smem_u32(&all.top[rank * n + lane]), 0);
         asm volatile("st.shared::cluster.b64 [%0], %1;" ::"r"(at), "l"(sh.top[lane]) : "memory");
       }
     }
     cluster_sync_all();
     if (rank != 0) return;
     if (n > 0) {
-      lp_rank(sh.all, cluster * n, n, sh.cand);
+      lp_rank<W>(all.top, cluster * n, n, sh.cand);
       top = sh.cand;
       __syncthreads();
     }
     if (warp != 0) return;
     z = LpSums();
-    if (lane < cluster) z.m = sh.sums[lane].x, z.s = sh.sums[lane].y, z.h = sh.sums[lane].z;
+    if (lane < cluster) z.m = all.sums[lane].x, z.s = all.sums[lane].y, z.h = all.sums[lane].z;
     z.join();
   }
   const bool ok = z.s >= 1.f && z.m < INFINITY;  // false for a NaN too: a NaN, +inf, or only -inf
@@ -527,30 +592,39 @@ __global__ void __launch_bounds__(LP_THREADS, SM ? LP_CTAS_PER_SM : 2) logprobs_
   if (lane == 31 && a.entropy) a.entropy[r] = ok ? log_s - LP_LN2 * (z.h / z.s) : nan;
 }
 
-// CTAs per row: enough that a slice fits shared memory, and for few rows as
-// many as leave a slice of LP_SLICE_MIN logits and still run at once (three
-// a SM with full slices).
+// For few rows a cluster: as many CTAs a row as leave a slice of LP_SLICE_MIN
+// logits and no more than two CTAs to an SM (32768 fp32 logits, 1 row: 4.4 us
+// in 8 slices, 6.4 in one; 64 rows: 7.6 in 4, 8.1 in one, 9.0 in 8; 300 rows:
+// 10.3 in one, 11.0 in 2).
 constexpr int LP_SLICE_MIN = 2048;
 
+template <class T, int W>
+static cudaError_t launch_logprobs(const LogprobArgs& a, int cluster, cudaStream_t s) {
+  constexpr int smem = lp_ring_bytes(W) + static_cast<int>(sizeof(LpCluster));
+  const cudaError_t e = smem_opt_in<logprobs_kernel<T, W>>(smem);
+  if (e != cudaSuccess) return e;
+  return launch_k(logprobs_kernel<T, W>, dim3(static_cast<unsigned>(a.rows) * cluster), dim3(32 * W),
+                  cluster > 1 ? smem : lp_ring_bytes(W), s, cluster, a, cluster);
+}
+
 template <class T>
-static cudaError_t launch_logprobs(LogprobArgs a, int rows, cudaStream_t s) {
+static cudaError_t logprobs_of(LogprobArgs a, cudaStream_t s) {
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
   int cluster = 1;
   while (cluster < LP_CLUSTER_MAX && a.vocab / (2 * cluster) >= LP_SLICE_MIN &&
-         (static_cast<int64_t>(a.vocab) * sizeof(T) > static_cast<int64_t>(LP_SMEM_SLICE) * cluster ||
-          static_cast<int64_t>(rows) * 2 * cluster <= static_cast<int64_t>(LP_CTAS_PER_SM) * sms))
+         static_cast<int64_t>(a.rows) * 2 * cluster <= 2 * sms)
     cluster *= 2;
   a.slice = ((a.vocab + cluster - 1) / cluster + 7) / 8 * 8;
-  const dim3 grid(static_cast<unsigned>(rows) * cluster);
-  const int64_t bytes = static_cast<int64_t>(a.slice) * sizeof(T);
-  if (bytes > LP_SMEM_SLICE) return launch_k(logprobs_kernel<T, false>, grid, dim3(LP_THREADS), 0, s, cluster, a, cluster);
-  e = smem_opt_in<logprobs_kernel<T, true>>(LP_SMEM_SLICE + 16);
-  if (e != cudaSuccess) return e;
-  return launch_k(logprobs_kernel<T, true>, grid, dim3(LP_THREADS), static_cast<size_t>(bytes) + 16, s, cluster, a,
-                  cluster);
+  // Many short rows: CTAs of 4 warps, 8 to an SM, so that more rows are being
+  // begun or finished while others stream (4096 x 32768 bf16: 56 us, 66 with 8
+  // warps; 2000 x 32768 fp32 46.5, 48.9).  Longer rows want fewer at once
+  // (3000 x 50257 fp32: 110 us with 8 warps, 122 with 4), fewer rows more
+  // threads each (300 x 32768 fp32: 10.3, 12.7).
+  const bool four = a.rows >= 4 * sms && static_cast<int64_t>(a.vocab) * sizeof(T) <= 131072;
+  return four ? launch_logprobs<T, 4>(a, cluster, s) : launch_logprobs<T, 8>(a, cluster, s);
 }
 
 }  // namespace pf
@@ -574,10 +648,10 @@ extern "C" int pfop_logprobs(int32_t ltype, const void* logits_dev, int64_t ld, 
                         (n_top > 0 ? reinterpret_cast<uintptr_t>(top_id_dev) | reinterpret_cast<uintptr_t>(top_logp_dev) : 0);
   if ((out & 3) || (reinterpret_cast<uintptr_t>(logits_dev) & (ltype == PF_L_F32 ? 3 : 1)))
     return fail(PF_E_ARG, "misaligned buffer");
-  const LogprobArgs a{logits_dev, ld, vocab, 0, tok_dev, n_top, logp_dev, entropy_dev, top_id_dev, top_logp_dev};
+  const LogprobArgs a{logits_dev, ld, rows, vocab, 0, tok_dev, n_top, logp_dev, entropy_dev, top_id_dev, top_logp_dev};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const cudaError_t e =
-      ltype == PF_L_F32 ? launch_logprobs<float>(a, rows, s) : launch_logprobs<__nv_bfloat16>(a, rows, s);
+      ltype == PF_L_F32 ? logprobs_of<float>(a, s) : logprobs_of<__nv_bfloat16>(a, s);
   if (e != cudaSuccess) return fail(PF_E_CUDA, std::string("log probabilities launch: ") + cudaGetErrorString(e));
   return PF_OK;
 }
