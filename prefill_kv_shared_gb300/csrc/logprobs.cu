@@ -10,7 +10,7 @@
 // stays a NaN and marks the row as one without a distribution.
 //
 // The alternatives need no second look at the whole row: the n-th largest of
-// the maxima of 32 groups of threads is not above the n-th largest value, so
+// the maxima of 64 groups of threads is not above the n-th largest value, so
 // only what reaches it is listed, a few dozen logits as a rule, whose ranks
 // are then counted.  A thread keeps where its largest step of 16 logits began
 // and the next largest step's maximum: mostly that one step is all that has
@@ -24,12 +24,12 @@
 // copies of 2 KB, two on their way for every warp: no registers are held and
 // no warp waits for another until the row's end.  (Whole 64 KB slices in
 // shared memory, three to an SM, left too few rows in flight: 512 rows of
-// 32768 fp32 logits 21.7 us, now 14.4.)
+// 32768 fp32 logits 21.7 us, now 14.6.)
 //
 // Bound by the row's bytes for many rows, and by what a CTA does once a row
 // (launch, first copy, joins, ranks: about 4 us), by latency for few.  32768
-// logits, 5 or 8 alternatives: 1 row fp32 4.5 us; 512 rows fp32 14.4 us, 4.7
-// TB/s; 4096 rows bf16 56 us, 4.8 TB/s (59 with three in ten masked).
+// logits, 5 or 8 alternatives: 1 row fp32 4.5 us; 512 rows fp32 14.6 us, 4.6
+// TB/s; 4096 rows bf16 58 us, 4.6 TB/s (61 with three in ten masked).
 #include "../../include/prefill_ops.h"
 #include "common.cuh"
 #include "kernels.h"
@@ -39,7 +39,12 @@
 namespace pf {
 
 constexpr int LP_TOP_MAX = 32;
-constexpr int LP_CAND = 256;  // listed candidates
+constexpr int LP_GROUPS = 64;  // of a CTA's threads, whose maxima are compared
+// Alternatives found from 32 pairs of groups; more from the 64 groups: the
+// n-th of 32 has 44 logits at or above it for n = 24 and 130 for n = 32, where
+// the list now and then overflowed (26 us instead of 8 for 8 rows).
+constexpr int LP_PAIRS_MAX = 24;
+constexpr int LP_CAND = 256;   // listed candidates
 constexpr int LP_CLUSTER_MAX = 8;
 constexpr int LP_CHUNK_VECS = 128;  // 16-byte vectors of a warp's copy
 constexpr int LP_STAGES = 2;        // copies a warp has on their way
@@ -47,7 +52,7 @@ constexpr int LP_STAGES = 2;        // copies a warp has on their way
 constexpr int lp_ring_bytes(int w) { return w * LP_STAGES * LP_CHUNK_VECS * 16; }
 constexpr int lp_ctas_per_sm(int w) { return 32 / w; }
 constexpr float LP_LOG2E = 1.4426950408889634f, LP_LN2 = 0.6931471805599453f;
-static_assert(LP_TOP_MAX <= 32 && LP_CLUSTER_MAX * LP_TOP_MAX <= LP_CAND, "a lane per alternative, a list for a cluster's");
+static_assert(LP_GROUPS == 64 && LP_PAIRS_MAX <= 32 && LP_TOP_MAX <= 32 && LP_CLUSTER_MAX * LP_TOP_MAX <= LP_CAND, "a lane per alternative, a list for a cluster's");
 
 struct LogprobArgs {
   const void* logits;
@@ -200,13 +205,18 @@ struct LpSlice {
   static constexpr int TAKE = 16 / VN;  // vectors of a step: 16 logits
   const T* x;
   int n, head, nvec;
+  int chunk;  // vectors of a chunk, a multiple of 32
   __device__ LpSlice(const T* p, int len) : x(p), n(len) {
     const int mis = static_cast<int>((reinterpret_cast<uintptr_t>(p) & 15) / sizeof(T));
     head = min(len, mis ? VN - mis : 0);
     nvec = (len - head) / VN;
+    // a small slice is dealt out to all threads (else half its groups would be empty)
+    chunk = min(LP_CHUNK_VECS, max(1, (nvec + 32 * W - 1) / (32 * W)) * 32);
   }
   __device__ __forceinline__ const uint4* vecs() const { return reinterpret_cast<const uint4*>(x + head); }
-  __device__ __forceinline__ int chunks() const { return (nvec + LP_CHUNK_VECS - 1) / LP_CHUNK_VECS; }
+  __device__ __forceinline__ int chunks() const { return (nvec + chunk - 1) / chunk; }
+  // vectors of a step that one place stands for: those of 16 logits, in a small slice one
+  __device__ __forceinline__ int step_log() const { return chunk < LP_CHUNK_VECS ? 0 : TAKE == 4 ? 2 : 1; }
   // f(value, id in the slice) for the logits of vector v that are at least tau
   template <class F>
   __device__ __forceinline__ void look(int v, float tau, F&& f) const {
@@ -225,21 +235,21 @@ struct LpSlice {
   // few[0 .. n_few), and all of the threads many[0 .. n_many)'s
   template <class F>
   __device__ __forceinline__ void from(const int* few, int n_few, const int* many, int n_many, float tau, F&& f) const {
-    constexpr int PER = LP_CHUNK_VECS / 32;  // a thread's vectors of a chunk
+    const int per = chunk / 32;  // a thread's vectors of a chunk
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int steps = n_few * TAKE;
+    const int sl = step_log(), steps = n_few << sl;
     // vectors dealt out over the CTA, then those of a thread over a warp
-    const int per_thread = PER * ((chunks() + W - 1) / W);
+    const int per_thread = per * ((chunks() + W - 1) / W);
     int i = threadIdx.x, q = warp, k = lane;
 #pragma unroll 1
     for (;;) {  // (one copy of the code: what is run once a row costs its fetching)
       int v;
       if (i < steps) {
-        v = few[i / TAKE] + 32 * (i % TAKE);
+        v = few[i >> sl] + 32 * (i & ((1 << sl) - 1));
         i += (32 * W);
       } else if (q < n_many) {
         const int t = many[q];
-        v = k < per_thread ? ((t >> 5) + W * (k / PER)) * LP_CHUNK_VECS + (k % PER) * 32 + (t & 31) : nvec;
+        v = k < per_thread ? ((t >> 5) + W * (k / per)) * chunk + k % per * 32 + (t & 31) : nvec;
         k += 32;
         if (k >= per_thread) k = lane, q += W;
       } else {
@@ -287,8 +297,8 @@ struct LpSlice {
     const int cnt = warp < chunks() ? (chunks() - warp + W - 1) / W : 0;
     const int tail = head + nvec * VN;
     auto copy = [&](int i) {
-      const int v0 = (warp + i * W) * LP_CHUNK_VECS;
-      const uint32_t bytes = static_cast<uint32_t>(min(LP_CHUNK_VECS, nvec - v0)) * 16u;
+      const int v0 = (warp + i * W) * chunk;
+      const uint32_t bytes = static_cast<uint32_t>(min(chunk, nvec - v0)) * 16u;
       uint64_t* bar = landed + i % LP_STAGES;
       mbar_arrive_expect_tx(bar, bytes);
       bulk_load(ring + i % LP_STAGES * LP_CHUNK_VECS, vecs() + v0, bytes, bar);
@@ -308,7 +318,7 @@ struct LpSlice {
         for (int j = i + 1; j < min(i + LP_STAGES, cnt); ++j) wait(j);  // copies on their way
         return false;
       }
-      const int v0 = (warp + i * W) * LP_CHUNK_VECS;
+      const int v0 = (warp + i * W) * chunk;
       const uint4* c = ring + i % LP_STAGES * LP_CHUNK_VECS + lane;
       auto raise = [&](float mx, int v) {
         if (mx > a.m) {
@@ -319,7 +329,7 @@ struct LpSlice {
           m2 = fmaxf(m2, mx);
         }
       };
-      if (v0 + LP_CHUNK_VECS <= nvec) {
+      if (chunk == LP_CHUNK_VECS && v0 + chunk <= nvec) {
         static_assert(LP_CHUNK_VECS % (32 * TAKE) == 0, "a chunk is a number of whole steps");
 #pragma unroll 1
         for (int b = 0; b < LP_CHUNK_VECS / 32; b += TAKE) {
@@ -337,13 +347,13 @@ struct LpSlice {
         }
       } else {
 #pragma unroll 1
-        for (int b = 0; v0 + 32 * b + lane < nvec; ++b) {
+        for (int b = 0; b < chunk / 32 && v0 + 32 * b + lane < nvec; ++b) {
           float e[VN];
           LpVec<T>::get(c[32 * b], e);
           float mx = fmaxf(e[0], e[1]);
 #pragma unroll
           for (int k = 2; k < VN; k += 2) mx = lp_max3(mx, e[k], e[k + 1]);
-          raise(mx, v0 + 32 * (b - b % TAKE) + lane);
+          raise(mx, v0 + 32 * (b >> step_log() << step_log()) + lane);
           a.template add<VN, true>(e);
         }
       }
@@ -362,7 +372,7 @@ struct LpShared {
     int hist[256];
   };
   float m[W], s[W], h[W];
-  float group[32];
+  alignas(16) float group[LP_GROUPS];
   float tau;
   int queue[(32 * W)];  // steps that reach tau from its start, threads from its end
   int n_few, n_many, count, prefix, left, warp_count[W];
@@ -494,11 +504,11 @@ __global__ void __launch_bounds__(32 * W, lp_ctas_per_sm(W)) logprobs_kernel(con
   float m2 = -INFINITY;
   // a copy that never lands makes the row one without a distribution
   if (!sl.sums(q, best, m2, lp_ring + warp * (LP_STAGES * LP_CHUNK_VECS), landed)) q.s = __int_as_float(0x7fc00000);
-  // (earlier, the next call's CTAs would fill the SMs unevenly: 512 rows 15.4 us, not 14.6)
+  // (earlier, the next call's CTAs would fill the SMs unevenly: 512 rows 15.4 us instead of 14.8)
   pdl_launch();
   const float own = q.m;
-  constexpr int GROUP = W;  // threads of a group
-  // the warp's sums, and the maxima of the 32 groups of threads
+  constexpr int GROUP = 32 * W / LP_GROUPS;  // threads of a group
+  // the warp's sums, and the maxima of the groups of threads
   {
     float g = own;
 #pragma unroll
@@ -510,9 +520,21 @@ __global__ void __launch_bounds__(32 * W, lp_ctas_per_sm(W)) logprobs_kernel(con
   __syncthreads();
   const int n = a.n_top;
   if (n > 0) {
-    if (warp == 0) {
-      // the n-th largest of the groups' maxima
-      const float g = sh.group[lane];
+    // the n-th largest of the maxima, of pairs of groups or of the groups
+    if (n > LP_PAIRS_MAX) {
+      if (tid < LP_GROUPS) {
+        const float g = sh.group[tid];
+        int rk = 0;
+#pragma unroll 4
+        for (int i = 0; i < LP_GROUPS; i += 4) {
+          const float4 o = *reinterpret_cast<const float4*>(sh.group + i);
+          rk += (o.x > g || (o.x == g && i < tid)) + (o.y > g || (o.y == g && i + 1 < tid)) +
+                (o.z > g || (o.z == g && i + 2 < tid)) + (o.w > g || (o.w == g && i + 3 < tid));
+        }
+        if (rk == n - 1) sh.tau = g;
+      }
+    } else if (warp == 0) {
+      const float g = fmaxf(sh.group[2 * lane], sh.group[2 * lane + 1]);
       int rk = 0;
 #pragma unroll
       for (int i = 0; i < 32; ++i) {
@@ -593,9 +615,9 @@ __global__ void __launch_bounds__(32 * W, lp_ctas_per_sm(W)) logprobs_kernel(con
 }
 
 // For few rows a cluster: as many CTAs a row as leave a slice of LP_SLICE_MIN
-// logits and no more than two CTAs to an SM (32768 fp32 logits, 1 row: 4.4 us
-// in 8 slices, 6.4 in one; 64 rows: 7.6 in 4, 8.1 in one, 9.0 in 8; 300 rows:
-// 10.3 in one, 11.0 in 2).
+// logits and no more than two CTAs to an SM (32768 fp32 logits, 1 row: 4.5 us
+// in 8 slices, 6.5 in one; 64 rows: 7.8 in 4, 8.4 in one, 9.3 in 8; 300 rows:
+// 10.5 in one, 11.2 in 2).
 constexpr int LP_SLICE_MIN = 2048;
 
 template <class T, int W>
@@ -619,10 +641,10 @@ static cudaError_t logprobs_of(LogprobArgs a, cudaStream_t s) {
     cluster *= 2;
   a.slice = ((a.vocab + cluster - 1) / cluster + 7) / 8 * 8;
   // Many short rows: CTAs of 4 warps, 8 to an SM, so that more rows are being
-  // begun or finished while others stream (4096 x 32768 bf16: 56 us, 66 with 8
-  // warps; 2000 x 32768 fp32 46.5, 48.9).  Longer rows want fewer at once
-  // (3000 x 50257 fp32: 110 us with 8 warps, 122 with 4), fewer rows more
-  // threads each (300 x 32768 fp32: 10.3, 12.7).
+  // begun or finished while others stream (4096 x 32768 bf16: 58 us, 68 with 8
+  // warps; 2000 x 32768 fp32 47, 49).  Longer rows want fewer at once (3000 x
+  // 50257 fp32: 108 us with 8 warps, 124 with 4), fewer rows more threads each
+  // (300 x 32768 fp32: 10.5, 12.9).
   const bool four = a.rows >= 4 * sms && static_cast<int64_t>(a.vocab) * sizeof(T) <= 131072;
   return four ? launch_logprobs<T, 4>(a, cluster, s) : launch_logprobs<T, 8>(a, cluster, s);
 }

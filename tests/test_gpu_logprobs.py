@@ -203,3 +203,33 @@ def test_recorded_and_replayed(rows):
         graph.replay()
         torch.cuda.synchronize()
         _check(x, tokens, 5, out)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("rows", [3, 700])
+@pytest.mark.parametrize("vocab", [32, 127, 512, 1023, 2000, 2057, 4095, 4096, 6151, 8200, 12289, 16383, 16385])
+def test_small_slices(dtype, rows, vocab):
+    """Rows that fill the warps' copies in part, for CTAs of either size,
+    the rows' starts on and off 16-byte boundaries; with masked logits too."""
+    x, tokens = _logits(rows, vocab, dtype, vocab)
+    _check(x, tokens, 32, _run(x, tokens, 32))
+    x[:, ::3] = float("-inf")
+    x[:, -1] = 0.5
+    _check(x, torch.full_like(tokens, vocab - 1), 5, _run(x, torch.full_like(tokens, vocab - 1), 5))
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("rows,vocab", [(1, 32768), (700, 9000)])
+def test_alternatives_close_together(dtype, rows, vocab):
+    """All alternatives in one thread's step, in several steps of one thread,
+    and at a row's ragged ends."""
+    x, tokens = _logits(rows, vocab, dtype, 5)
+    g = torch.Generator(device="cuda").manual_seed(6)
+    high = (40 + torch.arange(24, device="cuda")).to(dtype)
+    for r in range(min(rows, 40)):
+        start = int(torch.randint(0, vocab - 24, (1,), generator=g, device="cuda")) if r % 4 else (0, vocab - 24)[r // 4 % 2]
+        span = (vocab - start - 1) // 24
+        at = start + torch.arange(24, device="cuda") * (1, 8, 32, max(1, span))[r // 4 % 4]
+        at = at[at < vocab]
+        x[r, at] = high[torch.randperm(24, generator=g, device="cuda")][:len(at)]
+    _check(x, tokens, 20, _run(x, tokens, 20))
