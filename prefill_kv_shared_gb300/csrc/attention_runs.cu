@@ -4,9 +4,11 @@
 //
 // MMA rows are (row, head-in-group) pairs of a run: row R = t*G + g is the
 // run's row t and query head kvh*G + g, so the G heads of a KV head share its
-// K/V.  256 consecutive rows of a run and KV head are an item.  A pair of CTAs
-// (a 2-CTA cluster, tcgen05 .cta_group::2) works through segments, a segment
-// being an item and a range of its 128-key chunks, with one online softmax:
+// K/V.  256 consecutive rows of a run and KV head are an item, worked on by a
+// pair of CTAs (a 2-CTA cluster, tcgen05 .cta_group::2); at hd 64, where rows
+// or items are few, 128 and one CTA (below a pair too).  A pair works through
+// segments, a segment being an item and a range of its 128-key chunks, with
+// one online softmax:
 //     S = Q K^T, m' = max(m, max_k s_k), p_k = 2^((s_k - m') c),
 //     l' = l 2^((m - m') c) + sum_k p_k, O' = O 2^((m - m') c) + fp16(P) V
 // with c = log2(e)/sqrt(hd), S, O, m, l in fp32.
@@ -58,8 +60,7 @@
 namespace pf {
 
 constexpr int RUNS_MAX = 128;
-constexpr int RCH = 128;    // keys of a chunk
-constexpr int RROWS = 256;  // MMA rows of a pair
+constexpr int RCH = 128;  // keys of a chunk
 
 // the call's runs, passed in the kernel's parameters; a run's items are its
 // row blocks, last (longest) first, once per KV head
@@ -73,6 +74,7 @@ struct RunTable {
 
 struct RunsShape {
   int Hq, Hkv, log_g;  // G = 1 << log_g query heads per KV head
+  int bs_log;          // 1 << bs_log of a run's rows are an item's
   int per;             // weight of a pair's share; 0: a pair per item
   int pairs;
   int merge;  // an item may be cut in three or more: the merge kernel joins all that are cut
@@ -84,12 +86,15 @@ struct RunsShape {
 // in chunk times
 constexpr int ITEM_FIXED = 2;
 
-template <int HD>
+// CL: CTAs of an item
+template <int HD, int CL>
 struct RunsCfg {
   static constexpr int Q_BYTES = 128 * HD * 2;  // [64-dim box][128 rows][128 B]
-  static constexpr int STAGE = 64 * HD * 2;     // half a chunk: K [box][64 keys][128 B], V [box][128 keys][hd/2 dims]
-  static constexpr int V_BOXES = HD == 256 ? 2 : 1;  // of a V half
-  static constexpr int NST = HD == 256 ? 5 : 16;
+  static constexpr int KEYS = RCH / CL;                // keys of a chunk in a CTA
+  static constexpr int STAGE = KEYS * HD * 2;          // K [box][KEYS][128 B] or V [box][128 keys][VB], hd/CL dims
+  static constexpr int VB = HD / CL >= 64 ? 128 : 64;  // bytes of a key's row in a box of V
+  static constexpr int V_BOXES = HD / CL * 2 / VB;
+  static constexpr int NST = HD == 256 ? 5 : CL == 2 ? 16 : 12;
   static constexpr int NG = HD == 256 ? 1 : 2;  // row warpgroups, taking chunks in turn
   static constexpr int NSB = NG + 1;            // S buffers
   static constexpr int LA = NSB - 1;            // chunks that S is formed ahead of P V
@@ -105,9 +110,9 @@ struct RunsCfg {
   // Row (in the pair's 256) of row i of CTA `rank`.  At hd 64 the CTAs take
   // 32-row groups in turn, so that an item of few rows loads the exponential
   // units of both SMs.
-  static constexpr int Q_ROWS = HD == 256 ? 128 : 32;  // rows of a copy of Q
+  static constexpr int Q_ROWS = HD == 256 || CL == 1 ? 128 : 32;  // rows of a copy of Q
   static __device__ __forceinline__ int row_of(int rank, int i) {
-    return HD == 256 ? rank * 128 + i : ((i >> 5) * 2 + rank) * 32 + (i & 31);
+    return Q_ROWS == 128 ? rank * 128 + i : ((i >> 5) * 2 + rank) * 32 + (i & 31);
   }
   // Registers (setmaxnreg, hd 64): a row thread holds its 128 scores.
   // 128 * 88 + 256 * 208 of the 384 * 168 that the block is launched with.
@@ -244,13 +249,13 @@ __host__ __device__ __forceinline__ int find_last(const int* first, int n, int x
 }
 
 // A run's row blocks and their chunks.  Block i (counted from the run's
-// end) has block b = nb-1-i of 256 >> log_g rows; causal, it needs the
+// end) has block b = nb-1-i of 1 << bs_log rows; causal, it needs the
 // chunks up to its last row.
 template <bool TREE>
 struct RunBlocks {
   int n, pos0, bs_log, nb, last;  // last: chunks of the whole run
-  __host__ __device__ RunBlocks(int n_rows, int p0, int log_g)
-      : n(n_rows), pos0(p0), bs_log(8 - log_g), nb((n_rows + (1 << bs_log) - 1) >> bs_log),
+  __host__ __device__ RunBlocks(int n_rows, int p0, int bl)
+      : n(n_rows), pos0(p0), bs_log(bl), nb((n_rows + (1 << bs_log) - 1) >> bs_log),
         last(static_cast<int>((static_cast<unsigned>(p0) + n_rows + RCH - 1) / RCH)) {}
   // sum over x' < x of floor(x' / (128 / bs)); modulo 2^32 (differences of it are exact)
   __host__ __device__ unsigned floors(unsigned x) const {
@@ -284,7 +289,7 @@ struct ItemAt {
   __host__ __device__ static ItemAt number(const RunTable& rt, const RunsShape& sh, int idx) {
     ItemAt a;
     a.run = find_last(rt.item0, rt.n_runs, idx);
-    const RunBlocks<TREE> rb(rt.n[a.run], rt.pos0[a.run], sh.log_g);
+    const RunBlocks<TREE> rb(rt.n[a.run], rt.pos0[a.run], sh.bs_log);
     const int loc = idx - rt.item0[a.run];
     a.kvh = loc / rb.nb;
     a.i = loc % rb.nb;
@@ -295,7 +300,7 @@ struct ItemAt {
   __host__ __device__ static ItemAt weight(const RunTable& rt, const RunsShape& sh, int x) {
     ItemAt a;
     a.run = find_last(rt.w0, rt.n_runs, x);
-    const RunBlocks<TREE> rb(rt.n[a.run], rt.pos0[a.run], sh.log_g);
+    const RunBlocks<TREE> rb(rt.n[a.run], rt.pos0[a.run], sh.bs_log);
     const int head = rb.weight(rb.nb);
     int rem = x - rt.w0[a.run];
     a.kvh = rem / head;
@@ -349,13 +354,13 @@ struct Segments {
   }
   __host__ __device__ bool next() {
     while (left) {
-      const RunBlocks<TREE> rb(rt.n[at.run], rt.pos0[at.run], sh.log_g);
+      const RunBlocks<TREE> rb(rt.n[at.run], rt.pos0[at.run], sh.bs_log);
       const int ch = rb.chunks(at.i), w = at.w + ITEM_FIXED;
       const bool all = sh.per == 0;
       const int k0 = all || lo < w ? 0 : lo - w, k1 = all || hi - w > ch ? ch : hi - w;
       run = at.run;
       kvh = at.kvh;
-      R0 = (rb.nb - 1 - at.i) * RROWS;
+      R0 = (rb.nb - 1 - at.i) << (sh.bs_log + sh.log_g);
       ch0 = k0;
       n = k1 - k0;
       slot = 2 * pair + (k0 == 0 ? 1 : 0);
@@ -378,9 +383,9 @@ struct Segments {
             at.kvh = sh.Hkv - 1;
             --at.run;
           }
-          at.i = RunBlocks<TREE>(rt.n[at.run], rt.pos0[at.run], sh.log_g).nb - 1;
+          at.i = RunBlocks<TREE>(rt.n[at.run], rt.pos0[at.run], sh.bs_log).nb - 1;
         }
-        at.w -= ITEM_FIXED + RunBlocks<TREE>(rt.n[at.run], rt.pos0[at.run], sh.log_g).chunks(at.i);
+        at.w -= ITEM_FIXED + RunBlocks<TREE>(rt.n[at.run], rt.pos0[at.run], sh.bs_log).chunks(at.i);
       }
       if (n > 0) return true;
     }
@@ -433,13 +438,13 @@ __device__ __forceinline__ void exp_scores(const uint32_t (&x)[32], uint64_t c2,
   }
 }
 
-template <int HD, bool TREE>
-__global__ void __launch_bounds__(RunsCfg<HD>::THREADS, 1)
+template <int HD, int CL, bool TREE>
+__global__ void __launch_bounds__(RunsCfg<HD, CL>::THREADS, 1)
     attn_runs_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                      const __grid_constant__ CUtensorMap tmV, const __grid_constant__ RunTable rt, const RunsShape sh,
                      const uint64_t* __restrict__ mask, int words, __nv_bfloat16* __restrict__ out,
                      float* part, int* __restrict__ desc, int* err, int* flags) {
-  using C = RunsCfg<HD>;
+  using C = RunsCfg<HD, CL>;
   constexpr float cexp = attn_c<HD>();
   extern __shared__ uint8_t smem_raw[];
   // The two CTAs' buffers lie at the same shared-memory offset (one
@@ -447,7 +452,7 @@ __global__ void __launch_bounds__(RunsCfg<HD>::THREADS, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
   uint64_t* full = bars;            // NST, in the even CTA: a stage has landed in both; in the odd CTA: a
-                                    // V to be cleared has landed there
+                                    // V to be cleared has landed there (one CTA: the even one)
   uint64_t* empty = bars + C::NST;  // NST: the MMAs that read the stage are done (its S or P V too)
   uint64_t* cleared = bars + 2 * C::NST;  // NST, in the even CTA: the odd CTA's V is cleared
   uint64_t* q_full = bars + 3 * C::NST;   // in the even CTA: Q of both has landed
@@ -459,7 +464,9 @@ __global__ void __launch_bounds__(RunsCfg<HD>::THREADS, 1)
   static_assert((3 * C::NST + 6 + C::NSB) * 8 <= 512 && C::NG <= 2, "barrier layout");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rank = static_cast<int>(cluster_ctarank());
+  const int rank = CL == 2 ? static_cast<int>(cluster_ctarank()) : 0;
+  const int pair = static_cast<int>(blockIdx.x) / CL;
+  auto in_even = [](const void* p) { return CL == 2 ? map_to_rank(smem_u32(p), 0) : smem_u32(p); };
   pdl_launch();
 
   if (threadIdx.x == 0) {
@@ -470,8 +477,8 @@ __global__ void __launch_bounds__(RunsCfg<HD>::THREADS, 1)
     }
     mbar_init(q_full, 1);
     mbar_init(q_empty, 1);
-    for (int b = 0; b < C::NSB; ++b) mbar_init(&p_full[b], 8);
-    mbar_init(o_free, 8 * C::NG);
+    for (int b = 0; b < C::NSB; ++b) mbar_init(&p_full[b], 4 * CL);
+    mbar_init(o_free, 4 * CL * C::NG);
     mbar_init(&drain[0], 1);
     mbar_init(&drain[1], 1);
     fence_mbar_init();
@@ -481,11 +488,16 @@ __global__ void __launch_bounds__(RunsCfg<HD>::THREADS, 1)
     prefetch_tensormap(&tmV);
   }
   if (warp == 2 && lane == 0) prefetch_tensormap(&tmQ);
-  if (warp == 0) tmem_alloc_pair(tmem_slot, C::TMEM_COLS);
-  Segments<TREE> sg(rt, sh, static_cast<int>(blockIdx.x >> 1));
+  if (warp == 0) {
+    if constexpr (CL == 2)
+      tmem_alloc_pair(tmem_slot, C::TMEM_COLS);
+    else
+      tmem_alloc(tmem_slot, C::TMEM_COLS);
+  }
+  Segments<TREE> sg(rt, sh, pair);
   tc_fence_before();
   __syncthreads();
-  cluster_sync_all();
+  if constexpr (CL == 2) cluster_sync_all();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   pdl_wait();
@@ -512,13 +524,32 @@ __global__ void __launch_bounds__(RunsCfg<HD>::THREADS, 1)
   // a bit per stage holds the parity of the next such fill.
   auto tail_keys = [&]() { return rt.pos0[sg.run] + rt.n[sg.run] - (sg.ch0 + sg.n - 1) * RCH; };
   auto clear_tail = [&](uint32_t fill) {
-    constexpr int VB = HD == 256 ? 128 : 64;  // bytes of a key's row in a box
     uint8_t* v = smem + C::OFF_ST + (fill % C::NST) * C::STAGE;
-    for (int box = 0; box < C::STAGE / (RCH * VB); ++box)
-      for (int o = tail_keys() * VB + lane * 16; o < RCH * VB; o += 512)
-        *reinterpret_cast<uint4*>(v + box * RCH * VB + o) = make_uint4(0u, 0u, 0u, 0u);
+    for (int box = 0; box < C::V_BOXES; ++box)
+      for (int o = tail_keys() * C::VB + lane * 16; o < RCH * C::VB; o += 512)
+        *reinterpret_cast<uint4*>(v + box * RCH * C::VB + o) = make_uint4(0u, 0u, 0u, 0u);
     fence_proxy_async_smem();
     __syncwarp();
+  };
+
+  // what the merge kernel has to know of this pair
+  auto leave_table = [&]() {
+    if (sh.per == 0) return;
+    int4* d = reinterpret_cast<int4*>(desc);
+    if (!sh.desc_by_item) d[2 * pair] = make_int4(0, 0, 0, 0);
+    Segments<TREE> all(rt, sh, pair);
+    while (all.next()) {
+      if (all.ch0 > 0 || (all.kind != SEG_PART && !sh.desc_by_item)) continue;
+      // the item's first segment: its pairs (0: nothing to join), rows, first packed row, KV head; first row
+      const RunBlocks<TREE> rb(rt.n[all.run], rt.pos0[all.run], sh.bs_log);
+      const int rows_log = sh.bs_log + sh.log_g;
+      const int i = rb.nb - 1 - (all.R0 >> rows_log);
+      const int left = rb.chunks(i) - all.n;  // chunks in the pairs after this one
+      const int at = sh.desc_by_item ? rt.item0[all.run] + all.kvh * rb.nb + i : pair;
+      d[2 * at] = make_int4(all.kind == SEG_PART ? 1 + (left + sh.per - 1) / sh.per : 0,
+                            min(1 << rows_log, (rt.n[all.run] << sh.log_g) - all.R0), rt.row0[all.run], all.kvh);
+      d[2 * at + 1] = make_int4(all.R0, pair, 0, 0);
+    }
   };
 
   if (warp >= 4) {
@@ -529,8 +560,8 @@ __global__ void __launch_bounds__(RunsCfg<HD>::THREADS, 1)
     const uint32_t o_at = lanes + C::TMEM_O + h * HD;
     constexpr int NB = RCH / 32;
     const uint64_t c2 = pack_f32x2(cexp, cexp);
-    const uint32_t o_free_at = map_to_rank(smem_u32(o_free), 0);
-    const uint32_t p_full_at = map_to_rank(smem_u32(p_full), 0);
+    const uint32_t o_free_at = in_even(o_free);
+    const uint32_t p_full_at = in_even(p_full);
     bool ok = true;
     uint32_t j0 = 0, f0 = 0;
     // the MMAs of fill f are done
@@ -657,7 +688,7 @@ __global__ void __launch_bounds__(RunsCfg<HD>::THREADS, 1)
         float w_other = 0.f;
         int* flag = nullptr;
         if (kind == SEG_SECOND) {
-          flag = flags + (sg.pair - 1) * 8 + rank * 4 + qw;
+          flag = flags + (sg.pair - 1) * (4 * CL) + rank * 4 + qw;
           if (!wait_flag(flag, C::NG, err)) ok = false;
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
@@ -744,7 +775,7 @@ __global__ void __launch_bounds__(RunsCfg<HD>::THREADS, 1)
           // the warp's rows of the state are there; or read, and the flag as it was
           if (kind == SEG_FIRST) {
             __threadfence();
-            atomicAdd(flags + sg.pair * 8 + rank * 4 + qw, 1);
+            atomicAdd(flags + sg.pair * (4 * CL) + rank * 4 + qw, 1);
           } else if (kind == SEG_SECOND && atomicAdd(flag, 1) == 2 * C::NG - 1) {
             atomicExch(flag, 0);
           }
@@ -774,21 +805,19 @@ __global__ void __launch_bounds__(RunsCfg<HD>::THREADS, 1)
           uint8_t* dst = smem + C::OFF_ST + s * C::STAGE;
           const int cell = rt.cell0[sg.run] + (sg.ch0 + jl) * RCH;
           const bool last = !is_k && has_tail && jl == sg.n - 1;
-          const uint32_t bar = map_to_rank(smem_u32(&full[s]), 0);
           if (lane == 0) {
-            if (rank == 0) mbar_arrive_expect_tx(&full[s], last ? C::STAGE : 2 * C::STAGE);
+            if (rank == 0) mbar_arrive_expect_tx(&full[s], last ? C::STAGE : CL * C::STAGE);
             if (rank == 1 && last) mbar_arrive_expect_tx(&full[s], C::STAGE);
           }
           __syncwarp();
-          if (is_k) {
-            if (lane < HD / 64)
-              tma_load_3d_pair(dst + lane * (64 * 128), &tmK, bar, sg.kvh * HD, cell + rank * 64, lane);
-          } else if (lane < C::V_BOXES) {
-            const int c0 = sg.kvh * HD + rank * (HD / 2);
-            if (last && rank == 1)
-              tma_load_3d(dst + lane * (C::STAGE / C::V_BOXES), &tmV, &full[s], c0, cell, lane);
+          if (lane < (is_k ? HD / 64 : C::V_BOXES)) {
+            const CUtensorMap* map = is_k ? &tmK : &tmV;
+            uint8_t* box = dst + lane * (is_k ? C::KEYS * 128 : RCH * C::VB);
+            const int c0 = sg.kvh * HD + (is_k ? 0 : rank * (HD / 2)), c1 = cell + (is_k ? rank * C::KEYS : 0);
+            if (CL == 1 || (last && rank == 1))
+              tma_load_3d(box, map, &full[s], c0, c1, lane);
             else
-              tma_load_3d_pair(dst + lane * (C::STAGE / C::V_BOXES), &tmV, bar, c0, cell, lane);
+              tma_load_3d_pair(box, map, in_even(&full[s]), c0, c1, lane);
           }
           if (last) tails ^= 1u << s;
           ++f;
@@ -818,17 +847,22 @@ __global__ void __launch_bounds__(RunsCfg<HD>::THREADS, 1)
         if (seg > 0) ok = mbar_wait(q_empty, (seg - 1) & 1, err, PF_DEV_TIMEOUT_PRODUCER);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        if (lane == 0 && rank == 0) mbar_arrive_expect_tx(q_full, 2 * C::Q_BYTES);
+        if (lane == 0 && rank == 0) mbar_arrive_expect_tx(q_full, CL * C::Q_BYTES);
         __syncwarp();
         constexpr int GROUPS = 128 / C::Q_ROWS;
         if (lane < GROUPS * (HD / 64)) {
           const int box = lane / GROUPS, g = lane % GROUPS;
-          tma_load_4d_pair(smem + box * (128 * 128) + g * C::Q_ROWS * 128, &tmQ, map_to_rank(smem_u32(q_full), 0), 0,
-                           sg.kvh << sh.log_g,
-                           rt.row0[sg.run] + ((sg.R0 + C::row_of(rank, g * C::Q_ROWS)) >> sh.log_g), box);
+          uint8_t* dst = smem + box * (128 * 128) + g * C::Q_ROWS * 128;
+          const int head = sg.kvh << sh.log_g;
+          const int row = rt.row0[sg.run] + ((sg.R0 + C::row_of(rank, g * C::Q_ROWS)) >> sh.log_g);
+          if constexpr (CL == 2)
+            tma_load_4d_pair(dst, &tmQ, in_even(q_full), 0, head, row, box);
+          else
+            tma_load_4d(dst, &tmQ, q_full, 0, head, row, box);
         }
       }
       if (lane == 0 && (!ok || read_error(err) != 0) && rank == 0 && seg > 0) runs_drain(q_full, (seg - 1) & 1);
+      if (CL == 1 && lane == 0) leave_table();
       __syncwarp();
     } else if (warp == 0 && rank == 1) {
       // ---------------- the odd CTA's half of the run's last V
@@ -843,27 +877,12 @@ __global__ void __launch_bounds__(RunsCfg<HD>::THREADS, 1)
         if (!ok) break;
         tails ^= 1u << s;
         clear_tail(f - 1);
-        if (lane == 0) mbar_arrive_cluster(map_to_rank(smem_u32(&cleared[s]), 0));
+        if (lane == 0) mbar_arrive_cluster(in_even(&cleared[s]));
       }
       __syncwarp();
     } else if (rank == 1) {
-      // ---------------- warp 3: what the merge kernel has to know of this pair
-      if (lane == 0 && sh.per != 0) {
-        int4* d = reinterpret_cast<int4*>(desc);
-        const int pair = static_cast<int>(blockIdx.x >> 1);
-        if (!sh.desc_by_item) d[2 * pair] = make_int4(0, 0, 0, 0);
-        while (sg.next()) {
-          if (sg.ch0 > 0 || (sg.kind != SEG_PART && !sh.desc_by_item)) continue;
-          // the item's first segment: its pairs (0: nothing to join), rows, first packed row, KV head; first row
-          const RunBlocks<TREE> rb(rt.n[sg.run], rt.pos0[sg.run], sh.log_g);
-          const int i = rb.nb - 1 - sg.R0 / RROWS;
-          const int left = rb.chunks(i) - sg.n;  // chunks in the pairs after this one
-          const int at = sh.desc_by_item ? rt.item0[sg.run] + sg.kvh * rb.nb + i : pair;
-          d[2 * at] = make_int4(sg.kind == SEG_PART ? 1 + (left + sh.per - 1) / sh.per : 0,
-                                min(RROWS, (rt.n[sg.run] << sh.log_g) - sg.R0), rt.row0[sg.run], sg.kvh);
-          d[2 * at + 1] = make_int4(sg.R0, pair, 0, 0);
-        }
-      }
+      // ---------------- warp 3 of the odd CTA
+      if (lane == 0) leave_table();
       __syncwarp();
     } else {
       // ---------------- MMA issue for the pair: a warp runs its loop in step,
@@ -871,12 +890,20 @@ __global__ void __launch_bounds__(RunsCfg<HD>::THREADS, 1)
       // success lets MMAs go.
       const bool leader = elect_one();
       const uint32_t ring = smem_u32(smem + C::OFF_ST);
-      const uint32_t empty0 = map_to_rank(smem_u32(empty), 0), empty1 = map_to_rank(smem_u32(empty), 1);
+      // arrives on a barrier of every CTA of the item once the MMAs issued so far are done
+      auto commit = [&](uint64_t* bar) {
+        if constexpr (CL == 2) {
+          tc_commit_pair(map_to_rank(smem_u32(bar), 0));
+          tc_commit_pair(map_to_rank(smem_u32(bar), 1));
+        } else {
+          tc_commit(bar);
+        }
+      };
       bool ok = true, issued = false;
       uint32_t f0 = 0, j0 = 0, seg = 0, tails = 0;
       constexpr bool TWO = C::NG > 1;  // S and P V have a warp each
-      constexpr uint32_t id_qk = idesc_f16_f32(256, RCH, false);
-      constexpr uint32_t id_pv = idesc_f16_f32(256, HD, true);
+      constexpr uint32_t id_qk = idesc_f16_f32(128 * CL, RCH, false);
+      constexpr uint32_t id_pv = idesc_f16_f32(128 * CL, HD, true);
       const uint64_t qd0 = sdesc_sw128(smem_u32(smem));
       uint32_t v_of[C::NSB];  // fills of V of the last NSB chunks, oldest first
 #pragma unroll
@@ -899,15 +926,14 @@ __global__ void __launch_bounds__(RunsCfg<HD>::THREADS, 1)
 #pragma unroll
           for (int kk = 0; kk < HD / 16; ++kk) {
             const int bx = kk >> 2, w = kk & 3;  // 64-dim box, 16-dim step within it
-            tc_mma_f16_pair(tmem + C::TMEM_S + b * RCH, qd0 + ((bx * (128 * 128) + w * 32) >> 4),
-                            kd0 + ((bx * (64 * 128) + w * 32) >> 4), id_qk, kk > 0 ? 1u : 0u);
+            const uint64_t qd = qd0 + ((bx * (128 * 128) + w * 32) >> 4), kd = kd0 + ((bx * (C::KEYS * 128) + w * 32) >> 4);
+            if constexpr (CL == 2)
+              tc_mma_f16_pair(tmem + C::TMEM_S + b * RCH, qd, kd, id_qk, kk > 0 ? 1u : 0u);
+            else
+              tc_mma_f16(tmem + C::TMEM_S + b * RCH, qd, kd, id_qk, kk > 0 ? 1u : 0u);
           }
-          tc_commit_pair(empty0 + s * 8);
-          tc_commit_pair(empty1 + s * 8);
-          if (jl == sg.n - 1) {
-            tc_commit_pair(map_to_rank(smem_u32(q_empty), 0));
-            tc_commit_pair(map_to_rank(smem_u32(q_empty), 1));
-          }
+          commit(&empty[s]);
+          if (jl == sg.n - 1) commit(q_empty);
           issued = true;
         }
         __syncwarp();
@@ -917,8 +943,10 @@ __global__ void __launch_bounds__(RunsCfg<HD>::THREADS, 1)
         const uint32_t f = f0 + v_fill(jl, sg.n), s = f % C::NST, j = j0 + jl, b = j % C::NSB;
         ok = ok && mbar_wait_spin(&full[s], (f / C::NST) & 1, err, PF_DEV_TIMEOUT_MMA);
         if (jl == sg.n - 1 && tail_keys() < RCH) {
-          ok = ok && mbar_wait<true>(&cleared[s], tails >> s & 1u, err, PF_DEV_TIMEOUT_MMA);
-          tails ^= 1u << s;
+          if constexpr (CL == 2) {
+            ok = ok && mbar_wait<true>(&cleared[s], tails >> s & 1u, err, PF_DEV_TIMEOUT_MMA);
+            tails ^= 1u << s;
+          }
           ok = __all_sync(0xffffffffu, ok);
           if (ok) clear_tail(f);
         }
@@ -928,14 +956,17 @@ __global__ void __launch_bounds__(RunsCfg<HD>::THREADS, 1)
         tc_fence_after();
         if (leader && ok) {
           const uint32_t st = ring + s * C::STAGE;
-          const uint64_t vd0 = HD == 256 ? sdesc_sw128_lbo_sbo(st, RCH * 128, 1024) : sdesc_sw64_mn(st);
-          constexpr int KSTEP = 16 * (HD == 256 ? 128 : 64);  // bytes of 16 keys
+          const uint64_t vd0 = C::VB == 128 ? sdesc_sw128_lbo_sbo(st, RCH * 128, 1024) : sdesc_sw64_mn(st);
           const uint32_t a = tmem + C::TMEM_S + b * RCH, d = tmem + C::TMEM_O + (j % C::NG) * HD;
 #pragma unroll
-          for (int kk = 0; kk < RCH / 16; ++kk)
-            tc_mma_f16_ts_pair(d, a + kk * 8, vd0 + ((kk * KSTEP) >> 4), id_pv, (jl >= C::NG || kk > 0) ? 1u : 0u);
-          tc_commit_pair(empty0 + s * 8);
-          tc_commit_pair(empty1 + s * 8);
+          for (int kk = 0; kk < RCH / 16; ++kk) {
+            const uint64_t vd = vd0 + ((kk * 16 * C::VB) >> 4);
+            if constexpr (CL == 2)
+              tc_mma_f16_ts_pair(d, a + kk * 8, vd, id_pv, (jl >= C::NG || kk > 0) ? 1u : 0u);
+            else
+              tc_mma_f16_ts(d, a + kk * 8, vd, id_pv, (jl >= C::NG || kk > 0) ? 1u : 0u);
+          }
+          commit(&empty[s]);
           issued = true;
         }
       };
@@ -958,7 +989,10 @@ __global__ void __launch_bounds__(RunsCfg<HD>::THREADS, 1)
       if (!ok && issued && leader) {
         // the MMAs already issued finish before TMEM is freed
         uint64_t* bar = &drain[warp == 0 ? 0 : 1];
-        tc_commit_pair(map_to_rank(smem_u32(bar), 0));
+        if constexpr (CL == 2)
+          tc_commit_pair(map_to_rank(smem_u32(bar), 0));
+        else
+          tc_commit(bar);
         runs_drain(bar, 0);
       }
       __syncwarp();
@@ -967,10 +1001,13 @@ __global__ void __launch_bounds__(RunsCfg<HD>::THREADS, 1)
   tc_fence_before();
   __syncthreads();
   // neither CTA leaves (or frees TMEM) while the pair's MMAs may still use it
-  cluster_sync_all();
+  if constexpr (CL == 2) cluster_sync_all();
   if (warp == 0) {
     tc_fence_after();
-    tmem_dealloc_pair(tmem, C::TMEM_COLS);
+    if constexpr (CL == 2)
+      tmem_dealloc_pair(tmem, C::TMEM_COLS);
+    else
+      tmem_dealloc(tmem, C::TMEM_COLS);
   }
 }
 
@@ -1069,6 +1106,7 @@ __global__ void __launch_bounds__(256) attn_runs_merge_kernel(const RunsShape sh
 struct RunsPlan {
   RunTable rt;
   RunsShape sh;
+  int cl;  // CTAs of an item
   int items = 0;
   int64_t desc_bytes = 0;   // the merge kernel's table, ahead of the states
   int64_t state_bytes = 0;  // both
@@ -1093,7 +1131,7 @@ static int sm_count() {
 // else even shares over the resident pairs, but none below MIN_SHARE.
 // False: more work than the line of weights can count.
 constexpr int JOIN_COST = 4, MERGE_COST = 6;
-constexpr int MAX_PAIRS = 120;  // flags of 8 words each in the scratch's header
+constexpr int MAX_PAIRS = 120;  // twice as many of one CTA: flags of 4 words a CTA in the scratch's header
 constexpr int MIN_SHARE = ITEM_FIXED + 2;
 
 template <bool TREE>
@@ -1102,11 +1140,24 @@ static bool make_plan(RunsPlan& p, const pfop_attn_run* runs, int n_runs, int Hq
   p.sh.Hkv = Hkv;
   p.sh.log_g = 0;
   while ((1 << p.sh.log_g) < Hq / Hkv) ++p.sh.log_g;
+  int most = 0;
+  int64_t ones = 0;  // items of 128 rows
+  for (int r = 0; r < n_runs; ++r) {
+    most = std::max(most, runs[r].n_rows);
+    ones += ((int64_t(runs[r].n_rows) << p.sh.log_g) + 127) / 128 * Hkv;
+  }
+  // At hd 64 a CTA works alone where no item would fill a pair (64 trees of
+  // 16 rows of 8 heads: 26.5 us, with pairs 35.3) or where there is not an
+  // item for every SM (25 rows: 4.9 us, 5.8); else the pair's half as many
+  // K/V copies count (64 x 32 rows: 28.6 us with pairs, 29.9 without; prompts
+  // of 4096 and 2048: 126, 142).
+  const int cl = p.cl = hd == 64 && ((most << p.sh.log_g) <= 128 || ones <= sm_count()) ? 1 : 2, item_rows = 128 * cl;
+  p.sh.bs_log = (cl == 2 ? 8 : 7) - p.sh.log_g;
   int row = 0, n = 0, longest = 0, max_rows = 0;
   int64_t items = 0, weight = 0;
   for (int r = 0; r < n_runs; ++r) {
     if (runs[r].n_rows > 0) {
-      const RunBlocks<TREE> rb(runs[r].n_rows, runs[r].pos0, p.sh.log_g);
+      const RunBlocks<TREE> rb(runs[r].n_rows, runs[r].pos0, p.sh.bs_log);
       // an upper bound first: the weights below are 32-bit
       if (weight + int64_t(rb.nb) * Hkv * (int64_t(rb.last) + ITEM_FIXED) >= (int64_t(1) << 30)) return false;
       p.rt.row0[n] = row;
@@ -1119,7 +1170,7 @@ static bool make_plan(RunsPlan& p, const pfop_attn_run* runs, int n_runs, int Hq
       items += int64_t(rb.nb) * Hkv;
       weight += int64_t(rb.weight(rb.nb)) * Hkv;
       longest = std::max(longest, rb.last);
-      max_rows = std::max(max_rows, std::min(RROWS, runs[r].n_rows << p.sh.log_g));
+      max_rows = std::max(max_rows, std::min(item_rows, runs[r].n_rows << p.sh.log_g));
     }
     row += runs[r].n_rows;
   }
@@ -1128,7 +1179,7 @@ static bool make_plan(RunsPlan& p, const pfop_attn_run* runs, int n_runs, int Hq
   p.rt.w0[n] = static_cast<int>(weight);
   p.items = static_cast<int>(items);
   p.sh.slot_rows = (max_rows + 31) / 32 * 32;
-  const int units = std::min(MAX_PAIRS, std::max(1, sm_count() / 2));
+  const int units = std::min(MAX_PAIRS * 2 / cl, std::max(1, sm_count() / cl));
   const int share = std::max<int>(MIN_SHARE, static_cast<int>((weight + units - 1) / units));
   if (items <= units && longest + ITEM_FIXED <= share + (longest > share + 1 ? MERGE_COST : JOIN_COST)) {
     p.sh.per = p.sh.desc_by_item = 0;
@@ -1147,17 +1198,17 @@ static bool make_plan(RunsPlan& p, const pfop_attn_run* runs, int n_runs, int Hq
   return true;
 }
 
-template <int HD, bool TREE>
+template <int HD, int CL, bool TREE>
 static cudaError_t launch_runs(const RunsPlan& p, const __half* q, const __half* k, const __half* v, int64_t n_cells,
                                int total, const uint64_t* mask, int words, __nv_bfloat16* out, uint8_t* states,
                                int* err, int* flags, cudaStream_t s) {
-  using C = RunsCfg<HD>;
-  cudaError_t e = smem_opt_in<attn_runs_kernel<HD, TREE>>(C::SMEM);
+  using C = RunsCfg<HD, CL>;
+  cudaError_t e = smem_opt_in<attn_runs_kernel<HD, CL, TREE>>(C::SMEM);
   if (e != cudaSuccess) return e;
   const int Hq = p.sh.Hq, Hkv = p.sh.Hkv, G = Hq / Hkv;
   // Q as [64-dim box][row][head][64 dims], K as [64-dim box][cell][64 dims],
-  // V as [box][cell][dims of one box]: hd/2 dims a CTA, in 64-dim boxes
-  // (128-byte swizzle) at hd 256, one 32-dim box (64-byte swizzle) at hd 64
+  // V as [box][cell][dims of one box]: 64 (128-byte swizzle) or, of a pair at
+  // hd 64, 32 (64-byte swizzle)
   CUtensorMap tq, tk, tv;
   std::string why;
   {
@@ -1169,16 +1220,16 @@ static cudaError_t launch_runs(const RunsPlan& p, const __half* q, const __half*
   {
     const uint64_t dims[3] = {static_cast<uint64_t>(Hkv) * HD, static_cast<uint64_t>(n_cells), HD / 64};
     const uint64_t st[2] = {static_cast<uint64_t>(Hkv) * HD * 2, 128};
-    const uint32_t box[3] = {64, 64, 1};
+    const uint32_t box[3] = {64, C::KEYS, 1};
     if (!encode_fp16_sw128(&tk, k, 3, dims, st, box, &why)) return cudaErrorInvalidValue;
-    const uint32_t vbox[3] = {HD == 256 ? 64u : 32u, RCH, 1};
-    if (!(HD == 256 ? encode_fp16_sw128(&tv, v, 3, dims, st, vbox, &why)
-                    : encode_fp16_sw64(&tv, v, 3, dims, st, vbox, &why)))
+    const uint32_t vbox[3] = {C::VB / 2, RCH, 1};
+    if (!(C::VB == 128 ? encode_fp16_sw128(&tv, v, 3, dims, st, vbox, &why)
+                       : encode_fp16_sw64(&tv, v, 3, dims, st, vbox, &why)))
       return cudaErrorInvalidValue;
   }
   int* desc = reinterpret_cast<int*>(states);
   float* part = reinterpret_cast<float*>(states + p.desc_bytes);
-  e = launch_k(attn_runs_kernel<HD, TREE>, dim3(2u * p.sh.pairs), dim3(C::THREADS), C::SMEM, s, 2, tq, tk, tv, p.rt,
+  e = launch_k(attn_runs_kernel<HD, CL, TREE>, dim3(CL * p.sh.pairs), dim3(C::THREADS), C::SMEM, s, CL, tq, tk, tv, p.rt,
                p.sh, mask, words, out, part, desc, err, flags);
   if (e != cudaSuccess || !p.sh.merge) return e;
   // an item lies in about pairs / items pairs: one round of loads each
@@ -1254,8 +1305,9 @@ int run_attention(bool tree, const void* q, const void* k, const void* v, int64_
     return launch(p, static_cast<const __half*>(q), static_cast<const __half*>(k), static_cast<const __half*>(v),
                   n_cells, static_cast<int>(total), mask, words, static_cast<__nv_bfloat16*>(out), states, err, err + FLAGS_AT, s);
   };
-  const cudaError_t e = hd == 256 ? (tree ? go(launch_runs<256, true>) : go(launch_runs<256, false>))
-                                  : (tree ? go(launch_runs<64, true>) : go(launch_runs<64, false>));
+  const cudaError_t e = hd == 256   ? (tree ? go(launch_runs<256, 2, true>) : go(launch_runs<256, 2, false>))
+                        : p.cl == 2 ? (tree ? go(launch_runs<64, 2, true>) : go(launch_runs<64, 2, false>))
+                                    : (tree ? go(launch_runs<64, 1, true>) : go(launch_runs<64, 1, false>));
   if (e != cudaSuccess) return fail(PF_E_CUDA, std::string("attention launch: ") + cudaGetErrorString(e));
   return PF_OK;
 }

@@ -358,6 +358,26 @@ def test_two_streams_at_once():
         _check(heads, runs, q, k, v, out)
 
 
+@pytest.mark.parametrize("rows,past", [
+    ([16], [130]), ([17], [130]), ([16], [20000]), ([1], [30000]), ([16] * 5, [3000, 10, 700, 0, 9000]),
+    ([16, 17, 1], [500, 4000, 6000]), ([1] * 100, [37 * i for i in range(100)]),
+    ([4, 0, 12, 1] * 10, [100 + 150 * i for i in range(40)]),
+])
+def test_few_rows_a_run(rows, past):
+    """Up to 128 MMA rows a run and more, whole, cut in two and cut in many;
+    a tree's and a prompt's masks."""
+    heads = (32, 4, 64)
+    runs, cells = _layout(rows, past)
+    q, k, v, out = _inputs(heads, runs, cells, 67)
+    plan = _packed(heads, runs, q, k, v, out)
+    _check(heads, runs, q, k, v, out)
+    mask_np = _random_tree(runs, 1, 3)
+    out.fill_(7)
+    binding.attention_tree(q, k, v, plan, torch.from_numpy(mask_np.view(np.int64)).cuda(), out)
+    plan.check()
+    _check(heads, runs, q, k, v, out, mask_np)
+
+
 @pytest.mark.parametrize("heads", [(8, 1, 256), (32, 4, 64)])
 def test_runs_made_on_one_stream_used_on_another(heads):
     """A scratch that is made behind long work of one stream, in memory that
