@@ -1126,11 +1126,16 @@ static int sm_count() {
 }
 
 // Which cut: a pair per item where the items fit the GPU at once and the
-// longest takes no longer than an even share would with what joining costs
-// (JOIN_COST chunk times in the pairs, MERGE_COST with the merge kernel);
+// longest takes no longer than an even share would with what joining costs;
 // else even shares over the resident pairs, but none below MIN_SHARE.
+// Joining costs MERGE_COST chunk times and one for every MERGE_BYTES of
+// states written and read.  (hd 256: a 2048-row prompt of 8 heads 24.6 us
+// with a pair per item, 35.3 in shares; 4 trees of 16 rows of 8 heads over
+// 1300 keys 19.4 and 14.9.)  Where no item covers a whole share, a pair per
+// item is better throughout (512 rows: 10.6 and 14.9 us).
 // False: more work than the line of weights can count.
-constexpr int JOIN_COST = 4, MERGE_COST = 6;
+constexpr int MERGE_COST = 6;
+constexpr int64_t merge_bytes(int hd) { return (hd == 256 ? 4 : 2) << 20; }
 constexpr int MAX_PAIRS = 120;  // twice as many of one CTA: flags of 4 words a CTA in the scratch's header
 constexpr int MIN_SHARE = ITEM_FIXED + 2;
 
@@ -1181,14 +1186,17 @@ static bool make_plan(RunsPlan& p, const pfop_attn_run* runs, int n_runs, int Hq
   p.sh.slot_rows = (max_rows + 31) / 32 * 32;
   const int units = std::min(MAX_PAIRS * 2 / cl, std::max(1, sm_count() / cl));
   const int share = std::max<int>(MIN_SHARE, static_cast<int>((weight + units - 1) / units));
-  if (items <= units && longest + ITEM_FIXED <= share + (longest > share + 1 ? MERGE_COST : JOIN_COST)) {
+  const int pairs = static_cast<int>((weight + share - 1) / share);
+  const int64_t states = (pairs + items) * p.sh.slot_rows * hd * 4 * 2;
+  if (items <= units &&
+      (longest <= share + 1 || longest + ITEM_FIXED <= share + MERGE_COST + states / merge_bytes(hd))) {
     p.sh.per = p.sh.desc_by_item = 0;
     p.sh.pairs = p.items;
     p.desc_bytes = p.state_bytes = 0;
     p.sh.merge = 0;
   } else {
     p.sh.per = share;
-    p.sh.pairs = static_cast<int>((weight + share - 1) / share);
+    p.sh.pairs = pairs;
     p.sh.merge = longest > share + 1 ? 1 : 0;  // else no item covers a whole share
     p.sh.desc_by_item = p.items < p.sh.pairs ? 1 : 0;
     p.desc_bytes = (int64_t(std::min(p.sh.pairs, p.items)) * 32 + 255) / 256 * 256;
