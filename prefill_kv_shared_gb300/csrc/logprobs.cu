@@ -46,7 +46,7 @@ constexpr int LP_GROUPS = 64;  // of a CTA's threads, whose maxima are compared
 constexpr int LP_PAIRS_MAX = 24;
 constexpr int LP_CAND = 256;   // listed candidates
 constexpr int LP_CLUSTER_MAX = 8;
-constexpr int LP_CHUNK_VECS = 128;  // 16-byte vectors of a warp's copy
+constexpr int LP_CHUNK_LOG = 7, LP_CHUNK_VECS = 1 << LP_CHUNK_LOG;  // 16-byte vectors of a warp's copy
 constexpr int LP_STAGES = 2;        // copies a warp has on their way
 // W: warps of a CTA
 constexpr int lp_ring_bytes(int w) { return w * LP_STAGES * LP_CHUNK_VECS * 16; }
@@ -205,18 +205,18 @@ struct LpSlice {
   static constexpr int TAKE = 16 / VN;  // vectors of a step: 16 logits
   const T* x;
   int n, head, nvec;
-  int chunk;  // vectors of a chunk, a multiple of 32
+  int chunk_log;  // 1 << chunk_log vectors are a chunk, at least 32
   __device__ LpSlice(const T* p, int len) : x(p), n(len) {
     const int mis = static_cast<int>((reinterpret_cast<uintptr_t>(p) & 15) / sizeof(T));
     head = min(len, mis ? VN - mis : 0);
     nvec = (len - head) / VN;
     // a small slice is dealt out to all threads (else half its groups would be empty)
-    chunk = min(LP_CHUNK_VECS, max(1, (nvec + 32 * W - 1) / (32 * W)) * 32);
+    chunk_log = nvec <= 32 * W ? 5 : nvec <= 64 * W ? 6 : LP_CHUNK_LOG;
   }
   __device__ __forceinline__ const uint4* vecs() const { return reinterpret_cast<const uint4*>(x + head); }
-  __device__ __forceinline__ int chunks() const { return (nvec + chunk - 1) / chunk; }
+  __device__ __forceinline__ int chunks() const { return (nvec + (1 << chunk_log) - 1) >> chunk_log; }
   // vectors of a step that one place stands for: those of 16 logits, in a small slice one
-  __device__ __forceinline__ int step_log() const { return chunk < LP_CHUNK_VECS ? 0 : TAKE == 4 ? 2 : 1; }
+  __device__ __forceinline__ int step_log() const { return chunk_log < LP_CHUNK_LOG ? 0 : TAKE == 4 ? 2 : 1; }
   // f(value, id in the slice) for the logits of vector v that are at least tau
   template <class F>
   __device__ __forceinline__ void look(int v, float tau, F&& f) const {
@@ -235,11 +235,11 @@ struct LpSlice {
   // few[0 .. n_few), and all of the threads many[0 .. n_many)'s
   template <class F>
   __device__ __forceinline__ void from(const int* few, int n_few, const int* many, int n_many, float tau, F&& f) const {
-    const int per = chunk / 32;  // a thread's vectors of a chunk
+    const int per_log = chunk_log - 5;  // 1 << per_log vectors of a chunk are a thread's
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int sl = step_log(), steps = n_few << sl;
     // vectors dealt out over the CTA, then those of a thread over a warp
-    const int per_thread = per * ((chunks() + W - 1) / W);
+    const int per_thread = ((chunks() + W - 1) / W) << per_log;
     int i = threadIdx.x, q = warp, k = lane;
 #pragma unroll 1
     for (;;) {  // (one copy of the code: what is run once a row costs its fetching)
@@ -249,7 +249,7 @@ struct LpSlice {
         i += (32 * W);
       } else if (q < n_many) {
         const int t = many[q];
-        v = k < per_thread ? ((t >> 5) + W * (k / per)) * chunk + k % per * 32 + (t & 31) : nvec;
+        v = k < per_thread ? (((t >> 5) + W * (k >> per_log)) << chunk_log) + (k & ((1 << per_log) - 1)) * 32 + (t & 31) : nvec;
         k += 32;
         if (k >= per_thread) k = lane, q += W;
       } else {
@@ -297,8 +297,8 @@ struct LpSlice {
     const int cnt = warp < chunks() ? (chunks() - warp + W - 1) / W : 0;
     const int tail = head + nvec * VN;
     auto copy = [&](int i) {
-      const int v0 = (warp + i * W) * chunk;
-      const uint32_t bytes = static_cast<uint32_t>(min(chunk, nvec - v0)) * 16u;
+      const int v0 = (warp + i * W) << chunk_log;
+      const uint32_t bytes = static_cast<uint32_t>(min(1 << chunk_log, nvec - v0)) * 16u;
       uint64_t* bar = landed + i % LP_STAGES;
       mbar_arrive_expect_tx(bar, bytes);
       bulk_load(ring + i % LP_STAGES * LP_CHUNK_VECS, vecs() + v0, bytes, bar);
@@ -318,7 +318,7 @@ struct LpSlice {
         for (int j = i + 1; j < min(i + LP_STAGES, cnt); ++j) wait(j);  // copies on their way
         return false;
       }
-      const int v0 = (warp + i * W) * chunk;
+      const int v0 = (warp + i * W) << chunk_log;
       const uint4* c = ring + i % LP_STAGES * LP_CHUNK_VECS + lane;
       auto raise = [&](float mx, int v) {
         if (mx > a.m) {
@@ -329,7 +329,7 @@ struct LpSlice {
           m2 = fmaxf(m2, mx);
         }
       };
-      if (chunk == LP_CHUNK_VECS && v0 + chunk <= nvec) {
+      if (chunk_log == LP_CHUNK_LOG && v0 + LP_CHUNK_VECS <= nvec) {
         static_assert(LP_CHUNK_VECS % (32 * TAKE) == 0, "a chunk is a number of whole steps");
 #pragma unroll 1
         for (int b = 0; b < LP_CHUNK_VECS / 32; b += TAKE) {
@@ -347,7 +347,7 @@ struct LpSlice {
         }
       } else {
 #pragma unroll 1
-        for (int b = 0; b < chunk / 32 && v0 + 32 * b + lane < nvec; ++b) {
+        for (int b = 0; b < 1 << (chunk_log - 5) && v0 + 32 * b + lane < nvec; ++b) {
           float e[VN];
           LpVec<T>::get(c[32 * b], e);
           float mx = fmaxf(e[0], e[1]);
@@ -472,12 +472,13 @@ __device__ __noinline__ void lp_select(const LpSlice<T, W>& sl, int id0, int n, 
 }
 
 template <class T, int W>
-__global__ void __launch_bounds__(32 * W, lp_ctas_per_sm(W)) logprobs_kernel(const LogprobArgs a, int cluster) {
+__global__ void __launch_bounds__(32 * W, lp_ctas_per_sm(W)) logprobs_kernel(const LogprobArgs a, int cluster_log) {
   __shared__ LpShared<W> sh;
   extern __shared__ __align__(16) uint4 lp_ring[];
   LpCluster& all = *reinterpret_cast<LpCluster*>(lp_ring + lp_ring_bytes(W) / 16);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int r = static_cast<int>(blockIdx.x) / cluster, rank = static_cast<int>(blockIdx.x) % cluster;
+  const int cluster = 1 << cluster_log;
+  const int r = static_cast<int>(blockIdx.x >> cluster_log), rank = static_cast<int>(blockIdx.x) & (cluster - 1);
   const T* x = static_cast<const T*>(a.logits) + static_cast<int64_t>(r) * a.ld;
   const int id0 = rank * a.slice;
   const LpSlice<T, W> sl(x + id0, min(a.vocab - id0, a.slice));
@@ -626,7 +627,7 @@ static cudaError_t launch_logprobs(const LogprobArgs& a, int cluster, cudaStream
   const cudaError_t e = smem_opt_in<logprobs_kernel<T, W>>(smem);
   if (e != cudaSuccess) return e;
   return launch_k(logprobs_kernel<T, W>, dim3(static_cast<unsigned>(a.rows) * cluster), dim3(32 * W),
-                  cluster > 1 ? smem : lp_ring_bytes(W), s, cluster, a, cluster);
+                  cluster > 1 ? smem : lp_ring_bytes(W), s, cluster, a, __builtin_ctz(cluster));
 }
 
 template <class T>
