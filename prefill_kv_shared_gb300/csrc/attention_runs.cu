@@ -49,6 +49,17 @@
 // maximum or hands over, and three S buffers keep both supplied.  All waits
 // are bounded (PF_WAIT_CYCLES): one that gives up flags the scratch's error
 // word and the pair unwinds.
+//
+// Bounds and figures (one call, GB300): long prompts at hd 256 are bound by
+// the MMAs (2058 clocks a chunk, 2048 at the full rate; six prompts, 15845
+// rows in all, 8 heads over 2: 224 us, 1630 TFLOP/s); at hd 64 by the chain of
+// a chunk's softmax and hand-overs (1085 clocks, of which the exponential
+// unit is busy for 512; prompts of 4096 and 2048, 32 heads over 4: 126 us, 680
+// TFLOP/s).  Drafted trees read each context once: 12 trees of 1 to 64 rows,
+// 159 MB, 40.5 us, 3.9 TB/s; 64 trees of 16 rows, 69 MB, 26.4 us, 2.6 TB/s,
+// where a segment's first scores and output (4000 to 5000 clocks) count as
+// much as its chunks.  Small calls are bound by latency: 25 rows 4.9 us, 512
+// rows of 8 heads 10.6 us.
 #include "../../include/prefill_ops.h"
 #include "attn.cuh"
 #include "common.cuh"
@@ -94,6 +105,8 @@ struct RunsCfg {
   static constexpr int STAGE = KEYS * HD * 2;          // K [box][KEYS][128 B] or V [box][128 keys][VB], hd/CL dims
   static constexpr int VB = HD / CL >= 64 ? 128 : 64;  // bytes of a key's row in a box of V
   static constexpr int V_BOXES = HD / CL * 2 / VB;
+  // as many stages as fit beside Q (at hd 256 four, with the output staged
+  // through the room of the fifth, took 354 us for 254)
   static constexpr int NST = HD == 256 ? 5 : CL == 2 ? 16 : 12;
   static constexpr int NG = HD == 256 ? 1 : 2;  // row warpgroups, taking chunks in turn
   static constexpr int NSB = NG + 1;            // S buffers
@@ -1017,7 +1030,9 @@ __global__ void __launch_bounds__(RunsCfg<HD, CL>::THREADS, 1)
 // first segment (desc: 8 ints each); blockIdx.y 32-row groups; `ways` warps
 // take four dims of the group's rows (lane = row), the states dealt out among
 // them and their sums joined in warp order.  Bound by the latency of reading
-// the states from L2: eight are in flight, and many states want many warps.
+// the states from L2: eight are in flight, and many states want many warps
+// (25 rows over 32768 keys, 76 states: 20.4 us with 8 ways, 30.8 with one; few
+// states do not: 4 trees, 15 states over 4 items, 14.9 with one, 19.6 with 8).
 template <int HD>
 __global__ void __launch_bounds__(256) attn_runs_merge_kernel(const RunsShape sh, int ways, const int* desc,
                                                               const float* part, __nv_bfloat16* out) {
