@@ -23,7 +23,7 @@ from tests.gpu_util import need_gpu, torch
 
 pytestmark = pytest.mark.gpu
 
-HEADS = [(8, 1, 256), (8, 2, 256), (32, 4, 64), (4, 1, 64), (4, 4, 64), (16, 1, 256), (2, 2, 256)]
+HEADS = [(8, 1, 256), (8, 2, 256), (32, 4, 64), (4, 1, 64), (4, 4, 64), (16, 1, 256), (2, 2, 256), (16, 1, 64)]
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -376,6 +376,47 @@ def test_few_rows_a_run(rows, past):
     binding.attention_tree(q, k, v, plan, torch.from_numpy(mask_np.view(np.int64)).cuda(), out)
     plan.check()
     _check(heads, runs, q, k, v, out, mask_np)
+
+
+@pytest.mark.parametrize("rows,past", [
+    ([700, 33, 900], [0, 2000, 50]), ([40] * 20, [10] * 20), ([40] * 20 + [33], [10] * 20 + [40000]),
+    ([160, 17] * 12, [1000, 0] * 12),
+])
+def test_many_rows_at_head_dim_64(rows, past):
+    """Items of up to 256 MMA rows, more of them than SMs, whole, cut in two
+    and in many, and recorded; the tree's masks where its rows allow them."""
+    heads = (32, 4, 64)
+    runs, cells = _layout(rows, past)
+    q, k, v, out = _inputs(heads, runs, cells, 71)
+    plan = _packed(heads, runs, q, k, v, out)
+    _check(heads, runs, q, k, v, out)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        binding.attention_packed(q, k, v, plan, out)
+    first = out.clone()
+    out.fill_(7)
+    for _ in range(3):
+        graph.replay()
+    torch.cuda.synchronize()
+    plan.check()
+    assert torch.equal(out, first)
+    if max(rows) > 256:
+        return
+    mask_np = _random_tree(runs, 3, 3)
+    binding.attention_tree(q, k, v, plan, torch.from_numpy(mask_np.view(np.int64)).cuda(), out)
+    plan.check()
+    _check(heads, runs, q, k, v, out, mask_np)
+
+
+@pytest.mark.parametrize("heads", [(8, 2, 256), (32, 4, 64)])
+def test_runs_that_share_cells(heads):
+    """Several sequences over the same prefix, and one over another's cells."""
+    runs = [(5, 300, 0), (9, 300, 0), (1, 0, 0), (40, 100, 37), (1, 308, 0)]
+    q, k, v, out = _inputs(heads, runs, 320, 73)
+    _packed(heads, runs, q, k, v, out)
+    _check(heads, runs, q, k, v, out)
 
 
 @pytest.mark.parametrize("heads", [(8, 1, 256), (32, 4, 64)])
