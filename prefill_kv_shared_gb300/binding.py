@@ -365,7 +365,7 @@ def _call_on(index: int, stream, fn, *args):
     """fn(*args, stream) with CUDA device `index` current; stream None: the
     device's current torch stream, so that the call is ordered with the torch
     work around it."""
-    c = _t()._C
+    c = (_torch or _t())._C
     if c._cuda_getDevice() != index:
         with _torch.cuda.device(index):
             return _call_on(index, stream, fn, *args)
@@ -410,20 +410,24 @@ class AttnRuns:
 
     def _fit(self, q, k, v, out):
         """The number of cells; raises where a buffer does not fit."""
+        # (len() of a tensor takes as long as five of these checks)
         hq, hkv, hd = self.shape
-        rows, cells, d = len(q), len(k), self.device
-        f16, kv = _torch.float16, (cells, hkv, hd)
+        qs, ks, os, d, f16 = q.shape, k.shape, out.shape, self.device, _torch.float16
         if not (q.dtype is f16 and k.dtype is f16 and v.dtype is f16 and out.dtype is _torch.bfloat16
-                and q.shape == (rows, hq, hd) and k.shape == kv and v.shape == kv and out.shape[1:] == (hq, hd)
+                and len(qs) == 3 and len(ks) == 3 and len(os) == 3 and v.shape == ks
+                and qs[0] >= self.n_rows and qs[1] == hq and qs[2] == hd and ks[1] == hkv and ks[2] == hd
+                and os[0] >= self.n_rows and os[1] == hq and os[2] == hd
                 and q.get_device() == d and k.get_device() == d and v.get_device() == d and out.get_device() == d
-                and q.is_contiguous() and k.is_contiguous() and v.is_contiguous() and out.is_contiguous()
-                and rows >= self.n_rows and len(out) >= self.n_rows):
+                and q.is_contiguous() and k.is_contiguous() and v.is_contiguous() and out.is_contiguous()):
             self._refuse(q, k, v, out)
-        return cells
+        return ks[0]
 
     def _refuse(self, q, k, v, out):
         """Say which buffer does not fit."""
         hq, hkv, hd = self.shape
+        for t, what in ((q, "q"), (k, "k"), (v, "v"), (out, "out")):
+            if t.dim() != 3:
+                raise ValueError(f"{what}: needs [rows or cells, heads, head_dim], got {tuple(t.shape)}")
         if len(q) < self.n_rows or len(out) < self.n_rows:
             raise ValueError(f"q and out: the runs have {self.n_rows} rows")
         _on_device(q, "q", _torch.float16, (len(q), hq, hd), self.device)
@@ -446,13 +450,13 @@ def attention_tree(q, k, v, runs: AttnRuns, mask, out, stream=None):
     """Attention of drafted token trees (pfop_attention_tree): as
     attention_packed, with mask [T, words] int64, bit j % 64 of word j / 64
     set where the row sees drafted token j of its run."""
-    if mask.dim() != 2 or len(mask) < runs.n_rows:
+    ms = mask.shape
+    if len(ms) != 2 or ms[0] < runs.n_rows:
         raise ValueError(f"mask: needs [{runs.n_rows}, words]")
     cells = runs._fit(q, k, v, out)
-    words = mask.shape[1]
-    m = _on_device(mask, "mask", _torch.int64, (len(mask), words), runs.device)
+    m = _on_device(mask, "mask", _torch.int64, ms, runs.device)
     _call_on(runs.device, stream, runs._lib.pfop_attention_tree, q.data_ptr(), k.data_ptr(), v.data_ptr(), cells,
-             *runs.shape, runs.runs, runs.n_runs, m, words, out.data_ptr(), runs.work_at, runs.work_bytes)
+             *runs.shape, runs.runs, runs.n_runs, m, ms[1], out.data_ptr(), runs.work_at, runs.work_bytes)
 
 
 def logprobs(logits, tokens=None, logp=None, entropy=None, top_id=None, top_logp=None, stream=None):
@@ -469,17 +473,18 @@ def logprobs(logits, tokens=None, logp=None, entropy=None, top_id=None, top_logp
         kind = PF_L_BF16
     else:
         raise ValueError(f"logits: element type must be float32 or bfloat16, got {logits.dtype}")
-    if logits.dim() != 2 or (logits.shape[1] > 1 and logits.stride(1) != 1):
+    shape, stride = logits.shape, logits.stride()
+    if len(shape) != 2 or (shape[1] > 1 and stride[1] != 1):
         raise ValueError("logits: needs [rows, vocab] with dense rows")
     if (tokens is None) != (logp is None) or (top_id is None) != (top_logp is None):
         raise ValueError("tokens and logp, top_id and top_logp go together")
     d = logits.get_device()
     if d < 0:
         raise ValueError(f"logits: must be on a CUDA device, is on {logits.device}")
-    rows, vocab = logits.shape
+    rows, vocab = shape
     f32, i32, one = torch.float32, torch.int32, (rows,)
     n_top = 0 if top_id is None else top_id.shape[-1]
-    _call_on(d, stream, load().pfop_logprobs, kind, logits.data_ptr(), logits.stride(0) if rows > 1 else vocab, rows,
+    _call_on(d, stream, load().pfop_logprobs, kind, logits.data_ptr(), stride[0] if rows > 1 else vocab, rows,
              vocab, None if tokens is None else _on_device(tokens, "tokens", i32, one, d), n_top,
              None if logp is None else _on_device(logp, "logp", f32, one, d),
              None if entropy is None else _on_device(entropy, "entropy", f32, one, d),

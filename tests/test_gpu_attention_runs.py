@@ -469,7 +469,8 @@ def test_wrappers_refuse_what_does_not_fit():
     plan = binding.AttnRuns(runs, *heads)
     mask = torch.zeros(4, 1, dtype=torch.int64, device="cuda")
     for bad in (dict(q=q.float()), dict(q=q[:3].contiguous()), dict(k=k[:, :1]), dict(k=k.cpu()), dict(v=v[:19]),
-                dict(out=out.half()), dict(out=out[:3]), dict(q=q.transpose(0, 1).contiguous().transpose(0, 1))):
+                dict(out=out.half()), dict(out=out[:3]), dict(q=q.transpose(0, 1).contiguous().transpose(0, 1)),
+                dict(q=q[:, 0]), dict(out=out.flatten()), dict(k=k[0, 0, 0]), dict(v=v[:, :, :32].contiguous())):
         a = dict(q=q, k=k, v=v, out=out)
         a.update(bad)
         with pytest.raises(ValueError):
