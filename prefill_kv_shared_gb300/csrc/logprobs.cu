@@ -624,8 +624,7 @@ constexpr int LP_SLICE_MIN = 2048;
 template <class T, int W>
 static cudaError_t launch_logprobs(const LogprobArgs& a, int cluster, cudaStream_t s) {
   constexpr int smem = lp_ring_bytes(W) + static_cast<int>(sizeof(LpCluster));
-  const cudaError_t e = smem_opt_in<logprobs_kernel<T, W>>(smem);
-  if (e != cudaSuccess) return e;
+  static_assert(smem + sizeof(LpShared<W>) <= 48 * 1024, "more shared memory has to be asked for");
   return launch_k(logprobs_kernel<T, W>, dim3(static_cast<unsigned>(a.rows) * cluster), dim3(32 * W),
                   cluster > 1 ? smem : lp_ring_bytes(W), s, cluster, a, __builtin_ctz(cluster));
 }
