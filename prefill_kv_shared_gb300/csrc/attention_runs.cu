@@ -412,12 +412,18 @@ __device__ __forceinline__ uint32_t tree_bits(const uint64_t* row_mask, int word
   const int d = kk - pos0;  // drafted token of the word's first bit
   if (d <= -32) return 0xffffffffu;
   if (d >= n) return 0u;
+  // (volatile: loaded where it stands in the program, not where it is used)
+  auto word = [&](int i) {
+    uint64_t v;
+    asm volatile("ld.global.nc.b64 %0, [%1];" : "=l"(v) : "l"(row_mask + i));
+    return v;
+  };
   uint64_t w;
   if (d < 0) {
-    w = (__ldg(row_mask) << -d) | ((1ull << -d) - 1ull);
+    w = (word(0) << -d) | ((1ull << -d) - 1ull);
   } else {
-    w = __ldg(row_mask + (d >> 6)) >> (d & 63);
-    if ((d & 63) > 32 && (d >> 6) + 1 < words) w |= __ldg(row_mask + (d >> 6) + 1) << (64 - (d & 63));
+    w = word(d >> 6) >> (d & 63);
+    if ((d & 63) > 32 && (d >> 6) + 1 < words) w |= word((d >> 6) + 1) << (64 - (d & 63));
   }
   if (n - d < 32) w &= (1ull << (n - d)) - 1ull;
   return static_cast<uint32_t>(w);
@@ -597,29 +603,32 @@ __global__ void __launch_bounds__(RunsCfg<HD, CL>::THREADS, 1)
       const int first = C::NG == 1 ? 0 : static_cast<int>((j0 + h) & 1);  // of the warpgroup's chunks
       for (int jl = first; jl < sg.n; jl += C::NG) {
         const int b = (j0 + jl) % C::NSB;
+        const int key0 = (sg.ch0 + jl) * RCH;
+        // the row's view of its keys, skipped where every row of the warp sees
+        // all of them; a tree's comes from memory, which the wait for S hides
+        const bool all = TREE ? key0 + RCH <= pos0 : __all_sync(0xffffffffu, pos >= key0 + RCH - 1);
+        uint32_t bits[NB];
+        if (TREE && !all) {
+#pragma unroll
+          for (int w = 0; w < NB; ++w) bits[w] = row ? tree_bits(row_mask, words, pos0, n_rows, key0 + 32 * w) : 0u;
+        }
         if (!done(f0 + k_fill(jl))) break;
         if (active) {
-          const int key0 = (sg.ch0 + jl) * RCH;
           const uint32_t ts = lanes + C::TMEM_S + b * RCH;
           tc_fence_after();
           uint32_t x[NB][32];
 #pragma unroll
           for (int w = 0; w < NB; ++w) tmem_ld32(ts + 32 * w, x[w]);
-          // the row's view of its keys, skipped where every row of the warp sees all of them
-          const bool all = TREE ? key0 + RCH <= pos0 : __all_sync(0xffffffffu, pos >= key0 + RCH - 1);
 #pragma unroll
           for (int w = 0; w < NB; ++w) tmem_ld_wait32(x[w]);
           if (!all) {
 #pragma unroll
             for (int w = 0; w < NB; ++w) {
-              uint32_t bits;
-              if (TREE) {
-                bits = row ? tree_bits(row_mask, words, pos0, n_rows, key0 + 32 * w) : 0u;
-              } else {
+              if (!TREE) {
                 const int nv = pos - key0 - 32 * w + 1;
-                bits = nv >= 32 ? 0xffffffffu : nv <= 0 ? 0u : (1u << nv) - 1u;
+                bits[w] = nv >= 32 ? 0xffffffffu : nv <= 0 ? 0u : (1u << nv) - 1u;
               }
-              mask_scores(x[w], bits);
+              mask_scores(x[w], bits[w]);
             }
           }
           float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
