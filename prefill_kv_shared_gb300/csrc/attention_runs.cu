@@ -479,8 +479,9 @@ __global__ void __launch_bounds__(RunsCfg<HD, CL>::THREADS, 1)
   uint64_t* o_free = q_full + 2;          // in the even CTA: the row warps of both have read O
   uint64_t* drain = q_full + 3;           // 2, error path only
   uint64_t* p_full = q_full + 5;          // by S buffer, in the even CTA: a warpgroup of both CTAs
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(p_full + C::NSB);
-  static_assert((3 * C::NST + 6 + C::NSB) * 8 <= 512 && C::NG <= 2, "barrier layout");
+  uint64_t* state_out = p_full + C::NSB;  // this CTA's rows of a first part's state are written
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(state_out + 1);
+  static_assert((3 * C::NST + 7 + C::NSB) * 8 <= 512 && C::NG <= 2, "barrier layout");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = CL == 2 ? static_cast<int>(cluster_ctarank()) : 0;
@@ -498,6 +499,7 @@ __global__ void __launch_bounds__(RunsCfg<HD, CL>::THREADS, 1)
     mbar_init(q_empty, 1);
     for (int b = 0; b < C::NSB; ++b) mbar_init(&p_full[b], 4 * CL);
     mbar_init(o_free, 4 * CL * C::NG);
+    mbar_init(state_out, 4 * C::NG);
     mbar_init(&drain[0], 1);
     mbar_init(&drain[1], 1);
     fence_mbar_init();
@@ -793,19 +795,15 @@ __global__ void __launch_bounds__(RunsCfg<HD, CL>::THREADS, 1)
         }
         if (!whole && h == 0) reinterpret_cast<float2*>(own_state + 32 * HD)[lane] = make_float2(m, l);
         __syncwarp();
-        if (lane == 0) {
-          // the warp's rows of the state are there; or read, and the flag as it was
-          if (kind == SEG_FIRST) {
-            __threadfence();
-            atomicAdd(flags + sg.pair * (4 * CL) + rank * 4 + qw, 1);
-          } else if (kind == SEG_SECOND && atomicAdd(flag, 1) == 2 * C::NG - 1) {
-            atomicExch(flag, 0);
-          }
-        }
+        // the warp's rows of the first part's state are read: the flag as it was
+        if (lane == 0 && kind == SEG_SECOND && atomicAdd(flag, 1) == 2 * C::NG - 1) atomicExch(flag, 0);
         tc_fence_before();
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive_pair_relaxed(o_free_at);
+      if (lane == 0) {
+        mbar_arrive_pair_relaxed(o_free_at);
+        if (kind == SEG_FIRST) mbar_arrive(state_out);
+      }
       j0 += n;
       f0 += 2 * n;
     }
@@ -863,9 +861,30 @@ __global__ void __launch_bounds__(RunsCfg<HD, CL>::THREADS, 1)
       __syncwarp();
     } else if (warp == 2) {
       // ---------------- Q producer: a copy per 64-dim box, or per 32 rows
-      bool ok = true;
+      bool ok = true, first = false;
+      int active = 0;  // row warps of a first part that have rows
+      // A first part (only a pair's first segment is one): its state is passed
+      // on from here, so that the row warps need not wait until their stores
+      // have reached L2.
+      auto pass_on = [&]() {
+        ok = mbar_wait(state_out, 0, err, PF_DEV_TIMEOUT_EPILOGUE);
+        ok = __all_sync(0xffffffffu, ok);
+        if (ok && lane < active) {
+          __threadfence();
+          atomicAdd(flags + pair * (4 * CL) + rank * 4 + lane, C::NG);
+        }
+        __syncwarp();
+        first = false;
+      };
       uint32_t seg = 0;
       for (; ok && sg.next(); ++seg) {
+        if (seg == 0) {
+          first = sg.kind == SEG_FIRST;
+          for (int qw = 0; qw < 4; ++qw)
+            if (sg.R0 + C::row_of(rank, 32 * qw) < rt.n[sg.run] << sh.log_g) active = qw + 1;
+        }
+        if (seg == 2 && first) pass_on();
+        if (!ok) break;
         if (seg > 0) ok = mbar_wait(q_empty, (seg - 1) & 1, err, PF_DEV_TIMEOUT_PRODUCER);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
@@ -884,6 +903,7 @@ __global__ void __launch_bounds__(RunsCfg<HD, CL>::THREADS, 1)
         }
       }
       if (lane == 0 && (!ok || read_error(err) != 0) && rank == 0 && seg > 0) runs_drain(q_full, (seg - 1) & 1);
+      if (ok && first) pass_on();
       if (CL == 1 && lane == 0) leave_table();
       __syncwarp();
     } else if (warp == 0 && rank == 1) {
