@@ -52,11 +52,11 @@
 //
 // Bounds and figures (one call, GB300): long prompts at hd 256 are bound by
 // the MMAs (2058 clocks a chunk, 2048 at the full rate; six prompts, 15845
-// rows in all, 8 heads over 2: 224 us, 1630 TFLOP/s); at hd 64 by the chain of
+// rows in all, 8 heads over 2: 225 us, 1630 TFLOP/s); at hd 64 by the chain of
 // a chunk's softmax and hand-overs (1085 clocks, of which the exponential
-// unit is busy for 512; prompts of 4096 and 2048, 32 heads over 4: 126 us, 680
+// unit is busy for 512; prompts of 4096 and 2048, 32 heads over 4: 124 us, 690
 // TFLOP/s).  Drafted trees read each context once: 12 trees of 1 to 64 rows,
-// 159 MB, 40.5 us, 3.9 TB/s; 64 trees of 16 rows, 69 MB, 26.4 us, 2.6 TB/s,
+// 159 MB, 41 us, 3.9 TB/s; 64 trees of 16 rows, 69 MB, 25.2 us, 2.7 TB/s,
 // where a segment's first scores and output (4000 to 5000 clocks) count as
 // much as its chunks.  Small calls are bound by latency: 25 rows 4.9 us, 512
 // rows of 8 heads 10.6 us.
@@ -1196,10 +1196,10 @@ static bool make_plan(RunsPlan& p, const pfop_attn_run* runs, int n_runs, int Hq
     ones += ((int64_t(runs[r].n_rows) << p.sh.log_g) + 127) / 128 * Hkv;
   }
   // At hd 64 a CTA works alone where no item would fill a pair (64 trees of
-  // 16 rows of 8 heads: 26.5 us, with pairs 35.3) or where there is not an
-  // item for every SM (25 rows: 4.9 us, 5.8); else the pair's half as many
-  // K/V copies count (64 x 32 rows: 28.6 us with pairs, 29.9 without; prompts
-  // of 4096 and 2048: 126, 142).
+  // 16 rows of 8 heads: 26.4 us, with pairs 35.3 when both were measured) or
+  // where there is not an item for every SM (25 rows: 4.9 us, 5.8); else the
+  // pair's half as many K/V copies count (64 x 32 rows: 28.6 us with pairs,
+  // 29.9 without; prompts of 4096 and 2048: 126, 142).
   const int cl = p.cl = hd == 64 && ((most << p.sh.log_g) <= 128 || ones <= sm_count()) ? 1 : 2, item_rows = 128 * cl;
   p.sh.bs_log = (cl == 2 ? 8 : 7) - p.sh.log_g;
   int row = 0, n = 0, longest = 0, max_rows = 0;
