@@ -1060,7 +1060,7 @@ __global__ void __launch_bounds__(RunsCfg<HD, CL>::THREADS, 1)
 // take four dims of the group's rows (lane = row), the states dealt out among
 // them and their sums joined in warp order.  Bound by the latency of reading
 // the states from L2: eight are in flight, and many states want many warps
-// (25 rows over 32768 keys, 76 states: 20.4 us with 8 ways, 30.8 with one; few
+// (25 rows over 32768 keys, 65 states: 20.4 us with 8 ways, 30.8 with one; few
 // states do not: 4 trees, 15 states over 4 items, 14.9 with one, 19.6 with 8).
 template <int HD>
 __global__ void __launch_bounds__(256) attn_runs_merge_kernel(const RunsShape sh, int ways, const int* desc,

@@ -410,6 +410,18 @@ def test_many_rows_at_head_dim_64(rows, past):
     _check(heads, runs, q, k, v, out, mask_np)
 
 
+@pytest.mark.parametrize("heads", [(1024, 64, 64), (1024, 1024, 64), (64, 64, 256), (256, 16, 256)])
+def test_many_heads(heads):
+    runs, cells = _layout([3, 20, 1], [40, 0, 300])
+    q, k, v, out = _inputs(heads, runs, cells, 79)
+    plan = _packed(heads, runs, q, k, v, out)
+    _check(heads, runs, q, k, v, out)
+    mask_np = _random_tree(runs, 1, 7)
+    binding.attention_tree(q, k, v, plan, torch.from_numpy(mask_np.view(np.int64)).cuda(), out)
+    plan.check()
+    _check(heads, runs, q, k, v, out, mask_np)
+
+
 @pytest.mark.parametrize("heads", [(8, 2, 256), (32, 4, 64)])
 def test_runs_that_share_cells(heads):
     """Several sequences over the same prefix, and one over another's cells."""
