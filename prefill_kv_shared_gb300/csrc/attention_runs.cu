@@ -1060,8 +1060,8 @@ __global__ void __launch_bounds__(RunsCfg<HD, CL>::THREADS, 1)
 // take four dims of the group's rows (lane = row), the states dealt out among
 // them and their sums joined in warp order.  Bound by the latency of reading
 // the states from L2: eight are in flight, and many states want many warps
-// (25 rows over 32768 keys, 65 states: 20.4 us with 8 ways, 30.8 with one; few
-// states do not: 4 trees, 15 states over 4 items, 14.9 with one, 19.6 with 8).
+// (25 rows over 32768 keys, 65 states: 20.0 us with 8 ways, 30.8 with one; few
+// states do not: 4 trees, 15 states over 4 items, 14.3 with one, 19.6 with 8).
 template <int HD>
 __global__ void __launch_bounds__(256) attn_runs_merge_kernel(const RunsShape sh, int ways, const int* desc,
                                                               const float* part, __nv_bfloat16* out) {
@@ -1085,13 +1085,16 @@ __global__ void __launch_bounds__(256) attn_runs_merge_kernel(const RunsShape sh
     float2 ml[FLY];
 #pragma unroll
     for (int k = 0; k < FLY; ++k) {
-      const int p = min(q + k * ways, np - 1);
+      const int p = q + k * ways;
       // the first pair's slot is its second
       const float* s = part + (static_cast<size_t>(p == 0 ? 2 * p0 + 1 : 2 * (p0 + p)) * (sh.slot_rows / 32) + blockIdx.y) *
                                   runs_state_floats(HD);
-      ml[k] = __ldcg(reinterpret_cast<const float2*>(s + 32 * HD) + lane);
-      o[k] = __ldcg(reinterpret_cast<const float4*>(s) + quad * 32 + lane);
-      if (q + k * ways >= np) ml[k].x = -INFINITY;
+      ml[k] = make_float2(-INFINITY, 0.f);
+      o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (p < np) {
+        ml[k] = __ldcg(reinterpret_cast<const float2*>(s + 32 * HD) + lane);
+        o[k] = __ldcg(reinterpret_cast<const float4*>(s) + quad * 32 + lane);
+      }
     }
     float mn = m;
 #pragma unroll
