@@ -86,6 +86,7 @@ struct RunTable {
 struct RunsShape {
   int Hq, Hkv, log_g;  // G = 1 << log_g query heads per KV head
   int bs_log;          // 1 << bs_log of a run's rows are an item's
+  int fixed;           // item_fixed
   int per;             // weight of a pair's share; 0: a pair per item
   int pairs;
   int merge;  // an item may be cut in three or more: the merge kernel joins all that are cut
@@ -94,8 +95,10 @@ struct RunsShape {
 };
 
 // weight of an item besides its chunks: its Q copy, first scores and output,
-// in chunk times
-constexpr int ITEM_FIXED = 2;
+// in chunk times.  (hd 256: 15845 rows of 6 prompts 225, 206 and 210 us with 2,
+// 3 and 4; hd 64: prompts of 4096 and 2048 124, 112, 108, 108 and 115 with 2,
+// 3, 4, 5 and 8.)
+constexpr int item_fixed(int hd) { return hd == 256 ? 3 : 4; }
 
 // CL: CTAs of an item
 template <int HD, int CL>
@@ -266,9 +269,9 @@ __host__ __device__ __forceinline__ int find_last(const int* first, int n, int x
 // chunks up to its last row.
 template <bool TREE>
 struct RunBlocks {
-  int n, pos0, bs_log, nb, last;  // last: chunks of the whole run
-  __host__ __device__ RunBlocks(int n_rows, int p0, int bl)
-      : n(n_rows), pos0(p0), bs_log(bl), nb((n_rows + (1 << bs_log) - 1) >> bs_log),
+  int n, pos0, bs_log, fixed, nb, last;  // last: chunks of the whole run
+  __host__ __device__ RunBlocks(int n_rows, int p0, const RunsShape& sh)
+      : n(n_rows), pos0(p0), bs_log(sh.bs_log), fixed(sh.fixed), nb((n_rows + (1 << bs_log) - 1) >> bs_log),
         last(static_cast<int>((static_cast<unsigned>(p0) + n_rows + RCH - 1) / RCH)) {}
   // sum over x' < x of floor(x' / (128 / bs)); modulo 2^32 (differences of it are exact)
   __host__ __device__ unsigned floors(unsigned x) const {
@@ -289,8 +292,8 @@ struct RunBlocks {
   }
   // weight of items 0 .. i-1
   __host__ __device__ int weight(int i) const {
-    if (TREE || i == 0) return i * (last + ITEM_FIXED);
-    return i * ITEM_FIXED + last + from_start(nb - 1) - from_start(nb - i);
+    if (TREE || i == 0) return i * (last + fixed);
+    return i * fixed + last + from_start(nb - 1) - from_start(nb - i);
   }
 };
 
@@ -302,7 +305,7 @@ struct ItemAt {
   __host__ __device__ static ItemAt number(const RunTable& rt, const RunsShape& sh, int idx) {
     ItemAt a;
     a.run = find_last(rt.item0, rt.n_runs, idx);
-    const RunBlocks<TREE> rb(rt.n[a.run], rt.pos0[a.run], sh.bs_log);
+    const RunBlocks<TREE> rb(rt.n[a.run], rt.pos0[a.run], sh);
     const int loc = idx - rt.item0[a.run];
     a.kvh = loc / rb.nb;
     a.i = loc % rb.nb;
@@ -313,14 +316,14 @@ struct ItemAt {
   __host__ __device__ static ItemAt weight(const RunTable& rt, const RunsShape& sh, int x) {
     ItemAt a;
     a.run = find_last(rt.w0, rt.n_runs, x);
-    const RunBlocks<TREE> rb(rt.n[a.run], rt.pos0[a.run], sh.bs_log);
+    const RunBlocks<TREE> rb(rt.n[a.run], rt.pos0[a.run], sh);
     const int head = rb.weight(rb.nb);
     int rem = x - rt.w0[a.run];
     a.kvh = rem / head;
     rem -= a.kvh * head;
     int lo = 0, hi = rb.nb - 1;
     if (TREE) {
-      lo = rem / (rb.last + ITEM_FIXED);
+      lo = rem / (rb.last + sh.fixed);
     } else {
       while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
@@ -337,7 +340,7 @@ struct ItemAt {
 };
 
 // The segments of a pair, from the end of its share.  The share is a range of
-// the line of weights; the chunk k of an item lies at w + ITEM_FIXED + k.
+// the line of weights; the chunk k of an item lies at w + fixed + k.
 enum SegKind : int {
   SEG_WHOLE = 0,  // all of its item
   SEG_FIRST = 1,  // first of two: leaves its state to the next pair
@@ -367,8 +370,8 @@ struct Segments {
   }
   __host__ __device__ bool next() {
     while (left) {
-      const RunBlocks<TREE> rb(rt.n[at.run], rt.pos0[at.run], sh.bs_log);
-      const int ch = rb.chunks(at.i), w = at.w + ITEM_FIXED;
+      const RunBlocks<TREE> rb(rt.n[at.run], rt.pos0[at.run], sh);
+      const int ch = rb.chunks(at.i), w = at.w + sh.fixed;
       const bool all = sh.per == 0;
       const int k0 = all || lo < w ? 0 : lo - w, k1 = all || hi - w > ch ? ch : hi - w;
       run = at.run;
@@ -396,9 +399,9 @@ struct Segments {
             at.kvh = sh.Hkv - 1;
             --at.run;
           }
-          at.i = RunBlocks<TREE>(rt.n[at.run], rt.pos0[at.run], sh.bs_log).nb - 1;
+          at.i = RunBlocks<TREE>(rt.n[at.run], rt.pos0[at.run], sh).nb - 1;
         }
-        at.w -= ITEM_FIXED + RunBlocks<TREE>(rt.n[at.run], rt.pos0[at.run], sh.bs_log).chunks(at.i);
+        at.w -= sh.fixed + RunBlocks<TREE>(rt.n[at.run], rt.pos0[at.run], sh).chunks(at.i);
       }
       if (n > 0) return true;
     }
@@ -562,7 +565,7 @@ __global__ void __launch_bounds__(RunsCfg<HD, CL>::THREADS, 1)
     while (all.next()) {
       if (all.ch0 > 0 || (all.kind != SEG_PART && !sh.desc_by_item)) continue;
       // the item's first segment: its pairs (0: nothing to join), rows, first packed row, KV head; first row
-      const RunBlocks<TREE> rb(rt.n[all.run], rt.pos0[all.run], sh.bs_log);
+      const RunBlocks<TREE> rb(rt.n[all.run], rt.pos0[all.run], sh);
       const int rows_log = sh.bs_log + sh.log_g;
       const int i = rb.nb - 1 - (all.R0 >> rows_log);
       const int left = rb.chunks(i) - all.n;  // chunks in the pairs after this one
@@ -1175,16 +1178,17 @@ static int sm_count() {
 // Which cut: a pair per item where the items fit the GPU at once and the
 // longest takes no longer than an even share would with what joining costs;
 // else even shares over the resident pairs, but none below MIN_SHARE.
-// Joining costs MERGE_COST chunk times and one for every MERGE_BYTES of
+// Joining costs merge_cost chunk times and one for every merge_bytes of
 // states written and read.  (hd 256: a 2048-row prompt of 8 heads 24.6 us
-// with a pair per item, 35.3 in shares; 4 trees of 16 rows of 8 heads over
-// 1300 keys 19.4 and 14.9.)  Where no item covers a whole share, a pair per
+// with a pair per item, 34.3 in shares; 4 trees of 16 rows of 8 heads over
+// 1300 keys 19.3 and 13.1; hd 64: 256 rows over
+// 2000 keys 14.7 and 16.2, a tree of 5 rows over 3000 17.1 and 8.7.)  Where no item covers a whole share, a pair per
 // item is better throughout (512 rows: 10.6 and 14.9 us).
 // False: more work than the line of weights can count.
-constexpr int MERGE_COST = 6;
+constexpr int merge_cost(int hd) { return hd == 256 ? 6 : 8; }
 constexpr int64_t merge_bytes(int hd) { return (hd == 256 ? 4 : 2) << 20; }
 constexpr int MAX_PAIRS = 120;  // twice as many of one CTA: flags of 4 words a CTA in the scratch's header
-constexpr int MIN_SHARE = ITEM_FIXED + 2;
+constexpr int MIN_SHARE = 4;
 
 template <bool TREE>
 static bool make_plan(RunsPlan& p, const pfop_attn_run* runs, int n_runs, int Hq, int Hkv, int hd) {
@@ -1205,13 +1209,14 @@ static bool make_plan(RunsPlan& p, const pfop_attn_run* runs, int n_runs, int Hq
   // 29.9 without; prompts of 4096 and 2048: 126, 142).
   const int cl = p.cl = hd == 64 && ((most << p.sh.log_g) <= 128 || ones <= sm_count()) ? 1 : 2, item_rows = 128 * cl;
   p.sh.bs_log = (cl == 2 ? 8 : 7) - p.sh.log_g;
+  p.sh.fixed = item_fixed(hd);
   int row = 0, n = 0, longest = 0, max_rows = 0;
   int64_t items = 0, weight = 0;
   for (int r = 0; r < n_runs; ++r) {
     if (runs[r].n_rows > 0) {
-      const RunBlocks<TREE> rb(runs[r].n_rows, runs[r].pos0, p.sh.bs_log);
+      const RunBlocks<TREE> rb(runs[r].n_rows, runs[r].pos0, p.sh);
       // an upper bound first: the weights below are 32-bit
-      if (weight + int64_t(rb.nb) * Hkv * (int64_t(rb.last) + ITEM_FIXED) >= (int64_t(1) << 30)) return false;
+      if (weight + int64_t(rb.nb) * Hkv * (int64_t(rb.last) + p.sh.fixed) >= (int64_t(1) << 30)) return false;
       p.rt.row0[n] = row;
       p.rt.n[n] = runs[r].n_rows;
       p.rt.pos0[n] = runs[r].pos0;
@@ -1236,7 +1241,7 @@ static bool make_plan(RunsPlan& p, const pfop_attn_run* runs, int n_runs, int Hq
   const int pairs = static_cast<int>((weight + share - 1) / share);
   const int64_t states = (pairs + items) * p.sh.slot_rows * hd * 4 * 2;
   if (items <= units &&
-      (longest <= share + 1 || longest + ITEM_FIXED <= share + MERGE_COST + states / merge_bytes(hd))) {
+      (longest <= share + 1 || longest + p.sh.fixed <= share + merge_cost(hd) + states / merge_bytes(hd))) {
     p.sh.per = p.sh.desc_by_item = 0;
     p.sh.pairs = p.items;
     p.desc_bytes = p.state_bytes = 0;
