@@ -1196,18 +1196,19 @@ static bool make_plan(RunsPlan& p, const pfop_attn_run* runs, int n_runs, int Hq
   p.sh.Hkv = Hkv;
   p.sh.log_g = 0;
   while ((1 << p.sh.log_g) < Hq / Hkv) ++p.sh.log_g;
-  int most = 0;
-  int64_t ones = 0;  // items of 128 rows
+  int64_t ones = 0, twos = 0;  // items of 128 rows, and of 256
   for (int r = 0; r < n_runs; ++r) {
-    most = std::max(most, runs[r].n_rows);
-    ones += ((int64_t(runs[r].n_rows) << p.sh.log_g) + 127) / 128 * Hkv;
+    const int64_t rows = int64_t(runs[r].n_rows) << p.sh.log_g;
+    ones += (rows + 127) / 128 * Hkv;
+    twos += (rows + 255) / 256 * Hkv;
   }
-  // At hd 64 a CTA works alone where no item would fill a pair (64 trees of
-  // 16 rows of 8 heads: 26.4 us, with pairs 35.3 when both were measured) or
-  // where there is not an item for every SM (25 rows: 4.9 us, 5.8); else the
-  // pair's half as many K/V copies count (64 x 32 rows: 28.6 us with pairs,
-  // 29.9 without; prompts of 4096 and 2048: 126, 142).
-  const int cl = p.cl = hd == 64 && ((most << p.sh.log_g) <= 128 || ones <= sm_count()) ? 1 : 2, item_rows = 128 * cl;
+  // At hd 64 a CTA works alone where there is not an item of 128 rows for
+  // every SM (25 rows of 8 heads: 4.9 us, with pairs 5.6) or where pairs would
+  // hold 15% more rows that are none (64 trees of 16 rows: 24.2 us, 32.6; 20
+  // runs of 40 rows 23.0, 25.8); else the pair's half as many K/V copies count
+  // (64 x 32 rows: 28.2 us with pairs, 31.0 without; prompts of 4096 and 2048:
+  // 107, 123).
+  const int cl = p.cl = hd == 64 && (ones <= sm_count() || 200 * twos > 115 * ones) ? 1 : 2, item_rows = 128 * cl;
   p.sh.bs_log = (cl == 2 ? 8 : 7) - p.sh.log_g;
   p.sh.fixed = item_fixed(hd);
   int row = 0, n = 0, longest = 0, max_rows = 0;
