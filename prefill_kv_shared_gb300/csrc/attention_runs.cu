@@ -52,11 +52,11 @@
 //
 // Bounds and figures (one call, GB300): long prompts at hd 256 are bound by
 // the MMAs (2058 clocks a chunk, 2048 at the full rate; six prompts, 15845
-// rows in all, 8 heads over 2: 225 us, 1630 TFLOP/s); at hd 64 by the chain of
+// rows in all, 8 heads over 2: 213 us, 1720 TFLOP/s); at hd 64 by the chain of
 // a chunk's softmax and hand-overs (1085 clocks, of which the exponential
-// unit is busy for 512; prompts of 4096 and 2048, 32 heads over 4: 124 us, 690
+// unit is busy for 512; prompts of 4096 and 2048, 32 heads over 4: 108 us, 795
 // TFLOP/s).  Drafted trees read each context once: 12 trees of 1 to 64 rows,
-// 159 MB, 41 us, 3.9 TB/s; 64 trees of 16 rows, 69 MB, 25.2 us, 2.7 TB/s,
+// 159 MB, 40.6 us, 3.9 TB/s; 64 trees of 16 rows, 69 MB, 24.4 us, 2.8 TB/s,
 // where a segment's first scores and output (4000 to 5000 clocks) count as
 // much as its chunks.  Small calls are bound by latency: 25 rows 4.9 us, 512
 // rows of 8 heads 10.6 us.
