@@ -382,9 +382,12 @@ __global__ void __launch_bounds__(AttnTcCfg<HD>::THREADS, 1)
       // in the (now idle) K ring, so that the global stores cover whole row
       // segments: lane l stores rows 4i + l/8, columns 4(l%8) .. +3.
       tc_fence_after();
-      // this lane's row: 0 = nothing to write, 1 = output row, 2 = group state
+      // this lane's row: 0 = nothing to write, 1 = output row, 2 = group state.
+      // A row whose keys lie in group 0 alone is written by that group's CTA;
+      // a later group's block may hold such rows too, next to rows that reach
+      // into it, and has seen none of their keys (l = 0).
       const int n_g = pos >= 0 ? attn_row_groups(pos, sh.gc) : 0;
-      const int kind_own = pos < 0 ? 0 : (n_g == 1 ? 1 : (grp < n_g ? 2 : 0));
+      const int kind_own = grp >= n_g ? 0 : n_g == 1 ? 1 : 2;
       const float inv_l = kind_own == 1 ? __frcp_rn(l) : 1.f;  // output rows: O * (1/l)
       // destinations of the rows this lane writes in the transposed layout
       // (rows 4i + lane/8), fetched once from the rows' own lanes
