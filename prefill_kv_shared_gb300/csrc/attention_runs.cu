@@ -1408,7 +1408,11 @@ extern "C" int pfop_attention_status(void* work_dev, void* stream) {
   int h = 0;
   cudaError_t e = cudaMemcpyAsync(&h, work_dev, 4, cudaMemcpyDeviceToHost, s);
   if (e == cudaSuccess) e = cudaStreamSynchronize(s);
-  if (e == cudaSuccess && h) e = cudaMemsetAsync(work_dev, 0, WORK_HEADER, s);  // flags of a call that gave up too
+  if (e == cudaSuccess && h) {
+    // flags of a call that gave up too; over before this returns, since the next call may come on any stream
+    e = cudaMemsetAsync(work_dev, 0, WORK_HEADER, s);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+  }
   if (e != cudaSuccess) return fail(PF_E_CUDA, std::string("attention status: ") + cudaGetErrorString(e));
   if (h) return fail(PF_E_DEVICE_TIMEOUT, "attention gave up a bounded wait, code " + std::to_string(h));
   return PF_OK;

@@ -1,0 +1,55 @@
+"""What attention over runs does after a call that gave up a wait: the status
+call reports it, makes the scratch as good as new, and later calls in that
+scratch are right on any stream.  Reference and tolerance are those of
+test_gpu_attention_runs.py.
+
+The scratch's header (include/prefill_ops.h: 4096 bytes, zero before the first
+call) holds the error word first and from word 64 the flags of items cut in
+two; the tests write there what a call that gave up leaves."""
+import pytest
+
+from prefill_kv_shared_gb300 import binding
+from tests.gpu_util import need_gpu, torch
+from tests.test_gpu_attention_runs import _check, _inputs, _layout, _random_tree
+
+pytestmark = pytest.mark.gpu
+
+# cut in two, cut in many, and a pair (or CTA) per item
+RUNS = [([16, 17, 1], [500, 4000, 6000]), ([25], [9000]), ([64], [100])]
+
+
+@pytest.fixture(scope="module", autouse=True)
+def lib():
+    need_gpu()
+    from prefill_kv_shared_gb300 import build
+    build.build()
+    return binding.load()
+
+
+def _job(heads, rows, past, seed=83):
+    runs, cells = _layout(rows, past)
+    q, k, v, out = _inputs(heads, runs, cells, seed)
+    mask_np = _random_tree(runs, 1, 3)
+    return runs, q, k, v, out, mask_np, torch.from_numpy(mask_np.view("int64")).cuda(), binding.AttnRuns(runs, *heads)
+
+
+@pytest.mark.parametrize("heads", [(8, 1, 256), (32, 4, 64)])
+@pytest.mark.parametrize("rows,past", RUNS)
+def test_status_makes_the_scratch_as_good_as_new(heads, rows, past):
+    runs, q, k, v, out, mask_np, mask, plan = _job(heads, rows, past)
+    side = torch.cuda.Stream()
+    for _ in range(3):
+        header = plan.work[:4096].view(torch.int32)
+        header[0] = 4           # a wait given up
+        header[64:64 + 960] = 1  # parts that were counted and never joined
+        with pytest.raises(binding.PrefillError, match="gave up"):
+            plan.check()
+        with torch.cuda.stream(side):  # not ordered behind the status call's stream
+            assert not plan.work[:4096].any()
+            out.fill_(7)
+            binding.attention_packed(q, k, v, plan, out)
+        plan.check(side)
+        _check(heads, runs, q, k, v, out)
+        binding.attention_tree(q, k, v, plan, mask, out)
+        plan.check()
+        _check(heads, runs, q, k, v, out, mask_np)
