@@ -1162,17 +1162,15 @@ struct RunsPlan {
   int64_t state_bytes = 0;  // both
 };
 
+// of the current device; without one, a GB300's
 static int sm_count() {
-  static const int n = [] {
-    int dev = 0, v = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
-      cudaGetLastError();
-      return 152;
-    }
-    return v > 0 ? v : 152;
-  }();
-  return n;
+  int dev = 0, v = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+    cudaGetLastError();
+    return 152;
+  }
+  return v > 0 ? v : 152;
 }
 
 // Which cut: a pair per item where the items fit the GPU at once and the
@@ -1208,7 +1206,8 @@ static bool make_plan(RunsPlan& p, const pfop_attn_run* runs, int n_runs, int Hq
   // runs of 40 rows 23.0, 25.8); else the pair's half as many K/V copies count
   // (64 x 32 rows: 28.2 us with pairs, 31.0 without; prompts of 4096 and 2048:
   // 107, 123).
-  const int cl = p.cl = hd == 64 && (ones <= sm_count() || 200 * twos > 115 * ones) ? 1 : 2, item_rows = 128 * cl;
+  const int sms = sm_count();
+  const int cl = p.cl = hd == 64 && (ones <= sms || 200 * twos > 115 * ones) ? 1 : 2, item_rows = 128 * cl;
   p.sh.bs_log = (cl == 2 ? 8 : 7) - p.sh.log_g;
   p.sh.fixed = item_fixed(hd);
   int row = 0, n = 0, longest = 0, max_rows = 0;
@@ -1237,7 +1236,7 @@ static bool make_plan(RunsPlan& p, const pfop_attn_run* runs, int n_runs, int Hq
   p.rt.w0[n] = static_cast<int>(weight);
   p.items = static_cast<int>(items);
   p.sh.slot_rows = (max_rows + 31) / 32 * 32;
-  const int units = std::min(MAX_PAIRS * 2 / cl, std::max(1, sm_count() / cl));
+  const int units = std::min(MAX_PAIRS * 2 / cl, std::max(1, sms / cl));
   const int share = std::max<int>(MIN_SHARE, static_cast<int>((weight + units - 1) / units));
   const int pairs = static_cast<int>((weight + share - 1) / share);
   const int64_t states = (pairs + items) * p.sh.slot_rows * hd * 4 * 2;

@@ -47,3 +47,30 @@ def test_status_after_an_error_returns_with_the_scratch_cleared(lib):
     lib.fake_reset(0, 152, 152, 4)
     assert lib.pfop_attention_status(WORK, None) == PF_E_DEVICE_TIMEOUT
     assert _log(lib) == ["copy", "sync", "set:0x4096", "sync"]
+
+
+class _Run(C.Structure):
+    _fields_ = [("n_rows", C.c_int32), ("pos0", C.c_int32), ("cell0", C.c_int32)]
+
+
+def _launches(lib, device, sms0, sms1, rows, past, heads=(8, 1, 256)):
+    """The grids of a call on `device`, and the scratch it needs."""
+    lib.fake_reset(device, sms0, sms1, 0)
+    runs = (_Run * 1)(_Run(rows, past, 0))
+    lib.pfop_attention_work_bytes.restype = C.c_int64
+    need = lib.pfop_attention_work_bytes(*heads, runs, 1)
+    p = C.c_void_p
+    rc = lib.pfop_attention_packed(p(0x10000), p(0x20000), p(0x30000), C.c_int64(rows + past), *heads, runs, 1,
+                                   p(0x40000), p(WORK), C.c_int64(need), None)
+    assert rc == PF_OK
+    return [int(w.split(":")[1].split("x")[0]) for w in _log(lib) if w.startswith("launch")], need
+
+
+def test_the_cut_is_that_of_the_current_device(lib):
+    """Each call's share of the work is cut for the multiprocessors of the
+    device that is current, whichever device the first call was made on."""
+    big, big_need = _launches(lib, 0, 152, 20, 25, 30000)
+    small, small_need = _launches(lib, 1, 152, 20, 25, 30000)
+    assert 100 < big[0] <= 152 and small[0] == 20
+    assert small_need < big_need
+    assert _launches(lib, 0, 152, 20, 25, 30000) == (big, big_need)
