@@ -1020,16 +1020,20 @@ __global__ void __launch_bounds__(RunsCfg<HD, CL>::THREADS, 1)
           ok = ok && mbar_wait_spin(q_full, seg & 1, err, PF_DEV_TIMEOUT_MMA);
           for (int jl = 0; jl < (TWO ? sg.n : C::LA) && jl < sg.n; ++jl) {
             issue_s(jl);
-            if (!__all_sync(0xffffffffu, ok)) break;
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
           }
         }
         if (!TWO || warp == 3)
           for (int jl = 0; jl < sg.n; ++jl) {
             if (!TWO && jl + C::LA < sg.n) issue_s(jl + C::LA);
             issue_pv(jl);
-            if (!__all_sync(0xffffffffu, ok)) break;
+            // every lane knows of one that gave up: the leader then drains,
+            // whether or not its own waits ended
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
           }
-        if (!__all_sync(0xffffffffu, ok)) break;
+        if (!ok) break;
       }
       if (!ok && issued && leader) {
         // the MMAs already issued finish before TMEM is freed

@@ -14,8 +14,9 @@ from tests.test_gpu_attention_runs import _check, _inputs, _layout, _random_tree
 
 pytestmark = pytest.mark.gpu
 
-# cut in two, cut in many, and a pair (or CTA) per item
-RUNS = [([16, 17, 1], [500, 4000, 6000]), ([25], [9000]), ([64], [100])]
+# (rows, past): cut in two, in a few, in many, and a pair (or CTA) per item
+RUNS = [([64] * 40, [900 + 7 * i for i in range(40)]), ([40] * 20, [900] * 20), ([16, 17, 1], [500, 4000, 6000]),
+        ([25], [9000]), ([64], [100])]
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -49,6 +50,29 @@ def test_status_makes_the_scratch_as_good_as_new(heads, rows, past):
             out.fill_(7)
             binding.attention_packed(q, k, v, plan, out)
         plan.check(side)
+        _check(heads, runs, q, k, v, out)
+        binding.attention_tree(q, k, v, plan, mask, out)
+        plan.check()
+        _check(heads, runs, q, k, v, out, mask_np)
+
+
+# both lists hold items that are cut in two, for CTA pairs and (head_dim 64, 40
+# rows) for CTAs that work alone
+@pytest.mark.parametrize("heads,rows,past", [((8, 1, 256), *RUNS[0]), ((32, 4, 64), *RUNS[0]), ((32, 4, 64), *RUNS[1])])
+def test_a_wait_that_runs_out(heads, rows, past):
+    """Flags that never count to what the second parts wait for: their waits
+    end after their bound (about 2 s), the kernel returns, the status says
+    so, and the scratch is good again."""
+    runs, q, k, v, out, mask_np, mask, plan = _job(heads, rows, past)
+    plan.work[:4096].view(torch.int32)[64:64 + 960] = -1000
+    binding.attention_packed(q, k, v, plan, out)
+    with pytest.raises(binding.PrefillError, match="gave up") as e:
+        plan.check()
+    assert e.value.code == binding.PF_E_DEVICE_TIMEOUT
+    for _ in range(2):
+        out.fill_(7)
+        binding.attention_packed(q, k, v, plan, out)
+        plan.check()
         _check(heads, runs, q, k, v, out)
         binding.attention_tree(q, k, v, plan, mask, out)
         plan.check()
