@@ -695,6 +695,10 @@ __global__ void __launch_bounds__(RunsCfg<HD, CL>::THREADS, 1)
         ml[h * 128 + 32 * qw + lane] = make_float2(m, ok ? l : -1.f);  // -1: this warp gave up (l is a sum of p >= 0)
         asm volatile("bar.sync %0, 64;" ::"r"(1 + qw) : "memory");
         const float2 a = ml[32 * qw + lane], c = ml[128 + 32 * qw + lane];
+        // Both have read before either writes again.  (A warp that gives up in
+        // the next segment gets there without waiting for the other; its -1
+        // read here would leave it alone at the next barrier for good.)
+        asm volatile("bar.sync %0, 64;" ::"r"(1 + qw) : "memory");
         ok = __all_sync(0xffffffffu, a.y != -1.f && c.y != -1.f);
         m = fmaxf(a.x, c.x);
         w0 = a.x == -INFINITY ? 0.f : ex2_approx((a.x - m) * cexp);
