@@ -484,6 +484,7 @@ __global__ void __launch_bounds__(RunsCfg<HD, CL>::THREADS, 1)
   uint64_t* p_full = q_full + 5;          // by S buffer, in the even CTA: a warpgroup of both CTAs
   uint64_t* state_out = p_full + C::NSB;  // this CTA's rows of a first part's state are written
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(state_out + 1);
+  volatile int* left_early = reinterpret_cast<volatile int*>(tmem_slot + 1);  // a warp of the pair gave up a wait
   static_assert((3 * C::NST + 7 + C::NSB) * 8 <= 512 && C::NG <= 2, "barrier layout");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -505,6 +506,8 @@ __global__ void __launch_bounds__(RunsCfg<HD, CL>::THREADS, 1)
     mbar_init(state_out, 4 * C::NG);
     mbar_init(&drain[0], 1);
     mbar_init(&drain[1], 1);
+    // (a plain store costs the row threads 16 more spilled bytes at hd 64: prompts of 4096 and 2048 109 us for 107)
+    asm volatile("st.shared.u32 [%0], %1;" ::"r"(smem_u32(tmem_slot + 1)), "r"(0) : "memory");
     fence_mbar_init();
   }
   if (warp == 1 && lane == 0) {
@@ -525,6 +528,18 @@ __global__ void __launch_bounds__(RunsCfg<HD, CL>::THREADS, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   pdl_wait();
+
+  // What every role does on giving up: note it in both CTAs.
+  auto give_up = [&]() {
+    if (lane == 0) {
+      *left_early = 1;
+      if constexpr (CL == 2) {
+        const uint32_t at = map_to_rank(smem_u32(const_cast<const int*>(left_early)), static_cast<uint32_t>(rank ^ 1));
+        asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(at), "r"(1) : "memory");
+      }
+    }
+    __syncwarp();
+  };
 
   // Counters that run on over the pair's segments, the same in every role:
   // ring fills (fill f uses stage f % NST, in its use number f / NST), chunks
@@ -705,7 +720,10 @@ __global__ void __launch_bounds__(RunsCfg<HD, CL>::THREADS, 1)
         w1 = c.x == -INFINITY ? 0.f : ex2_approx((c.x - m) * cexp);
         l = w0 * a.y + w1 * c.y;
       }
-      if (!ok) break;
+      if (!ok) {
+        *left_early = 1;  // (this CTA's: MMAs that need the other's rows or copies make the MMA warp give up too)
+        break;
+      }
       if (active) {
         // a thread writes its row, 32-byte sectors at a time
         tc_fence_after();
@@ -866,6 +884,7 @@ __global__ void __launch_bounds__(RunsCfg<HD, CL>::THREADS, 1)
         }
       }
       __syncwarp();
+      if (!ok) give_up();
     } else if (warp == 2) {
       // ---------------- Q producer: a copy per 64-dim box, or per 32 rows
       bool ok = true, first = false;
@@ -913,6 +932,7 @@ __global__ void __launch_bounds__(RunsCfg<HD, CL>::THREADS, 1)
       if (ok && first) pass_on();
       if (CL == 1 && lane == 0) leave_table();
       __syncwarp();
+      if (!ok) give_up();
     } else if (warp == 0 && rank == 1) {
       // ---------------- the odd CTA's half of the run's last V
       bool ok = true;
@@ -929,6 +949,7 @@ __global__ void __launch_bounds__(RunsCfg<HD, CL>::THREADS, 1)
         if (lane == 0) mbar_arrive_cluster(in_even(&cleared[s]));
       }
       __syncwarp();
+      if (!ok) give_up();
     } else if (rank == 1) {
       // ---------------- warp 3 of the odd CTA
       if (lane == 0) leave_table();
@@ -1049,6 +1070,7 @@ __global__ void __launch_bounds__(RunsCfg<HD, CL>::THREADS, 1)
         runs_drain(bar, 0);
       }
       __syncwarp();
+      if (!ok) give_up();
     }
   }
   tc_fence_before();
@@ -1056,6 +1078,16 @@ __global__ void __launch_bounds__(RunsCfg<HD, CL>::THREADS, 1)
   // neither CTA leaves (or frees TMEM) while the pair's MMAs may still use it
   if constexpr (CL == 2) cluster_sync_all();
   if (warp == 0) {
+    // The roles' drains miss copies that one CTA's producer issued after the
+    // other's had given up (the even CTA's barriers count both), and those that
+    // were in flight when another role gave up.  Nothing is issued any more, a
+    // copy takes microseconds, and neither CTA's shared memory is given away
+    // before some milliseconds have passed.
+    if (*left_early) {
+      const long long t0 = clock64();
+      while (clock64() - t0 < 10000000ll) __nanosleep(1000);
+    }
+    __syncwarp();
     tc_fence_after();
     if constexpr (CL == 2)
       tmem_dealloc_pair(tmem, C::TMEM_COLS);

@@ -77,3 +77,29 @@ def test_a_wait_that_runs_out(heads, rows, past):
         binding.attention_tree(q, k, v, plan, mask, out)
         plan.check()
         _check(heads, runs, q, k, v, out, mask_np)
+
+
+@pytest.mark.parametrize("heads", [(8, 1, 256), (8, 2, 256), (32, 4, 64)])
+@pytest.mark.parametrize("rows,past", RUNS + [([128] * 30, [5000] * 30)])
+def test_calls_behind_one_that_gave_up(heads, rows, past):
+    """Calls that find the error word set, as those do that were enqueued
+    behind a call that gave up: all roles leave at whatever wait they look at
+    it in, with copies and MMAs on their way.  Their results are invalid; they
+    end, the status says so, and the scratch is good again."""
+    runs, q, k, v, out, mask_np, _, plan = _job(heads, rows, past)
+    mask_np = _random_tree(runs, 2, 3)
+    mask = torch.from_numpy(mask_np.view("int64")).cuda()
+    for _ in range(3):
+        plan.work[:4096].view(torch.int32)[0] = 4
+        for _ in range(4):
+            binding.attention_packed(q, k, v, plan, out)
+            binding.attention_tree(q, k, v, plan, mask, out)
+        with pytest.raises(binding.PrefillError, match="gave up"):
+            plan.check()
+        out.fill_(7)
+        binding.attention_packed(q, k, v, plan, out)
+        plan.check()
+        _check(heads, runs, q, k, v, out)
+        binding.attention_tree(q, k, v, plan, mask, out)
+        plan.check()
+    _check(heads, runs, q, k, v, out, mask_np)
