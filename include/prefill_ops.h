@@ -240,10 +240,14 @@ typedef struct pfop_attn_run {
    be zero before its first call.  Calls that share a scratch must not
    overlap on the GPU (one stream, or events; two recorded graphs that share
    one may not run at once).
-   PF_E_ARG: hd other than 64 or 256; n_head not a multiple of n_head_kv
-   with a group size dividing 16; more than 128 runs or 2^20 rows; a run
-   past n_cells; q, k, v not 16-byte or out not 32-byte aligned; a scratch too
-   small. */
+   PF_E_ARG: hd other than 64 or 256; n_head above 1024 or not a multiple of
+   n_head_kv with a group size dividing 16; more than 128 runs or 2^20 rows; a
+   run past n_cells or position 2^30; n_cells above 2^31 - 1024; q, k, v not
+   16-byte or out not 32-byte aligned; a scratch too small; 2^30 units of work
+   or more.  Units of work: for every KV head and every block of 256 / (n_head /
+   n_head_kv) rows of a run (half as many in small calls at hd 64) the 128-key
+   chunks up to its last row's position, and 3 (hd 256) or 4 (hd 64).  One
+   prompt of 2^20 rows with 32 heads over 8 of 64 is 2^29. */
 int pfop_attention_packed(const void* q_dev, const void* k_dev, const void* v_dev, int64_t n_cells, int32_t Hq,
                           int32_t Hkv, int32_t hd, const pfop_attn_run* runs, int32_t n_runs, void* out_dev,
                           void* work_dev, int64_t work_bytes, void* stream);
@@ -254,7 +258,8 @@ int pfop_attention_packed(const void* q_dev, const void* k_dev, const void* v_de
    j of its run (position pos0 + j) whose bit j % 64 of
    mask_dev[row * mask_words + j / 64] is set.  mask_dev: uint64, device, a
    row for every row of q; mask_words 1 .. 4 (at most 256 drafted tokens a
-   run, n_rows <= 64 * mask_words); bits from n_rows on are ignored.  A row
+   run, n_rows <= 64 * mask_words); bits from n_rows on are ignored.  Every
+   block's work counts the whole run's chunks.  A row
    that sees nothing (pos0 0 and no bit set) gives zeros.  One row with its
    own bit set is a plain decoding step. */
 int pfop_attention_tree(const void* q_dev, const void* k_dev, const void* v_dev, int64_t n_cells, int32_t Hq,
@@ -262,7 +267,9 @@ int pfop_attention_tree(const void* q_dev, const void* k_dev, const void* v_dev,
                         int32_t mask_words, void* out_dev, void* work_dev, int64_t work_bytes, void* stream);
 
 /* Scratch bytes that either call needs for these runs on the current device
-   (host only; without a device, as on a GB300; at least 4096), or PF_E_ARG. */
+   (host only; without a device, as on a GB300; at least 4096), or PF_E_ARG.
+   Runs that the tree call does not take (more than 256 rows, or too much work
+   as a tree) get what pfop_attention_packed needs. */
 int64_t pfop_attention_work_bytes(int32_t Hq, int32_t Hkv, int32_t hd, const pfop_attn_run* runs, int32_t n_runs);
 
 /* Wait for `stream` and report whether a call using this scratch gave up a

@@ -295,6 +295,21 @@ struct RunBlocks {
     if (TREE || i == 0) return i * (last + fixed);
     return i * fixed + last + from_start(nb - 1) - from_start(nb - i);
   }
+  // weight(nb), where 32 bits may not hold it: block b of a prompt's, the last
+  // one aside, has floor((c + b bs) / 128) chunks
+  __host__ int64_t whole() const {
+    const int64_t f = int64_t(nb) * fixed;
+    if (TREE) return f + int64_t(nb) * last;
+    const int64_t B = nb - 1, c = int64_t(pos0) + (1 << bs_log) + RCH - 1;
+    if (bs_log == 8) return f + last + B * (c / RCH) + B * (B - 1);
+    // sum over x' < x of x' >> sl, sl = 7 - bs_log
+    auto floors = [&](int64_t x) {
+      const int sl = 7 - bs_log;
+      const int64_t k = x >> sl;
+      return (k * (k - 1) / 2 << sl) + k * (x - (k << sl));
+    };
+    return f + last + floors((c >> bs_log) + B) - floors(c >> bs_log);
+  }
 };
 
 // an item: run, KV head, row block and its place on the line of weights
@@ -1227,6 +1242,7 @@ constexpr int merge_cost(int hd) { return hd == 256 ? 6 : 8; }
 constexpr int64_t merge_bytes(int hd) { return (hd == 256 ? 4 : 2) << 20; }
 constexpr int MAX_PAIRS = 120;  // twice as many of one CTA: flags of 4 words a CTA in the scratch's header
 constexpr int MIN_SHARE = 4;
+constexpr int64_t MAX_WEIGHT = int64_t(1) << 30;
 
 template <bool TREE>
 static bool make_plan(RunsPlan& p, const pfop_attn_run* runs, int n_runs, int Hq, int Hkv, int hd) {
@@ -1255,8 +1271,8 @@ static bool make_plan(RunsPlan& p, const pfop_attn_run* runs, int n_runs, int Hq
   for (int r = 0; r < n_runs; ++r) {
     if (runs[r].n_rows > 0) {
       const RunBlocks<TREE> rb(runs[r].n_rows, runs[r].pos0, p.sh);
-      // an upper bound first: the weights below are 32-bit
-      if (weight + int64_t(rb.nb) * Hkv * (int64_t(rb.last) + p.sh.fixed) >= (int64_t(1) << 30)) return false;
+      // the weights below are 32-bit
+      if (weight + rb.whole() * Hkv >= MAX_WEIGHT) return false;
       p.rt.row0[n] = row;
       p.rt.n[n] = runs[r].n_rows;
       p.rt.pos0[n] = runs[r].pos0;
@@ -1265,7 +1281,7 @@ static bool make_plan(RunsPlan& p, const pfop_attn_run* runs, int n_runs, int Hq
       p.rt.w0[n] = static_cast<int>(weight);
       ++n;
       items += int64_t(rb.nb) * Hkv;
-      weight += int64_t(rb.weight(rb.nb)) * Hkv;
+      weight += rb.whole() * Hkv;
       longest = std::max(longest, rb.last);
       max_rows = std::max(max_rows, std::min(item_rows, runs[r].n_rows << p.sh.log_g));
     }
@@ -1348,6 +1364,8 @@ using namespace pf;
 
 constexpr int64_t WORK_HEADER = 4096;  // the error word; from word FLAGS_AT the pairs' flags
 constexpr int FLAGS_AT = 64;
+constexpr int MASK_WORDS_MAX = 4;
+constexpr const char* TOO_MUCH = "more work than one call takes: 2^30 chunks of 128 keys over all blocks of MMA rows";
 static_assert((FLAGS_AT + 8 * MAX_PAIRS) * 4 <= WORK_HEADER, "scratch header");
 
 int fail(int code, const std::string& m) {
@@ -1384,7 +1402,7 @@ int run_attention(bool tree, const void* q, const void* k, const void* v, int64_
   int rc = check_runs(Hq, Hkv, hd, runs, n_runs, n_cells, &total);
   if (rc != PF_OK) return rc;
   if (tree) {
-    if (words < 1 || words > 4) return fail(PF_E_ARG, "mask_words outside [1, 4]");
+    if (words < 1 || words > MASK_WORDS_MAX) return fail(PF_E_ARG, "mask_words outside [1, 4]");
     for (int r = 0; r < n_runs; ++r)
       if (runs[r].n_rows > 64 * words) return fail(PF_E_ARG, "a run has more rows than its mask has bits");
   }
@@ -1397,7 +1415,7 @@ int run_attention(bool tree, const void* q, const void* k, const void* v, int64_
   if (reinterpret_cast<uintptr_t>(work) & 255) return fail(PF_E_ARG, "the scratch must be 256-byte aligned");
   RunsPlan p;
   if (!(tree ? make_plan<true>(p, runs, n_runs, Hq, Hkv, hd) : make_plan<false>(p, runs, n_runs, Hq, Hkv, hd)))
-    return fail(PF_E_ARG, "more work than one call takes (2^30 chunks of 256 rows by 128 keys)");
+    return fail(PF_E_ARG, TOO_MUCH);
   if (work_bytes < WORK_HEADER + p.state_bytes) return fail(PF_E_ARG, "the scratch is smaller than these runs need");
   int* err = static_cast<int*>(work);
   uint8_t* states = static_cast<uint8_t*>(work) + WORK_HEADER;
@@ -1436,9 +1454,13 @@ extern "C" int64_t pfop_attention_work_bytes(int32_t Hq, int32_t Hkv, int32_t hd
   if (rc != PF_OK) return rc;
   if (total == 0) return WORK_HEADER;
   RunsPlan a, b;
-  if (!make_plan<false>(a, runs, n_runs, Hq, Hkv, hd) || !make_plan<true>(b, runs, n_runs, Hq, Hkv, hd))
-    return fail(PF_E_ARG, "more work than one call takes (2^30 chunks of 256 rows by 128 keys)");
-  return WORK_HEADER + std::max(a.state_bytes, b.state_bytes);
+  if (!make_plan<false>(a, runs, n_runs, Hq, Hkv, hd)) return fail(PF_E_ARG, TOO_MUCH);
+  // a tree's rows all see the whole context: runs that no tree has are not
+  // counted as one, and what only the tree call refuses it refuses itself
+  bool tree = true;
+  for (int r = 0; r < n_runs; ++r) tree = tree && runs[r].n_rows <= 64 * MASK_WORDS_MAX;
+  const bool both = tree && make_plan<true>(b, runs, n_runs, Hq, Hkv, hd);
+  return WORK_HEADER + std::max(a.state_bytes, both ? b.state_bytes : 0);
 }
 
 extern "C" int pfop_attention_status(void* work_dev, void* stream) {
