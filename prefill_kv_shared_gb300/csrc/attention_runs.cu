@@ -47,8 +47,9 @@
 // chunks in turn, each with its own m, l and O (joined at the segment's
 // end), so that one's exponentials run while the other loads, looks for the
 // maximum or hands over, and three S buffers keep both supplied.  All waits
-// are bounded (PF_WAIT_CYCLES): one that gives up flags the scratch's error
-// word and the pair unwinds.
+// are bounded (PF_WAIT_CYCLES, and more where a wait lasts as long as a number
+// of chunks): one that gives up flags the scratch's error word and the pair
+// unwinds.
 //
 // Bounds and figures (one call, GB300): long prompts at hd 256 are bound by
 // the MMAs (2058 clocks a chunk, 2048 at the full rate; six prompts, 15845
@@ -219,6 +220,12 @@ __device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
   uint64_t d;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
+}
+
+// Bound of a wait that lasts while the pair works through that many chunks:
+// four times what the slowest kind takes (2058 clocks), beside the usual bound.
+__device__ __forceinline__ long long runs_wait_limit(uint32_t chunks) {
+  return PF_WAIT_CYCLES + static_cast<long long>(chunks) * 8192;
 }
 
 // bounded wait for a barrier on an error path (about 0.2 s)
@@ -904,11 +911,12 @@ __global__ void __launch_bounds__(RunsCfg<HD, CL>::THREADS, 1)
       // ---------------- Q producer: a copy per 64-dim box, or per 32 rows
       bool ok = true, first = false;
       int active = 0;  // row warps of a first part that have rows
+      int first_n = 0, last_n = 0;  // chunks of the first and of the last segment copied for
       // A first part (only a pair's first segment is one): its state is passed
       // on from here, so that the row warps need not wait until their stores
       // have reached L2.
       auto pass_on = [&]() {
-        ok = mbar_wait(state_out, 0, err, PF_DEV_TIMEOUT_EPILOGUE);
+        ok = mbar_wait(state_out, 0, err, PF_DEV_TIMEOUT_EPILOGUE, runs_wait_limit(first_n));
         ok = __all_sync(0xffffffffu, ok);
         if (ok && lane < active) {
           __threadfence();
@@ -921,14 +929,16 @@ __global__ void __launch_bounds__(RunsCfg<HD, CL>::THREADS, 1)
       for (; ok && sg.next(); ++seg) {
         if (seg == 0) {
           first = sg.kind == SEG_FIRST;
+          first_n = sg.n;
           for (int qw = 0; qw < 4; ++qw)
             if (sg.R0 + C::row_of(rank, 32 * qw) < rt.n[sg.run] << sh.log_g) active = qw + 1;
         }
         if (seg == 2 && first) pass_on();
         if (!ok) break;
-        if (seg > 0) ok = mbar_wait(q_empty, (seg - 1) & 1, err, PF_DEV_TIMEOUT_PRODUCER);
+        if (seg > 0) ok = mbar_wait(q_empty, (seg - 1) & 1, err, PF_DEV_TIMEOUT_PRODUCER, runs_wait_limit(last_n));
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
+        last_n = sg.n;
         if (lane == 0 && rank == 0) mbar_arrive_expect_tx(q_full, CL * C::Q_BYTES);
         __syncwarp();
         constexpr int GROUPS = 128 / C::Q_ROWS;
@@ -951,12 +961,13 @@ __global__ void __launch_bounds__(RunsCfg<HD, CL>::THREADS, 1)
     } else if (warp == 0 && rank == 1) {
       // ---------------- the odd CTA's half of the run's last V
       bool ok = true;
-      uint32_t f = 0, tails = 0;
+      uint32_t f = 0, f_seen = 0, tails = 0;
       while (ok && sg.next()) {
         f += 2 * sg.n;
         if (tail_keys() >= RCH) continue;
         const int s = (f - 1) % C::NST;
-        ok = mbar_wait(&full[s], tails >> s & 1u, err, PF_DEV_TIMEOUT_MMA);
+        ok = mbar_wait(&full[s], tails >> s & 1u, err, PF_DEV_TIMEOUT_MMA, runs_wait_limit((f - f_seen) / 2));
+        f_seen = f;
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tails ^= 1u << s;

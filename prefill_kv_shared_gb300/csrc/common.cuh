@@ -202,7 +202,8 @@ __device__ __forceinline__ bool mbar_try_wait(uint32_t bar_addr, uint32_t parity
 #define PF_WAIT_CYCLES 4000000000ll  // about 2 s
 #endif
 template <bool CL = false>
-__device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, int* err, int code) {
+__device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, int* err, int code,
+                                          long long limit = PF_WAIT_CYCLES) {
   const uint32_t a = smem_u32(bar);
   if (mbar_try_wait<CL>(a, parity)) return true;
   long long t0 = 0;
@@ -212,7 +213,7 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, int* e
       const long long now = clock64();
       if (t0 == 0) {
         t0 = now;
-      } else if (now - t0 > PF_WAIT_CYCLES) {
+      } else if (now - t0 > limit) {
         set_error(err, code);
         return false;
       }
