@@ -374,6 +374,14 @@ def _call_on(index: int, stream, fn, *args):
         check_op(rc)
 
 
+def _i32(x, what: str) -> int:
+    """x as the int32 of a C argument (ctypes drops what does not fit)."""
+    x = int(x)
+    if not -1 << 31 <= x < 1 << 31:
+        raise ValueError(f"{what}: {x} does not fit 32 bits")
+    return x
+
+
 class AttnRuns:
     """The runs of an attention_packed / attention_tree call and the call's
     scratch: runs = [(n_rows, pos0, cell0), ...] (see pfop_attn_run), for
@@ -387,14 +395,14 @@ class AttnRuns:
     def __init__(self, runs, n_head: int, n_head_kv: int, head_dim: int, device=None):
         torch = _t()
         self._lib = load()
-        self.shape = (n_head, n_head_kv, head_dim)
-        runs = [(int(n), int(p), int(c)) for n, p, c in runs]
+        self.shape = (_i32(n_head, "n_head"), _i32(n_head_kv, "n_head_kv"), _i32(head_dim, "head_dim"))
+        runs = [(_i32(n, "n_rows"), _i32(p, "pos0"), _i32(c, "cell0")) for n, p, c in runs]
         self.n_runs = len(runs)
         self.n_rows = sum(r[0] for r in runs)
         self.runs = (AttnRun * max(1, len(runs)))(*[AttnRun(*r) for r in runs])
         with torch.cuda.device(device if device is not None else torch.cuda.current_device()):
             self.device = torch.cuda.current_device()
-            need = int(self._lib.pfop_attention_work_bytes(n_head, n_head_kv, head_dim, self.runs, self.n_runs))
+            need = int(self._lib.pfop_attention_work_bytes(*self.shape, self.runs, self.n_runs))
             if need < 0:
                 check_op(need)
             self.work = torch.empty(need, dtype=torch.uint8, device="cuda")
@@ -453,6 +461,8 @@ def attention_tree(q, k, v, runs: AttnRuns, mask, out, stream=None):
     ms = mask.shape
     if len(ms) != 2 or ms[0] < runs.n_rows:
         raise ValueError(f"mask: needs [{runs.n_rows}, words]")
+    if ms[1] > 4:
+        raise ValueError(f"mask: at most 4 words a row, got {ms[1]}")
     cells = runs._fit(q, k, v, out)
     m = _on_device(mask, "mask", _torch.int64, ms, runs.device)
     _call_on(runs.device, stream, runs._lib.pfop_attention_tree, q.data_ptr(), k.data_ptr(), v.data_ptr(), cells,
@@ -478,12 +488,14 @@ def logprobs(logits, tokens=None, logp=None, entropy=None, top_id=None, top_logp
         raise ValueError("logits: needs [rows, vocab] with dense rows")
     if (tokens is None) != (logp is None) or (top_id is None) != (top_logp is None):
         raise ValueError("tokens and logp, top_id and top_logp go together")
+    rows, vocab = shape
+    if rows >= 1 << 31 or vocab >= 1 << 31:
+        raise ValueError(f"logits: {tuple(shape)} does not fit 32 bits")
     d = logits.get_device()
     if d < 0:
         raise ValueError(f"logits: must be on a CUDA device, is on {logits.device}")
-    rows, vocab = shape
     f32, i32, one = torch.float32, torch.int32, (rows,)
-    n_top = 0 if top_id is None else top_id.shape[-1]
+    n_top = 0 if top_id is None else _i32(top_id.shape[-1], "top_id")
     _call_on(d, stream, load().pfop_logprobs, kind, logits.data_ptr(), stride[0] if rows > 1 else vocab, rows,
              vocab, None if tokens is None else _on_device(tokens, "tokens", i32, one, d), n_top,
              None if logp is None else _on_device(logp, "logp", f32, one, d),
