@@ -209,10 +209,14 @@ int32_t pfop_qkv_row_order(int32_t Hq, int32_t Hkv, int32_t hd, int32_t with_kv,
 int64_t pfop_repack_q4(const void* w_host, int32_t N, int32_t K, int32_t bn, void* dst, int64_t dst_bytes);
 
 /* ---- several sequences in one call ----
-   The calls below work on rows of several sequences over the unified cache of
-   prefill_ubatch_seqs.  Unlike the calls above they only enqueue work on
-   `stream` (of the current device), allocate nothing and may be recorded
-   into a CUDA graph; arguments are checked on the host before any CUDA call.
+   Unlike the calls above, the calls below only enqueue work on `stream` (of
+   the current device), allocate nothing and may be recorded into a CUDA
+   graph; arguments are checked on the host before any CUDA call.
+
+   The attention calls work on one layer's K and V in the layout in which
+   prefill_ubatch_seqs keeps them: [cells][Hkv*hd], a sequence's cells one
+   after another.  The buffers are the caller's own: a prefill context gives
+   out no address of its cache (kv_save copies sequence 0 out of it).
 
    A run is n_rows consecutive rows of one sequence that continue it at
    position pos0; the sequence's position p lives in cache cell cell0 + p.
@@ -228,11 +232,12 @@ typedef struct pfop_attn_run {
 /* Causal GQA attention of up to 128 runs in one call: q fp16 [T][Hq*hd], T
    the runs' rows in all, K/V fp16 [n_cells][Hkv*hd], out bf16 [T][Hq*hd]
    (rows from T on are not touched).  Row i of a run sees its sequence's
-   positions 0 .. pos0 + i.  Cells of no run's positions 0 .. pos0 + n_rows
-   - 1 are never used, whatever they hold; the runs' own cells must hold
-   finite values (an infinity or NaN in V reaches the rows of its run that do
-   not see it too, but no other run's).  Probabilities are rounded to fp16 before P V, sums and
-   states are fp32.  A row's bits depend on its position, its keys and the
+   positions 0 .. pos0 + i, scores scaled by 1 / sqrt(hd).  Cells of no run's
+   positions 0 .. pos0 + n_rows - 1 are never used, whatever they hold; the
+   runs' own cells must hold finite values (an infinity or NaN in V reaches
+   the rows of its run that do not see it too, but no other run's).  Scores
+   may be as large as finite q and k make them.  Probabilities are rounded to
+   fp16 before P V, sums and states are fp32.  A row's bits depend on its position, its keys and the
    shapes of the call's runs, not on the other runs' values; a repeated call
    gives the same bits.
    work_dev: device scratch of the call, 256-byte aligned, work_bytes of it
@@ -274,8 +279,9 @@ int64_t pfop_attention_work_bytes(int32_t Hq, int32_t Hkv, int32_t hd, const pfo
 
 /* Wait for `stream` and report whether a call using this scratch gave up a
    bounded wait (PF_E_DEVICE_TIMEOUT: the results of that call and of those
-   after it are invalid).  Then it makes the scratch as good as new; until it
-   is called the scratch must not be used for further results. */
+   after it are invalid; all of them have ended).  Then it makes the scratch
+   as good as new, for any stream, before it returns; until it is called the
+   scratch must not be used for further results.  Not to be recorded. */
 int pfop_attention_status(void* work_dev, void* stream);
 
 /* Log probabilities over a vocabulary, for every row of logits [rows][ld]
@@ -288,7 +294,10 @@ int pfop_attention_status(void* work_dev, void* stream);
    All outputs are fp32 (top_id int32), rows dense.  -inf logits are allowed
    (probability 0).  A token outside [0, vocab) gives logp NaN.  A row
    without a distribution (a NaN, +inf, or only -inf) gives NaN throughout
-   and top_id -1.  Enqueue only, no scratch, recordable.
+   and top_id -1, and so does a row of which a copy did not arrive within the
+   bound of the library's waits (about 2 s of SM clock): with no scratch there
+   is no error word to tell the two apart.  Enqueue only, no scratch,
+   recordable.
    PF_E_ARG: rows < 0, vocab < 1 or >= 2^30, ld < vocab, n_top outside
    [0, min(32, vocab)], missing or misaligned buffers (logits to their
    element, outputs to 4 bytes). */

@@ -53,14 +53,16 @@
 //
 // Bounds and figures (one call, GB300): long prompts at hd 256 are bound by
 // the MMAs (2058 clocks a chunk, 2048 at the full rate; six prompts, 15845
-// rows in all, 8 heads over 2: 213 us, 1720 TFLOP/s); at hd 64 by the chain of
-// a chunk's softmax and hand-overs (1085 clocks, of which the exponential
-// unit is busy for 512; prompts of 4096 and 2048, 32 heads over 4: 108 us, 795
-// TFLOP/s).  Drafted trees read each context once: 12 trees of 1 to 64 rows,
-// 159 MB, 40.6 us, 3.9 TB/s; 64 trees of 16 rows, 69 MB, 24.4 us, 2.8 TB/s,
-// where a segment's first scores and output (4000 to 5000 clocks) count as
-// much as its chunks.  Small calls are bound by latency: 25 rows 4.9 us, 512
-// rows of 8 heads 10.6 us.
+// rows in all, 8 heads over 2: 223 to 235 us with the power limit, 206 without
+// it, 1560 to 1780 TFLOP/s); at hd 64 by the chain of a chunk's softmax and
+// hand-overs (about 1100 clocks, of which the exponential unit is busy for
+// 512; prompts of 4096 and 2048, 32 heads over 4: 108.6 us, 790 TFLOP/s).
+// Drafted trees read each context once: 12 trees of 1 to 64 rows, 159 MB, 40.6
+// us, 3.9 TB/s; 64 trees of 16 rows, 69 MB, 25.0 us, 2.8 TB/s, where a segment's
+// first scores and output (4000 to 5000 clocks) count as much as its chunks;
+// 64 sequences of one row over 4096 keys, 8 heads over 1, 268 MB, 45.8 us, 5.9
+// TB/s.  Small calls are bound by latency: 25 rows 5.1 us, 512 rows of 8 heads
+// 10.8 us.
 #include "../../include/prefill_ops.h"
 #include "attn.cuh"
 #include "common.cuh"
@@ -96,9 +98,9 @@ struct RunsShape {
 };
 
 // weight of an item besides its chunks: its Q copy, first scores and output,
-// in chunk times.  (hd 256: 15845 rows of 6 prompts 225, 206 and 210 us with 2,
-// 3 and 4; hd 64: prompts of 4096 and 2048 124, 112, 108, 108 and 115 with 2,
-// 3, 4, 5 and 8.)
+// in chunk times.  (hd 256: 15845 rows of 6 prompts 250, 228 and 238 us with 2,
+// 3 and 4; hd 64: prompts of 4096 and 2048 124, 114, 109, 108 and 116 with 2,
+// 3, 4, 5 and 8, 64 trees of 16 rows 25.7, 25.5, 24.8, 25.6 and 25.9.)
 constexpr int item_fixed(int hd) { return hd == 256 ? 3 : 4; }
 
 // CL: CTAs of an item
@@ -1276,11 +1278,11 @@ static int sm_count() {
 // longest takes no longer than an even share would with what joining costs;
 // else even shares over the resident pairs, but none below MIN_SHARE.
 // Joining costs merge_cost chunk times and one for every merge_bytes of
-// states written and read.  (hd 256: a 2048-row prompt of 8 heads 24.6 us
-// with a pair per item, 34.3 in shares; 4 trees of 16 rows of 8 heads over
-// 1300 keys 19.3 and 13.1; hd 64: 256 rows over
-// 2000 keys 14.7 and 16.2, a tree of 5 rows over 3000 17.1 and 8.7.)  Where no item covers a whole share, a pair per
-// item is better throughout (512 rows: 10.6 and 14.9 us).
+// states written and read.  (hd 256: a 2048-row prompt of 8 heads 24.8 us
+// with a pair per item, 34.2 in shares; 4 trees of 16 rows of 8 heads over
+// 1300 keys 18.5 and 13.7; hd 64: 256 rows over 2000 keys 15.2 and 16.2, a
+// tree of 5 rows over 3000 17.2 and 8.8.)  Where no item covers a whole share,
+// a pair per item is better throughout (512 rows: 10.8 and 15.4 us).
 // False: more work than the line of weights can count.
 constexpr int merge_cost(int hd) { return hd == 256 ? 6 : 8; }
 constexpr int64_t merge_bytes(int hd) { return (hd == 256 ? 4 : 2) << 20; }
@@ -1301,11 +1303,11 @@ static bool make_plan(RunsPlan& p, const pfop_attn_run* runs, int n_runs, int Hq
     twos += (rows + 255) / 256 * Hkv;
   }
   // At hd 64 a CTA works alone where there is not an item of 128 rows for
-  // every SM (25 rows of 8 heads: 4.9 us, with pairs 5.6) or where pairs would
-  // hold 15% more rows that are none (64 trees of 16 rows: 24.2 us, 32.6; 20
-  // runs of 40 rows 23.0, 25.8); else the pair's half as many K/V copies count
-  // (64 x 32 rows: 28.2 us with pairs, 31.0 without; prompts of 4096 and 2048:
-  // 107, 123).
+  // every SM (25 rows of 8 heads: 5.1 us, with pairs 5.7) or where pairs would
+  // hold 15% more rows that are none (64 trees of 16 rows: 25.1 us, 32.4; 20
+  // runs of 40 rows over 900 keys 20.8, 23.2); else the pair's half as many K/V
+  // copies count (64 x 32 rows: 28.5 us with pairs, 32.5 without; prompts of
+  // 4096 and 2048: 108, 123).
   const int sms = sm_count();
   const int cl = p.cl = hd == 64 && (ones <= sms || 200 * twos > 115 * ones) ? 1 : 2, item_rows = 128 * cl;
   p.sh.bs_log = (cl == 2 ? 8 : 7) - p.sh.log_g;

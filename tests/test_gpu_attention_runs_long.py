@@ -1,5 +1,5 @@
 """Attention over runs of the longest kind: one prompt of 2^20 - 1 rows of 16
-heads, whose launch takes longer (about 4 s) than the bound of a single wait
+heads, whose launch takes longer (about 6 s) than the bound of a single wait
 (about 2 s of SM clock).  A wait that lasts while a CTA pair works through its
 share must not be cut off by that bound.
 
