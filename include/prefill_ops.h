@@ -237,9 +237,9 @@ typedef struct pfop_attn_run {
    runs' own cells must hold finite values (an infinity or NaN in V reaches
    the rows of its run that do not see it too, but no other run's).  Scores
    may be as large as finite q and k make them.  Probabilities are rounded to
-   fp16 before P V, sums and states are fp32.  A row's bits depend on its position, its keys and the
-   shapes of the call's runs, not on the other runs' values; a repeated call
-   gives the same bits.
+   fp16 before P V, sums and states are fp32.  A row's bits depend on its
+   position, its keys and the shapes of the call's runs, not on the other
+   runs' values; a repeated call gives the same bits.
    work_dev: device scratch of the call, 256-byte aligned, work_bytes of it
    at least pfop_attention_work_bytes of the runs; its first 4096 bytes must
    be zero before its first call.  Calls that share a scratch must not
@@ -252,7 +252,7 @@ typedef struct pfop_attn_run {
    or more.  Units of work: for every KV head and every block of 256 / (n_head /
    n_head_kv) rows of a run (half as many in small calls at hd 64) the 128-key
    chunks up to its last row's position, and 3 (hd 256) or 4 (hd 64).  One
-   prompt of 2^20 rows with 32 heads over 8 of 64 is 2^29. */
+   prompt of 2^20 rows with 32 heads over 8 of 64 is about 2^29. */
 int pfop_attention_packed(const void* q_dev, const void* k_dev, const void* v_dev, int64_t n_cells, int32_t Hq,
                           int32_t Hkv, int32_t hd, const pfop_attn_run* runs, int32_t n_runs, void* out_dev,
                           void* work_dev, int64_t work_bytes, void* stream);
@@ -263,10 +263,10 @@ int pfop_attention_packed(const void* q_dev, const void* k_dev, const void* v_de
    j of its run (position pos0 + j) whose bit j % 64 of
    mask_dev[row * mask_words + j / 64] is set.  mask_dev: uint64, device, a
    row for every row of q; mask_words 1 .. 4 (at most 256 drafted tokens a
-   run, n_rows <= 64 * mask_words); bits from n_rows on are ignored.  Every
-   block's work counts the whole run's chunks.  A row
+   run, n_rows <= 64 * mask_words); bits from n_rows on are ignored.  A row
    that sees nothing (pos0 0 and no bit set) gives zeros.  One row with its
-   own bit set is a plain decoding step. */
+   own bit set is a plain decoding step.  Units of work count the whole run's
+   chunks for every block. */
 int pfop_attention_tree(const void* q_dev, const void* k_dev, const void* v_dev, int64_t n_cells, int32_t Hq,
                         int32_t Hkv, int32_t hd, const pfop_attn_run* runs, int32_t n_runs, const uint64_t* mask_dev,
                         int32_t mask_words, void* out_dev, void* work_dev, int64_t work_bytes, void* stream);
