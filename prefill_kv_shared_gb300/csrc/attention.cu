@@ -107,13 +107,13 @@ struct AttnTcCfg {
   static_assert(SMEM <= 232448, "shared memory");
 };
 
-// let issued MMAs finish before TMEM is freed on an error path (bounded;
-// `bar` completes once, on the commit that follows them)
-__device__ __forceinline__ void attn_drain(uint64_t* bar) {
+// wait (bounded, about 0.2 s) for the phase of `bar` that the last copies or
+// MMAs complete, before shared memory or TMEM is given up
+__device__ __forceinline__ void attn_drain(uint64_t* bar, uint32_t parity) {
   const uint32_t a = smem_u32(bar);
   const long long t0 = clock64();
-  while (!mbar_try_wait(a, 0)) {
-    if (clock64() - t0 > 400000000ll) return;  // about 0.2 s
+  while (!mbar_try_wait(a, parity)) {
+    if (clock64() - t0 > 400000000ll) return;
   }
 }
 
@@ -202,13 +202,18 @@ __global__ void __launch_bounds__(AttnTcCfg<HD>::THREADS, 1)
       uint8_t* ring = smem + (is_k ? C::OFF_K : C::OFF_V);
       const CUtensorMap* map = is_k ? &tmK : &tmV;
       const int ns = is_k ? C::NK : 2;  // ring stages
-      for (int j = 0; j < n && ok; ++j) {
+      int j = 0;
+      for (; j < n; ++j) {
         const int s = j % ns;
         if (j >= ns) ok = mbar_wait(&empty[s], ((j - ns) / ns) & 1, err, PF_DEV_TIMEOUT_PRODUCER);
         if (!ok) break;
         mbar_arrive_expect_tx(&full[s], C::KV_BYTES);
         tma_load_3d(ring + s * C::KV_BYTES, map, &full[s], kvh * HD, (ch_first + j) * CHUNK, 0);
       }
+      // whichever role gives up, and when: no copy is on its way when the CTA
+      // leaves (else they have landed long before)
+      for (int x = max(0, j - ns); x < j; ++x) attn_drain(&full[x % ns], (x / ns) & 1);
+      if (is_k) attn_drain(q_full, 0);
     }
     __syncwarp();
   } else if (warp == 0) {
@@ -270,10 +275,13 @@ __global__ void __launch_bounds__(AttnTcCfg<HD>::THREADS, 1)
           __syncwarp();
         }
       }
+      // the MMAs already issued finish before TMEM is freed, also where only
+      // the row warps gave up
       if (!ok && issued && leader) {
-        // the MMAs already issued finish before TMEM is freed
         tc_commit(drain);
-        attn_drain(drain);
+        attn_drain(drain, 0);
+      } else if (ok && leader) {
+        attn_drain(&pv_done[(n - 1) & 1], ((n - 1) >> 1) & 1);
       }
     }
     __syncwarp();
