@@ -307,6 +307,96 @@ int pfop_logprobs(int32_t ltype, const void* logits_dev, int64_t ld, int32_t row
                   const int32_t* tok_dev, int32_t n_top, float* logp_dev, float* entropy_dev, int32_t* top_id_dev,
                   float* top_logp_dev, void* stream);
 
+/* ---- a serving step over a paged cache ----
+   Enqueue only, like the calls above.  K and V are fp16
+   [n_pages][page_size][Hkv*hd]; a sequence's pages may lie anywhere among
+   them, in any order, and sequences may share pages.
+
+   Attention of runs (a prompt's chunk, single tokens, drafted tokens) over a
+   paged cache: as pfop_attention_packed, or with mask_dev not NULL as
+   pfop_attention_tree, but a run's position p lies in row p % page_size of
+   page table_dev[cell0 + p / page_size]: cell0 is the run's first entry in the
+   table (int32, device, n_entries of them), whose entries behind the run's
+   last position are not looked at.  page_size: a power of two, at least 8.
+   A page id outside [0, n_pages) stands for keys and values of zero, and
+   pfop_attention_paged_status reports it; no other memory is touched.  What a
+   run's last page holds behind the run's end is never used.
+   work_dev as there, at least pfop_attention_paged_work_bytes of the runs.
+   PF_E_ARG: as there (2^31 - 1024 cells in all); a page_size that is not as
+   above; a run past n_entries. */
+int pfop_attention_paged(const void* q_dev, const void* k_dev, const void* v_dev, int32_t n_pages, int32_t page_size,
+                         int32_t Hq, int32_t Hkv, int32_t hd, const pfop_attn_run* runs, int32_t n_runs,
+                         const int32_t* table_dev, int64_t n_entries, const uint64_t* mask_dev, int32_t mask_words,
+                         void* out_dev, void* work_dev, int64_t work_bytes, void* stream);
+int64_t pfop_attention_paged_work_bytes(int32_t Hq, int32_t Hkv, int32_t hd, const pfop_attn_run* runs,
+                                        int32_t n_runs);
+
+/* As pfop_attention_status, for a scratch that pfop_attention_paged used:
+   PF_E_ARG where a call met a page id outside its cache. */
+int pfop_attention_paged_status(void* work_dev, void* stream);
+
+/* Queries and keys of a step: RMS norm of each head, half-split rotation by
+   position, and the write of K and V into the cache, in one pass.
+     y = x / sqrt(mean x^2 + eps) * (1 + gain)       (gain NULL: y = x)
+     (y[i], y[i + hd/2]) turned by pos * rope_base^(-2i/hd), i < hd/2
+   q [rows][q_ld], its first Hq*hd values a row's heads, k and v likewise with
+   Hkv heads (all of itype PF_L_F32 or PF_L_BF16; parts of one projection's rows
+   as a rule): q_out fp16 [rows][Hq*hd]; k turned and v as it is go to
+   cell slots_dev[row] of kc, vc (fp16 [n_cells][Hkv*hd]: a cache of cells, or
+   of pages with n_cells = n_pages * page_size and slot = page * page_size +
+   row of the page).  A row whose slot is outside [0, n_cells) writes no K and
+   V; two rows may not share a slot.  Hkv 0: queries only, as the KV-shared
+   layers need them (k, v, slots, k_gain, kc, vc are not looked at).
+   pos int32 device, any value (angles are exact to about 2^-24 of a turn
+   everywhere); gains fp32 device [hd].  Norms and rotations are fp32, rounded
+   to fp16 once.  q_out may not overlap its input.
+   PF_E_ARG: hd other than 64 or 256; rows outside [0, 2^24], n_head or
+   n_head_kv above 1024; a row stride below the row's heads or no multiple of
+   16 bytes; eps below 0, rope_base below 1, or not finite; missing buffers;
+   q, k, v, q_out, kc, vc not 16-byte, the others not 4-byte aligned. */
+int pfop_qk_norm_rope(int32_t itype, const void* q_dev, int64_t q_ld, const void* k_dev, int64_t k_ld,
+                      const void* v_dev, int64_t v_ld, int32_t rows, int32_t Hq, int32_t Hkv, int32_t hd,
+                      const int32_t* pos_dev, const int32_t* slots_dev, const float* q_gain_dev,
+                      const float* k_gain_dev, float eps, float rope_base, void* q_out_dev, void* kc_dev, void* vc_dev,
+                      int64_t n_cells, void* stream);
+
+/* Verification of drafted tokens.  Sequence s has the rows first_dev[s] ..
+   first_dev[s + 1] - 1 of target (first_dev: int32, device, n_seq + 1 entries
+   from 0 up to rows): one for the token before its drafts and one for each
+   draft, in order, as attention over a run's rows gives them.  tokens_dev[r] is
+   row r's token, so the draft that row r judges is tokens_dev[r + 1] (for all
+   rows of a sequence but its last).  With p = softmax(target row r), q =
+   softmax of draft row r - s (draft has a row for every draft, packed; NULL:
+   drafts without a distribution, q = 1 on the drafted token):
+     the draft d is accepted where u_dev[r] * q(d) < p(d), sequence by
+     sequence up to the first that is not;
+     the token after the accepted ones is the v with the largest w(v) /
+     noise_dev[s][v] (the lowest where two are equal), w = max(p - q, 0) of the
+     first refused draft's row, or p of the last row when all are accepted (and
+     p where w is 0 throughout).
+   With u uniform in [0, 1) and noise exponential (fp32 [n_seq][vocab],
+   positive) the tokens are distributed as the target alone would give them.
+   Logits: ltype PF_L_F32 or PF_L_BF16, row strides target_ld, draft_ld, values
+   of -inf allowed (probability 0).  Outputs: n_accept[s] (int32), token[s]
+   (int32) and, where p_accept_dev is not NULL, for each row that judges a draft
+   min(1, p(d) / q(d)) (fp32 [rows]; 0 for a sequence's last row), whether or
+   not it is reached.  A draft outside [0, vocab) has probability 0.  A row
+   without a distribution (a NaN, +inf, or only -inf, in the target or the
+   draft) ends its sequence there: p_accept NaN, token -1.  A sequence whose
+   rows first_dev puts outside [0, rows), or of no rows, gives n_accept -1 and
+   token -1.
+   work_dev: device scratch, 256-byte aligned, at least
+   pfop_verify_draft_work_bytes(rows, n_seq); it needs no clearing; calls that
+   share it may not overlap on the GPU.  Recordable.
+   PF_E_ARG: rows outside [0, 2^20], n_seq outside [0, rows]; vocab < 1 or
+   >= 2^30, a row stride below it; missing or misaligned buffers (logits to
+   their element, others to 4 bytes); a scratch too small. */
+int pfop_verify_draft(int32_t ltype, const void* target_dev, int64_t target_ld, const void* draft_dev,
+                      int64_t draft_ld, int32_t rows, int32_t n_seq, int32_t vocab, const int32_t* tokens_dev,
+                      const int32_t* first_dev, const float* u_dev, const float* noise_dev, int32_t* n_accept_dev,
+                      int32_t* token_dev, float* p_accept_dev, void* work_dev, int64_t work_bytes, void* stream);
+int64_t pfop_verify_draft_work_bytes(int32_t rows, int32_t n_seq);
+
 /* Last error message of a pfop_* call on this thread. */
 const char* pfop_last_error(void);
 

@@ -52,7 +52,8 @@ EXPORTS = (
     "pfop_linear_wait_test", "prefill_ubatch_seqs", "prefill_seq_n_pos", "prefill_seq_reset",
     "prefill_graph_capture", "prefill_graph_launch", "pfop_set_gemm_pairs", "pfop_qkv_row_order",
     "pfop_repack_q4", "pfop_attention_packed", "pfop_attention_tree", "pfop_attention_work_bytes",
-    "pfop_attention_status", "pfop_logprobs",
+    "pfop_attention_status", "pfop_logprobs", "pfop_attention_paged", "pfop_attention_paged_work_bytes",
+    "pfop_attention_paged_status", "pfop_qk_norm_rope", "pfop_verify_draft", "pfop_verify_draft_work_bytes",
 )
 
 
@@ -174,6 +175,14 @@ def load(path: str = LIB_PATH) -> C.CDLL:
         "pfop_attention_work_bytes": (i64, [i32, i32, i32, C.POINTER(AttnRun), i32]),
         "pfop_attention_status": (C.c_int, [vp, vp]),
         "pfop_logprobs": (C.c_int, [i32, vp, i64, i32, i32, vp, i32, vp, vp, vp, vp, vp]),
+        "pfop_attention_paged": (C.c_int, [vp, vp, vp, i32, i32, i32, i32, i32, C.POINTER(AttnRun), i32, vp, i64, vp,
+                                           i32, vp, vp, i64, vp]),
+        "pfop_attention_paged_work_bytes": (i64, [i32, i32, i32, C.POINTER(AttnRun), i32]),
+        "pfop_attention_paged_status": (C.c_int, [vp, vp]),
+        "pfop_qk_norm_rope": (C.c_int, [i32, vp, i64, vp, i64, vp, i64, i32, i32, i32, i32, vp, vp, vp, vp, f32, f32,
+                                        vp, vp, vp, i64, vp]),
+        "pfop_verify_draft": (C.c_int, [i32, vp, i64, vp, i64, i32, i32, i32, vp, vp, vp, vp, vp, vp, vp, vp, i64, vp]),
+        "pfop_verify_draft_work_bytes": (i64, [i32, i32]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -383,8 +392,9 @@ def _i32(x, what: str) -> int:
 
 
 class AttnRuns:
-    """The runs of an attention_packed / attention_tree call and the call's
-    scratch: runs = [(n_rows, pos0, cell0), ...] (see pfop_attn_run), for
+    """The runs of an attention_packed / attention_tree / attention_paged call
+    and the call's scratch: runs = [(n_rows, pos0, cell0), ...] (see
+    pfop_attn_run; over pages cell0 is the run's first entry in the table), for
     n_head / n_head_kv heads of head_dim.  Kept by a program for as many
     calls as have these runs, and until the last of them is done; calls that
     use one AttnRuns share its scratch, so they must not overlap on the GPU
@@ -402,7 +412,7 @@ class AttnRuns:
         self.runs = (AttnRun * max(1, len(runs)))(*[AttnRun(*r) for r in runs])
         with torch.cuda.device(device if device is not None else torch.cuda.current_device()):
             self.device = torch.cuda.current_device()
-            need = int(self._lib.pfop_attention_work_bytes(*self.shape, self.runs, self.n_runs))
+            need = int(self._lib.pfop_attention_paged_work_bytes(*self.shape, self.runs, self.n_runs))
             if need < 0:
                 check_op(need)
             self.work = torch.empty(need, dtype=torch.uint8, device="cuda")
@@ -413,8 +423,8 @@ class AttnRuns:
 
     def check(self, stream=None):
         """Wait for the stream (None: the current one) and raise if a call
-        gave up a bounded wait."""
-        _call_on(self.device, stream, self._lib.pfop_attention_status, self.work_at)
+        gave up a bounded wait, or met a page id outside its cache."""
+        _call_on(self.device, stream, self._lib.pfop_attention_paged_status, self.work_at)
 
     def _fit(self, q, k, v, out):
         """The number of cells; raises where a buffer does not fit."""
@@ -454,19 +464,23 @@ def attention_packed(q, k, v, runs: AttnRuns, out, stream=None):
              *runs.shape, runs.runs, runs.n_runs, out.data_ptr(), runs.work_at, runs.work_bytes)
 
 
-def attention_tree(q, k, v, runs: AttnRuns, mask, out, stream=None):
-    """Attention of drafted token trees (pfop_attention_tree): as
-    attention_packed, with mask [T, words] int64, bit j % 64 of word j / 64
-    set where the row sees drafted token j of its run."""
+def _mask_sizes(mask, runs):
     ms = mask.shape
     if len(ms) != 2 or ms[0] < runs.n_rows:
         raise ValueError(f"mask: needs [{runs.n_rows}, words]")
     if ms[1] > 4:
         raise ValueError(f"mask: at most 4 words a row, got {ms[1]}")
+
+
+def attention_tree(q, k, v, runs: AttnRuns, mask, out, stream=None):
+    """Attention of drafted token trees (pfop_attention_tree): as
+    attention_packed, with mask [T, words] int64, bit j % 64 of word j / 64
+    set where the row sees drafted token j of its run."""
+    _mask_sizes(mask, runs)
     cells = runs._fit(q, k, v, out)
-    m = _on_device(mask, "mask", _torch.int64, ms, runs.device)
+    m = _on_device(mask, "mask", _torch.int64, mask.shape, runs.device)
     _call_on(runs.device, stream, runs._lib.pfop_attention_tree, q.data_ptr(), k.data_ptr(), v.data_ptr(), cells,
-             *runs.shape, runs.runs, runs.n_runs, m, ms[1], out.data_ptr(), runs.work_at, runs.work_bytes)
+             *runs.shape, runs.runs, runs.n_runs, m, mask.shape[1], out.data_ptr(), runs.work_at, runs.work_bytes)
 
 
 def logprobs(logits, tokens=None, logp=None, entropy=None, top_id=None, top_logp=None, stream=None):
@@ -502,6 +516,161 @@ def logprobs(logits, tokens=None, logp=None, entropy=None, top_id=None, top_logp
              None if entropy is None else _on_device(entropy, "entropy", f32, one, d),
              None if top_id is None else _on_device(top_id, "top_id", i32, (rows, n_top), d),
              None if top_logp is None else _on_device(top_logp, "top_logp", f32, (rows, n_top), d))
+
+
+# ---------------------------------------------------------------------------
+# a serving step over a paged cache
+
+
+def attention_paged(q, k, v, runs: AttnRuns, pages, out, mask=None, stream=None):
+    """Attention of new tokens over a paged cache (pfop_attention_paged): q
+    [T, n_head, head_dim] and k, v [n_pages, page_size, n_head_kv, head_dim]
+    float16, pages int32 (the runs' page ids: a run's cell0 counts from its
+    first element, row by row where it has two dimensions), out [T, n_head,
+    head_dim] bfloat16, mask as for attention_tree (None: causal), all on the
+    runs' device.  Enqueued on `stream` (None: the current torch stream)."""
+    ks = k.shape
+    if len(ks) != 4 or v.shape != ks:
+        raise ValueError(f"k and v: need [pages, page size, heads, head_dim], got {tuple(ks)}, {tuple(v.shape)}")
+    n_pages, page = _i32(ks[0], "pages of k"), _i32(ks[1], "page size")
+    kc, vc = k, v
+    if k.is_contiguous() and v.is_contiguous():
+        kc, vc = k.flatten(0, 1), v.flatten(0, 1)
+    runs._fit(q, kc, vc, out)
+    at = _on_device(pages, "pages", _torch.int32, pages.shape, runs.device)
+    m, words = None, 0
+    if mask is not None:
+        _mask_sizes(mask, runs)
+        words = mask.shape[1]
+        if words < 1:
+            raise ValueError("mask: needs at least a word a row")
+        m = _on_device(mask, "mask", _torch.int64, mask.shape, runs.device)
+    _call_on(runs.device, stream, runs._lib.pfop_attention_paged, q.data_ptr(), k.data_ptr(), v.data_ptr(), n_pages,
+             page, *runs.shape, runs.runs, runs.n_runs, at, pages.numel(), m, words, out.data_ptr(), runs.work_at,
+             runs.work_bytes)
+
+
+def _heads(t, what: str, dtype, index: int):
+    """(address, row stride, heads, head_dim) of [rows, heads, head_dim] whose
+    rows may be strided (parts of wider rows), their heads dense."""
+    if len(t.shape) != 3:
+        raise ValueError(f"{what}: needs [rows, heads, head_dim], got {tuple(t.shape)}")
+    if t.dtype is not dtype:
+        raise ValueError(f"{what}: element type must be {dtype}, got {t.dtype}")
+    if t.get_device() != index:
+        raise ValueError(f"{what}: must be on CUDA device {index}, is on {t.device}")
+    (n, h, d), (sn, sh, sd) = t.shape, t.stride()
+    if (d > 1 and sd != 1) or (h > 1 and sh != d):
+        raise ValueError(f"{what}: a row's heads must be dense")
+    return t.data_ptr(), sn if n > 1 else h * d, _i32(h, what), _i32(d, what)
+
+
+def qk_norm_rope(q, pos, q_out, k=None, v=None, slots=None, k_cache=None, v_cache=None, q_gain=None, k_gain=None,
+                 eps=1e-6, rope_base=10000.0, stream=None):
+    """Norm and rotation of queries and keys, K and V into the cache
+    (pfop_qk_norm_rope): q [T, n_head, head_dim], k, v [T, n_head_kv, head_dim]
+    float32 or bfloat16 (rows may be strided: parts of one projection's rows);
+    pos, slots [T] int32; q_out [T, n_head, head_dim] float16; k_cache, v_cache
+    [cells, n_head_kv, head_dim] or [pages, page size, n_head_kv, head_dim]
+    float16; gains [head_dim] float32 (None: no norm).  k None: queries only
+    (k_gain is then not looked at).
+    Enqueued on `stream` (None: the current torch stream)."""
+    torch = _t()
+    if q.dtype is torch.float32:
+        kind = PF_L_F32
+    elif q.dtype is torch.bfloat16:
+        kind = PF_L_BF16
+    else:
+        raise ValueError(f"q: element type must be float32 or bfloat16, got {q.dtype}")
+    d = q.get_device()
+    if d < 0:
+        raise ValueError(f"q: must be on a CUDA device, is on {q.device}")
+    qa, q_ld, hq, hd = _heads(q, "q", q.dtype, d)
+    rows = _i32(len(q), "q")
+    one, gain = (rows,), (hd,)
+    ka = va = sa = kca = vca = None
+    k_ld = v_ld = hkv = cells = 0
+    if k is not None:
+        if v is None or slots is None or k_cache is None or v_cache is None:
+            raise ValueError("k needs v, slots, k_cache and v_cache")
+        ka, k_ld, hkv, kd = _heads(k, "k", q.dtype, d)
+        va, v_ld, vh, vd = _heads(v, "v", q.dtype, d)
+        if (kd, vh, vd) != (hd, hkv, hd) or len(k) != rows or len(v) != rows or hkv < 1:
+            raise ValueError(f"k and v: shapes {tuple(k.shape)}, {tuple(v.shape)} do not fit q's {tuple(q.shape)}")
+        shape = k_cache.shape
+        if len(shape) not in (3, 4) or shape[-2:] != k.shape[1:]:
+            raise ValueError(f"k_cache: shape {tuple(shape)} does not fit {(hkv, hd)}")
+        kca = _on_device(k_cache, "k_cache", torch.float16, shape, d)
+        vca = _on_device(v_cache, "v_cache", torch.float16, shape, d)
+        cells = k_cache.numel() // (hkv * hd)
+        sa = _on_device(slots, "slots", torch.int32, one, d)
+    elif v is not None or slots is not None or k_cache is not None or v_cache is not None:
+        raise ValueError("v, slots, k_cache and v_cache go with k")
+    _call_on(d, stream, load().pfop_qk_norm_rope, kind, qa, q_ld, ka, k_ld, va, v_ld, rows, hq, hkv, hd,
+             _on_device(pos, "pos", torch.int32, one, d), sa,
+             None if q_gain is None else _on_device(q_gain, "q_gain", torch.float32, gain, d),
+             None if k is None or k_gain is None else _on_device(k_gain, "k_gain", torch.float32, gain, d), eps, rope_base,
+             _on_device(q_out, "q_out", torch.float16, q.shape, d), kca, vca, cells)
+
+
+class VerifyWork:
+    """The scratch of verify_draft calls of `rows` rows of `n_seq` sequences
+    (or fewer rows, or more sequences).  Calls that share one must not overlap
+    on the GPU."""
+
+    def __init__(self, rows: int, n_seq: int, device=None):
+        torch = _t()
+        need = int(load().pfop_verify_draft_work_bytes(_i32(rows, "rows"), _i32(n_seq, "n_seq")))
+        if need < 0:
+            check_op(need)
+        with torch.cuda.device(device if device is not None else torch.cuda.current_device()):
+            self.device = torch.cuda.current_device()
+            self.work = torch.empty(need, dtype=torch.uint8, device="cuda")
+        self.work_at, self.work_bytes = self.work.data_ptr(), need
+
+
+def verify_draft(target, tokens, first, u, noise, n_accept, token, p_accept, work: VerifyWork, draft=None,
+                 stream=None):
+    """Drafted tokens accepted or refused, and the token that follows
+    (pfop_verify_draft): target [rows, vocab] and draft [rows - sequences,
+    vocab] float32 or bfloat16 (rows may be strided; draft None: drafts without
+    a distribution); tokens [rows], first [sequences + 1] int32; u [rows],
+    noise [sequences, vocab] float32; outputs n_accept, token [sequences] int32
+    and p_accept [rows] float32 (None: not wanted).  Enqueued on `stream` (None:
+    the current torch stream)."""
+    torch = _t()
+    if target.dtype is torch.float32:
+        kind = PF_L_F32
+    elif target.dtype is torch.bfloat16:
+        kind = PF_L_BF16
+    else:
+        raise ValueError(f"target: element type must be float32 or bfloat16, got {target.dtype}")
+
+    def logits(t, what, rows, vocab):
+        shape, stride = t.shape, t.stride()
+        if shape != (rows, vocab) or t.dtype is not target.dtype or (vocab > 1 and stride[1] != 1):
+            raise ValueError(f"{what}: needs [{rows}, {vocab}] of {target.dtype} with dense rows")
+        if t.get_device() != work.device:
+            raise ValueError(f"{what}: must be on CUDA device {work.device}, is on {t.device}")
+        return t.data_ptr(), stride[0] if rows > 1 else vocab
+
+    if len(target.shape) != 2:
+        raise ValueError(f"target: needs [rows, vocab], got {tuple(target.shape)}")
+    rows, vocab = _i32(target.shape[0], "rows"), _i32(target.shape[1], "vocab")
+    n = first.numel() - 1
+    if n < 0 or n > rows:
+        raise ValueError(f"first: {n + 1} entries do not fit {rows} rows")
+    d, f32, i32 = work.device, torch.float32, torch.int32
+    ta, t_ld = logits(target, "target", rows, vocab)
+    da, d_ld = (None, 0) if draft is None else logits(draft, "draft", rows - n, vocab)
+    if rows == n:
+        da = None  # no drafts
+    _call_on(d, stream, load().pfop_verify_draft, kind, ta, t_ld, da, d_ld, rows, n, vocab,
+             _on_device(tokens, "tokens", i32, (rows,), d), _on_device(first, "first", i32, (n + 1,), d),
+             _on_device(u, "u", f32, (rows,), d), _on_device(noise, "noise", f32, (n, vocab), d),
+             _on_device(n_accept, "n_accept", i32, (n,), d), _on_device(token, "token", i32, (n,), d),
+             None if p_accept is None else _on_device(p_accept, "p_accept", f32, (rows,), d), work.work_at,
+             work.work_bytes)
 
 
 # ---------------------------------------------------------------------------
