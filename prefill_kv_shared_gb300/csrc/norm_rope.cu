@@ -76,94 +76,103 @@ __device__ __forceinline__ void nr_store(__half* dst, const float* v) {
     *reinterpret_cast<uint2*>(dst) = make_uint2(h[0], h[1]);
 }
 
-constexpr int NR_WARPS = 4;
+constexpr int NR_WARPS = 4, NR_CTAS = 6;  // of a CTA, of an SM
 constexpr int NR_BATCH = 2;  // steps whose loads are on their way together
 
 template <class T, int HD>
-__global__ void __launch_bounds__(32 * NR_WARPS) qk_norm_rope_kernel(const NormRopeArgs a,
-                                                                     const __grid_constant__ Turns<HD> turns) {
+__global__ void __launch_bounds__(32 * NR_WARPS, NR_CTAS) qk_norm_rope_kernel(const NormRopeArgs a,
+                                                                              const __grid_constant__ Turns<HD> turns) {
   constexpr int E = NrVec<T>::E, LANES = HD / 2 / E, HEADS = 32 / LANES;  // heads of a step
   __shared__ uint64_t f[HD / 2];
+  __shared__ alignas(16) float gain[2][HD];  // 1 + g of queries and of keys
   for (int i = threadIdx.x; i < HD / 2; i += 32 * NR_WARPS) f[i] = turns.f[i];
-  __syncthreads();
   pdl_launch();
   pdl_wait();
+  for (int i = threadIdx.x; i < HD; i += 32 * NR_WARPS) {
+    gain[0][i] = a.q_gain ? 1.f + a.q_gain[i] : 1.f;
+    gain[1][i] = a.k_gain ? 1.f + a.k_gain[i] : 1.f;
+  }
+  __syncthreads();
   const int lane = threadIdx.x & 31, sub = lane % LANES, in_step = lane / LANES, i0 = sub * E;
-  const int64_t unit = static_cast<int64_t>(blockIdx.x) * NR_WARPS + (threadIdx.x >> 5);
-  const int64_t t = unit / a.parts;
-  const int part = static_cast<int>(unit % a.parts);
-  if (t >= a.rows) return;
   const int heads = a.Hq + 2 * a.Hkv;
-  const int slot = a.Hkv > 0 ? a.slots[t] : -1;
-  const bool has_cell = slot >= 0 && slot < a.n_cells;
-  float cs[E], sn[E];
-  const int64_t pos = a.pos[t];
+  const int64_t units = static_cast<int64_t>(a.rows) * a.parts;
+  for (int64_t unit = static_cast<int64_t>(blockIdx.x) * NR_WARPS + (threadIdx.x >> 5); unit < units;
+       unit += static_cast<int64_t>(gridDim.x) * NR_WARPS) {
+    const int64_t t = a.parts == 1 ? unit : unit / a.parts;
+    const int part = static_cast<int>(unit - t * a.parts);
+    const int first = part * a.per * HEADS, end = min(heads, first + a.per * HEADS);
+    const int64_t pos = a.pos[t];
+    const int slot = a.Hkv > 0 ? a.slots[t] : -1;
+    const bool has_cell = slot >= 0 && slot < a.n_cells;
+    float cs[E], sn[E];
+    for (int h0 = first; h0 < end; h0 += NR_BATCH * HEADS) {
+      uint4 lo[NR_BATCH], hi[NR_BATCH];
 #pragma unroll
-  for (int i = 0; i < E; ++i) {
-    const uint64_t turn = static_cast<uint64_t>(pos) * f[i0 + i];
-    // the nearest of 2^32 steps of a turn, as half turns in [-1, 1)
-    const int phase = static_cast<int>(static_cast<uint32_t>((turn + 0x80000000ull) >> 32));
-    sincospif(static_cast<float>(phase) * 0x1p-31f, &sn[i], &cs[i]);
-  }
-  float qg[2 * E], kg[2 * E];
-#pragma unroll
-  for (int i = 0; i < 2 * E; ++i) {
-    const int at = i < E ? i0 + i : HD / 2 + i0 + i - E;
-    qg[i] = a.q_gain ? 1.f + a.q_gain[at] : 1.f;
-    kg[i] = a.k_gain ? 1.f + a.k_gain[at] : 1.f;
-  }
-  const int first = part * a.per * HEADS, end = min(heads, first + a.per * HEADS);
-  for (int h0 = first; h0 < end; h0 += NR_BATCH * HEADS) {
-    uint4 lo[NR_BATCH], hi[NR_BATCH];
-#pragma unroll
-    for (int b = 0; b < NR_BATCH; ++b) {
-      const int h = h0 + b * HEADS + in_step;
-      lo[b] = hi[b] = make_uint4(0u, 0u, 0u, 0u);
-      if (h < end) {
-        const T* src = h < a.Hq            ? static_cast<const T*>(a.q) + t * a.q_ld + h * HD
-                       : h < a.Hq + a.Hkv ? static_cast<const T*>(a.k) + t * a.k_ld + (h - a.Hq) * HD
-                                          : static_cast<const T*>(a.v) + t * a.v_ld + (h - a.Hq - a.Hkv) * HD;
-        lo[b] = *reinterpret_cast<const uint4*>(src + i0);
-        hi[b] = *reinterpret_cast<const uint4*>(src + HD / 2 + i0);
-      }
-    }
-#pragma unroll
-    for (int b = 0; b < NR_BATCH; ++b) {
-      const int h = h0 + b * HEADS + in_step;
-      float x[2 * E];
-      NrVec<T>::get(lo[b], x);
-      NrVec<T>::get(hi[b], x + E);
-      float s = 0.f;
-#pragma unroll
-      for (int i = 0; i < 2 * E; ++i) s = __fmaf_rn(x[i], x[i], s);
-#pragma unroll
-      for (int o = LANES / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-      if (h >= end) continue;
-      const bool is_q = h < a.Hq, is_v = h >= a.Hq + a.Hkv;
-      __half* dst;
-      if (is_q) {
-        dst = a.q_out + (t * a.Hq + h) * HD;
-      } else {
-        if (!has_cell) continue;
-        const int hk = is_v ? h - a.Hq - a.Hkv : h - a.Hq;
-        dst = (is_v ? a.v_cache : a.k_cache) + (static_cast<int64_t>(slot) * a.Hkv + hk) * HD;
-      }
-      float y[2 * E];
-      if (is_v) {
-#pragma unroll
-        for (int i = 0; i < 2 * E; ++i) y[i] = x[i];
-      } else {
-        const bool norm = is_q ? a.q_gain != nullptr : a.k_gain != nullptr;
-        const float r = norm ? rsqrtf(s * (1.f / HD) + a.eps) : 1.f;
-#pragma unroll
-        for (int i = 0; i < E; ++i) {
-          const float p = x[i] * r * (is_q ? qg[i] : kg[i]), q = x[E + i] * r * (is_q ? qg[E + i] : kg[E + i]);
-          y[i] = p * cs[i] - q * sn[i];
-          y[E + i] = p * sn[i] + q * cs[i];
+      for (int b = 0; b < NR_BATCH; ++b) {
+        const int h = h0 + b * HEADS + in_step;
+        lo[b] = hi[b] = make_uint4(0u, 0u, 0u, 0u);
+        if (h < end) {
+          const T* src = h < a.Hq           ? static_cast<const T*>(a.q) + t * a.q_ld + h * HD
+                         : h < a.Hq + a.Hkv ? static_cast<const T*>(a.k) + t * a.k_ld + (h - a.Hq) * HD
+                                            : static_cast<const T*>(a.v) + t * a.v_ld + (h - a.Hq - a.Hkv) * HD;
+          lo[b] = *reinterpret_cast<const uint4*>(src + i0);
+          hi[b] = *reinterpret_cast<const uint4*>(src + HD / 2 + i0);
         }
       }
-      nr_store<E>(dst + i0, y);
-      nr_store<E>(dst + HD / 2 + i0, y + E);
+      if (h0 == first) {
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+          const uint64_t turn = static_cast<uint64_t>(pos) * f[i0 + i];
+          // the nearest of 2^32 steps of a turn, in [-1/2, 1/2) turns
+          const int phase = static_cast<int>(static_cast<uint32_t>((turn + 0x80000000ull) >> 32));
+          // (sin.approx and cos.approx are off by 2^-20.9 there, 2^-9 of an fp16 step)
+          __sincosf(static_cast<float>(phase) * (6.283185307f * 0x1p-32f), &sn[i], &cs[i]);
+        }
+      }
+#pragma unroll
+      for (int b = 0; b < NR_BATCH; ++b) {
+        const int h = h0 + b * HEADS + in_step;
+        if (h0 + b * HEADS >= end) break;
+        float x[2 * E];
+        NrVec<T>::get(lo[b], x);
+        NrVec<T>::get(hi[b], x + E);
+        float s = 0.f;
+#pragma unroll
+        for (int i = 0; i < 2 * E; ++i) s = __fmaf_rn(x[i], x[i], s);
+#pragma unroll
+        for (int o = LANES / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        const bool is_q = h < a.Hq, is_v = h >= a.Hq + a.Hkv;
+        __half* dst = nullptr;
+        if (h < end) {
+          if (is_q)
+            dst = a.q_out + (t * a.Hq + h) * HD;
+          else if (has_cell)
+            dst = (is_v ? a.v_cache : a.k_cache) + (static_cast<int64_t>(slot) * a.Hkv + (h - a.Hq - (is_v ? a.Hkv : 0))) * HD;
+        }
+        if (!is_v) {
+          if (is_q ? a.q_gain != nullptr : a.k_gain != nullptr) {
+            const float r = rsqrtf(s * (1.f / HD) + a.eps);
+            const float* g = gain[is_q ? 0 : 1];
+#pragma unroll
+            for (int i = 0; i < E; i += 4) {
+              const float4 g0 = *reinterpret_cast<const float4*>(g + i0 + i);
+              const float4 g1 = *reinterpret_cast<const float4*>(g + HD / 2 + i0 + i);
+              x[i] *= r * g0.x, x[i + 1] *= r * g0.y, x[i + 2] *= r * g0.z, x[i + 3] *= r * g0.w;
+              x[E + i] *= r * g1.x, x[E + i + 1] *= r * g1.y, x[E + i + 2] *= r * g1.z, x[E + i + 3] *= r * g1.w;
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < E; ++i) {
+            const float p = x[i], q = x[E + i];
+            x[i] = p * cs[i] - q * sn[i];
+            x[E + i] = p * sn[i] + q * cs[i];
+          }
+        }
+        if (dst) {
+          nr_store<E>(dst + i0, x);
+          nr_store<E>(dst + HD / 2 + i0, x + E);
+        }
+      }
     }
   }
 }
@@ -197,9 +206,9 @@ static cudaError_t launch_norm_rope(NormRopeArgs a, float base, cudaStream_t s) 
   if (parts < 1) parts = 1;
   a.per = static_cast<int>((steps + parts - 1) / parts);
   a.parts = (steps + a.per - 1) / a.per;
-  const int64_t units = int64_t(a.rows) * a.parts;
-  return launch_k(qk_norm_rope_kernel<T, HD>, dim3(static_cast<unsigned>((units + NR_WARPS - 1) / NR_WARPS)),
-                  dim3(32 * NR_WARPS), 0, s, 1, a, turns_of<HD>(base));
+  const int64_t ctas = (int64_t(a.rows) * a.parts + NR_WARPS - 1) / NR_WARPS, fit = int64_t(sms) * NR_CTAS;
+  return launch_k(qk_norm_rope_kernel<T, HD>, dim3(static_cast<unsigned>(ctas < fit ? ctas : fit)), dim3(32 * NR_WARPS), 0,
+                  s, 1, a, turns_of<HD>(base));
 }
 
 }  // namespace pf

@@ -9,21 +9,31 @@
 // vocabulary decides.
 //
 // Two kernels.  draft_sums_kernel: maximum and sum of exponentials of each
-// row, target rows and draft rows alike, a row cut into slices where rows are
-// few.  draft_pick_kernel: a cluster a sequence; every CTA joins the slices'
-// sums of the sequence's rows, finds the first refusal, and looks through its
-// part of that row for the largest w / E.
+// row, target rows and draft rows alike.  The rows' chunks of 2 KB lie end to
+// end and every warp takes the same number of them, so that no row's end and
+// no last wave leaves SMs idle; a warp leaves a (maximum, sum) for each row
+// that it has a part of.  draft_pick_kernel: a cluster a sequence; every CTA
+// joins the parts of the sequence's rows, finds the first refusal, and looks
+// through its share of that row for the largest w / E.
 #include "../../include/prefill_ops.h"
 #include "common.cuh"
 #include "kernels.h"
 
+#include <algorithm>
 #include <string>
 
 namespace pf {
 
-constexpr int VD_THREADS = 256;
-constexpr int VD_SLICES_MAX = 8;
+constexpr int VD_SUM_WARPS = 4, VD_SUM_CTAS = 8;  // of a CTA, of an SM
+constexpr int VD_FLY = 4;                         // 16-byte vectors of a chunk per lane
+constexpr int VD_PARTS_MAX = 64;                  // warps that share a row
+// draft_pick_kernel, two CTAs to an SM.  (256 threads: 256 sequences of 32768
+// 28.2 to 33.0 us in all instead of 27.5, 64 ragged ones 16.6 to 17.9 instead
+// of 16.6, one sequence 7.9 instead of 8.1.)
+constexpr int VD_THREADS = 512;
 constexpr int VD_CLUSTER_MAX = 8;
+constexpr int VD_VECS = 2;  // vectors of four tokens that a thread looks at together
+constexpr int VD_GROUP = 32;  // rows whose decisions are made together
 constexpr float VD_LOG2E = 1.4426950408889634f;
 
 struct VerifyArgs {
@@ -34,8 +44,10 @@ struct VerifyArgs {
   const float *u, *noise;
   int *n_accept, *token;
   float* p_accept;
-  float2* sums;  // [target rows, then draft rows][slices]: maximum, sum
-  int slices, slice;
+  // [target rows, then draft rows][parts]: maximum and sum.  Row r's chunks are
+  // r chunks .. (r + 1) chunks - 1 of all; warp w takes per of them from w per on.
+  float2* sums;
+  int parts, chunks, per;
 };
 
 __device__ __forceinline__ float vd_ex2(float x) {
@@ -43,29 +55,90 @@ __device__ __forceinline__ float vd_ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+__device__ __forceinline__ float vd_rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 template <class T>
 struct VdVec;
 template <>
 struct VdVec<float> {
   static constexpr int N = 4;
+  static constexpr uint32_t NONE = 0xff800000u;  // -inf
+  // the largest of CNT vectors (NaNs aside)
+  template <int CNT>
+  static __device__ __forceinline__ float most(const uint4* r) {
+    float m[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+    for (int k = 0; k < CNT; ++k) {
+      m[0] = fmaxf(m[0], fmaxf(__uint_as_float(r[k].x), __uint_as_float(r[k].y)));
+      m[1] = fmaxf(m[1], fmaxf(__uint_as_float(r[k].z), __uint_as_float(r[k].w)));
+    }
+    return fmaxf(m[0], m[1]);
+  }
   static __device__ __forceinline__ void get(const uint4& r, float* v) {
     v[0] = __uint_as_float(r.x), v[1] = __uint_as_float(r.y), v[2] = __uint_as_float(r.z), v[3] = __uint_as_float(r.w);
   }
   static __device__ __forceinline__ float one(const float* p) { return *p; }
+  static __device__ __forceinline__ void four(const float* p, float* v) {
+    const float4 f = *reinterpret_cast<const float4*>(p);
+    v[0] = f.x, v[1] = f.y, v[2] = f.z, v[3] = f.w;
+  }
 };
 template <>
 struct VdVec<__nv_bfloat16> {
   static constexpr int N = 8;
-  static __device__ __forceinline__ void get(const uint4& r, float* v) {
-    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+  static constexpr uint32_t NONE = 0xff80ff80u;
+  static __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+  }
+  template <int CNT>
+  static __device__ __forceinline__ float most(const uint4* r) {
+    uint32_t m[2] = {NONE, NONE};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[2 * i] = __uint_as_float(w[i] << 16);
-      v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    for (int k = 0; k < CNT; ++k) {
+      m[0] = max2(m[0], max2(r[k].x, r[k].y));
+      m[1] = max2(m[1], max2(r[k].z, r[k].w));
     }
+    float v[2];
+    two(max2(m[0], m[1]), v);
+    return fmaxf(v[0], v[1]);
+  }
+  static __device__ __forceinline__ void two(uint32_t w, float* v) {
+    v[0] = __uint_as_float(w << 16);
+    v[1] = __uint_as_float(w & 0xffff0000u);
+  }
+  static __device__ __forceinline__ void get(const uint4& r, float* v) {
+    two(r.x, v), two(r.y, v + 2), two(r.z, v + 4), two(r.w, v + 6);
   }
   static __device__ __forceinline__ float one(const __nv_bfloat16* p) { return __bfloat162float(*p); }
+  static __device__ __forceinline__ void four(const __nv_bfloat16* p, float* v) {
+    const uint2 f = *reinterpret_cast<const uint2*>(p);
+    two(f.x, v), two(f.y, v + 2);
+  }
 };
+
+__device__ __forceinline__ uint64_t vd_pack(float a, float b) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
+  return d;
+}
+__device__ __forceinline__ float2 vd_unpack(uint64_t v) {
+  float2 f;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
+  return f;
+}
+// (x - m) log2 e of two.  The difference first: the rounding of m log2 e would
+// be a factor of the whole sum.
+__device__ __forceinline__ float2 vd_exponents(float a, float b, float minus_m) {
+  uint64_t d = vd_pack(a, b);
+  asm("add.rn.f32x2 %0, %0, %1;" : "+l"(d) : "l"(vd_pack(minus_m, minus_m)));
+  asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(d) : "l"(vd_pack(VD_LOG2E, VD_LOG2E)));
+  return vd_unpack(d);
+}
 
 // running maximum and sum of 2^((x - m) log2 e).  A NaN makes the sum one, and
 // so does +inf (inf - inf).
@@ -77,90 +150,260 @@ struct VdSum {
       m = to;
     }
   }
+  __device__ __forceinline__ void one(float x) {
+    raise(x);
+    z += vd_ex2((x - (m == -INFINITY ? 0.f : m)) * VD_LOG2E);
+  }
+  // CNT more, a multiple of 4, none above m
   template <int CNT>
   __device__ __forceinline__ void add(const float* x) {
-    float mx = x[0];
+    const float nm = m == -INFINITY ? 0.f : -m;
+    uint64_t s[2] = {0ull, 0ull};
 #pragma unroll
-    for (int i = 1; i < CNT; ++i) mx = fmaxf(mx, x[i]);
-    raise(mx);
-    const float at = m == -INFINITY ? 0.f : m;
-    float s = 0.f;
-#pragma unroll
-    for (int i = 0; i < CNT; ++i) s += vd_ex2((x[i] - at) * VD_LOG2E);
-    z += s;
+    for (int i = 0; i < CNT; i += 2) {
+      const float2 t = vd_exponents(x[i], x[i + 1], nm);
+      asm("add.rn.f32x2 %0, %0, %1;" : "+l"(s[(i >> 1) & 1]) : "l"(vd_pack(vd_ex2(t.x), vd_ex2(t.y))));
+    }
+    const float2 a = vd_unpack(s[0]), b = vd_unpack(s[1]);
+    z += (a.x + a.y) + (b.x + b.y);
   }
   __device__ __forceinline__ void join(float m2, float z2) {
     raise(m2);
     // (m2 -inf: nothing there but perhaps a NaN)
     z += m2 == -INFINITY ? (z2 != z2 ? z2 : 0.f) : z2 * vd_ex2((m2 - m) * VD_LOG2E);
   }
+  // over W lanes, the same in each
+  template <int W>
+  __device__ __forceinline__ void join_lanes() {
+    float to = m;
+#pragma unroll
+    for (int o = W / 2; o > 0; o >>= 1) to = fmaxf(to, __shfl_xor_sync(0xffffffffu, to, o));
+    raise(to);
+#pragma unroll
+    for (int o = W / 2; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+  }
 };
 
 template <class T>
-__global__ void __launch_bounds__(VD_THREADS) draft_sums_kernel(const VerifyArgs a) {
-  constexpr int N = VdVec<T>::N;
-  __shared__ float2 warps[VD_THREADS / 32];
-  const int tid = threadIdx.x;
-  pdl_launch();
+__global__ void __launch_bounds__(32 * VD_SUM_WARPS, VD_SUM_CTAS) draft_sums_kernel(const VerifyArgs a) {
+  constexpr int N = VdVec<T>::N, CHUNK = 32 * VD_FLY;  // vectors
+  const int lane = threadIdx.x & 31;
   pdl_wait();
-  const int r = static_cast<int>(blockIdx.x) / a.slices, sl = static_cast<int>(blockIdx.x) % a.slices;
-  const T* row = r < a.rows ? static_cast<const T*>(a.target) + r * a.t_ld
-                            : static_cast<const T*>(a.draft) + (r - a.rows) * a.d_ld;
-  const T* x = row + static_cast<int64_t>(sl) * a.slice;
-  const int n = max(0, min(a.slice, a.vocab - sl * a.slice));
-  const int mis = static_cast<int>((reinterpret_cast<uintptr_t>(x) & 15) / sizeof(T));
-  const int head = min(n, mis ? N - mis : 0), nvec = (n - head) / N, tail = head + nvec * N;
+  pdl_launch();  // after the wait: what the next kernel reads ahead of its own is there
+  const int64_t w = static_cast<int64_t>(blockIdx.x) * VD_SUM_WARPS + (threadIdx.x >> 5);
+  const int rows = a.rows + (a.draft ? a.rows - a.n_seq : 0);
+  const int64_t c0 = w * a.per, c1 = min(c0 + a.per, static_cast<int64_t>(rows) * a.chunks);
+  if (c0 >= c1) return;
+  int r = static_cast<int>(c0 / a.chunks), j = static_cast<int>(c0 % a.chunks);  // row and its chunk
+  int left = static_cast<int>(c1 - c0);
+  // a row: logits up to 16 bytes' alignment, vectors, the rest
+  const T* x;
+  int head, nvec;
+  auto begin_row = [&](int row) {
+    x = row < a.rows ? static_cast<const T*>(a.target) + row * a.t_ld : static_cast<const T*>(a.draft) + (row - a.rows) * a.d_ld;
+    const int mis = static_cast<int>((reinterpret_cast<uintptr_t>(x) & 15) / sizeof(T));
+    head = min(a.vocab, mis ? N - mis : 0);
+    nvec = (a.vocab - head) / N;
+  };
+  auto fetch = [&](uint4 (&v)[VD_FLY], int chunk) {
+    const uint4* p = reinterpret_cast<const uint4*>(x + head) + chunk * CHUNK + lane;
+    const int n = nvec - chunk * CHUNK - lane;
+    if (32 * (VD_FLY - 1) < n) {
+#pragma unroll
+      for (int k = 0; k < VD_FLY; ++k) v[k] = p[32 * k];
+    } else {
+      const uint32_t none = VdVec<T>::NONE;
+#pragma unroll
+      for (int k = 0; k < VD_FLY; ++k) v[k] = 32 * k < n ? p[32 * k] : make_uint4(none, none, none, none);
+    }
+  };
   VdSum s;
-  if (tid < head) {
-    const float v = VdVec<T>::one(x + tid);
-    s.add<1>(&v);
-  }
-  if (tid < n - tail) {
-    const float v = VdVec<T>::one(x + tail + tid);
-    s.add<1>(&v);
-  }
-  const uint4* vec = reinterpret_cast<const uint4*>(x + head);
-  constexpr int FLY = 32 / N;
-  for (int i = tid; i < nvec; i += FLY * VD_THREADS) {
-    uint4 v[FLY];
+  // one chunk in `v`, the next one on its way into `next`
+  auto chunk = [&](const uint4 (&v)[VD_FLY], uint4 (&next)[VD_FLY]) {
+    const bool ends = j == a.chunks - 1 || left == 1;
+    // the ragged ends go with the row's first and last chunk
+    float first = -INFINITY, last = -INFINITY;
+    if (j == 0 && lane < head) first = VdVec<T>::one(x + lane);
+    if (j == a.chunks - 1 && lane < a.vocab - head - nvec * N) last = VdVec<T>::one(x + head + nvec * N + lane);
+    const int row = r;
+    --left;
+    if (++j == a.chunks) {
+      j = 0, ++r;
+      if (left > 0) begin_row(r);
+    }
+    if (left > 0) fetch(next, j);
+    s.raise(VdVec<T>::template most<VD_FLY>(v));
 #pragma unroll
-    for (int k = 0; k < FLY; ++k)
-      if (i + k * VD_THREADS < nvec) v[k] = vec[i + k * VD_THREADS];
+    for (int k = 0; k < VD_FLY; k += 16 / N) {
+      float e[16];
 #pragma unroll
-    for (int k = 0; k < FLY; ++k)
-      if (i + k * VD_THREADS < nvec) {
-        float e[N];
-        VdVec<T>::get(v[k], e);
-        s.add<N>(e);
-      }
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) s.join(__shfl_xor_sync(0xffffffffu, s.m, o), __shfl_xor_sync(0xffffffffu, s.z, o));
-  if ((tid & 31) == 0) warps[tid >> 5] = make_float2(s.m, s.z);
-  __syncthreads();
-  if (tid == 0) {
-    for (int w = 1; w < VD_THREADS / 32; ++w) s.join(warps[w].x, warps[w].y);
-    a.sums[static_cast<int64_t>(r) * a.slices + sl] = make_float2(s.m, s.z);
+      for (int i = 0; i < 16 / N; ++i) VdVec<T>::get(v[k + i], e + i * N);
+      s.add<16>(e);
+    }
+    if (first != -INFINITY) s.one(first);
+    if (ends) {
+      if (last != -INFINITY) s.one(last);
+      s.join_lanes<32>();
+      const int part = static_cast<int>(w - static_cast<int64_t>(row) * a.chunks / a.per);
+      if (lane == 0) a.sums[static_cast<int64_t>(row) * a.parts + part] = make_float2(s.m, s.z);
+      s = VdSum();
+    }
+  };
+  uint4 even[VD_FLY], odd[VD_FLY];
+  begin_row(r);
+  fetch(even, j);
+#pragma unroll 1
+  for (;;) {
+    chunk(even, odd);
+    if (left == 0) break;
+    chunk(odd, even);
+    if (left == 0) break;
   }
 }
 
-// a candidate: the largest w / E and the lowest id at it (id -1: none)
+// a candidate: the largest w / E and the lowest token at it (id -1: none)
 struct VdBest {
-  float v = 0.f;
-  int id = -1;
+  float v;
+  int id;
   __device__ __forceinline__ void take(float v2, int id2) {
-    if (v2 > v || (v2 == v && id2 >= 0 && id2 < id)) v = v2, id = id2;
+    if (v2 > v || (v2 == v && id2 >= 0 && (id < 0 || id2 < id))) v = v2, id = id2;
   }
 };
 
 // what the next token is drawn from
 enum VdKind : int { VD_NONE = -1, VD_P = 0, VD_P_MINUS_Q = 1, VD_P_BUT_DRAFTED = 2 };
 
-template <class T>
-__global__ void __launch_bounds__(VD_THREADS) draft_pick_kernel(const VerifyArgs a, int cluster_log) {
+// Bound of the fast forms' errors, of p (and of q <= p).  ex2.approx is off by
+// 2^-22, its argument by three roundings of at most 126 2^-24 (times ln 2),
+// the reciprocal and the products by 2^-22: below 2^-16 each.
+constexpr float VD_OFF = 0x1p-15f;
+
+// The thread's share of the tokens: vectors of four, VD_VECS of them at once
+// (a batch), v0 + i step.  ALIGNED: a vector is one load in each array.
+template <class T, bool ALIGNED>
+struct VdScan {
+  const T *x, *y;  // target and draft row (null: none)
+  const float* noise;
+  float nm_p, nm_q;  // minus the maxima
+  float share;       // (1 / sum of q) / (1 / sum of p): w in units of 1 / sum of p
+  float z_p, z_q;    // 1 / sum
+  int vocab, d, v0, step;
+
+  __device__ __forceinline__ void logits(const T* row, int v, float* e) const {
+    if (ALIGNED) {
+      if (4 * v < vocab) {
+        VdVec<T>::four(row + 4 * v, e);
+      } else {
+        e[0] = e[1] = e[2] = e[3] = -INFINITY;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) e[i] = 4 * v + i < vocab ? VdVec<T>::one(row + 4 * v + i) : -INFINITY;
+    }
+  }
+  __device__ __forceinline__ void noises(int v, float* e) const {
+    if (ALIGNED) {
+      if (4 * v < vocab) {
+        VdVec<float>::four(noise + 4 * v, e);
+      } else {
+        e[0] = e[1] = e[2] = e[3] = 1.f;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) e[i] = 4 * v + i < vocab ? noise[4 * v + i] : 1.f;
+    }
+  }
+  // the same for a whole batch
+  __device__ __forceinline__ void noises_of(int v, float (&e)[VD_VECS][4]) const {
+#pragma unroll
+    for (int g = 0; g < VD_VECS; ++g) noises(v + g * step, e[g]);
+  }
+
+  // Bounds of the largest w / E: hi of the thread's best batch, hi2 of the
+  // others, lo of the true value.  e: the first batch's noise.
+  template <bool Q>
+  __device__ __forceinline__ void bounds(float (&e)[VD_VECS][4], float& hi, float& hi2, float& lo, int& at) const {
+    hi = hi2 = lo = 0.f;
+    at = v0;
+#pragma unroll 1
+    for (int v = v0; 4 * v < vocab; v += VD_VECS * step) {
+      float px[VD_VECS][4], qx[VD_VECS][4], next[VD_VECS][4];
+#pragma unroll
+      for (int g = 0; g < VD_VECS; ++g) {
+        logits(x, v + g * step, px[g]);
+        if (Q) logits(y, v + g * step, qx[g]);
+      }
+      noises_of(v + VD_VECS * step, next);
+      float h = 0.f, l = 0.f;
+#pragma unroll
+      for (int g = 0; g < VD_VECS; ++g) {
+        if (!Q && static_cast<unsigned>(d - 4 * (v + g * step)) < 4u) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (4 * (v + g * step) + i == d) px[g][i] = -INFINITY;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; i += 2) {
+          const float2 tp = vd_exponents(px[g][i], px[g][i + 1], nm_p);
+          float p[2] = {vd_ex2(tp.x), vd_ex2(tp.y)};
+          const float r[2] = {vd_rcp(e[g][i]), vd_rcp(e[g][i + 1])};
+          if (Q) {
+            const float2 tq = vd_exponents(qx[g][i], qx[g][i + 1], nm_q);
+            const float q[2] = {vd_ex2(tq.x), vd_ex2(tq.y)};
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const float w = __fmaf_rn(-q[k], share, p[k]);
+              h = fmaxf(h, __fmaf_rn(p[k], VD_OFF, w) * r[k]);
+              l = fmaxf(l, __fmaf_rn(p[k], -VD_OFF, w) * r[k]);
+            }
+          } else {
+            h = fmaxf(h, fmaxf(p[0] * r[0], p[1] * r[1]));
+          }
+        }
+      }
+      hi2 = fmaxf(hi2, fminf(hi, h));
+      if (h > hi) hi = h, at = v;
+      lo = fmaxf(lo, l);
+#pragma unroll
+      for (int g = 0; g < VD_VECS; ++g)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) e[g][i] = next[g][i];
+    }
+    if (!Q) {
+      lo = hi * (1.f - VD_OFF);
+      hi *= 1.f + VD_OFF;
+      hi2 *= 1.f + VD_OFF;
+    }
+  }
+  // the batch at v, with expf and a division
+  __device__ __forceinline__ void exact(int v, bool minus_q, bool but_d, VdBest& best) const {
+    float px[VD_VECS][4], qx[VD_VECS][4], e[VD_VECS][4];
+#pragma unroll
+    for (int g = 0; g < VD_VECS; ++g) {
+      logits(x, v + g * step, px[g]);
+      if (minus_q) logits(y, v + g * step, qx[g]);
+      noises(v + g * step, e[g]);
+    }
+#pragma unroll
+    for (int g = 0; g < VD_VECS; ++g)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int id = 4 * (v + g * step) + i;
+        // (a fused w would leave p's rounding where p and q are alike)
+        float w = __fmul_rn(expf(px[g][i] + nm_p), z_p);
+        if (minus_q) w = __fsub_rn(w, __fmul_rn(expf(qx[g][i] + nm_q), z_q));
+        if (w > 0.f && !(but_d && id == d)) best.take(w / e[g][i], id);
+      }
+  }
+};
+
+template <class T, bool ALIGNED>
+__global__ void __launch_bounds__(VD_THREADS, 2) draft_pick_kernel(const VerifyArgs a, int cluster_log) {
+  constexpr int WARPS = VD_THREADS / 32;
   __shared__ int sh_at, sh_kind;
   __shared__ float2 sh_p, sh_q;
-  __shared__ VdBest sh_warp[VD_THREADS / 32];
+  __shared__ float2 sh_sums[2][VD_GROUP];  // maximum and 1 / sum (0: no distribution) of target and draft rows
+  __shared__ VdBest sh_warp[WARPS];
   __shared__ float2 sh_all[2][VD_CLUSTER_MAX];  // each CTA's candidate, of both rounds
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int cluster = 1 << cluster_log;
@@ -168,45 +411,72 @@ __global__ void __launch_bounds__(VD_THREADS) draft_pick_kernel(const VerifyArgs
   // no CTA writes into another before that one runs: arrive now, wait there
   if (cluster > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
   pdl_launch();
-  pdl_wait();
-  const int r0 = a.first[s], r1 = a.first[s + 1];
-  const bool fits = r0 >= 0 && r1 > r0 && r1 <= a.rows && r1 - s - 1 <= a.rows - a.n_seq && r0 >= s;
   const T* target = static_cast<const T*>(a.target);
   const T* draft = static_cast<const T*>(a.draft);
-  if (warp == 0) {
-    // maximum and 1 / sum of row r of the sums; y 0: no distribution
-    auto joined = [&](int r) {
+  VdScan<T, ALIGNED> scan;
+  scan.noise = a.noise + static_cast<int64_t>(s) * a.vocab;
+  scan.vocab = a.vocab;
+  scan.v0 = rank * VD_THREADS + tid;
+  scan.step = cluster * VD_THREADS;
+  // the first noise is fetched while the sums are still being formed
+  float e[VD_VECS][4];
+  scan.noises_of(scan.v0, e);
+  const int r0 = a.first[s], r1 = a.first[s + 1];
+  const bool fits = r0 >= 0 && r1 > r0 && r1 <= a.rows && r1 - s - 1 <= a.rows - a.n_seq && r0 >= s;
+  bool waited = false;
+  if (tid == 0) sh_at = -1, sh_kind = VD_NONE, sh_p = sh_q = make_float2(0.f, 0.f);
+  // VD_GROUP rows at a time; rank 0 also writes the shares of those behind the stop
+  for (int base = r0; fits && base < r1; base += VD_GROUP) {
+    const int r = base + lane, dr = r - s;
+    const bool judges = warp == 0 && r < r1 - 1;
+    const int d = judges ? a.tokens[r + 1] : -1;
+    const float u = judges ? a.u[r] : 0.f;
+    const bool known = d >= 0 && d < a.vocab;
+    const float xd = known ? VdVec<T>::one(target + r * a.t_ld + d) : -INFINITY;
+    const float yd = known && draft ? VdVec<T>::one(draft + dr * a.d_ld + d) : -INFINITY;
+    if (!waited) pdl_wait();
+    waited = true;
+    // the parts of a row in 16 lanes
+    const int count = min(VD_GROUP, r1 - base), items = draft ? 2 * count : count;
+    for (int it0 = 2 * warp; it0 < items; it0 += 2 * WARPS) {
+      const int it = it0 + (lane >> 4), of_draft = it >= count ? 1 : 0, i = it - (of_draft ? count : 0);
+      const bool is = it < items && (!of_draft || base + i < r1 - 1);
       VdSum z;
-      for (int i = 0; i < a.slices; ++i) {
-        const float2 p = __ldcg(a.sums + static_cast<int64_t>(r) * a.slices + i);
-        z.join(p.x, p.y);
+      if (is) {
+        const int64_t row = of_draft ? a.rows + base + i - s : base + i;
+        const int n = static_cast<int>(((row + 1) * a.chunks - 1) / a.per - row * a.chunks / a.per) + 1;
+        float2 p[VD_PARTS_MAX / 16];
+#pragma unroll
+        for (int k = 0; k < VD_PARTS_MAX / 16; ++k) {
+          p[k] = make_float2(-INFINITY, 0.f);
+          if ((lane & 15) + 16 * k < n) p[k] = __ldcg(a.sums + row * a.parts + (lane & 15) + 16 * k);
+        }
+#pragma unroll
+        for (int k = 0; k < VD_PARTS_MAX / 16; ++k) z.join(p[k].x, p[k].y);
       }
-      return make_float2(z.m, z.z >= 0.5f && z.m < INFINITY ? 1.f / z.z : 0.f);
-    };
-    int at = -1, kind = VD_NONE;
-    float2 zp = make_float2(0.f, 0.f), zq = zp;
-    // 32 rows at a time; rank 0 also writes the shares of those behind the stop
-    for (int base = r0; fits && base < r1 && (at < 0 || rank == 0); base += 32) {
-      const int r = base + lane;
+      z.join_lanes<16>();
+      if (is && (lane & 15) == 0)
+        sh_sums[of_draft][i] = make_float2(z.m, z.z >= 0.5f && z.m < INFINITY ? 1.f / z.z : 0.f);
+    }
+    __syncthreads();
+    if (warp == 0) {
       float2 p = make_float2(0.f, 0.f), q = p;
       int k = VD_NONE;
       bool stop = false;
       if (r < r1) {
-        p = joined(r);
+        p = sh_sums[0][lane];
         float share = 0.f;
-        if (r == r1 - 1) {
+        if (!judges) {
           stop = true;
           if (p.y > 0.f) k = VD_P;
         } else {
-          const int d = a.tokens[r + 1], dr = r - s;
-          const bool known = d >= 0 && d < a.vocab;
-          if (draft) q = joined(a.rows + dr);
+          if (draft) q = sh_sums[1][lane];
           if (p.y > 0.f && (!draft || q.y > 0.f)) {
             k = draft ? VD_P_MINUS_Q : VD_P_BUT_DRAFTED;
-            const float pd = known ? expf(VdVec<T>::one(target + r * a.t_ld + d) - p.x) * p.y : 0.f;
-            const float qd = known && draft ? expf(VdVec<T>::one(draft + dr * a.d_ld + d) - q.x) * q.y : 1.f;
+            const float pd = known ? expf(xd - p.x) * p.y : 0.f;
+            const float qd = known && draft ? expf(yd - q.x) * q.y : 1.f;
             share = pd >= qd ? (pd > 0.f ? 1.f : 0.f) : pd / qd;
-            stop = !(a.u[r] * qd < pd);
+            stop = !(u * qd < pd);
           } else {
             share = __int_as_float(0x7fc00000);
             stop = true;
@@ -215,48 +485,65 @@ __global__ void __launch_bounds__(VD_THREADS) draft_pick_kernel(const VerifyArgs
         if (rank == 0 && a.p_accept) a.p_accept[r] = share;
       }
       const unsigned stops = __ballot_sync(0xffffffffu, stop);
-      if (at < 0 && stops) {
-        const int src = __ffs(stops) - 1;
-        at = base + src;
-        kind = __shfl_sync(0xffffffffu, k, src);
-        zp = make_float2(__shfl_sync(0xffffffffu, p.x, src), __shfl_sync(0xffffffffu, p.y, src));
-        zq = make_float2(__shfl_sync(0xffffffffu, q.x, src), __shfl_sync(0xffffffffu, q.y, src));
+      if (stops && sh_at < 0 && lane == __ffs(stops) - 1) {
+        sh_kind = k, sh_p = p, sh_q = q;
+        if (rank == 0) a.n_accept[s] = r - r0;
+        sh_at = r;
       }
     }
-    if (lane == 0) {
-      sh_at = at, sh_kind = kind, sh_p = zp, sh_q = zq;
-      if (rank == 0) a.n_accept[s] = fits ? at - r0 : -1;
-    }
+    __syncthreads();
+    if (sh_at >= 0 && (rank != 0 || !a.p_accept)) break;
   }
+  if (!waited) pdl_wait();
+  if (!fits && rank == 0 && tid == 0) a.n_accept[s] = -1;
   __syncthreads();
   const int at = sh_at;
   int kind = sh_kind;
   const float2 zp = sh_p, zq = sh_q;
-  const int d = kind == VD_P_BUT_DRAFTED ? a.tokens[at + 1] : -1;
-  VdBest best;
-  if (cluster > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-  // Where nothing is left to draw from (p and q alike, or all of p on the
-  // drafted token), p itself, in a second round.
+  scan.d = kind == VD_P_BUT_DRAFTED ? a.tokens[at + 1] : -1;
+  scan.x = target + max(at, 0) * a.t_ld;
+  scan.y = kind == VD_P_MINUS_Q ? draft + (at - s) * a.d_ld : nullptr;
+  scan.nm_p = -zp.x, scan.z_p = zp.y;
+  scan.nm_q = -zq.x, scan.z_q = zq.y;
+  scan.share = zq.y / zp.y;
+  VdBest best{0.f, -1};
+  // A second round, of p itself, where nothing is left to draw from (p and q
+  // alike, or all of p on the drafted token).
   for (int round = 0; round < 2; ++round) {
     if (kind != VD_NONE) {
-      const T* x = target + at * a.t_ld;
-      const T* y = kind == VD_P_MINUS_Q ? draft + (at - s) * a.d_ld : nullptr;
-      const float* noise = a.noise + static_cast<int64_t>(s) * a.vocab;
-      for (int v = rank * VD_THREADS + tid; v < a.vocab; v += cluster * VD_THREADS) {
-        // (a fused w would leave p's rounding where p and q are alike)
-        float w = __fmul_rn(expf(VdVec<T>::one(x + v) - zp.x), zp.y);
-        if (y) w = __fsub_rn(w, __fmul_rn(expf(VdVec<T>::one(y + v) - zq.x), zq.y));
-        if (kind == VD_P_BUT_DRAFTED && v == d) w = 0.f;
-        if (w > 0.f) best.take(w / noise[v], v);
+      // Batches to be looked at exactly: the thread's best one where it may
+      // hold the warp's answer, all of the warp's where others may too.
+      int v = scan.v0;
+      bool all = true, mine = true;
+      if (round == 0) {
+        float hi, hi2, lo;
+        int batch;
+        if (kind == VD_P_MINUS_Q)
+          scan.template bounds<true>(e, hi, hi2, lo, batch);
+        else
+          scan.template bounds<false>(e, hi, hi2, lo, batch);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) lo = fmaxf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+        all = __any_sync(0xffffffffu, hi2 > 0.f && hi2 >= lo);
+        mine = all || (hi > 0.f && hi >= lo);
+        if (!all) v = batch;
+      }
+      for (; mine && 4 * v < a.vocab; v += VD_VECS * scan.step) {
+        scan.exact(v, kind == VD_P_MINUS_Q, kind == VD_P_BUT_DRAFTED, best);
+        if (!all) break;
       }
     }
+    // over the warp, the CTA, the cluster
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) best.take(__shfl_xor_sync(0xffffffffu, best.v, o), __shfl_xor_sync(0xffffffffu, best.id, o));
     if (lane == 0) sh_warp[warp] = best;
     __syncthreads();
-    best = sh_warp[0];
-    for (int w = 1; w < VD_THREADS / 32; ++w) best.take(sh_warp[w].v, sh_warp[w].id);
+    best = sh_warp[lane % WARPS];
+#pragma unroll
+    for (int o = WARPS / 2; o > 0; o >>= 1)
+      best.take(__shfl_xor_sync(0xffffffffu, best.v, o), __shfl_xor_sync(0xffffffffu, best.id, o));
     if (cluster > 1) {
+      if (round == 0) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
       if (tid < cluster) {
         const uint32_t to = map_to_rank(smem_u32(&sh_all[round][rank]), tid);
         asm volatile("st.shared::cluster.v2.b32 [%0], {%1, %2};" ::"r"(to), "r"(__float_as_int(best.v)), "r"(best.id) : "memory");
@@ -271,6 +558,12 @@ __global__ void __launch_bounds__(VD_THREADS) draft_pick_kernel(const VerifyArgs
   if (rank == 0 && tid == 0) a.token[s] = best.id;
 }
 
+// logits of a chunk
+template <class T>
+constexpr int vd_chunk() {
+  return 32 * VD_FLY * VdVec<T>::N;
+}
+
 template <class T>
 static cudaError_t launch_verify(VerifyArgs a, cudaStream_t s) {
   int dev = 0, sms = 0;
@@ -278,16 +571,26 @@ static cudaError_t launch_verify(VerifyArgs a, cudaStream_t s) {
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
   const int64_t rows = a.rows + (a.draft ? a.rows - a.n_seq : 0);
-  int slices = 1;
-  while (slices < VD_SLICES_MAX && rows * slices * 2 <= 4 * sms && a.vocab / (2 * slices) >= 2048) slices *= 2;
-  a.slices = slices;
-  a.slice = ((a.vocab + slices - 1) / slices + 7) / 8 * 8;
-  e = launch_k(draft_sums_kernel<T>, dim3(static_cast<unsigned>(rows * slices)), dim3(VD_THREADS), 0, s, 1, a);
+  a.chunks = (a.vocab + vd_chunk<T>() - 1) / vd_chunk<T>();
+  // even shares over the resident warps; a row in at most VD_PARTS_MAX of them
+  const int64_t all = rows * a.chunks, warps = int64_t(sms) * VD_SUM_CTAS * VD_SUM_WARPS;
+  a.per = static_cast<int>(std::max((all + warps - 1) / warps, (int64_t(a.chunks) + VD_PARTS_MAX - 2) / (VD_PARTS_MAX - 1)));
+  a.parts = static_cast<int>(std::min<int64_t>(VD_PARTS_MAX, (a.chunks - 1) / a.per + 2));
+  const int64_t used = (all + a.per - 1) / a.per;
+  e = launch_k(draft_sums_kernel<T>, dim3(static_cast<unsigned>((used + VD_SUM_WARPS - 1) / VD_SUM_WARPS)),
+               dim3(32 * VD_SUM_WARPS), 0, s, 1, a);
   if (e != cudaSuccess) return e;
+  auto at = [](const void* p) { return reinterpret_cast<uintptr_t>(p); };
+  const bool aligned = a.vocab % 4 == 0 && a.t_ld % 4 == 0 && (!a.draft || a.d_ld % 4 == 0) &&
+                       ((at(a.target) | at(a.draft)) & (4 * sizeof(T) - 1)) == 0 && (at(a.noise) & 15) == 0;
+  // more CTAs a sequence while all fit the GPU at once and each thread has a batch
   int cluster = 1;
-  while (cluster < VD_CLUSTER_MAX && int64_t(a.n_seq) * cluster * 2 <= 4 * sms) cluster *= 2;
-  return launch_k(draft_pick_kernel<T>, dim3(static_cast<unsigned>(a.n_seq) * cluster), dim3(VD_THREADS), 0, s, cluster, a,
-                  __builtin_ctz(cluster));
+  while (cluster < VD_CLUSTER_MAX && int64_t(a.n_seq) * cluster * 2 <= 2 * sms &&
+         a.vocab > cluster * VD_THREADS * VD_VECS * 4)
+    cluster *= 2;
+  const dim3 grid(static_cast<unsigned>(a.n_seq) * cluster), block(VD_THREADS);
+  return aligned ? launch_k(draft_pick_kernel<T, true>, grid, block, 0, s, cluster, a, __builtin_ctz(cluster))
+                 : launch_k(draft_pick_kernel<T, false>, grid, block, 0, s, cluster, a, __builtin_ctz(cluster));
 }
 
 }  // namespace pf
@@ -297,7 +600,7 @@ extern "C" int64_t pfop_verify_draft_work_bytes(int32_t rows, int32_t n_seq) {
     pf::set_op_error("rows outside [0, 2^20] or n_seq outside [0, rows]");
     return PF_E_ARG;
   }
-  return (2 * int64_t(rows) - n_seq) * pf::VD_SLICES_MAX * static_cast<int64_t>(sizeof(float2)) + 256;
+  return (2 * int64_t(rows) - n_seq) * pf::VD_PARTS_MAX * static_cast<int64_t>(sizeof(float2)) + 256;
 }
 
 extern "C" int pfop_verify_draft(int32_t ltype, const void* target_dev, int64_t target_ld, const void* draft_dev,
@@ -323,7 +626,7 @@ extern "C" int pfop_verify_draft(int32_t ltype, const void* target_dev, int64_t 
     return fail(PF_E_ARG, "misaligned buffer");
   if (work_bytes < pfop_verify_draft_work_bytes(rows, n_seq)) return fail(PF_E_ARG, "the scratch is smaller than these rows need");
   const VerifyArgs a{target_dev, draft_dev, target_ld, draft_ld, rows, n_seq, vocab, tokens_dev, first_dev, u_dev,
-                     noise_dev, n_accept_dev, token_dev, p_accept_dev, static_cast<float2*>(work_dev), 1, 0};
+                     noise_dev, n_accept_dev, token_dev, p_accept_dev, static_cast<float2*>(work_dev), 1, 1, 1};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const cudaError_t e = ltype == PF_L_F32 ? launch_verify<float>(a, s) : launch_verify<__nv_bfloat16>(a, s);
   if (e != cudaSuccess) return fail(PF_E_CUDA, std::string("draft verification launch: ") + cudaGetErrorString(e));
