@@ -12,8 +12,9 @@
 // position 2^31), where fp32 would be off by whole radians at 2^24.
 //
 // A lane holds E = 16 bytes' elements of each half of a head (the pair of a
-// rotation lies in one thread), HD / 2 / E lanes a head.  A warp takes some of
-// a row's heads one after another, so its sines serve all of them.
+// rotation lies in one thread), HD / 2 / E lanes a head; the heads that a warp
+// holds at once are a step.  All rows' steps lie end to end and every warp
+// takes the same number of them, so that its sines serve most of a row.
 #include "../../include/prefill_ops.h"
 #include "common.cuh"
 #include "kernels.h"
@@ -32,7 +33,7 @@ struct NormRopeArgs {
   const float *q_gain, *k_gain;
   int rows, Hq, Hkv;
   float eps;
-  int parts, per;  // warps that share a row, and the steps of each
+  int steps, per;  // of a row, of a warp
 };
 template <int HD>
 struct Turns {
@@ -44,14 +45,14 @@ template <class T>
 struct NrVec;
 template <>
 struct NrVec<float> {
-  static constexpr int E = 4;
+  static constexpr int E = 4, CTAS = 8;  // elements, CTAs that an SM's registers hold
   static __device__ __forceinline__ void get(const uint4& r, float* v) {
     v[0] = __uint_as_float(r.x), v[1] = __uint_as_float(r.y), v[2] = __uint_as_float(r.z), v[3] = __uint_as_float(r.w);
   }
 };
 template <>
 struct NrVec<__nv_bfloat16> {
-  static constexpr int E = 8;
+  static constexpr int E = 8, CTAS = 5;
   static __device__ __forceinline__ void get(const uint4& r, float* v) {
     const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
@@ -76,103 +77,153 @@ __device__ __forceinline__ void nr_store(__half* dst, const float* v) {
     *reinterpret_cast<uint2*>(dst) = make_uint2(h[0], h[1]);
 }
 
-constexpr int NR_WARPS = 4, NR_CTAS = 6;  // of a CTA, of an SM
-constexpr int NR_BATCH = 2;  // steps whose loads are on their way together
+// two fp32 operations in one instruction
+__device__ __forceinline__ uint64_t nr_pack(float a, float b) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
+  return d;
+}
+__device__ __forceinline__ float2 nr_unpack(uint64_t v) {
+  float2 f;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
+  return f;
+}
+__device__ __forceinline__ uint64_t nr_mul(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t nr_fma(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+
+constexpr int NR_WARPS = 4;
+// steps whose loads are on their way (8192 rows of 32 heads over 4 of 64, fp32:
+// 22.3 us with 2, 29.6 with 3, whose registers do not fit)
+constexpr int NR_FLY = 2;
 
 template <class T, int HD>
-__global__ void __launch_bounds__(32 * NR_WARPS, NR_CTAS) qk_norm_rope_kernel(const NormRopeArgs a,
-                                                                              const __grid_constant__ Turns<HD> turns) {
+__global__ void __launch_bounds__(32 * NR_WARPS, NrVec<T>::CTAS) qk_norm_rope_kernel(const NormRopeArgs a,
+    const __grid_constant__ Turns<HD> turns) {
   constexpr int E = NrVec<T>::E, LANES = HD / 2 / E, HEADS = 32 / LANES;  // heads of a step
   __shared__ uint64_t f[HD / 2];
   __shared__ alignas(16) float gain[2][HD];  // 1 + g of queries and of keys
   for (int i = threadIdx.x; i < HD / 2; i += 32 * NR_WARPS) f[i] = turns.f[i];
   pdl_launch();
   pdl_wait();
+  const int lane = threadIdx.x & 31, i0 = lane % LANES * E, in_step = lane / LANES;
+  const int heads = a.Hq + 2 * a.Hkv;
+  const int64_t g0 = (static_cast<int64_t>(blockIdx.x) * NR_WARPS + (threadIdx.x >> 5)) * a.per;
+  int left = static_cast<int>(min(static_cast<int64_t>(a.per), static_cast<int64_t>(a.rows) * a.steps - g0));
+  // a step on its way
+  struct Step {
+    uint4 lo, hi;
+    int pos, slot, row, h;  // h: this lane's head (from `heads` on: none)
+  };
+  int row = static_cast<int>(g0 / a.steps), step = static_cast<int>(g0 - static_cast<int64_t>(row) * a.steps), ahead = left;
+  auto fetch = [&](Step& s) {
+    if (ahead <= 0) return;
+    --ahead;
+    const int64_t t = row;
+    s.row = row;
+    s.h = step * HEADS + in_step;
+    s.pos = a.pos[t];
+    s.slot = a.Hkv > 0 ? a.slots[t] : -1;
+    if (s.h < heads) {
+      const T* src = s.h < a.Hq           ? static_cast<const T*>(a.q) + t * a.q_ld + s.h * HD
+                     : s.h < a.Hq + a.Hkv ? static_cast<const T*>(a.k) + t * a.k_ld + (s.h - a.Hq) * HD
+                                          : static_cast<const T*>(a.v) + t * a.v_ld + (s.h - a.Hq - a.Hkv) * HD;
+      s.lo = *reinterpret_cast<const uint4*>(src + i0);
+      s.hi = *reinterpret_cast<const uint4*>(src + HD / 2 + i0);
+    }
+    if (++step == a.steps) step = 0, ++row;
+  };
+  uint64_t cs[E / 2], sn[E / 2], ns[E / 2];  // cosines, sines, minus the sines
+  int of_row = -1;                           // whose they are
+  auto work = [&](const Step& st) {
+    if (st.row != of_row) {
+      of_row = st.row;
+      float c[E], n[E];
+#pragma unroll
+      for (int i = 0; i < E; ++i) {
+        const uint64_t turn = static_cast<uint64_t>(static_cast<int64_t>(st.pos)) * f[i0 + i];
+        // the nearest of 2^32 steps of a turn, in [-1/2, 1/2) turns
+        const int phase = static_cast<int>(static_cast<uint32_t>((turn + 0x80000000ull) >> 32));
+        // (sin.approx and cos.approx are off by 2^-20.9 there, 2^-9 of an fp16 step)
+        __sincosf(static_cast<float>(phase) * (6.283185307f * 0x1p-32f), &n[i], &c[i]);
+      }
+#pragma unroll
+      for (int i = 0; i < E / 2; ++i) {
+        cs[i] = nr_pack(c[2 * i], c[2 * i + 1]);
+        sn[i] = nr_pack(n[2 * i], n[2 * i + 1]);
+        ns[i] = nr_pack(-n[2 * i], -n[2 * i + 1]);
+      }
+    }
+    float x[2 * E];
+    NrVec<T>::get(st.lo, x);
+    NrVec<T>::get(st.hi, x + E);
+    uint64_t p[E / 2], q[E / 2], sq[2] = {0ull, 0ull};
+#pragma unroll
+    for (int i = 0; i < E / 2; ++i) {
+      p[i] = nr_pack(x[2 * i], x[2 * i + 1]);
+      q[i] = nr_pack(x[E + 2 * i], x[E + 2 * i + 1]);
+      sq[0] = nr_fma(p[i], p[i], sq[0]);
+      sq[1] = nr_fma(q[i], q[i], sq[1]);
+    }
+    const float2 s0 = nr_unpack(sq[0]), s1 = nr_unpack(sq[1]);
+    float s = (s0.x + s0.y) + (s1.x + s1.y);
+#pragma unroll
+    for (int o = LANES / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    const bool is_q = st.h < a.Hq, is_v = st.h >= a.Hq + a.Hkv;
+    __half* dst;
+    if (is_q) {
+      dst = a.q_out + (static_cast<int64_t>(st.row) * a.Hq + st.h) * HD;
+    } else {
+      if (st.h >= heads || st.slot < 0 || st.slot >= a.n_cells) return;
+      dst = (is_v ? a.v_cache : a.k_cache) + (static_cast<int64_t>(st.slot) * a.Hkv + (st.h - a.Hq - (is_v ? a.Hkv : 0))) * HD;
+    }
+    if (!is_v) {
+      if (is_q ? a.q_gain != nullptr : a.k_gain != nullptr) {
+        const float r = rsqrtf(s * (1.f / HD) + a.eps);
+        const uint64_t r2 = nr_pack(r, r);
+        const ulonglong2* g = reinterpret_cast<const ulonglong2*>(gain[is_q ? 0 : 1] + i0);
+#pragma unroll
+        for (int i = 0; i < E / 4; ++i) {
+          const ulonglong2 a0 = g[i], a1 = g[HD / 8 + i];
+          p[2 * i] = nr_mul(p[2 * i], nr_mul(r2, a0.x));
+          p[2 * i + 1] = nr_mul(p[2 * i + 1], nr_mul(r2, a0.y));
+          q[2 * i] = nr_mul(q[2 * i], nr_mul(r2, a1.x));
+          q[2 * i + 1] = nr_mul(q[2 * i + 1], nr_mul(r2, a1.y));
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < E / 2; ++i) {
+        const float2 lo = nr_unpack(nr_fma(q[i], ns[i], nr_mul(p[i], cs[i])));
+        const float2 hi = nr_unpack(nr_fma(p[i], sn[i], nr_mul(q[i], cs[i])));
+        x[2 * i] = lo.x, x[2 * i + 1] = lo.y, x[E + 2 * i] = hi.x, x[E + 2 * i + 1] = hi.y;
+      }
+    }
+    nr_store<E>(dst + i0, x);
+    nr_store<E>(dst + HD / 2 + i0, x + E);
+  };
+  Step st[NR_FLY] = {};
+#pragma unroll
+  for (int i = 0; i < NR_FLY; ++i) fetch(st[i]);
   for (int i = threadIdx.x; i < HD; i += 32 * NR_WARPS) {
     gain[0][i] = a.q_gain ? 1.f + a.q_gain[i] : 1.f;
     gain[1][i] = a.k_gain ? 1.f + a.k_gain[i] : 1.f;
   }
   __syncthreads();
-  const int lane = threadIdx.x & 31, sub = lane % LANES, in_step = lane / LANES, i0 = sub * E;
-  const int heads = a.Hq + 2 * a.Hkv;
-  const int64_t units = static_cast<int64_t>(a.rows) * a.parts;
-  for (int64_t unit = static_cast<int64_t>(blockIdx.x) * NR_WARPS + (threadIdx.x >> 5); unit < units;
-       unit += static_cast<int64_t>(gridDim.x) * NR_WARPS) {
-    const int64_t t = a.parts == 1 ? unit : unit / a.parts;
-    const int part = static_cast<int>(unit - t * a.parts);
-    const int first = part * a.per * HEADS, end = min(heads, first + a.per * HEADS);
-    const int64_t pos = a.pos[t];
-    const int slot = a.Hkv > 0 ? a.slots[t] : -1;
-    const bool has_cell = slot >= 0 && slot < a.n_cells;
-    float cs[E], sn[E];
-    for (int h0 = first; h0 < end; h0 += NR_BATCH * HEADS) {
-      uint4 lo[NR_BATCH], hi[NR_BATCH];
+  while (left > 0) {
 #pragma unroll
-      for (int b = 0; b < NR_BATCH; ++b) {
-        const int h = h0 + b * HEADS + in_step;
-        lo[b] = hi[b] = make_uint4(0u, 0u, 0u, 0u);
-        if (h < end) {
-          const T* src = h < a.Hq           ? static_cast<const T*>(a.q) + t * a.q_ld + h * HD
-                         : h < a.Hq + a.Hkv ? static_cast<const T*>(a.k) + t * a.k_ld + (h - a.Hq) * HD
-                                            : static_cast<const T*>(a.v) + t * a.v_ld + (h - a.Hq - a.Hkv) * HD;
-          lo[b] = *reinterpret_cast<const uint4*>(src + i0);
-          hi[b] = *reinterpret_cast<const uint4*>(src + HD / 2 + i0);
-        }
-      }
-      if (h0 == first) {
-#pragma unroll
-        for (int i = 0; i < E; ++i) {
-          const uint64_t turn = static_cast<uint64_t>(pos) * f[i0 + i];
-          // the nearest of 2^32 steps of a turn, in [-1/2, 1/2) turns
-          const int phase = static_cast<int>(static_cast<uint32_t>((turn + 0x80000000ull) >> 32));
-          // (sin.approx and cos.approx are off by 2^-20.9 there, 2^-9 of an fp16 step)
-          __sincosf(static_cast<float>(phase) * (6.283185307f * 0x1p-32f), &sn[i], &cs[i]);
-        }
-      }
-#pragma unroll
-      for (int b = 0; b < NR_BATCH; ++b) {
-        const int h = h0 + b * HEADS + in_step;
-        if (h0 + b * HEADS >= end) break;
-        float x[2 * E];
-        NrVec<T>::get(lo[b], x);
-        NrVec<T>::get(hi[b], x + E);
-        float s = 0.f;
-#pragma unroll
-        for (int i = 0; i < 2 * E; ++i) s = __fmaf_rn(x[i], x[i], s);
-#pragma unroll
-        for (int o = LANES / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-        const bool is_q = h < a.Hq, is_v = h >= a.Hq + a.Hkv;
-        __half* dst = nullptr;
-        if (h < end) {
-          if (is_q)
-            dst = a.q_out + (t * a.Hq + h) * HD;
-          else if (has_cell)
-            dst = (is_v ? a.v_cache : a.k_cache) + (static_cast<int64_t>(slot) * a.Hkv + (h - a.Hq - (is_v ? a.Hkv : 0))) * HD;
-        }
-        if (!is_v) {
-          if (is_q ? a.q_gain != nullptr : a.k_gain != nullptr) {
-            const float r = rsqrtf(s * (1.f / HD) + a.eps);
-            const float* g = gain[is_q ? 0 : 1];
-#pragma unroll
-            for (int i = 0; i < E; i += 4) {
-              const float4 g0 = *reinterpret_cast<const float4*>(g + i0 + i);
-              const float4 g1 = *reinterpret_cast<const float4*>(g + HD / 2 + i0 + i);
-              x[i] *= r * g0.x, x[i + 1] *= r * g0.y, x[i + 2] *= r * g0.z, x[i + 3] *= r * g0.w;
-              x[E + i] *= r * g1.x, x[E + i + 1] *= r * g1.y, x[E + i + 2] *= r * g1.z, x[E + i + 3] *= r * g1.w;
-            }
-          }
-#pragma unroll
-          for (int i = 0; i < E; ++i) {
-            const float p = x[i], q = x[E + i];
-            x[i] = p * cs[i] - q * sn[i];
-            x[E + i] = p * sn[i] + q * cs[i];
-          }
-        }
-        if (dst) {
-          nr_store<E>(dst + i0, x);
-          nr_store<E>(dst + HD / 2 + i0, x + E);
-        }
-      }
+    for (int i = 0; i < NR_FLY; ++i) {
+      if (left <= 0) break;
+      --left;
+      work(st[i]);
+      __syncwarp();
+      fetch(st[i]);
     }
   }
 }
@@ -195,20 +246,17 @@ static const Turns<HD>& turns_of(float base) {
 template <class T, int HD>
 static cudaError_t launch_norm_rope(NormRopeArgs a, float base, cudaStream_t s) {
   constexpr int HEADS = 32 / (HD / 2 / NrVec<T>::E);
-  const int steps = (a.Hq + 2 * a.Hkv + HEADS - 1) / HEADS;
+  a.steps = (a.Hq + 2 * a.Hkv + HEADS - 1) / HEADS;
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
-  // a warp a row where that fills the GPU, else a row's heads over more warps
-  int64_t parts = (int64_t(sms) * 16 + a.rows - 1) / a.rows;
-  if (parts > steps) parts = steps;
-  if (parts < 1) parts = 1;
-  a.per = static_cast<int>((steps + parts - 1) / parts);
-  a.parts = (steps + a.per - 1) / a.per;
-  const int64_t ctas = (int64_t(a.rows) * a.parts + NR_WARPS - 1) / NR_WARPS, fit = int64_t(sms) * NR_CTAS;
-  return launch_k(qk_norm_rope_kernel<T, HD>, dim3(static_cast<unsigned>(ctas < fit ? ctas : fit)), dim3(32 * NR_WARPS), 0,
-                  s, 1, a, turns_of<HD>(base));
+  // even shares of all rows' steps
+  const int64_t all = int64_t(a.rows) * a.steps, warps = int64_t(sms) * NrVec<T>::CTAS * NR_WARPS;
+  a.per = static_cast<int>((all + warps - 1) / warps);
+  const int64_t used = (all + a.per - 1) / a.per;
+  return launch_k(qk_norm_rope_kernel<T, HD>, dim3(static_cast<unsigned>((used + NR_WARPS - 1) / NR_WARPS)),
+                  dim3(32 * NR_WARPS), 0, s, 1, a, turns_of<HD>(base));
 }
 
 }  // namespace pf
