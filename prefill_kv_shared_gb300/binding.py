@@ -530,39 +530,47 @@ def attention_paged(q, k, v, runs: AttnRuns, pages, out, mask=None, stream=None)
     head_dim] bfloat16, mask as for attention_tree (None: causal), all on the
     runs' device.  Enqueued on `stream` (None: the current torch stream)."""
     ks = k.shape
-    if len(ks) != 4 or v.shape != ks:
-        raise ValueError(f"k and v: need [pages, page size, heads, head_dim], got {tuple(ks)}, {tuple(v.shape)}")
-    n_pages, page = _i32(ks[0], "pages of k"), _i32(ks[1], "page size")
-    kc, vc = k, v
-    if k.is_contiguous() and v.is_contiguous():
-        kc, vc = k.flatten(0, 1), v.flatten(0, 1)
-    runs._fit(q, kc, vc, out)
-    at = _on_device(pages, "pages", _torch.int32, pages.shape, runs.device)
+    if len(ks) != 4:
+        raise ValueError(f"k and v: need [pages, page size, heads, head_dim], got {tuple(ks)}")
+    # (one expression: each of these takes a tenth of a microsecond, a call of one token 8 on the GPU)
+    qs, os, d, f16 = q.shape, out.shape, runs.device, _torch.float16
+    hq, hkv, hd = runs.shape
+    if not (q.dtype is f16 and k.dtype is f16 and v.dtype is f16 and out.dtype is _torch.bfloat16
+            and pages.dtype is _torch.int32 and len(qs) == 3 and len(os) == 3 and v.shape == ks
+            and qs[0] >= runs.n_rows and qs[1] == hq and qs[2] == hd and ks[2] == hkv and ks[3] == hd
+            and os[0] >= runs.n_rows and os[1] == hq and os[2] == hd and q.get_device() == d and k.get_device() == d
+            and v.get_device() == d and out.get_device() == d and pages.get_device() == d and q.is_contiguous()
+            and k.is_contiguous() and v.is_contiguous() and out.is_contiguous() and pages.is_contiguous()):
+        _on_device(k, "k", f16, (*ks[:2], hkv, hd), d)
+        _on_device(v, "v", f16, ks, d)
+        _on_device(pages, "pages", _torch.int32, pages.shape, d)
+        runs._refuse(q, k.view(-1, hkv, hd), v.view(-1, hkv, hd), out)
     m, words = None, 0
     if mask is not None:
         _mask_sizes(mask, runs)
         words = mask.shape[1]
         if words < 1:
             raise ValueError("mask: needs at least a word a row")
-        m = _on_device(mask, "mask", _torch.int64, mask.shape, runs.device)
-    _call_on(runs.device, stream, runs._lib.pfop_attention_paged, q.data_ptr(), k.data_ptr(), v.data_ptr(), n_pages,
-             page, *runs.shape, runs.runs, runs.n_runs, at, pages.numel(), m, words, out.data_ptr(), runs.work_at,
-             runs.work_bytes)
+        m = _on_device(mask, "mask", _torch.int64, mask.shape, d)
+    _call_on(d, stream, runs._lib.pfop_attention_paged, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+             _i32(ks[0], "pages of k"), _i32(ks[1], "page size"), hq, hkv, hd, runs.runs, runs.n_runs,
+             pages.data_ptr(), pages.numel(), m, words, out.data_ptr(), runs.work_at, runs.work_bytes)
 
 
 def _heads(t, what: str, dtype, index: int):
     """(address, row stride, heads, head_dim) of [rows, heads, head_dim] whose
     rows may be strided (parts of wider rows), their heads dense."""
-    if len(t.shape) != 3:
-        raise ValueError(f"{what}: needs [rows, heads, head_dim], got {tuple(t.shape)}")
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 3:
+        raise ValueError(f"{what}: needs [rows, heads, head_dim], got {tuple(shape)}")
     if t.dtype is not dtype:
         raise ValueError(f"{what}: element type must be {dtype}, got {t.dtype}")
     if t.get_device() != index:
         raise ValueError(f"{what}: must be on CUDA device {index}, is on {t.device}")
-    (n, h, d), (sn, sh, sd) = t.shape, t.stride()
-    if (d > 1 and sd != 1) or (h > 1 and sh != d):
+    n, h, d = shape
+    if (d > 1 and stride[2] != 1) or (h > 1 and stride[1] != d):
         raise ValueError(f"{what}: a row's heads must be dense")
-    return t.data_ptr(), sn if n > 1 else h * d, _i32(h, what), _i32(d, what)
+    return t.data_ptr(), stride[0] if n > 1 else h * d, _i32(h, what), _i32(d, what)
 
 
 def qk_norm_rope(q, pos, q_out, k=None, v=None, slots=None, k_cache=None, v_cache=None, q_gain=None, k_gain=None,
@@ -576,41 +584,44 @@ def qk_norm_rope(q, pos, q_out, k=None, v=None, slots=None, k_cache=None, v_cach
     (k_gain is then not looked at).
     Enqueued on `stream` (None: the current torch stream)."""
     torch = _t()
-    if q.dtype is torch.float32:
+    dt = q.dtype
+    if dt is torch.float32:
         kind = PF_L_F32
-    elif q.dtype is torch.bfloat16:
+    elif dt is torch.bfloat16:
         kind = PF_L_BF16
     else:
-        raise ValueError(f"q: element type must be float32 or bfloat16, got {q.dtype}")
+        raise ValueError(f"q: element type must be float32 or bfloat16, got {dt}")
     d = q.get_device()
     if d < 0:
         raise ValueError(f"q: must be on a CUDA device, is on {q.device}")
-    qa, q_ld, hq, hd = _heads(q, "q", q.dtype, d)
-    rows = _i32(len(q), "q")
-    one, gain = (rows,), (hd,)
-    ka = va = sa = kca = vca = None
+    qa, q_ld, hq, hd = _heads(q, "q", dt, d)
+    qs = q.shape
+    rows, i32, f16, f32 = qs[0], torch.int32, torch.float16, torch.float32
+    one, gain = qs[:1], qs[2:]
+    ka = va = sa = kca = vca = kga = None
     k_ld = v_ld = hkv = cells = 0
     if k is not None:
         if v is None or slots is None or k_cache is None or v_cache is None:
             raise ValueError("k needs v, slots, k_cache and v_cache")
-        ka, k_ld, hkv, kd = _heads(k, "k", q.dtype, d)
-        va, v_ld, vh, vd = _heads(v, "v", q.dtype, d)
-        if (kd, vh, vd) != (hd, hkv, hd) or len(k) != rows or len(v) != rows or hkv < 1:
-            raise ValueError(f"k and v: shapes {tuple(k.shape)}, {tuple(v.shape)} do not fit q's {tuple(q.shape)}")
-        shape = k_cache.shape
-        if len(shape) not in (3, 4) or shape[-2:] != k.shape[1:]:
-            raise ValueError(f"k_cache: shape {tuple(shape)} does not fit {(hkv, hd)}")
-        kca = _on_device(k_cache, "k_cache", torch.float16, shape, d)
-        vca = _on_device(v_cache, "v_cache", torch.float16, shape, d)
-        cells = k_cache.numel() // (hkv * hd)
-        sa = _on_device(slots, "slots", torch.int32, one, d)
+        ka, k_ld, hkv, _ = _heads(k, "k", dt, d)
+        va, v_ld, _, _ = _heads(v, "v", dt, d)
+        ks, cs = k.shape, k_cache.shape
+        if v.shape != ks or ks[0] != rows or ks[2] != hd or hkv < 1:
+            raise ValueError(f"k and v: shapes {tuple(ks)}, {tuple(v.shape)} do not fit q's {tuple(qs)}")
+        if len(cs) not in (3, 4) or cs[-2:] != ks[1:]:
+            raise ValueError(f"k_cache: shape {tuple(cs)} does not fit {(hkv, hd)}")
+        kca = _on_device(k_cache, "k_cache", f16, cs, d)
+        vca = _on_device(v_cache, "v_cache", f16, cs, d)
+        cells = cs[0] if len(cs) == 3 else cs[0] * cs[1]
+        sa = _on_device(slots, "slots", i32, one, d)
+        if k_gain is not None:
+            kga = _on_device(k_gain, "k_gain", f32, gain, d)
     elif v is not None or slots is not None or k_cache is not None or v_cache is not None:
         raise ValueError("v, slots, k_cache and v_cache go with k")
-    _call_on(d, stream, load().pfop_qk_norm_rope, kind, qa, q_ld, ka, k_ld, va, v_ld, rows, hq, hkv, hd,
-             _on_device(pos, "pos", torch.int32, one, d), sa,
-             None if q_gain is None else _on_device(q_gain, "q_gain", torch.float32, gain, d),
-             None if k is None or k_gain is None else _on_device(k_gain, "k_gain", torch.float32, gain, d), eps, rope_base,
-             _on_device(q_out, "q_out", torch.float16, q.shape, d), kca, vca, cells)
+    _call_on(d, stream, load().pfop_qk_norm_rope, kind, qa, q_ld, ka, k_ld, va, v_ld, _i32(rows, "rows"), hq, hkv, hd,
+             _on_device(pos, "pos", i32, one, d), sa,
+             None if q_gain is None else _on_device(q_gain, "q_gain", f32, gain, d), kga, eps, rope_base,
+             _on_device(q_out, "q_out", f16, qs, d), kca, vca, cells)
 
 
 class VerifyWork:
