@@ -14,11 +14,10 @@ namespace pf {
 // have for a CTA of its own, which saves the merge kernel (about 3 us).
 constexpr int few_min(int hd) { return hd == 64 ? 16 : 8; }
 constexpr int few_cost(int hd) { return hd == 64 ? 64 : 12; }
-// Most columns and rows of a run.  (hd 256 with 16 columns: 64 runs of 2 rows of
-// 8 heads over 1024 keys 28 us, 22.7 with the other kernel; 1 over 500 9.3, 11.9.)
-constexpr int few_cols(int hd) { return hd == 64 ? 40 : 8; }
-constexpr int few_nt(int cols) { return cols <= 8 ? 1 : cols <= 16 ? 2 : 5; }
-constexpr int FEW_ROWS = 16;
+// Most columns of a run.  (hd 256 with 16: 64 runs of 2 rows of 8 heads over 1024
+// keys 28 us, 22.7 with the other kernel; hd 64 with 40: 16 runs of 5 rows of 8
+// heads a KV head over 2000 keys 22.3, 22.5.)
+constexpr int few_cols(int hd) { return hd == 64 ? 16 : 8; }
 
 // attn_few_kernel.  With C columns (row, head) of a run and KV head:
 //     S^T = K Q^T       (m16n8k16: 16 keys by 8 columns, hd deep)
@@ -57,7 +56,7 @@ struct FewShape {
 
 template <int HD, int NT>
 struct FewCfg {
-  static constexpr int WARPS = HD == 64 && NT <= 2 ? 8 : 4, CTAS = 2;
+  static constexpr int WARPS = HD == 64 ? 8 : 4, CTAS = 2;
   static constexpr int COLS = 8 * NT;
   static constexpr int UNIT = HD * 32;                 // bytes of a tile's K or V
   static constexpr int SLOTS = 98304 / (WARPS * UNIT);  // units that a warp has place for
@@ -218,7 +217,7 @@ __global__ void __launch_bounds__(32 * FewCfg<HD, NT>::WARPS, FewCfg<HD, NT>::CT
         const int row = (8 * nt + 2 * t + e) >> sh.log_g;
         seen[nt][e] = 0u;
         if (row < n_rows) {
-          const uint32_t all = (1u << n_rows) - 1u;  // (at most FEW_ROWS rows)
+          const uint32_t all = (1u << n_rows) - 1u;  // (at most 16 rows)
           seen[nt][e] = mask ? static_cast<uint32_t>(mask[static_cast<int64_t>(row0 + row) * words]) & all : (2u << row) - 1u;
         }
       }
@@ -507,8 +506,10 @@ struct FewPlan {
   int64_t state_bytes = 0;
 };
 
-// Which calls: no run of more columns or rows than the kernel takes, and so few
-// tiles that they can be counted.
+// Which calls: no run of more columns than the kernel takes, and so few tiles
+// that they can be counted.  (Taken apart from longer runs in the same call,
+// single tokens were slower: 512 rows of 8 heads over 2 of 256 with 13 single
+// tokens and 10 drafted 65.7 us, 44.0 together.)
 static bool few_plan(FewPlan& p, const pfop_attn_run* runs, int n_runs, int Hq, int Hkv, int hd) {
   const int group = Hq / Hkv, most = few_cols(hd);
   p.sh.Hq = Hq, p.sh.Hkv = Hkv, p.sh.log_g = 0;
@@ -517,12 +518,11 @@ static bool few_plan(FewPlan& p, const pfop_attn_run* runs, int n_runs, int Hq, 
   int row = 0, n = 0;
   for (int r = 0; r < n_runs; ++r) {
     if (runs[r].n_rows > 0) {
-      if (runs[r].n_rows > FEW_ROWS || runs[r].n_rows * group > most) return false;
-      const int cols = runs[r].n_rows * group;
+      if (runs[r].n_rows > most / group) return false;
       const int64_t t = (static_cast<int64_t>(runs[r].pos0) + runs[r].n_rows + 15) / 16;
       p.ft.run[n] = FewRun{row, runs[r].n_rows, runs[r].pos0, runs[r].cell0};
       p.ft.at[n] = static_cast<int>(tiles);
-      p.cols = std::max(p.cols, cols);
+      p.cols = std::max(p.cols, runs[r].n_rows * group);
       ++n;
       tiles += t * Hkv;
       longest = std::max(longest, t);
@@ -533,7 +533,7 @@ static bool few_plan(FewPlan& p, const pfop_attn_run* runs, int n_runs, int Hq, 
   if (n == 0) return false;
   p.ft.n_runs = n;
   p.ft.at[n] = static_cast<int>(tiles);
-  const int nt = few_nt(p.cols);
+  const int nt = p.cols > 8 ? 2 : 1;
   const int64_t slots = int64_t(sm_count()) * 2, items = int64_t(n) * Hkv;
   const int64_t share = std::max<int64_t>(few_min(hd), (tiles + slots - 1) / slots);
   if (longest <= share + few_cost(hd) && items <= slots) {
@@ -630,11 +630,7 @@ extern "C" int pfop_attention_paged(const void* q_dev, const void* k_dev, const 
                     static_cast<const __half*>(v_dev), pages, mask_dev, mask_words, static_cast<__nv_bfloat16*>(out_dev),
                     reinterpret_cast<float*>(static_cast<uint8_t*>(work_dev) + WORK_HEADER), static_cast<cudaStream_t>(stream));
     };
-    const int nt = few_nt(few.cols);
-    const cudaError_t e = hd == 256 ? go(launch_few<256, 1>)
-                          : nt == 1 ? go(launch_few<64, 1>)
-                          : nt == 2 ? go(launch_few<64, 2>)
-                                    : go(launch_few<64, 5>);
+    const cudaError_t e = hd == 256 ? go(launch_few<256, 1>) : few.cols > 8 ? go(launch_few<64, 2>) : go(launch_few<64, 1>);
     if (e != cudaSuccess) return runs_fail(PF_E_CUDA, std::string("paged attention launch: ") + cudaGetErrorString(e));
     return PF_OK;
   }
