@@ -610,18 +610,26 @@ def qk_norm_rope(q, pos, q_out, k=None, v=None, slots=None, k_cache=None, v_cach
             raise ValueError(f"k and v: shapes {tuple(ks)}, {tuple(v.shape)} do not fit q's {tuple(qs)}")
         if len(cs) not in (3, 4) or cs[-2:] != ks[1:]:
             raise ValueError(f"k_cache: shape {tuple(cs)} does not fit {(hkv, hd)}")
-        kca = _on_device(k_cache, "k_cache", f16, cs, d)
-        vca = _on_device(v_cache, "v_cache", f16, cs, d)
+        if not (k_cache.dtype is f16 and v_cache.dtype is f16 and slots.dtype is i32 and v_cache.shape == cs
+                and slots.shape == one and k_cache.get_device() == d and v_cache.get_device() == d
+                and slots.get_device() == d and k_cache.is_contiguous() and v_cache.is_contiguous()
+                and slots.is_contiguous()):
+            _on_device(k_cache, "k_cache", f16, cs, d)
+            _on_device(v_cache, "v_cache", f16, cs, d)
+            _on_device(slots, "slots", i32, one, d)
+        kca, vca, sa = k_cache.data_ptr(), v_cache.data_ptr(), slots.data_ptr()
         cells = cs[0] if len(cs) == 3 else cs[0] * cs[1]
-        sa = _on_device(slots, "slots", i32, one, d)
         if k_gain is not None:
             kga = _on_device(k_gain, "k_gain", f32, gain, d)
     elif v is not None or slots is not None or k_cache is not None or v_cache is not None:
         raise ValueError("v, slots, k_cache and v_cache go with k")
+    if not (pos.dtype is i32 and q_out.dtype is f16 and pos.shape == one and q_out.shape == qs
+            and pos.get_device() == d and q_out.get_device() == d and pos.is_contiguous() and q_out.is_contiguous()):
+        _on_device(pos, "pos", i32, one, d)
+        _on_device(q_out, "q_out", f16, qs, d)
     _call_on(d, stream, load().pfop_qk_norm_rope, kind, qa, q_ld, ka, k_ld, va, v_ld, _i32(rows, "rows"), hq, hkv, hd,
-             _on_device(pos, "pos", i32, one, d), sa,
-             None if q_gain is None else _on_device(q_gain, "q_gain", f32, gain, d), kga, eps, rope_base,
-             _on_device(q_out, "q_out", f16, qs, d), kca, vca, cells)
+             pos.data_ptr(), sa, None if q_gain is None else _on_device(q_gain, "q_gain", f32, gain, d), kga, eps,
+             rope_base, q_out.data_ptr(), kca, vca, cells)
 
 
 class VerifyWork:
@@ -659,15 +667,17 @@ def verify_draft(target, tokens, first, u, noise, n_accept, token, p_accept, wor
 
     def logits(t, what, rows, vocab):
         shape, stride = t.shape, t.stride()
-        if shape != (rows, vocab) or t.dtype is not target.dtype or (vocab > 1 and stride[1] != 1):
+        if (len(shape) != 2 or shape[0] != rows or shape[1] != vocab or t.dtype is not target.dtype
+                or (vocab > 1 and stride[1] != 1)):
             raise ValueError(f"{what}: needs [{rows}, {vocab}] of {target.dtype} with dense rows")
-        if t.get_device() != work.device:
-            raise ValueError(f"{what}: must be on CUDA device {work.device}, is on {t.device}")
+        if t.get_device() != d:
+            raise ValueError(f"{what}: must be on CUDA device {d}, is on {t.device}")
         return t.data_ptr(), stride[0] if rows > 1 else vocab
 
-    if len(target.shape) != 2:
-        raise ValueError(f"target: needs [rows, vocab], got {tuple(target.shape)}")
-    rows, vocab = _i32(target.shape[0], "rows"), _i32(target.shape[1], "vocab")
+    shape = target.shape
+    if len(shape) != 2:
+        raise ValueError(f"target: needs [rows, vocab], got {tuple(shape)}")
+    rows, vocab = _i32(shape[0], "rows"), _i32(shape[1], "vocab")
     n = first.numel() - 1
     if n < 0 or n > rows:
         raise ValueError(f"first: {n + 1} entries do not fit {rows} rows")
@@ -676,11 +686,21 @@ def verify_draft(target, tokens, first, u, noise, n_accept, token, p_accept, wor
     da, d_ld = (None, 0) if draft is None else logits(draft, "draft", rows - n, vocab)
     if rows == n:
         da = None  # no drafts
-    _call_on(d, stream, load().pfop_verify_draft, kind, ta, t_ld, da, d_ld, rows, n, vocab,
-             _on_device(tokens, "tokens", i32, (rows,), d), _on_device(first, "first", i32, (n + 1,), d),
-             _on_device(u, "u", f32, (rows,), d), _on_device(noise, "noise", f32, (n, vocab), d),
-             _on_device(n_accept, "n_accept", i32, (n,), d), _on_device(token, "token", i32, (n,), d),
-             None if p_accept is None else _on_device(p_accept, "p_accept", f32, (rows,), d), work.work_at,
+    ns, one = noise.shape, shape[:1]
+    if not (tokens.dtype is i32 and first.dtype is i32 and u.dtype is f32 and noise.dtype is f32
+            and n_accept.dtype is i32 and token.dtype is i32 and len(ns) == 2 and ns[0] == n and ns[1] == vocab
+            and tokens.shape == one and u.shape == one and n_accept.shape == ns[:1] and token.shape == ns[:1]
+            and first.dim() == 1 and tokens.get_device() == d and first.get_device() == d and u.get_device() == d
+            and noise.get_device() == d and n_accept.get_device() == d and token.get_device() == d
+            and tokens.is_contiguous() and first.is_contiguous() and u.is_contiguous() and noise.is_contiguous()
+            and n_accept.is_contiguous() and token.is_contiguous()):
+        for t, what, dtype, size in ((tokens, "tokens", i32, (rows,)), (first, "first", i32, (n + 1,)),
+                                     (u, "u", f32, (rows,)), (noise, "noise", f32, (n, vocab)),
+                                     (n_accept, "n_accept", i32, (n,)), (token, "token", i32, (n,))):
+            _on_device(t, what, dtype, size, d)
+    _call_on(d, stream, load().pfop_verify_draft, kind, ta, t_ld, da, d_ld, rows, n, vocab, tokens.data_ptr(),
+             first.data_ptr(), u.data_ptr(), noise.data_ptr(), n_accept.data_ptr(), token.data_ptr(),
+             None if p_accept is None else _on_device(p_accept, "p_accept", f32, one, d), work.work_at,
              work.work_bytes)
 
 

@@ -261,14 +261,11 @@ __global__ void __launch_bounds__(32 * VD_SUM_WARPS, VD_SUM_CTAS) draft_sums_ker
   }
 }
 
-// a candidate: the largest w / E and the lowest token at it (id -1: none)
-struct VdBest {
-  float v;
-  int id;
-  __device__ __forceinline__ void take(float v2, int id2) {
-    if (v2 > v || (v2 == v && id2 >= 0 && (id < 0 || id2 < id))) v = v2, id = id2;
-  }
-};
+// a score above 0 and its token as one key: larger scores first, then lower
+// tokens (0: none)
+__device__ __forceinline__ unsigned long long vd_key(float score, int id) {
+  return static_cast<unsigned long long>(__float_as_uint(score)) << 32 | (0xffffffffu - static_cast<uint32_t>(id));
+}
 
 // what the next token is drawn from
 enum VdKind : int { VD_NONE = -1, VD_P = 0, VD_P_MINUS_Q = 1, VD_P_BUT_DRAFTED = 2 };
@@ -376,7 +373,7 @@ struct VdScan {
     }
   }
   // the batch at v, with expf and a division
-  __device__ __forceinline__ void exact(int v, bool minus_q, bool but_d, VdBest& best) const {
+  __device__ __forceinline__ void exact(int v, bool minus_q, bool but_d, unsigned long long& best) const {
     float px[VD_VECS][4], qx[VD_VECS][4], e[VD_VECS][4];
 #pragma unroll
     for (int g = 0; g < VD_VECS; ++g) {
@@ -392,7 +389,8 @@ struct VdScan {
         // (a fused w would leave p's rounding where p and q are alike)
         float w = __fmul_rn(expf(px[g][i] + nm_p), z_p);
         if (minus_q) w = __fsub_rn(w, __fmul_rn(expf(qx[g][i] + nm_q), z_q));
-        if (w > 0.f && !(but_d && id == d)) best.take(w / e[g][i], id);
+        const float score = w / e[g][i];
+        if (w > 0.f && score >= 0.f && !(but_d && id == d)) best = max(best, vd_key(score, id));
       }
   }
 };
@@ -403,8 +401,8 @@ __global__ void __launch_bounds__(VD_THREADS, 2) draft_pick_kernel(const VerifyA
   __shared__ int sh_at, sh_kind;
   __shared__ float2 sh_p, sh_q;
   __shared__ float2 sh_sums[2][VD_GROUP];  // maximum and 1 / sum (0: no distribution) of target and draft rows
-  __shared__ VdBest sh_warp[WARPS];
-  __shared__ float2 sh_all[2][VD_CLUSTER_MAX];  // each CTA's candidate, of both rounds
+  __shared__ float sh_lo[WARPS];
+  __shared__ unsigned long long sh_best[2], sh_all[2][VD_CLUSTER_MAX];  // the CTA's, and each CTA's; of both rounds
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int cluster = 1 << cluster_log;
   const int s = static_cast<int>(blockIdx.x >> cluster_log), rank = static_cast<int>(blockIdx.x) & (cluster - 1);
@@ -424,7 +422,7 @@ __global__ void __launch_bounds__(VD_THREADS, 2) draft_pick_kernel(const VerifyA
   const int r0 = a.first[s], r1 = a.first[s + 1];
   const bool fits = r0 >= 0 && r1 > r0 && r1 <= a.rows && r1 - s - 1 <= a.rows - a.n_seq && r0 >= s;
   bool waited = false;
-  if (tid == 0) sh_at = -1, sh_kind = VD_NONE, sh_p = sh_q = make_float2(0.f, 0.f);
+  if (tid == 0) sh_at = -1, sh_kind = VD_NONE, sh_p = sh_q = make_float2(0.f, 0.f), sh_best[0] = sh_best[1] = 0ull;
   // VD_GROUP rows at a time; rank 0 also writes the shares of those behind the stop
   for (int base = r0; fits && base < r1; base += VD_GROUP) {
     const int r = base + lane, dr = r - s;
@@ -506,13 +504,13 @@ __global__ void __launch_bounds__(VD_THREADS, 2) draft_pick_kernel(const VerifyA
   scan.nm_p = -zp.x, scan.z_p = zp.y;
   scan.nm_q = -zq.x, scan.z_q = zq.y;
   scan.share = zq.y / zp.y;
-  VdBest best{0.f, -1};
+  unsigned long long best = 0ull;
   // A second round, of p itself, where nothing is left to draw from (p and q
   // alike, or all of p on the drafted token).
   for (int round = 0; round < 2; ++round) {
     if (kind != VD_NONE) {
       // Batches to be looked at exactly: the thread's best one where it may
-      // hold the warp's answer, all of the warp's where others may too.
+      // hold the CTA's answer, all of the warp's where others may too.
       int v = scan.v0;
       bool all = true, mine = true;
       if (round == 0) {
@@ -524,6 +522,11 @@ __global__ void __launch_bounds__(VD_THREADS, 2) draft_pick_kernel(const VerifyA
           scan.template bounds<false>(e, hi, hi2, lo, batch);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) lo = fmaxf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+        if (lane == 0) sh_lo[warp] = lo;
+        __syncthreads();
+        lo = sh_lo[lane % WARPS];
+#pragma unroll
+        for (int o = WARPS / 2; o > 0; o >>= 1) lo = fmaxf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
         all = __any_sync(0xffffffffu, hi2 > 0.f && hi2 >= lo);
         mine = all || (hi > 0.f && hi >= lo);
         if (!all) v = batch;
@@ -532,30 +535,23 @@ __global__ void __launch_bounds__(VD_THREADS, 2) draft_pick_kernel(const VerifyA
         scan.exact(v, kind == VD_P_MINUS_Q, kind == VD_P_BUT_DRAFTED, best);
         if (!all) break;
       }
+      if (best) atomicMax(&sh_best[round], best);
     }
-    // over the warp, the CTA, the cluster
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) best.take(__shfl_xor_sync(0xffffffffu, best.v, o), __shfl_xor_sync(0xffffffffu, best.id, o));
-    if (lane == 0) sh_warp[warp] = best;
     __syncthreads();
-    best = sh_warp[lane % WARPS];
-#pragma unroll
-    for (int o = WARPS / 2; o > 0; o >>= 1)
-      best.take(__shfl_xor_sync(0xffffffffu, best.v, o), __shfl_xor_sync(0xffffffffu, best.id, o));
+    best = sh_best[round];
     if (cluster > 1) {
       if (round == 0) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
       if (tid < cluster) {
         const uint32_t to = map_to_rank(smem_u32(&sh_all[round][rank]), tid);
-        asm volatile("st.shared::cluster.v2.b32 [%0], {%1, %2};" ::"r"(to), "r"(__float_as_int(best.v)), "r"(best.id) : "memory");
+        asm volatile("st.shared::cluster.b64 [%0], %1;" ::"r"(to), "l"(best) : "memory");
       }
       cluster_sync_all();
-      for (int c = 0; c < cluster; ++c) best.take(sh_all[round][c].x, __float_as_int(sh_all[round][c].y));
+      for (int c = 0; c < cluster; ++c) best = max(best, sh_all[round][c]);
     }
-    if (best.id >= 0 || kind == VD_NONE || kind == VD_P) break;
+    if (best || kind == VD_NONE || kind == VD_P) break;
     kind = VD_P;
-    __syncthreads();
   }
-  if (rank == 0 && tid == 0) a.token[s] = best.id;
+  if (rank == 0 && tid == 0) a.token[s] = best ? static_cast<int>(0xffffffffu - static_cast<uint32_t>(best)) : -1;
 }
 
 // logits of a chunk
