@@ -81,6 +81,7 @@ struct VdVec<float> {
     v[0] = __uint_as_float(r.x), v[1] = __uint_as_float(r.y), v[2] = __uint_as_float(r.z), v[3] = __uint_as_float(r.w);
   }
   static __device__ __forceinline__ float one(const float* p) { return *p; }
+  static __device__ __forceinline__ float one_l2(const float* p) { return __ldcg(p); }
   static __device__ __forceinline__ void four(const float* p, float* v) {
     const float4 f = *reinterpret_cast<const float4*>(p);
     v[0] = f.x, v[1] = f.y, v[2] = f.z, v[3] = f.w;
@@ -115,6 +116,9 @@ struct VdVec<__nv_bfloat16> {
     two(r.x, v), two(r.y, v + 2), two(r.z, v + 4), two(r.w, v + 6);
   }
   static __device__ __forceinline__ float one(const __nv_bfloat16* p) { return __bfloat162float(*p); }
+  static __device__ __forceinline__ float one_l2(const __nv_bfloat16* p) {
+    return __uint_as_float(static_cast<uint32_t>(__ldcg(reinterpret_cast<const unsigned short*>(p))) << 16);
+  }
   static __device__ __forceinline__ void four(const __nv_bfloat16* p, float* v) {
     const uint2 f = *reinterpret_cast<const uint2*>(p);
     two(f.x, v), two(f.y, v + 2);
@@ -298,22 +302,27 @@ struct VdScan {
       for (int i = 0; i < 4; ++i) e[i] = 4 * v + i < vocab ? VdVec<T>::one(row + 4 * v + i) : -INFINITY;
     }
   }
+  // (L2: read from L2, not by what the SM may still hold of it)
+  template <bool L2 = false>
   __device__ __forceinline__ void noises(int v, float* e) const {
     if (ALIGNED) {
       if (4 * v < vocab) {
-        VdVec<float>::four(noise + 4 * v, e);
+        const float4* p = reinterpret_cast<const float4*>(noise + 4 * v);
+        const float4 f = L2 ? __ldcg(p) : *p;
+        e[0] = f.x, e[1] = f.y, e[2] = f.z, e[3] = f.w;
       } else {
         e[0] = e[1] = e[2] = e[3] = 1.f;
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) e[i] = 4 * v + i < vocab ? noise[4 * v + i] : 1.f;
+      for (int i = 0; i < 4; ++i) e[i] = 4 * v + i < vocab ? (L2 ? __ldcg(noise + 4 * v + i) : noise[4 * v + i]) : 1.f;
     }
   }
   // the same for a whole batch
+  template <bool L2 = false>
   __device__ __forceinline__ void noises_of(int v, float (&e)[VD_VECS][4]) const {
 #pragma unroll
-    for (int g = 0; g < VD_VECS; ++g) noises(v + g * step, e[g]);
+    for (int g = 0; g < VD_VECS; ++g) noises<L2>(v + g * step, e[g]);
   }
 
   // Bounds of the largest w / E: hi of the thread's best batch, hi2 of the
@@ -416,10 +425,12 @@ __global__ void __launch_bounds__(VD_THREADS, 2) draft_pick_kernel(const VerifyA
   scan.vocab = a.vocab;
   scan.v0 = rank * VD_THREADS + tid;
   scan.step = cluster * VD_THREADS;
-  // the first noise is fetched while the sums are still being formed
+  // What the sums do not make is fetched while they are still being formed:
+  // draft_sums_kernel lets this one start only when the kernels before both are
+  // over.  From L2, since this kernel itself has not waited for them.
   float e[VD_VECS][4];
-  scan.noises_of(scan.v0, e);
-  const int r0 = a.first[s], r1 = a.first[s + 1];
+  scan.template noises_of<true>(scan.v0, e);
+  const int r0 = __ldcg(a.first + s), r1 = __ldcg(a.first + s + 1);
   const bool fits = r0 >= 0 && r1 > r0 && r1 <= a.rows && r1 - s - 1 <= a.rows - a.n_seq && r0 >= s;
   bool waited = false;
   if (tid == 0) sh_at = -1, sh_kind = VD_NONE, sh_p = sh_q = make_float2(0.f, 0.f), sh_best[0] = sh_best[1] = 0ull;
@@ -427,11 +438,11 @@ __global__ void __launch_bounds__(VD_THREADS, 2) draft_pick_kernel(const VerifyA
   for (int base = r0; fits && base < r1; base += VD_GROUP) {
     const int r = base + lane, dr = r - s;
     const bool judges = warp == 0 && r < r1 - 1;
-    const int d = judges ? a.tokens[r + 1] : -1;
-    const float u = judges ? a.u[r] : 0.f;
+    const int d = judges ? __ldcg(a.tokens + r + 1) : -1;
+    const float u = judges ? __ldcg(a.u + r) : 0.f;
     const bool known = d >= 0 && d < a.vocab;
-    const float xd = known ? VdVec<T>::one(target + r * a.t_ld + d) : -INFINITY;
-    const float yd = known && draft ? VdVec<T>::one(draft + dr * a.d_ld + d) : -INFINITY;
+    const float xd = known ? VdVec<T>::one_l2(target + r * a.t_ld + d) : -INFINITY;
+    const float yd = known && draft ? VdVec<T>::one_l2(draft + dr * a.d_ld + d) : -INFINITY;
     if (!waited) pdl_wait();
     waited = true;
     // the parts of a row in 16 lanes
