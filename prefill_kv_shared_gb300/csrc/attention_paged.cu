@@ -10,14 +10,23 @@
 
 namespace pf {
 
+// CTAs of 8 warps, of an SM.  (hd 256 with two of 4 warps: 64 tokens over 1024
+// keys, 8 heads over 2, 28.2 us instead of 23.5, one over 32768 14.5 instead of
+// 13.6; one over 500 6.2 instead of 8.6, since the next call's CTAs then fit
+// beside the last one's.)
+constexpr int few_ctas(int hd) { return hd == 64 ? 2 : 1; }
 // Least tiles of a CTA, and how many more tiles than an even share an item may
-// have for a CTA of its own, which saves the merge kernel (about 3 us).
-constexpr int few_min(int hd) { return hd == 64 ? 16 : 8; }
-constexpr int few_cost(int hd) { return hd == 64 ? 64 : 12; }
+// have for a CTA of its own (beside an eighth of the share), which saves the
+// merge kernel, about 3 us.  (hd 64: 64 tokens over 500 to 1319 keys, 32 heads
+// over 4, 13.4 us with 64, 18.1 with 32; hd 256: 16 over 1024 keys, 8 heads over
+// 2, 12.0 with 24, 14.4 with 48.)
+constexpr int FEW_MIN = 16;
+constexpr int few_cost(int hd) { return hd == 64 ? 64 : 24; }
 // Most columns of a run.  (hd 256 with 16: 64 runs of 2 rows of 8 heads over 1024
 // keys 28 us, 22.7 with the other kernel; hd 64 with 40: 16 runs of 5 rows of 8
 // heads a KV head over 2000 keys 22.3, 22.5.)
 constexpr int few_cols(int hd) { return hd == 64 ? 16 : 8; }
+static_assert(few_cols(64) <= 16 && few_cols(256) <= 8, "the columns of the kernels that are launched");
 
 // attn_few_kernel.  With C columns (row, head) of a run and KV head:
 //     S^T = K Q^T       (m16n8k16: 16 keys by 8 columns, hd deep)
@@ -56,10 +65,10 @@ struct FewShape {
 
 template <int HD, int NT>
 struct FewCfg {
-  static constexpr int WARPS = HD == 64 ? 8 : 4, CTAS = 2;
+  static constexpr int WARPS = 8, CTAS = few_ctas(HD);
   static constexpr int COLS = 8 * NT;
   static constexpr int UNIT = HD * 32;                 // bytes of a tile's K or V
-  static constexpr int SLOTS = 98304 / (WARPS * UNIT);  // units that a warp has place for
+  static constexpr int SLOTS = 196608 / CTAS / (WARPS * UNIT);  // units that a warp has place for
   static constexpr int STATE_SLOTS = COLS * HD * 4 / UNIT;  // the last ones hold its O at a segment's end
   static constexpr int OFF_Q = WARPS * SLOTS * UNIT;
   static constexpr int OFF_ML = OFF_Q + HD / 32 * NT * 512;
@@ -534,9 +543,9 @@ static bool few_plan(FewPlan& p, const pfop_attn_run* runs, int n_runs, int Hq, 
   p.ft.n_runs = n;
   p.ft.at[n] = static_cast<int>(tiles);
   const int nt = p.cols > 8 ? 2 : 1;
-  const int64_t slots = int64_t(sm_count()) * 2, items = int64_t(n) * Hkv;
-  const int64_t share = std::max<int64_t>(few_min(hd), (tiles + slots - 1) / slots);
-  if (longest <= share + few_cost(hd) && items <= slots) {
+  const int64_t slots = int64_t(sm_count()) * few_ctas(hd), items = int64_t(n) * Hkv;
+  const int64_t share = std::max<int64_t>(FEW_MIN, (tiles + slots - 1) / slots);
+  if (longest <= share + share / 8 + few_cost(hd) && items <= slots) {
     p.sh.share = 0;
     p.ctas = static_cast<int>(items);
   } else {
