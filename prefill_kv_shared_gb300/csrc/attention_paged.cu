@@ -22,11 +22,14 @@ constexpr int few_ctas(int hd) { return hd == 64 ? 2 : 1; }
 // 2, 12.0 with 24, 14.4 with 48.)
 constexpr int FEW_MIN = 16;
 constexpr int few_cost(int hd) { return hd == 64 ? 64 : 24; }
-// Most columns of a run.  (hd 256 with 16: 64 runs of 2 rows of 8 heads over 1024
-// keys 28 us, 22.7 with the other kernel; hd 64 with 40: 16 runs of 5 rows of 8
-// heads a KV head over 2000 keys 22.3, 22.5.)
-constexpr int few_cols(int hd) { return hd == 64 ? 16 : 8; }
-static_assert(few_cols(64) <= 16 && few_cols(256) <= 8, "the columns of the kernels that are launched");
+// Most columns of a run.  (hd 64 with 40: 16 runs of 5 rows of 8 heads a KV head
+// over 2000 keys 22.3 us, 22.5 with the other kernel.)  More than 8 at hd 256
+// only where a CTA's share is long: what a segment costs grows with the columns
+// (64 runs of 3 rows of 8 heads over 2, 1024 keys: 27.7 us, 39.8 with the other
+// kernel; of 2 rows of 8 heads over 1 24.6 and 22.8; 8 of those over 3000 20.4
+// and 15.7).
+constexpr int FEW_COLS = 16;
+constexpr int few_share(int hd, int cols) { return hd == 256 && cols > 8 ? 32 : 0; }
 
 // attn_few_kernel.  With C columns (row, head) of a run and KV head:
 //     S^T = K Q^T       (m16n8k16: 16 keys by 8 columns, hd deep)
@@ -520,7 +523,7 @@ struct FewPlan {
 // single tokens were slower: 512 rows of 8 heads over 2 of 256 with 13 single
 // tokens and 10 drafted 65.7 us, 44.0 together.)
 static bool few_plan(FewPlan& p, const pfop_attn_run* runs, int n_runs, int Hq, int Hkv, int hd) {
-  const int group = Hq / Hkv, most = few_cols(hd);
+  const int group = Hq / Hkv, most = FEW_COLS;
   p.sh.Hq = Hq, p.sh.Hkv = Hkv, p.sh.log_g = 0;
   while ((1 << p.sh.log_g) < group) ++p.sh.log_g;
   int64_t tiles = 0, longest = 0;
@@ -544,6 +547,7 @@ static bool few_plan(FewPlan& p, const pfop_attn_run* runs, int n_runs, int Hq, 
   p.ft.at[n] = static_cast<int>(tiles);
   const int nt = p.cols > 8 ? 2 : 1;
   const int64_t slots = int64_t(sm_count()) * few_ctas(hd), items = int64_t(n) * Hkv;
+  if (tiles < few_share(hd, p.cols) * slots) return false;
   const int64_t share = std::max<int64_t>(FEW_MIN, (tiles + slots - 1) / slots);
   if (longest <= share + share / 8 + few_cost(hd) && items <= slots) {
     p.sh.share = 0;
@@ -639,7 +643,7 @@ extern "C" int pfop_attention_paged(const void* q_dev, const void* k_dev, const 
                     static_cast<const __half*>(v_dev), pages, mask_dev, mask_words, static_cast<__nv_bfloat16*>(out_dev),
                     reinterpret_cast<float*>(static_cast<uint8_t*>(work_dev) + WORK_HEADER), static_cast<cudaStream_t>(stream));
     };
-    const cudaError_t e = hd == 256 ? go(launch_few<256, 1>) : few.cols > 8 ? go(launch_few<64, 2>) : go(launch_few<64, 1>);
+    const cudaError_t e = hd == 256 ? (few.cols > 8 ? go(launch_few<256, 2>) : go(launch_few<256, 1>)) : few.cols > 8 ? go(launch_few<64, 2>) : go(launch_few<64, 1>);
     if (e != cudaSuccess) return runs_fail(PF_E_CUDA, std::string("paged attention launch: ") + cudaGetErrorString(e));
     return PF_OK;
   }

@@ -139,6 +139,24 @@ def test_trees(heads, page, rows, past, words):
     c.check(mask)
 
 
+@pytest.mark.parametrize("heads,rows", [((8, 1, 256), 2), ((8, 2, 256), 4), ((8, 2, 256), 3), ((16, 1, 256), 1),
+                                        ((16, 16, 256), 16), ((32, 4, 64), 2), ((4, 4, 64), 16), ((16, 1, 64), 1)])
+@pytest.mark.parametrize("page", [8, 64])
+def test_up_to_16_columns_over_much_work(heads, rows, page):
+    """Runs of up to 16 (row, head) pairs a KV head, as many keys as a large
+    batch has: causal, and each row with its own mask."""
+    n = 70 if heads[1] < 16 else 6
+    c = Paged(heads, page, [rows] * n, [1100 + 37 * i for i in range(n)], 83 + rows)
+    c.go()
+    c.plan.check()
+    c.check()
+    mask = _random_tree(c.runs, 1, 3)
+    c.out[:c.total] = 7
+    c.go(np.concatenate([mask, np.zeros((3, 1), np.uint64)]))
+    c.plan.check()
+    c.check(mask)
+
+
 @pytest.mark.parametrize("heads", [(8, 1, 256), (32, 4, 64), (4, 4, 64)])
 def test_masks_that_leave_nothing(heads):
     """Rows without any key give zeros, single tokens among them."""
