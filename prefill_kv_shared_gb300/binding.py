@@ -558,19 +558,15 @@ def attention_paged(q, k, v, runs: AttnRuns, pages, out, mask=None, stream=None)
 
 
 def _heads(t, what: str, dtype, index: int):
-    """(address, row stride, heads, head_dim) of [rows, heads, head_dim] whose
-    rows may be strided (parts of wider rows), their heads dense."""
-    shape, stride = t.shape, t.stride()
-    if len(shape) != 3:
-        raise ValueError(f"{what}: needs [rows, heads, head_dim], got {tuple(shape)}")
+    """Refuse what is not [rows, heads, head_dim] with a row's heads dense (the
+    rows may be parts of wider ones)."""
     if t.dtype is not dtype:
         raise ValueError(f"{what}: element type must be {dtype}, got {t.dtype}")
     if t.get_device() != index:
         raise ValueError(f"{what}: must be on CUDA device {index}, is on {t.device}")
-    n, h, d = shape
-    if (d > 1 and stride[2] != 1) or (h > 1 and stride[1] != d):
+    (_, h, d), (_, sh, se) = t.shape, t.stride()
+    if se != 1 or (h > 1 and sh != d):
         raise ValueError(f"{what}: a row's heads must be dense")
-    return t.data_ptr(), stride[0] if n > 1 else h * d, _i32(h, what), _i32(d, what)
 
 
 def qk_norm_rope(q, pos, q_out, k=None, v=None, slots=None, k_cache=None, v_cache=None, q_gain=None, k_gain=None,
@@ -583,7 +579,7 @@ def qk_norm_rope(q, pos, q_out, k=None, v=None, slots=None, k_cache=None, v_cach
     float16; gains [head_dim] float32 (None: no norm).  k None: queries only
     (k_gain is then not looked at).
     Enqueued on `stream` (None: the current torch stream)."""
-    torch = _t()
+    torch = _torch or _t()
     dt = q.dtype
     if dt is torch.float32:
         kind = PF_L_F32
@@ -594,42 +590,55 @@ def qk_norm_rope(q, pos, q_out, k=None, v=None, slots=None, k_cache=None, v_cach
     d = q.get_device()
     if d < 0:
         raise ValueError(f"q: must be on a CUDA device, is on {q.device}")
-    qa, q_ld, hq, hd = _heads(q, "q", dt, d)
-    qs = q.shape
-    rows, i32, f16, f32 = qs[0], torch.int32, torch.float16, torch.float32
-    one, gain = qs[:1], qs[2:]
-    ka = va = sa = kca = vca = kga = None
+    # One expression a group of tensors: a step of one row takes 2 us on the
+    # GPU, a tensor checked in a call of its own 0.6 us here.
+    i32, f16, f32, qs = torch.int32, torch.float16, torch.float32, q.shape
+    if len(qs) != 3:
+        raise ValueError(f"q: needs [rows, heads, head_dim], got {tuple(qs)}")
+    rows, hq, hd = qs
+    q_ld, sh, se = q.stride()
+    if not (se == 1 and (sh == hd or hq == 1) and pos.dtype is i32 and q_out.dtype is f16 and pos.numel() == rows
+            and q_out.shape == qs and pos.get_device() == d and q_out.get_device() == d and pos.is_contiguous()
+            and q_out.is_contiguous() and rows < 1 << 31 and hq < 1 << 31):
+        _heads(q, "q", dt, d)
+        _on_device(pos, "pos", i32, qs[:1], d)
+        _on_device(q_out, "q_out", f16, qs, d)
+        _i32(rows, "rows")
+    qga = kga = ka = va = sa = kca = vca = None
+    if q_gain is not None:
+        qga = _on_device(q_gain, "q_gain", f32, qs[2:], d)
     k_ld = v_ld = hkv = cells = 0
     if k is not None:
         if v is None or slots is None or k_cache is None or v_cache is None:
             raise ValueError("k needs v, slots, k_cache and v_cache")
-        ka, k_ld, hkv, _ = _heads(k, "k", dt, d)
-        va, v_ld, _, _ = _heads(v, "v", dt, d)
         ks, cs = k.shape, k_cache.shape
-        if v.shape != ks or ks[0] != rows or ks[2] != hd or hkv < 1:
+        if len(ks) != 3 or ks[0] != rows or ks[1] < 1 or ks[2] != hd or v.shape != ks:
             raise ValueError(f"k and v: shapes {tuple(ks)}, {tuple(v.shape)} do not fit q's {tuple(qs)}")
-        if len(cs) not in (3, 4) or cs[-2:] != ks[1:]:
+        hkv = ks[1]
+        if len(cs) not in (3, 4) or cs[-2] != hkv or cs[-1] != hd:
             raise ValueError(f"k_cache: shape {tuple(cs)} does not fit {(hkv, hd)}")
-        if not (k_cache.dtype is f16 and v_cache.dtype is f16 and slots.dtype is i32 and v_cache.shape == cs
-                and slots.shape == one and k_cache.get_device() == d and v_cache.get_device() == d
-                and slots.get_device() == d and k_cache.is_contiguous() and v_cache.is_contiguous()
-                and slots.is_contiguous()):
+        k_ld, sh, se = k.stride()
+        v_ld, vsh, vse = v.stride()
+        if not (se == 1 and vse == 1 and (hkv == 1 or (sh == hd and vsh == hd)) and k.dtype is dt and v.dtype is dt
+                and k_cache.dtype is f16 and v_cache.dtype is f16 and slots.dtype is i32 and v_cache.shape == cs
+                and slots.numel() == rows and k.get_device() == d and v.get_device() == d
+                and k_cache.get_device() == d and v_cache.get_device() == d and slots.get_device() == d
+                and k_cache.is_contiguous() and v_cache.is_contiguous() and slots.is_contiguous()):
+            _heads(k, "k", dt, d)
+            _heads(v, "v", dt, d)
             _on_device(k_cache, "k_cache", f16, cs, d)
             _on_device(v_cache, "v_cache", f16, cs, d)
-            _on_device(slots, "slots", i32, one, d)
-        kca, vca, sa = k_cache.data_ptr(), v_cache.data_ptr(), slots.data_ptr()
+            _on_device(slots, "slots", i32, qs[:1], d)
+        ka, va, kca, vca, sa = k.data_ptr(), v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), slots.data_ptr()
         cells = cs[0] if len(cs) == 3 else cs[0] * cs[1]
         if k_gain is not None:
-            kga = _on_device(k_gain, "k_gain", f32, gain, d)
+            kga = _on_device(k_gain, "k_gain", f32, qs[2:], d)
     elif v is not None or slots is not None or k_cache is not None or v_cache is not None:
         raise ValueError("v, slots, k_cache and v_cache go with k")
-    if not (pos.dtype is i32 and q_out.dtype is f16 and pos.shape == one and q_out.shape == qs
-            and pos.get_device() == d and q_out.get_device() == d and pos.is_contiguous() and q_out.is_contiguous()):
-        _on_device(pos, "pos", i32, one, d)
-        _on_device(q_out, "q_out", f16, qs, d)
-    _call_on(d, stream, load().pfop_qk_norm_rope, kind, qa, q_ld, ka, k_ld, va, v_ld, _i32(rows, "rows"), hq, hkv, hd,
-             pos.data_ptr(), sa, None if q_gain is None else _on_device(q_gain, "q_gain", f32, gain, d), kga, eps,
-             rope_base, q_out.data_ptr(), kca, vca, cells)
+    if rows < 2:  # (the stride of one row says nothing)
+        q_ld, k_ld, v_ld = hq * hd, hkv * hd, hkv * hd
+    _call_on(d, stream, (_lib or load()).pfop_qk_norm_rope, kind, q.data_ptr(), q_ld, ka, k_ld, va, v_ld, rows, hq, hkv,
+             hd, pos.data_ptr(), sa, qga, kga, eps, rope_base, q_out.data_ptr(), kca, vca, cells)
 
 
 class VerifyWork:
@@ -648,6 +657,15 @@ class VerifyWork:
         self.work_at, self.work_bytes = self.work.data_ptr(), need
 
 
+def _rows_of(t, what: str, dtype, shape, index: int) -> int:
+    """The row stride of logits of this type and shape, their rows dense."""
+    if t.shape != shape or t.dtype is not dtype or (shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{what}: needs {list(shape)} of {dtype} with dense rows")
+    if t.get_device() != index:
+        raise ValueError(f"{what}: must be on CUDA device {index}, is on {t.device}")
+    return t.stride(0) if shape[0] > 1 else shape[1]
+
+
 def verify_draft(target, tokens, first, u, noise, n_accept, token, p_accept, work: VerifyWork, draft=None,
                  stream=None):
     """Drafted tokens accepted or refused, and the token that follows
@@ -657,51 +675,47 @@ def verify_draft(target, tokens, first, u, noise, n_accept, token, p_accept, wor
     noise [sequences, vocab] float32; outputs n_accept, token [sequences] int32
     and p_accept [rows] float32 (None: not wanted).  Enqueued on `stream` (None:
     the current torch stream)."""
-    torch = _t()
-    if target.dtype is torch.float32:
+    torch = _torch or _t()
+    dt = target.dtype
+    if dt is torch.float32:
         kind = PF_L_F32
-    elif target.dtype is torch.bfloat16:
+    elif dt is torch.bfloat16:
         kind = PF_L_BF16
     else:
-        raise ValueError(f"target: element type must be float32 or bfloat16, got {target.dtype}")
-
-    def logits(t, what, rows, vocab):
-        shape, stride = t.shape, t.stride()
-        if (len(shape) != 2 or shape[0] != rows or shape[1] != vocab or t.dtype is not target.dtype
-                or (vocab > 1 and stride[1] != 1)):
-            raise ValueError(f"{what}: needs [{rows}, {vocab}] of {target.dtype} with dense rows")
-        if t.get_device() != d:
-            raise ValueError(f"{what}: must be on CUDA device {d}, is on {t.device}")
-        return t.data_ptr(), stride[0] if rows > 1 else vocab
-
-    shape = target.shape
-    if len(shape) != 2:
-        raise ValueError(f"target: needs [rows, vocab], got {tuple(shape)}")
-    rows, vocab = _i32(shape[0], "rows"), _i32(shape[1], "vocab")
-    n = first.numel() - 1
+        raise ValueError(f"target: element type must be float32 or bfloat16, got {dt}")
+    ts, n, d, f32, i32 = target.shape, first.numel() - 1, work.device, torch.float32, torch.int32
+    if len(ts) != 2:
+        raise ValueError(f"target: needs [rows, vocab], got {tuple(ts)}")
+    rows, vocab = ts
     if n < 0 or n > rows:
         raise ValueError(f"first: {n + 1} entries do not fit {rows} rows")
-    d, f32, i32 = work.device, torch.float32, torch.int32
-    ta, t_ld = logits(target, "target", rows, vocab)
-    da, d_ld = (None, 0) if draft is None else logits(draft, "draft", rows - n, vocab)
-    if rows == n:
-        da = None  # no drafts
-    ns, one = noise.shape, shape[:1]
-    if not (tokens.dtype is i32 and first.dtype is i32 and u.dtype is f32 and noise.dtype is f32
-            and n_accept.dtype is i32 and token.dtype is i32 and len(ns) == 2 and ns[0] == n and ns[1] == vocab
-            and tokens.shape == one and u.shape == one and n_accept.shape == ns[:1] and token.shape == ns[:1]
-            and first.dim() == 1 and tokens.get_device() == d and first.get_device() == d and u.get_device() == d
-            and noise.get_device() == d and n_accept.get_device() == d and token.get_device() == d
-            and tokens.is_contiguous() and first.is_contiguous() and u.is_contiguous() and noise.is_contiguous()
-            and n_accept.is_contiguous() and token.is_contiguous()):
+    t_ld, se = target.stride()
+    ns = noise.shape
+    if not ((se == 1 or vocab < 2) and target.get_device() == d and tokens.dtype is i32 and first.dtype is i32
+            and u.dtype is f32 and noise.dtype is f32 and n_accept.dtype is i32 and token.dtype is i32 and len(ns) == 2
+            and ns[0] == n and ns[1] == vocab and tokens.numel() == rows and u.numel() == rows
+            and n_accept.numel() == n and token.numel() == n and tokens.get_device() == d and first.get_device() == d
+            and u.get_device() == d and noise.get_device() == d and n_accept.get_device() == d
+            and token.get_device() == d and tokens.is_contiguous() and first.is_contiguous() and u.is_contiguous()
+            and noise.is_contiguous() and n_accept.is_contiguous() and token.is_contiguous()
+            and rows < 1 << 31 and vocab < 1 << 31):
+        _i32(rows, "rows"), _i32(vocab, "vocab")
+        _rows_of(target, "target", dt, (rows, vocab), d)
         for t, what, dtype, size in ((tokens, "tokens", i32, (rows,)), (first, "first", i32, (n + 1,)),
                                      (u, "u", f32, (rows,)), (noise, "noise", f32, (n, vocab)),
                                      (n_accept, "n_accept", i32, (n,)), (token, "token", i32, (n,))):
             _on_device(t, what, dtype, size, d)
-    _call_on(d, stream, load().pfop_verify_draft, kind, ta, t_ld, da, d_ld, rows, n, vocab, tokens.data_ptr(),
-             first.data_ptr(), u.data_ptr(), noise.data_ptr(), n_accept.data_ptr(), token.data_ptr(),
-             None if p_accept is None else _on_device(p_accept, "p_accept", f32, one, d), work.work_at,
-             work.work_bytes)
+    da, d_ld = None, 0
+    if draft is not None:
+        d_ld = _rows_of(draft, "draft", dt, (rows - n, vocab), d)
+        if rows > n:  # else there are no drafts
+            da = draft.data_ptr()
+    pa = None
+    if p_accept is not None:
+        pa = _on_device(p_accept, "p_accept", f32, ts[:1], d)
+    _call_on(d, stream, (_lib or load()).pfop_verify_draft, kind, target.data_ptr(), t_ld if rows > 1 else vocab, da,
+             d_ld, rows, n, vocab, tokens.data_ptr(), first.data_ptr(), u.data_ptr(), noise.data_ptr(),
+             n_accept.data_ptr(), token.data_ptr(), pa, work.work_at, work.work_bytes)
 
 
 # ---------------------------------------------------------------------------
