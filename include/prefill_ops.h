@@ -323,7 +323,7 @@ int pfop_logprobs(int32_t ltype, const void* logits_dev, int64_t ld, int32_t row
    run's last page holds behind the run's end is never used.
    work_dev as there, at least pfop_attention_paged_work_bytes of the runs.
    PF_E_ARG: as there (2^31 - 1024 cells in all); a page_size that is not as
-   above; a run past n_entries. */
+   above; a run past n_entries or past entry 2^31 - 1. */
 int pfop_attention_paged(const void* q_dev, const void* k_dev, const void* v_dev, int32_t n_pages, int32_t page_size,
                          int32_t Hq, int32_t Hkv, int32_t hd, const pfop_attn_run* runs, int32_t n_runs,
                          const int32_t* table_dev, int64_t n_entries, const uint64_t* mask_dev, int32_t mask_words,

@@ -628,7 +628,8 @@ extern "C" int pfop_attention_paged(const void* q_dev, const void* k_dev, const 
   const int page_log = pages_log(page_size);
   for (int r = 0; r < n_runs; ++r) {
     const int64_t end = static_cast<int64_t>(runs[r].pos0) + runs[r].n_rows;
-    if (runs[r].n_rows > 0 && runs[r].cell0 + ((end + page_size - 1) >> page_log) > n_entries)
+    // (the kernels count entries in 32 bits)
+    if (runs[r].n_rows > 0 && runs[r].cell0 + ((end + page_size - 1) >> page_log) > std::min<int64_t>(n_entries, INT32_MAX))
       return runs_fail(PF_E_ARG, "a run past the table's entries");
   }
   if (total == 0) return PF_OK;

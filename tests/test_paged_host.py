@@ -41,7 +41,8 @@ def test_page_counts(lib, pages, page):
 @pytest.mark.parametrize("run,entries", [
     ((4, 0, 0), 0), ((16, 0, 0), 0), ((17, 0, 0), 1), ((1, 16, 0), 1), ((4, 0, 5), 5), ((4, 0, 100), 100),
     ((1, 1600, 0), 100), ((4, 0, (1 << 31) - 1), 1 << 20), ((-1, 0, 0), 100), ((4, -1, 0), 100), ((4, 0, -1), 100),
-    ((4, (1 << 30) - 3, 0), 1 << 40), ((4, 0, 0), -1),
+    ((4, (1 << 30) - 3, 0), 1 << 40), ((4, 0, 0), -1), ((17, 0, (1 << 31) - 2), 1 << 40),
+    ((1, 16, (1 << 31) - 2), 1 << 33),
 ])
 def test_runs_outside_the_table(lib, run, entries):
     assert _paged(lib, [run], entries=entries) == PF_E_ARG
