@@ -18,8 +18,8 @@
 //
 // Bound by HBM from fp32 (8192 rows of 32 heads over 4 of 64: 22.4 us, 5.6 TB/s,
 // 84% of a measured copy); from bf16, with twice the elements a byte, by
-// instructions and their latency (16384 rows of 8 heads over 1 of 256: 35 us,
-// 4.8 TB/s; 240 instructions a step, 20 warps an SM).  One row: 2 us, 512 rows
+// instructions and their latency (16384 rows of 8 heads over 1 of 256: 34 us,
+// 4.9 TB/s; over 200 instructions a step, 20 warps an SM).  One row: 2 us, 512 rows
 // of queries 3.
 #include "../../include/prefill_ops.h"
 #include "common.cuh"
@@ -27,6 +27,7 @@
 
 #include <cmath>
 #include <string>
+#include <type_traits>
 
 namespace pf {
 
@@ -126,29 +127,40 @@ __global__ void __launch_bounds__(32 * NR_WARPS, NrVec<T>::CTAS) qk_norm_rope_ke
   // a step on its way
   struct Step {
     uint4 lo, hi;
-    int pos, slot, row, h;  // h: this lane's head (from `heads` on: none)
+    int pos, slot, row, step;
   };
+  const int lane_at = in_step * HD + i0;
+  // (a step of queries only, as most are, needs no choice between three tensors)
+  auto all_q = [&](int step) { return (step + 1) * HEADS <= a.Hq; };
   int row = static_cast<int>(g0 / a.steps), step = static_cast<int>(g0 - static_cast<int64_t>(row) * a.steps), ahead = left;
   auto fetch = [&](Step& s) {
     if (ahead <= 0) return;
     --ahead;
     const int64_t t = row;
     s.row = row;
-    s.h = step * HEADS + in_step;
+    s.step = step;
     s.pos = a.pos[t];
-    s.slot = a.Hkv > 0 ? a.slots[t] : -1;
-    if (s.h < heads) {
-      const T* src = s.h < a.Hq           ? static_cast<const T*>(a.q) + t * a.q_ld + s.h * HD
-                     : s.h < a.Hq + a.Hkv ? static_cast<const T*>(a.k) + t * a.k_ld + (s.h - a.Hq) * HD
-                                          : static_cast<const T*>(a.v) + t * a.v_ld + (s.h - a.Hq - a.Hkv) * HD;
-      s.lo = *reinterpret_cast<const uint4*>(src + i0);
-      s.hi = *reinterpret_cast<const uint4*>(src + HD / 2 + i0);
+    if (all_q(step)) {
+      const T* src = static_cast<const T*>(a.q) + t * a.q_ld + step * (HEADS * HD) + lane_at;
+      s.lo = *reinterpret_cast<const uint4*>(src);
+      s.hi = *reinterpret_cast<const uint4*>(src + HD / 2);
+    } else {
+      const int h = step * HEADS + in_step;
+      s.slot = a.Hkv > 0 ? a.slots[t] : -1;
+      if (h < heads) {
+        const T* src = h < a.Hq           ? static_cast<const T*>(a.q) + t * a.q_ld + h * HD
+                       : h < a.Hq + a.Hkv ? static_cast<const T*>(a.k) + t * a.k_ld + (h - a.Hq) * HD
+                                          : static_cast<const T*>(a.v) + t * a.v_ld + (h - a.Hq - a.Hkv) * HD;
+        s.lo = *reinterpret_cast<const uint4*>(src + i0);
+        s.hi = *reinterpret_cast<const uint4*>(src + HD / 2 + i0);
+      }
     }
     if (++step == a.steps) step = 0, ++row;
   };
   uint64_t cs[E / 2], sn[E / 2], ns[E / 2];  // cosines, sines, minus the sines
   int of_row = -1;                           // whose they are
-  auto work = [&](const Step& st) {
+  auto work = [&](const Step& st, auto only_q) {
+    constexpr bool ALL_Q = decltype(only_q)::value;
     if (st.row != of_row) {
       of_row = st.row;
       float c[E], n[E];
@@ -182,13 +194,14 @@ __global__ void __launch_bounds__(32 * NR_WARPS, NrVec<T>::CTAS) qk_norm_rope_ke
     float s = (s0.x + s0.y) + (s1.x + s1.y);
 #pragma unroll
     for (int o = LANES / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    const bool is_q = st.h < a.Hq, is_v = st.h >= a.Hq + a.Hkv;
+    const int h = st.step * HEADS + in_step;
+    const bool is_q = ALL_Q || h < a.Hq, is_v = !ALL_Q && h >= a.Hq + a.Hkv;
     __half* dst;
     if (is_q) {
-      dst = a.q_out + (static_cast<int64_t>(st.row) * a.Hq + st.h) * HD;
+      dst = a.q_out + (static_cast<int64_t>(st.row) * a.Hq + st.step * HEADS) * HD + lane_at;
     } else {
-      if (st.h >= heads || st.slot < 0 || st.slot >= a.n_cells) return;
-      dst = (is_v ? a.v_cache : a.k_cache) + (static_cast<int64_t>(st.slot) * a.Hkv + (st.h - a.Hq - (is_v ? a.Hkv : 0))) * HD;
+      if (h >= heads || st.slot < 0 || st.slot >= a.n_cells) return;
+      dst = (is_v ? a.v_cache : a.k_cache) + (static_cast<int64_t>(st.slot) * a.Hkv + (h - a.Hq - (is_v ? a.Hkv : 0))) * HD + i0;
     }
     if (!is_v) {
       if (is_q ? a.q_gain != nullptr : a.k_gain != nullptr) {
@@ -211,8 +224,8 @@ __global__ void __launch_bounds__(32 * NR_WARPS, NrVec<T>::CTAS) qk_norm_rope_ke
         x[2 * i] = lo.x, x[2 * i + 1] = lo.y, x[E + 2 * i] = hi.x, x[E + 2 * i + 1] = hi.y;
       }
     }
-    nr_store<E>(dst + i0, x);
-    nr_store<E>(dst + HD / 2 + i0, x + E);
+    nr_store<E>(dst, x);
+    nr_store<E>(dst + HD / 2, x + E);
   };
   Step st[NR_FLY] = {};
 #pragma unroll
@@ -227,7 +240,10 @@ __global__ void __launch_bounds__(32 * NR_WARPS, NrVec<T>::CTAS) qk_norm_rope_ke
     for (int i = 0; i < NR_FLY; ++i) {
       if (left <= 0) break;
       --left;
-      work(st[i]);
+      if (all_q(st[i].step))
+        work(st[i], std::true_type());
+      else
+        work(st[i], std::false_type());
       __syncwarp();
       fetch(st[i]);
     }
