@@ -557,6 +557,14 @@ def attention_paged(q, k, v, runs: AttnRuns, pages, out, mask=None, stream=None)
              pages.data_ptr(), pages.numel(), m, words, out.data_ptr(), runs.work_at, runs.work_bytes)
 
 
+def _vector(t, what: str, dtype, n: int, index: int) -> int:
+    """Address of a contiguous tensor of n elements (as _on_device, without
+    making a shape to compare with)."""
+    if t.dtype is dtype and t.numel() == n and t.get_device() == index and t.is_contiguous():
+        return t.data_ptr()
+    return _on_device(t, what, dtype, (n,), index)
+
+
 def _heads(t, what: str, dtype, index: int):
     """Refuse what is not [rows, heads, head_dim] with a row's heads dense (the
     rows may be parts of wider ones)."""
@@ -606,7 +614,7 @@ def qk_norm_rope(q, pos, q_out, k=None, v=None, slots=None, k_cache=None, v_cach
         _i32(rows, "rows")
     qga = kga = ka = va = sa = kca = vca = None
     if q_gain is not None:
-        qga = _on_device(q_gain, "q_gain", f32, qs[2:], d)
+        qga = _vector(q_gain, "q_gain", f32, hd, d)
     k_ld = v_ld = hkv = cells = 0
     if k is not None:
         if v is None or slots is None or k_cache is None or v_cache is None:
@@ -632,7 +640,7 @@ def qk_norm_rope(q, pos, q_out, k=None, v=None, slots=None, k_cache=None, v_cach
         ka, va, kca, vca, sa = k.data_ptr(), v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), slots.data_ptr()
         cells = cs[0] if len(cs) == 3 else cs[0] * cs[1]
         if k_gain is not None:
-            kga = _on_device(k_gain, "k_gain", f32, qs[2:], d)
+            kga = _vector(k_gain, "k_gain", f32, hd, d)
     elif v is not None or slots is not None or k_cache is not None or v_cache is not None:
         raise ValueError("v, slots, k_cache and v_cache go with k")
     if rows < 2:  # (the stride of one row says nothing)
@@ -712,7 +720,7 @@ def verify_draft(target, tokens, first, u, noise, n_accept, token, p_accept, wor
             da = draft.data_ptr()
     pa = None
     if p_accept is not None:
-        pa = _on_device(p_accept, "p_accept", f32, ts[:1], d)
+        pa = _vector(p_accept, "p_accept", f32, rows, d)
     _call_on(d, stream, (_lib or load()).pfop_verify_draft, kind, target.data_ptr(), t_ld if rows > 1 else vocab, da,
              d_ld, rows, n, vocab, tokens.data_ptr(), first.data_ptr(), u.data_ptr(), noise.data_ptr(),
              n_accept.data_ptr(), token.data_ptr(), pa, work.work_at, work.work_bytes)
