@@ -385,7 +385,6 @@ __global__ void __launch_bounds__(32 * FewCfg<HD, NT>::WARPS, FewCfg<HD, NT>::CT
     // the CTA's: a warp a column
     const bool whole = tile1 - tile0 == it.tiles;
     float* state = part + static_cast<int64_t>(2 * blockIdx.x + (tile0 == 0 ? 1 : 0)) * C::STATE;
-    constexpr int D = HD / 32;  // dims of a lane
     for (int col = warp; col < cols; col += C::WARPS) {
       float mm = -INFINITY, ll = 0.f, w[C::WARPS];
 #pragma unroll
@@ -396,36 +395,29 @@ __global__ void __launch_bounds__(32 * FewCfg<HD, NT>::WARPS, FewCfg<HD, NT>::CT
         w[i] = x.x == -INFINITY ? 0.f : ex2_approx((x.x - mm) * cexp);
         ll = __fmaf_rn(w[i], x.y, ll);
       }
-      float acc[D];
+      // the lane's dims: pairs, 64 apart
+      float2 acc[VC];
 #pragma unroll
-      for (int d = 0; d < D; ++d) acc[d] = 0.f;
+      for (int c = 0; c < VC; ++c) acc[c] = make_float2(0.f, 0.f);
 #pragma unroll
       for (int i = 0; i < C::WARPS; ++i)
 #pragma unroll
-        for (int d = 0; d < D; d += 2) {
-          const float2 x = *state_of(i, col, (D * lane + d) >> 1);
-          acc[d] = __fmaf_rn(w[i], x.x, acc[d]);
-          acc[d + 1] = __fmaf_rn(w[i], x.y, acc[d + 1]);
+        for (int c = 0; c < VC; ++c) {
+          const float2 x = *state_of(i, col, 32 * c + lane);
+          acc[c].x = __fmaf_rn(w[i], x.x, acc[c].x);
+          acc[c].y = __fmaf_rn(w[i], x.y, acc[c].y);
         }
       if (whole) {
         const float inv = ll == 0.f ? 0.f : __frcp_rn(ll);  // a row that sees nothing: zeros
-        __nv_bfloat16* dst = out + (static_cast<int64_t>(row0 + (col >> sh.log_g)) * sh.Hq + (kvh << sh.log_g) +
-                                    (col & ((1 << sh.log_g) - 1))) * HD + D * lane;
-        uint32_t h[D / 2];
+        __nv_bfloat162* dst = reinterpret_cast<__nv_bfloat162*>(
+            out + (static_cast<int64_t>(row0 + (col >> sh.log_g)) * sh.Hq + (kvh << sh.log_g) + (col & ((1 << sh.log_g) - 1))) * HD);
 #pragma unroll
-        for (int d = 0; d < D; d += 2) {
-          const __nv_bfloat162 x = __floats2bfloat162_rn(acc[d] * inv, acc[d + 1] * inv);
-          h[d / 2] = *reinterpret_cast<const uint32_t*>(&x);
-        }
-        if constexpr (D == 8)
-          *reinterpret_cast<uint4*>(dst) = make_uint4(h[0], h[1], h[2], h[3]);
-        else
-          *reinterpret_cast<uint32_t*>(dst) = h[0];
+        for (int c = 0; c < VC; ++c) dst[32 * c + lane] = __floats2bfloat162_rn(acc[c].x * inv, acc[c].y * inv);
       } else {
         if (lane == 0) reinterpret_cast<float2*>(state)[col] = make_float2(mm, ll);
-        float* dst = state + 2 * C::COLS + col * HD + D * lane;
+        float2* dst = reinterpret_cast<float2*>(state + 2 * C::COLS + col * HD);
 #pragma unroll
-        for (int d = 0; d < D; d += 2) *reinterpret_cast<float2*>(dst + d) = make_float2(acc[d], acc[d + 1]);
+        for (int c = 0; c < VC; ++c) dst[32 * c + lane] = acc[c];
       }
     }
     // on to the next item
