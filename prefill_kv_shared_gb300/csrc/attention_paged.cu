@@ -2,11 +2,11 @@
 //
 // Chunks of prompts and drafted trees run on the kernel of attention_runs.cuh
 // with its copies going through the page table.  Where no run has more MMA rows
-// (rows times the heads of a KV head) than the 8 or 16 columns of a small
-// matrix product, as in plain decoding, attn_few_kernel takes the call: there
+// (rows times the heads of a KV head) than the 8 to 24 columns of a few small
+// matrix products, as in plain decoding, attn_few_kernel takes the call: there
 // the keys and values are the work, and 128 or 256 rows of tcgen05 would be
 // mostly padding with a TMEM round trip and four hand-overs per chunk (64 rows
-// over 4096 keys: 56.5 us for 47.5 at 8 heads over 1 of 256, 66.5 for 44 at 32
+// over 4096 keys: 56.5 us for 45 at 8 heads over 1 of 256, 66.5 for 44 at 32
 // over 4 of 64).
 #include "attention_runs.cuh"
 
@@ -14,9 +14,8 @@ namespace pf {
 
 // CTAs of 8 warps, of an SM.  (hd 256 with two of 4 warps: 64 tokens over 1024
 // keys, 8 heads over 2, 28.2 us instead of 23.5, one over 32768 14.5 instead of
-// 13.6; one over 500 6.2 instead of 8.6, since the next call's CTAs then fit
-// beside the last one's.)
-constexpr int few_ctas(int hd) { return hd == 64 ? 2 : 1; }
+// 13.6.)
+constexpr int few_ctas(int hd, int cols) { return hd == 64 && cols <= 16 ? 2 : 1; }
 // Least tiles of a CTA, and how many more tiles than an even share an item may
 // have for a CTA of its own (beside an eighth of the share), which saves the
 // merge kernel, about 3 us.  (hd 64: 64 tokens over 500 to 1319 keys, 32 heads
@@ -24,14 +23,15 @@ constexpr int few_ctas(int hd) { return hd == 64 ? 2 : 1; }
 // 2, 12.0 with 24, 14.4 with 48.)
 constexpr int FEW_MIN = 16;
 constexpr int few_cost(int hd) { return hd == 64 ? 64 : 24; }
-// Most columns of a run.  (hd 64 with 40: 16 runs of 5 rows of 8 heads a KV head
-// over 2000 keys 22.3 us, 22.5 with the other kernel.)  More than 8 at hd 256
-// only where a CTA's share is long: what a segment costs grows with the columns
-// (64 runs of 3 rows of 8 heads over 2, 1024 keys: 27.7 us, 39.8 with the other
-// kernel; of 2 rows of 8 heads over 1 24.6 and 22.8; 8 of those over 3000 20.4
-// and 15.7).
-constexpr int FEW_COLS = 16;
-constexpr int few_share(int hd, int cols) { return hd == 256 && cols > 8 ? 32 : 0; }
+// Most columns of a run (as many as O's registers allow at hd 256).  (hd 64, 8
+// heads a KV head: 64 runs of 3 rows over 900 keys 23.7 us, 24.8 with the other
+// kernel, over 4096 56.3 and 68.9; with 40 columns 64 of 5 rows over 900 30.2
+// and 26.8, 16 over 2000 18.1 and 22.5.  hd 256, 8 heads over 2: 16 runs of 4
+// rows over 2000 keys 19.9 and 23.4, 64 over 4096 85.7 and 105.9.)
+constexpr int few_cols(int hd) { return hd == 64 ? 24 : 16; }
+constexpr int FEW_ROWS = 16;  // bits that are looked at of a row's mask
+constexpr int few_nt(int cols) { return (cols + 7) / 8; }
+static_assert(few_cols(64) <= 24 && few_cols(256) <= 16, "the kernels that are launched");
 
 // attn_few_kernel.  With C columns (row, head) of a run and KV head:
 //     S^T = K Q^T       (m16n8k16: 16 keys by 8 columns, hd deep)
@@ -57,10 +57,10 @@ constexpr int few_share(int hd, int cols) { return hd == 256 && cols > 8 ? 32 : 
 // by attn_few_merge_kernel.
 //
 // Bound by HBM for long contexts (64 sequences over 16384 keys: 6.8 TB/s for 8
-// heads over 1 of 256, 6.4 for 32 over 4 of 64; over 4096 47.5 and 44 us, 5.7
+// heads over 1 of 256, 6.4 for 32 over 4 of 64; over 4096 45 and 44 us, 6.0
 // and 6.1 TB/s), by the chain launch, page ids, first keys, states for short
 // ones (64 sequences over 500 to 1319 keys, 32 heads over 4 of 64, 60 MB: 13.1
-// us; one over 32768, 8 heads over 1 of 256: 13.6; one over 532: 4.4).
+// us; one over 32768, 8 heads over 1 of 256: 12.3; one over 532: 4.3).
 struct FewRun {
   int row0, n, pos0, entry0;
 };
@@ -76,7 +76,7 @@ struct FewShape {
 
 template <int HD, int NT>
 struct FewCfg {
-  static constexpr int WARPS = 8, CTAS = few_ctas(HD);
+  static constexpr int WARPS = 8, CTAS = few_ctas(HD, 8 * NT);
   static constexpr int COLS = 8 * NT;
   static constexpr int UNIT = HD * 32;                 // bytes of a tile's K or V
   static constexpr int SLOTS = 196608 / CTAS / (WARPS * UNIT);  // units that a warp has place for
@@ -218,15 +218,23 @@ __global__ void __launch_bounds__(32 * FewCfg<HD, NT>::WARPS, FewCfg<HD, NT>::CT
       asm volatile("cp.async.wait_group %0;" ::"n"(C::SLOTS - 1) : "memory");
       __syncwarp();
     };
-    for (int i = 0; i < C::SLOTS; ++i) send();
-    // Q, while the first keys are on their way
-    for (int i = tid; i < KC * NT * 32; i += 32 * C::WARPS) {
-      const int l = i & 31, nt = (i >> 5) % NT, c = (i >> 5) / NT, col = 8 * nt + (l >> 2);
-      sq[c][nt][l] = make_uint4(0u, 0u, 0u, 0u);
-      if (col < cols)
-        sq[c][nt][l] = __ldcg(reinterpret_cast<const uint4*>(
+    // Q, asked for before the page ids and the first keys
+    constexpr int QV = (KC * NT + C::WARPS - 1) / C::WARPS;
+    uint4 qv[QV];
+#pragma unroll
+    for (int j = 0; j < QV; ++j) {
+      const int i = tid + j * 32 * C::WARPS, l = i & 31, col = 8 * ((i >> 5) % NT) + (l >> 2), c = i / (32 * NT);
+      qv[j] = make_uint4(0u, 0u, 0u, 0u);
+      if (i < KC * NT * 32 && col < cols)
+        qv[j] = __ldcg(reinterpret_cast<const uint4*>(
             q + (static_cast<int64_t>(row0 + (col >> sh.log_g)) * sh.Hq + (kvh << sh.log_g) + (col & ((1 << sh.log_g) - 1))) * HD +
             32 * c + 8 * (l & 3)));
+    }
+    for (int i = 0; i < C::SLOTS; ++i) send();
+#pragma unroll
+    for (int j = 0; j < QV; ++j) {
+      const int i = tid + j * 32 * C::WARPS;
+      if (i < KC * NT * 32) sq[i / (32 * NT)][(i >> 5) % NT][i & 31] = qv[j];
     }
     // which of the run's own tokens the lane's columns see
     uint32_t seen[NT][2];
@@ -523,14 +531,14 @@ struct FewPlan {
 // single tokens were slower: 512 rows of 8 heads over 2 of 256 with 13 single
 // tokens and 10 drafted 65.7 us, 44.0 together.)
 static bool few_plan(FewPlan& p, const pfop_attn_run* runs, int n_runs, int Hq, int Hkv, int hd) {
-  const int group = Hq / Hkv, most = FEW_COLS;
+  const int group = Hq / Hkv, most = std::min(FEW_ROWS, few_cols(hd) / group);
   p.sh.Hq = Hq, p.sh.Hkv = Hkv, p.sh.log_g = 0;
   while ((1 << p.sh.log_g) < group) ++p.sh.log_g;
   int64_t tiles = 0, longest = 0;
   int row = 0, n = 0;
   for (int r = 0; r < n_runs; ++r) {
     if (runs[r].n_rows > 0) {
-      if (runs[r].n_rows > most / group) return false;
+      if (runs[r].n_rows > most) return false;
       const int64_t t = (static_cast<int64_t>(runs[r].pos0) + runs[r].n_rows + 15) / 16;
       p.ft.run[n] = FewRun{row, runs[r].n_rows, runs[r].pos0, runs[r].cell0};
       p.ft.at[n] = static_cast<int>(tiles);
@@ -545,9 +553,8 @@ static bool few_plan(FewPlan& p, const pfop_attn_run* runs, int n_runs, int Hq, 
   if (n == 0) return false;
   p.ft.n_runs = n;
   p.ft.at[n] = static_cast<int>(tiles);
-  const int nt = p.cols > 8 ? 2 : 1;
-  const int64_t slots = int64_t(sm_count()) * few_ctas(hd), items = int64_t(n) * Hkv;
-  if (tiles < few_share(hd, p.cols) * slots) return false;
+  const int nt = few_nt(p.cols);
+  const int64_t slots = int64_t(sm_count()) * few_ctas(hd, p.cols), items = int64_t(n) * Hkv;
   const int64_t share = std::max<int64_t>(FEW_MIN, (tiles + slots - 1) / slots);
   if (longest <= share + share / 8 + few_cost(hd) && items <= slots) {
     p.sh.share = 0;
@@ -644,7 +651,11 @@ extern "C" int pfop_attention_paged(const void* q_dev, const void* k_dev, const 
                     static_cast<const __half*>(v_dev), pages, mask_dev, mask_words, static_cast<__nv_bfloat16*>(out_dev),
                     reinterpret_cast<float*>(static_cast<uint8_t*>(work_dev) + WORK_HEADER), static_cast<cudaStream_t>(stream));
     };
-    const cudaError_t e = hd == 256 ? (few.cols > 8 ? go(launch_few<256, 2>) : go(launch_few<256, 1>)) : few.cols > 8 ? go(launch_few<64, 2>) : go(launch_few<64, 1>);
+    const int nt = few_nt(few.cols);
+    const cudaError_t e = hd == 256 ? (nt == 2 ? go(launch_few<256, 2>) : go(launch_few<256, 1>))
+                          : nt == 1 ? go(launch_few<64, 1>)
+                          : nt == 2 ? go(launch_few<64, 2>)
+                                    : go(launch_few<64, 3>);
     if (e != cudaSuccess) return runs_fail(PF_E_CUDA, std::string("paged attention launch: ") + cudaGetErrorString(e));
     return PF_OK;
   }

@@ -140,10 +140,11 @@ def test_trees(heads, page, rows, past, words):
 
 
 @pytest.mark.parametrize("heads,rows", [((8, 1, 256), 2), ((8, 2, 256), 4), ((8, 2, 256), 3), ((16, 1, 256), 1),
-                                        ((16, 16, 256), 16), ((32, 4, 64), 2), ((4, 4, 64), 16), ((16, 1, 64), 1)])
+                                        ((16, 16, 256), 16), ((32, 4, 64), 2), ((4, 4, 64), 16), ((16, 1, 64), 1),
+                                        ((32, 4, 64), 3), ((4, 1, 64), 6), ((4, 2, 64), 11), ((32, 4, 64), 5)])
 @pytest.mark.parametrize("page", [8, 64])
-def test_up_to_16_columns_over_much_work(heads, rows, page):
-    """Runs of up to 16 (row, head) pairs a KV head, as many keys as a large
+def test_up_to_24_columns_over_much_work(heads, rows, page):
+    """Runs of up to 24 (row, head) pairs a KV head (and of 40), as many keys as a large
     batch has: causal, and each row with its own mask."""
     n = 70 if heads[1] < 16 else 6
     c = Paged(heads, page, [rows] * n, [1100 + 37 * i for i in range(n)], 83 + rows)
