@@ -18,11 +18,12 @@ namespace pf {
 constexpr int few_ctas(int hd, int cols) { return hd == 64 && cols <= 16 ? 2 : 1; }
 // Least tiles of a CTA, and how many more tiles than an even share an item may
 // have for a CTA of its own (beside an eighth of the share), which saves the
-// merge kernel, about 3 us.  (hd 64: 64 tokens over 500 to 1319 keys, 32 heads
-// over 4, 13.4 us with 64, 18.1 with 32; hd 256: 16 over 1024 keys, 8 heads over
-// 2, 12.0 with 24, 14.4 with 48.)
-constexpr int FEW_MIN = 16;
-constexpr int few_cost(int hd) { return hd == 64 ? 64 : 24; }
+// merge kernel.  `little`: work for less than half of the CTAs.  (hd 64: 64
+// tokens over 500 to 1319 keys, 32 heads over 4, 13.4 us with 64, 18.1 with 32.
+// hd 256: 16 over 1024 keys, 8 heads over 2, 11.0 with 16 tiles and 24, 12.5
+// with 8; one over 500, 8 heads over 1, 5.5 with 8 and 12, 7.7 with 16 and 24.)
+constexpr int few_min(bool little) { return little ? 8 : 16; }
+constexpr int few_cost(int hd, bool little) { return hd == 64 ? 64 : little ? 12 : 24; }
 // Most columns of a run (as many as O's registers allow at hd 256).  (hd 64, 8
 // heads a KV head: 64 runs of 3 rows over 900 keys 23.7 us, 24.8 with the other
 // kernel, over 4096 56.3 and 68.9; with 40 columns 64 of 5 rows over 900 30.2
@@ -555,8 +556,9 @@ static bool few_plan(FewPlan& p, const pfop_attn_run* runs, int n_runs, int Hq, 
   p.ft.at[n] = static_cast<int>(tiles);
   const int nt = few_nt(p.cols);
   const int64_t slots = int64_t(sm_count()) * few_ctas(hd, p.cols), items = int64_t(n) * Hkv;
-  const int64_t share = std::max<int64_t>(FEW_MIN, (tiles + slots - 1) / slots);
-  if (longest <= share + share / 8 + few_cost(hd) && items <= slots) {
+  const bool little = 2 * tiles < few_min(false) * slots;
+  const int64_t share = std::max<int64_t>(few_min(little), (tiles + slots - 1) / slots);
+  if (longest <= share + share / 8 + few_cost(hd, little) && items <= slots) {
     p.sh.share = 0;
     p.ctas = static_cast<int>(items);
   } else {
