@@ -17,9 +17,9 @@
 // through its share of that row for the largest w / E.  (Sums by CTAs of a slice
 // of a row each: 42.6 us for the 256 chains below, 70.6 with short slices.)
 //
-// Figures: one chain of 4 over 32768 fp32 7.0 us, two launches' latency; 64
-// chains of 0 to 5 over 32000 fp32 15.5 us, latency of few chunks a warp; 256
-// of 4 over 32768 bf16 without a draft model, 117 MB, 26.6 us: the sums at 70%
+// Figures: one chain of 4 over 32768 fp32 6.7 us, two launches' latency; 64
+// chains of 0 to 5 over 32000 fp32 15.1 us, latency of few chunks a warp; 256
+// of 4 over 32768 bf16 without a draft model, 117 MB, 27 us: the sums at 70%
 // of a measured copy, then eight batches a thread of one CTA a sequence.
 #include "../../include/prefill_ops.h"
 #include "common.cuh"
@@ -54,6 +54,11 @@ struct VerifyArgs {
   // r chunks .. (r + 1) chunks - 1 of all; warp w takes per of them from w per on.
   float2* sums;
   int parts, chunks, per;
+  bool narrow;  // all chunks count to less than 2^31
+
+  __device__ __forceinline__ int64_t over(int64_t x, int d) const {
+    return narrow ? static_cast<int64_t>(static_cast<uint32_t>(x) / static_cast<uint32_t>(d)) : x / d;
+  }
 };
 
 __device__ __forceinline__ float vd_ex2(float x) {
@@ -204,7 +209,7 @@ __global__ void __launch_bounds__(32 * VD_SUM_WARPS, VD_SUM_CTAS) draft_sums_ker
   const int rows = a.rows + (a.draft ? a.rows - a.n_seq : 0);
   const int64_t c0 = w * a.per, c1 = min(c0 + a.per, static_cast<int64_t>(rows) * a.chunks);
   if (c0 >= c1) return;
-  int r = static_cast<int>(c0 / a.chunks), j = static_cast<int>(c0 % a.chunks);  // row and its chunk
+  int r = static_cast<int>(a.over(c0, a.chunks)), j = static_cast<int>(c0 - static_cast<int64_t>(r) * a.chunks);  // row and its chunk
   int left = static_cast<int>(c1 - c0);
   // a row: logits up to 16 bytes' alignment, vectors, the rest
   const T* x;
@@ -254,7 +259,7 @@ __global__ void __launch_bounds__(32 * VD_SUM_WARPS, VD_SUM_CTAS) draft_sums_ker
     if (ends) {
       if (last != -INFINITY) s.one(last);
       s.join_lanes<32>();
-      const int part = static_cast<int>(w - static_cast<int64_t>(row) * a.chunks / a.per);
+      const int part = static_cast<int>(w - a.over(static_cast<int64_t>(row) * a.chunks, a.per));
       if (lane == 0) a.sums[static_cast<int64_t>(row) * a.parts + part] = make_float2(s.m, s.z);
       s = VdSum();
     }
@@ -387,24 +392,28 @@ struct VdScan {
       hi2 *= 1.f + VD_OFF;
     }
   }
-  // the batch at v, with expf and a division
-  __device__ __forceinline__ void exact(int v, bool minus_q, bool but_d, unsigned long long& best) const {
+  // a batch's logits and noise, and its scores with expf and a division
+  struct Batch {
     float px[VD_VECS][4], qx[VD_VECS][4], e[VD_VECS][4];
+  };
+  __device__ __forceinline__ void fetch(int v, bool minus_q, Batch& f) const {
 #pragma unroll
     for (int g = 0; g < VD_VECS; ++g) {
-      logits(x, v + g * step, px[g]);
-      if (minus_q) logits(y, v + g * step, qx[g]);
-      noises(v + g * step, e[g]);
+      logits(x, v + g * step, f.px[g]);
+      if (minus_q) logits(y, v + g * step, f.qx[g]);
+      noises(v + g * step, f.e[g]);
     }
+  }
+  __device__ __forceinline__ void exact(int v, bool minus_q, bool but_d, const Batch& f, unsigned long long& best) const {
 #pragma unroll
     for (int g = 0; g < VD_VECS; ++g)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int id = 4 * (v + g * step) + i;
         // (a fused w would leave p's rounding where p and q are alike)
-        float w = __fmul_rn(expf(px[g][i] + nm_p), z_p);
-        if (minus_q) w = __fsub_rn(w, __fmul_rn(expf(qx[g][i] + nm_q), z_q));
-        const float score = w / e[g][i];
+        float w = __fmul_rn(expf(f.px[g][i] + nm_p), z_p);
+        if (minus_q) w = __fsub_rn(w, __fmul_rn(expf(f.qx[g][i] + nm_q), z_q));
+        const float score = w / f.e[g][i];
         if (w > 0.f && score >= 0.f && !(but_d && id == d)) best = max(best, vd_key(score, id));
       }
   }
@@ -439,6 +448,9 @@ __global__ void __launch_bounds__(VD_THREADS, 2) draft_pick_kernel(const VerifyA
   const int r0 = __ldcg(a.first + s), r1 = __ldcg(a.first + s + 1);
   const bool fits = r0 >= 0 && r1 > r0 && r1 <= a.rows && r1 - s - 1 <= a.rows - a.n_seq && r0 >= s;
   bool waited = false;
+  // of the first rows the outputs are written at the end: a cluster's barriers
+  // wait for what a thread has written (2000 clocks)
+  float first_share = 0.f;
   if (tid == 0) sh_at = -1, sh_kind = VD_NONE, sh_p = sh_q = make_float2(0.f, 0.f), sh_best[0] = sh_best[1] = 0ull;
   // VD_GROUP rows at a time; rank 0 also writes the shares of those behind the stop
   for (int base = r0; fits && base < r1; base += VD_GROUP) {
@@ -459,7 +471,7 @@ __global__ void __launch_bounds__(VD_THREADS, 2) draft_pick_kernel(const VerifyA
       VdSum z;
       if (is) {
         const int64_t row = of_draft ? a.rows + base + i - s : base + i;
-        const int n = static_cast<int>(((row + 1) * a.chunks - 1) / a.per - row * a.chunks / a.per) + 1;
+        const int n = static_cast<int>(a.over((row + 1) * a.chunks - 1, a.per) - a.over(row * a.chunks, a.per)) + 1;
         float2 p[VD_PARTS_MAX / 16];
 #pragma unroll
         for (int k = 0; k < VD_PARTS_MAX / 16; ++k) {
@@ -476,41 +488,41 @@ __global__ void __launch_bounds__(VD_THREADS, 2) draft_pick_kernel(const VerifyA
     __syncthreads();
     if (warp == 0) {
       float2 p = make_float2(0.f, 0.f), q = p;
+      float pd = 0.f, qd = 1.f;
       int k = VD_NONE;
       bool stop = false;
       if (r < r1) {
         p = sh_sums[0][lane];
-        float share = 0.f;
+        stop = true;
         if (!judges) {
-          stop = true;
           if (p.y > 0.f) k = VD_P;
         } else {
           if (draft) q = sh_sums[1][lane];
           if (p.y > 0.f && (!draft || q.y > 0.f)) {
             k = draft ? VD_P_MINUS_Q : VD_P_BUT_DRAFTED;
-            const float pd = known ? expf(xd - p.x) * p.y : 0.f;
-            const float qd = known && draft ? expf(yd - q.x) * q.y : 1.f;
-            share = pd >= qd ? (pd > 0.f ? 1.f : 0.f) : pd / qd;
+            pd = known ? expf(xd - p.x) * p.y : 0.f;
+            qd = known && draft ? expf(yd - q.x) * q.y : 1.f;
             stop = !(u * qd < pd);
-          } else {
-            share = __int_as_float(0x7fc00000);
-            stop = true;
           }
         }
-        if (rank == 0 && a.p_accept) a.p_accept[r] = share;
       }
       const unsigned stops = __ballot_sync(0xffffffffu, stop);
       if (stops && sh_at < 0 && lane == __ffs(stops) - 1) {
         sh_kind = k, sh_p = p, sh_q = q;
-        if (rank == 0) a.n_accept[s] = r - r0;
         sh_at = r;
+      }
+      if (rank == 0 && a.p_accept && r < r1) {
+        const float share = !judges ? 0.f : k == VD_NONE ? __int_as_float(0x7fc00000) : pd >= qd ? (pd > 0.f ? 1.f : 0.f) : pd / qd;
+        if (base == r0)
+          first_share = share;
+        else
+          a.p_accept[r] = share;
       }
     }
     __syncthreads();
     if (sh_at >= 0 && (rank != 0 || !a.p_accept)) break;
   }
   if (!waited) pdl_wait();
-  if (!fits && rank == 0 && tid == 0) a.n_accept[s] = -1;
   __syncthreads();
   const int at = sh_at;
   int kind = sh_kind;
@@ -530,6 +542,7 @@ __global__ void __launch_bounds__(VD_THREADS, 2) draft_pick_kernel(const VerifyA
       // hold the CTA's answer, all of the warp's where others may too.
       int v = scan.v0;
       bool all = true, mine = true;
+      typename VdScan<T, ALIGNED>::Batch f;
       if (round == 0) {
         float hi, hi2, lo;
         int batch;
@@ -537,6 +550,7 @@ __global__ void __launch_bounds__(VD_THREADS, 2) draft_pick_kernel(const VerifyA
           scan.template bounds<true>(e, hi, hi2, lo, batch);
         else
           scan.template bounds<false>(e, hi, hi2, lo, batch);
+        v = batch;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) lo = fmaxf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
         if (lane == 0) sh_lo[warp] = lo;
@@ -546,11 +560,17 @@ __global__ void __launch_bounds__(VD_THREADS, 2) draft_pick_kernel(const VerifyA
         for (int o = WARPS / 2; o > 0; o >>= 1) lo = fmaxf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
         all = __any_sync(0xffffffffu, hi2 > 0.f && hi2 >= lo);
         mine = all || (hi > 0.f && hi >= lo);
-        if (!all) v = batch;
       }
-      for (; mine && 4 * v < a.vocab; v += VD_VECS * scan.step) {
-        scan.exact(v, kind == VD_P_MINUS_Q, kind == VD_P_BUT_DRAFTED, best);
-        if (!all) break;
+      if (!all) {
+        if (mine) {
+          scan.fetch(v, kind == VD_P_MINUS_Q, f);
+          scan.exact(v, kind == VD_P_MINUS_Q, kind == VD_P_BUT_DRAFTED, f, best);
+        }
+      } else {
+        for (v = scan.v0; 4 * v < a.vocab; v += VD_VECS * scan.step) {
+          scan.fetch(v, kind == VD_P_MINUS_Q, f);
+          scan.exact(v, kind == VD_P_MINUS_Q, kind == VD_P_BUT_DRAFTED, f, best);
+        }
       }
       if (best) atomicMax(&sh_best[round], best);
     }
@@ -568,7 +588,12 @@ __global__ void __launch_bounds__(VD_THREADS, 2) draft_pick_kernel(const VerifyA
     if (best || kind == VD_NONE || kind == VD_P) break;
     kind = VD_P;
   }
-  if (rank == 0 && tid == 0) a.token[s] = best ? static_cast<int>(0xffffffffu - static_cast<uint32_t>(best)) : -1;
+  if (rank != 0 || warp != 0) return;
+  if (fits && a.p_accept && r0 + lane < r1) a.p_accept[r0 + lane] = first_share;
+  if (lane == 0) {
+    a.n_accept[s] = fits ? at - r0 : -1;
+    a.token[s] = best ? static_cast<int>(0xffffffffu - static_cast<uint32_t>(best)) : -1;
+  }
 }
 
 // logits of a chunk
@@ -589,6 +614,7 @@ static cudaError_t launch_verify(VerifyArgs a, cudaStream_t s) {
   const int64_t all = rows * a.chunks, warps = int64_t(sms) * VD_SUM_CTAS * VD_SUM_WARPS;
   a.per = static_cast<int>(std::max((all + warps - 1) / warps, (int64_t(a.chunks) + VD_PARTS_MAX - 2) / (VD_PARTS_MAX - 1)));
   a.parts = static_cast<int>(std::min<int64_t>(VD_PARTS_MAX, (a.chunks - 1) / a.per + 2));
+  a.narrow = all < int64_t(1) << 31;
   const int64_t used = (all + a.per - 1) / a.per;
   e = launch_k(draft_sums_kernel<T>, dim3(static_cast<unsigned>((used + VD_SUM_WARPS - 1) / VD_SUM_WARPS)),
                dim3(32 * VD_SUM_WARPS), 0, s, 1, a);
@@ -639,7 +665,7 @@ extern "C" int pfop_verify_draft(int32_t ltype, const void* target_dev, int64_t 
     return fail(PF_E_ARG, "misaligned buffer");
   if (work_bytes < pfop_verify_draft_work_bytes(rows, n_seq)) return fail(PF_E_ARG, "the scratch is smaller than these rows need");
   const VerifyArgs a{target_dev, draft_dev, target_ld, draft_ld, rows, n_seq, vocab, tokens_dev, first_dev, u_dev,
-                     noise_dev, n_accept_dev, token_dev, p_accept_dev, static_cast<float2*>(work_dev), 1, 1, 1};
+                     noise_dev, n_accept_dev, token_dev, p_accept_dev, static_cast<float2*>(work_dev), 1, 1, 1, false};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const cudaError_t e = ltype == PF_L_F32 ? launch_verify<float>(a, s) : launch_verify<__nv_bfloat16>(a, s);
   if (e != cudaSuccess) return fail(PF_E_CUDA, std::string("draft verification launch: ") + cudaGetErrorString(e));
