@@ -348,6 +348,35 @@ def test_one_scratch_for_changing_runs(heads):
         c.check()
 
 
+@pytest.mark.parametrize("heads", [(8, 1, 256), (32, 4, 64), (16, 16, 64)])
+@pytest.mark.parametrize("words", [2, 4])
+def test_wide_masks_over_few_rows(heads, words):
+    """A single word would do: the others are skipped, whatever they hold."""
+    c = Paged(heads, 16, [2, 1, 2, 0, 1], [700, 33, 0, 5, 2000], 89)
+    mask = np.concatenate([_random_tree(c.runs, 1, 3)] + [np.full((6, 1), 2**64 - 1, np.uint64)] * (words - 1), 1)
+    c.go(np.concatenate([mask, np.zeros((3, words), np.uint64)]))
+    c.plan.check()
+    c.check(mask)
+
+
+@pytest.mark.parametrize("page", [1024, 4096])
+@pytest.mark.parametrize("rows", [1, 70])
+def test_large_pages(page, rows):
+    c = Paged((8, 2, 256), page, [rows] * 3, [5000, 10, 4096], 97)
+    c.go()
+    c.plan.check()
+    c.check()
+
+
+def test_no_rows():
+    c = Paged((8, 2, 64), 16, [4], [10], 71)
+    for runs in ([], [(0, 0, 0), (0, 30, 5)]):
+        plan = binding.AttnRuns(runs, 8, 2, 64)
+        binding.attention_paged(c.q[:0], c.k, c.v, plan, c.table, c.out)
+        plan.check()
+    assert (c.out == 7).all()
+
+
 @pytest.mark.parametrize("heads", [(1024, 64, 64), (1024, 1024, 64), (64, 64, 256), (256, 16, 256)])
 def test_many_heads(heads):
     for rows, past in (([3, 20, 1], [40, 0, 300]), ([1, 1], [40, 2000])):

@@ -214,6 +214,16 @@ def test_recorded_and_on_another_stream():
     e.check()
 
 
+def test_no_rows_and_many_heads():
+    c = Step((8, 2, 64), 0, torch.float32, 47)
+    c.go()
+    assert (c.kc == 5).all()
+    for heads, dtype in (((1024, 8, 64), torch.float32), ((128, 1024, 64), torch.bfloat16), ((33, 7, 256), torch.bfloat16)):
+        c = Step(heads, 3, dtype, 53)
+        c.go()
+        c.check()
+
+
 def test_two_bases_in_turn():
     for _ in range(2):
         for base in (10000.0, 1e6):

@@ -374,6 +374,20 @@ def test_repeats_and_streams():
             assert torch.equal(a, b)
 
 
+def test_no_sequences():
+    c = Draft([1], 100, torch.float32, 79)
+    binding.verify_draft(c.target[:0], c.tokens[:0], c.first[:1], c.u[:0], c.noise[:0], c.n_accept[:0], c.token[:0],
+                         c.p_accept[:0], c.work, draft=c.draft[:0])
+    torch.cuda.synchronize()
+    assert c.n_accept.tolist() == [-9]
+
+
+def test_more_sequences_than_fit_the_gpu_at_once():
+    c = Draft([1, 0, 2] * 400, 700, torch.bfloat16, 83, near=0.5, scale=2.0)
+    c.go()
+    c.check()
+
+
 def test_wrapper_refuses_what_does_not_fit():
     c = Draft([2, 1], 100, torch.float32, 73)
 
