@@ -175,8 +175,9 @@ def load(path: str = LIB_PATH) -> C.CDLL:
         "pfop_attention_work_bytes": (i64, [i32, i32, i32, C.POINTER(AttnRun), i32]),
         "pfop_attention_status": (C.c_int, [vp, vp]),
         "pfop_logprobs": (C.c_int, [i32, vp, i64, i32, i32, vp, i32, vp, vp, vp, vp, vp]),
-        "pfop_attention_paged": (C.c_int, [vp, vp, vp, i32, i32, i32, i32, i32, C.POINTER(AttnRun), i32, vp, i64, vp,
-                                           i32, vp, vp, i64, vp]),
+        # (the runs by address: a POINTER argument takes ctypes a third of a microsecond)
+        "pfop_attention_paged": (C.c_int, [vp, vp, vp, i32, i32, i32, i32, i32, vp, i32, vp, i64, vp, i32, vp, vp, i64,
+                                           vp]),
         "pfop_attention_paged_work_bytes": (i64, [i32, i32, i32, C.POINTER(AttnRun), i32]),
         "pfop_attention_paged_status": (C.c_int, [vp, vp]),
         "pfop_qk_norm_rope": (C.c_int, [i32, vp, i64, vp, i64, vp, i64, i32, i32, i32, i32, vp, vp, vp, vp, f32, f32,
@@ -410,6 +411,7 @@ class AttnRuns:
         self.n_runs = len(runs)
         self.n_rows = sum(r[0] for r in runs)
         self.runs = (AttnRun * max(1, len(runs)))(*[AttnRun(*r) for r in runs])
+        self.runs_at = C.addressof(self.runs)
         with torch.cuda.device(device if device is not None else torch.cuda.current_device()):
             self.device = torch.cuda.current_device()
             need = int(self._lib.pfop_attention_paged_work_bytes(*self.shape, self.runs, self.n_runs))
@@ -540,7 +542,9 @@ def attention_paged(q, k, v, runs: AttnRuns, pages, out, mask=None, stream=None)
             and qs[0] >= runs.n_rows and qs[1] == hq and qs[2] == hd and ks[2] == hkv and ks[3] == hd
             and os[0] >= runs.n_rows and os[1] == hq and os[2] == hd and q.get_device() == d and k.get_device() == d
             and v.get_device() == d and out.get_device() == d and pages.get_device() == d and q.is_contiguous()
-            and k.is_contiguous() and v.is_contiguous() and out.is_contiguous() and pages.is_contiguous()):
+            and k.is_contiguous() and v.is_contiguous() and out.is_contiguous() and pages.is_contiguous()
+            and ks[0] < 1 << 31 and ks[1] < 1 << 31):
+        _i32(ks[0], "pages of k"), _i32(ks[1], "page size")
         _on_device(k, "k", f16, (*ks[:2], hkv, hd), d)
         _on_device(v, "v", f16, ks, d)
         _on_device(pages, "pages", _torch.int32, pages.shape, d)
@@ -553,7 +557,7 @@ def attention_paged(q, k, v, runs: AttnRuns, pages, out, mask=None, stream=None)
             raise ValueError("mask: needs at least a word a row")
         m = _on_device(mask, "mask", _torch.int64, mask.shape, d)
     _call_on(d, stream, runs._lib.pfop_attention_paged, q.data_ptr(), k.data_ptr(), v.data_ptr(),
-             _i32(ks[0], "pages of k"), _i32(ks[1], "page size"), hq, hkv, hd, runs.runs, runs.n_runs,
+             ks[0], ks[1], hq, hkv, hd, runs.runs_at, runs.n_runs,
              pages.data_ptr(), pages.numel(), m, words, out.data_ptr(), runs.work_at, runs.work_bytes)
 
 
