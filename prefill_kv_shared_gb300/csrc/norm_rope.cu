@@ -312,7 +312,8 @@ extern "C" int pfop_qk_norm_rope(int32_t itype, const void* q_dev, int64_t q_ld,
   if (Hkv > 0) wide |= at(k_dev) | at(v_dev) | at(kc_dev) | at(vc_dev), words |= at(slots_dev) | at(k_gain_dev);
   if ((wide & 15) || (words & 3)) return fail(PF_E_ARG, "a buffer that is not 16-byte (pos, slots, gains: 4-byte) aligned");
   const NormRopeArgs a{q_dev, k_dev, v_dev, q_ld, k_ld, v_ld, pos_dev, slots_dev, static_cast<__half*>(q_out_dev),
-                       static_cast<__half*>(kc_dev), static_cast<__half*>(vc_dev), n_cells, q_gain_dev, k_gain_dev,
+                       static_cast<__half*>(kc_dev), static_cast<__half*>(vc_dev), n_cells, q_gain_dev,
+                       Hkv > 0 ? k_gain_dev : nullptr,  // (the kernel reads what is not null)
                        rows, Hq, Hkv, eps, 1, 1};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const cudaError_t e =
