@@ -384,7 +384,10 @@ int pfop_qk_norm_rope(int32_t itype, const void* q_dev, int64_t q_ld, const void
    without a distribution (a NaN, +inf, or only -inf, in the target or the
    draft) ends its sequence there: p_accept NaN, token -1.  A sequence whose
    rows first_dev puts outside [0, rows), or of no rows, gives n_accept -1 and
-   token -1, and no p_accept is written for it.
+   token -1, and no p_accept is written for it; the others are not touched by
+   that.  With a draft_dev (it has rows - n_seq rows) so does one whose drafts'
+   rows r - s lie outside those: give every sequence a row there, since an
+   empty one has the draft rows of those behind it counted one lower.
    work_dev: device scratch, 256-byte aligned, at least
    pfop_verify_draft_work_bytes(rows, n_seq); it needs no clearing; calls that
    share it may not overlap on the GPU.  Recordable.

@@ -720,8 +720,8 @@ def verify_draft(target, tokens, first, u, noise, n_accept, token, p_accept, wor
     da, d_ld = None, 0
     if draft is not None:
         d_ld = _rows_of(draft, "draft", dt, (rows - n, vocab), d)
-        if rows > n:  # else there are no drafts
-            da = draft.data_ptr()
+        # (of no rows: an address that no row is read from, since none means drafts without a distribution)
+        da = draft.data_ptr() if rows > n else target.data_ptr()
     pa = None
     if p_accept is not None:
         pa = _vector(p_accept, "p_accept", f32, rows, d)

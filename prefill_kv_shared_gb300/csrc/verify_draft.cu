@@ -446,7 +446,9 @@ __global__ void __launch_bounds__(VD_THREADS, 2) draft_pick_kernel(const VerifyA
   float e[VD_VECS][4];
   scan.template noises_of<true>(scan.v0, e);
   const int r0 = __ldcg(a.first + s), r1 = __ldcg(a.first + s + 1);
-  const bool fits = r0 >= 0 && r1 > r0 && r1 <= a.rows && r1 - s - 1 <= a.rows - a.n_seq && r0 >= s;
+  // in the target's rows, and its drafts' rows r - s in the draft's
+  const bool fits = r0 >= 0 && r1 > r0 && r1 <= a.rows &&
+                    (!a.draft || r1 - r0 == 1 || (r0 >= s && r1 - s - 1 <= a.rows - a.n_seq));
   bool waited = false;
   // of the first rows the outputs are written at the end: a cluster's barriers
   // wait for what a thread has written (2000 clocks)

@@ -1,0 +1,80 @@
+"""Verification of drafted tokens in batches as a server forms them, with slots
+that have no rows.  Definition and margins as in test_gpu_verify_draft; here every
+decision has to have its margin (the seeds are such), so that all of them are
+compared."""
+import pytest
+
+from prefill_kv_shared_gb300 import binding
+from tests.gpu_util import need_gpu, torch
+from tests.test_gpu_verify_draft import CLOSE, Draft, _expected
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def lib():
+    need_gpu()
+    from prefill_kv_shared_gb300 import build
+    build.build()
+    return binding.load()
+
+
+def _slots(lens, vocab, seed, model, dtype=torch.float32):
+    """A batch whose sequence s has lens[s] rows, none where it is 0."""
+    c = Draft([n - 1 for n in lens if n], vocab, dtype, seed, model=model)
+    first = [0]
+    for n in lens:
+        first.append(first[-1] + n)
+    c.first = torch.tensor(first, dtype=torch.int32, device="cuda")
+    n = len(lens)
+    g = torch.Generator(device="cuda").manual_seed(seed + 1)
+    c.noise = torch.empty(n, vocab, device="cuda").exponential_(generator=g).clamp_min_(1e-30)
+    c.n_accept = torch.full((n,), -9, dtype=torch.int32, device="cuda")
+    c.token = torch.full((n,), -9, dtype=torch.int32, device="cuda")
+    c.work = binding.VerifyWork(first[-1], n)
+    if model:
+        c.draft = c.draft[:first[-1] - n]
+    return c
+
+
+def _check(c, refused=()):
+    """Every sequence against the definition; `refused` and empty ones give -1,
+    and no share is written for their rows."""
+    t, d = c.target.cpu(), None if c.draft is None else c.draft.cpu()
+    tok, first, u, noise = c.tokens.tolist(), c.first.tolist(), c.u.tolist(), c.noise.cpu()
+    share = c.p_accept.tolist()
+    for s, (r0, r1) in enumerate(zip(first, first[1:])):
+        got = (int(c.n_accept[s]), int(c.token[s]))
+        if r0 == r1 or s in refused:
+            assert got == (-1, -1), (s, got)
+            assert share[r0:r1] == [-9.0] * (r1 - r0)
+            continue
+        n, token, shares, sure = _expected(t, d, tok, first, u, noise, s)
+        assert sure, s
+        assert got == (n, token), (s, got, n, token)
+        for r, p in enumerate(shares, r0):
+            assert abs(share[r] - p) <= CLOSE * p + 1e-37, (s, r)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("lens", [[5, 0], [0, 5], [0, 0, 5, 0], [3, 0, 4, 0, 1, 0], [0, 1, 0, 1, 2, 0, 0, 6], [2, 0]])
+def test_slots_without_rows(lens, dtype):
+    """No draft model: each sequence for itself, whatever the others have."""
+    c = _slots(lens, 900, 5 + sum(lens), False, dtype)
+    c.go()
+    _check(c)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("lens,refused", [
+    ([4, 0, 1], (0,)), ([3, 0], (0,)), ([0, 3], (1,)), ([1, 0, 1, 3], (3,)), ([2, 3, 0, 0, 1], (1,)), ([0, 0, 5, 0], (2,)),
+    ([3, 1, 0, 2], ()), ([1, 0, 1, 1, 2, 1, 1], (4,)), ([2, 1, 1, 0, 1], (0,)), ([2, 0], (0,)), ([0, 2], (1,)),
+])
+def test_slots_without_rows_with_a_draft_model(lens, refused, dtype):
+    """Draft row r - s of row r: refused are the sequences of which that lies
+    outside the draft's rows, and no others; a sequence without drafts needs
+    none."""
+    c = _slots(lens, 900, 7 + sum(lens), True, dtype)
+    assert len(c.draft) == sum(lens) - len(lens)
+    c.go()
+    _check(c, refused)
