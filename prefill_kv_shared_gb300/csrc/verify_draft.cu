@@ -290,6 +290,10 @@ enum VdKind : int { VD_NONE = -1, VD_P = 0, VD_P_MINUS_Q = 1, VD_P_BUT_DRAFTED =
 // the reciprocal and the products by 2^-22: below 2^-16 each.
 constexpr float VD_OFF = 0x1p-15f;
 
+// How far the sums of rows that are alike may be apart: each has terms of
+// 2^-22, of an exponent rounded by 2^-24 of itself, and fp32 additions.
+constexpr float VD_ALIKE = 0x1p-17f;
+
 // The thread's share of the tokens: vectors of four, VD_VECS of them at once
 // (a batch), v0 + i step.  ALIGNED: a vector is one load in each array.
 template <class T, bool ALIGNED>
@@ -500,6 +504,11 @@ __global__ void __launch_bounds__(VD_THREADS, 2) draft_pick_kernel(const VerifyA
           if (p.y > 0.f) k = VD_P;
         } else {
           if (draft) q = sh_sums[1][lane];
+          // Rows that are alike up to a shift: their sums, formed in other
+          // orders, differ by their roundings, and those would be drawn from.
+          // Taken as equal, w is 0 throughout, as it is.  (Rows that are alike
+          // in sum and drafted token only get a q that is off by that much.)
+          if (draft && xd - p.x == yd - q.x && fabsf(q.y - p.y) <= VD_ALIKE * p.y) q.y = p.y;
           if (p.y > 0.f && (!draft || q.y > 0.f)) {
             k = draft ? VD_P_MINUS_Q : VD_P_BUT_DRAFTED;
             pd = known ? expf(xd - p.x) * p.y : 0.f;

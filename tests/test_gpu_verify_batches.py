@@ -1,7 +1,7 @@
 """Verification of drafted tokens in batches as a server forms them, with slots
-that have no rows.  Definition and margins as in test_gpu_verify_draft; here every
-decision has to have its margin (the seeds are such), so that all of them are
-compared."""
+that have no rows, and rows in which target and draft agree.  Definition and
+margins as in test_gpu_verify_draft; here every decision has to have its margin
+(the seeds are such), so that all of them are compared."""
 import pytest
 
 from prefill_kv_shared_gb300 import binding
@@ -78,3 +78,40 @@ def test_slots_without_rows_with_a_draft_model(lens, refused, dtype):
     assert len(c.draft) == sum(lens) - len(lens)
     c.go()
     _check(c, refused)
+
+
+@pytest.mark.parametrize("drafts,vocab", [([3], 32000), ([2] * 5, 50257), ([1, 0, 4], 131072), ([2] * 90, 9001)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("shift", [0.0, 0.5])
+def test_a_refused_draft_whose_rows_agree(drafts, vocab, dtype, shift):
+    """w is 0 throughout where p and q are alike (or a shift apart, which a
+    softmax does not see): drawn from p.  The two rows' sums are formed in
+    other orders, so that they differ by their roundings; u of 2 refuses all
+    the same."""
+    c = Draft(drafts, vocab, dtype, 11 + vocab, near=0.0)
+    if dtype is torch.float32:
+        c.target.copy_((c.target * 64).round() / 64)  # (so that the shift rounds nothing)
+        c.draft.copy_(c.target[[r for r in range(len(c.target)) if r + 1 not in c.first.tolist()]] + shift)
+    c.u[:] = 2.0
+    c.go()
+    p = torch.softmax(c.target.double(), -1)
+    first = c.first.tolist()
+    for s, r in enumerate(first[:-1]):
+        score = p[r] / c.noise[s].double()
+        best, second = score.topk(2).values.tolist()
+        assert best > second * (1 + 4 * CLOSE)
+        assert (int(c.n_accept[s]), int(c.token[s])) == (0, int(score.argmax())), s
+
+
+@pytest.mark.parametrize("vocab", [32000, 50257])
+@pytest.mark.parametrize("sequences", [1, 3, 60])
+def test_all_of_p_on_the_refused_draft(vocab, sequences):
+    """Without a draft model: nothing is left but the drafted token, which is p
+    itself; few sequences share their rows among several CTAs."""
+    c = Draft([2] * sequences, vocab, torch.float32, 13 + vocab, model=False)
+    c.target[:] = float("-inf")
+    c.target[torch.arange(3 * sequences - 1), c.tokens[1:].long()] = 1.0
+    c.target[3 * sequences - 1, 5] = 1.0
+    c.u[:] = 2.0
+    c.go()
+    assert (c.n_accept == 0).all() and torch.equal(c.token, c.tokens[1::3])
