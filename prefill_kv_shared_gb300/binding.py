@@ -654,15 +654,19 @@ def qk_norm_rope(q, pos, q_out, k=None, v=None, slots=None, k_cache=None, v_cach
 
 
 class VerifyWork:
-    """The scratch of verify_draft calls of `rows` rows of `n_seq` sequences
-    (or fewer rows, or more sequences).  Calls that share one must not overlap
-    on the GPU."""
+    """The scratch of verify_draft calls of up to `rows` rows, of any number of
+    sequences (n_seq of them: checked only).  Kept until the last call with it
+    is done; calls that share one must not overlap on the GPU.  It needs no
+    clearing, but like any tensor it is the current stream's: a call on another
+    stream comes after that one's work."""
 
     def __init__(self, rows: int, n_seq: int, device=None):
         torch = _t()
-        need = int(load().pfop_verify_draft_work_bytes(_i32(rows, "rows"), _i32(n_seq, "n_seq")))
+        lib, rows = load(), _i32(rows, "rows")
+        need = int(lib.pfop_verify_draft_work_bytes(rows, _i32(n_seq, "n_seq")))
         if need < 0:
             check_op(need)
+        need = int(lib.pfop_verify_draft_work_bytes(rows, 0))  # (fewer sequences, more draft rows)
         with torch.cuda.device(device if device is not None else torch.cuda.current_device()):
             self.device = torch.cuda.current_device()
             self.work = torch.empty(need, dtype=torch.uint8, device="cuda")

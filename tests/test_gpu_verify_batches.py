@@ -115,3 +115,17 @@ def test_all_of_p_on_the_refused_draft(vocab, sequences):
     c.u[:] = 2.0
     c.go()
     assert (c.n_accept == 0).all() and torch.equal(c.token, c.tokens[1::3])
+
+
+def test_a_scratch_serves_every_batch_of_no_more_rows():
+    """Fewer rows, and fewer or more sequences than it was made for."""
+    work = binding.VerifyWork(64, 64)
+    for drafts in ([0] * 64, [4] * 8, [31, 30], [63], [62], [0, 0, 0]):
+        c = Draft(drafts, 500, torch.float32, 19 + len(drafts))
+        c.work = work
+        c.go()
+        c.check()
+    c = Draft([64], 500, torch.float32, 23)
+    c.work = work
+    with pytest.raises(binding.PrefillError, match="scratch"):
+        c.go()
