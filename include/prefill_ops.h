@@ -235,7 +235,8 @@ typedef struct pfop_attn_run {
    positions 0 .. pos0 + i, scores scaled by 1 / sqrt(hd).  Cells of no run's
    positions 0 .. pos0 + n_rows - 1 are never used, whatever they hold; the
    runs' own cells must hold finite values (an infinity or NaN in V reaches
-   the rows of its run that do not see it too, but no other run's).  Scores
+   the rows of its run that do not see it too, but no other run's).  A NaN in a
+   row's query, or in a key that it sees, makes that row and head NaN.  Scores
    may be as large as finite q and k make them.  Probabilities are rounded to
    fp16 before P V, sums and states are fp32.  A row's bits depend on its
    position, its keys and the shapes of the call's runs, not on the other

@@ -477,7 +477,11 @@ __global__ void __launch_bounds__(32 * FEW_MERGE_WARPS)
     float mn = m;
 #pragma unroll
     for (int i = 0; i < FLY; ++i) mn = fmaxf(mn, ml[i].x);
-    if (mn == -INFINITY) continue;
+    if (mn == -INFINITY) {  // nothing seen, or no numbers: their sum is NaN and stays it
+#pragma unroll
+      for (int i = 0; i < FLY; ++i) l += ml[i].y;
+      continue;
+    }
     const float w = m == -INFINITY ? 0.f : ex2_approx((m - mn) * c);
     l *= w;
     acc.x *= w, acc.y *= w;

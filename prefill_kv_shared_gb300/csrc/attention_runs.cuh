@@ -1269,14 +1269,21 @@ __global__ void __launch_bounds__(256) attn_runs_merge_kernel(const RunsShape sh
     float mn = m;
 #pragma unroll
     for (int k = 0; k < FLY; ++k) mn = fmaxf(mn, ml[k].x);
-    if (mn == -INFINITY) continue;
+    if (mn == -INFINITY) {  // nothing seen, or no numbers: their sum is NaN and stays it
+#pragma unroll
+      for (int k = 0; k < FLY; ++k) l += ml[k].y;
+      continue;
+    }
     const float w = m == -INFINITY ? 0.f : ex2_approx((m - mn) * c);
     l *= w;
     acc.x *= w, acc.y *= w, acc.z *= w, acc.w *= w;
     m = mn;
 #pragma unroll
     for (int k = 0; k < FLY; ++k) {
-      if (ml[k].x == -INFINITY) continue;
+      if (ml[k].x == -INFINITY) {
+        l += ml[k].y;
+        continue;
+      }
       const float wk = ex2_approx((ml[k].x - m) * c);
       l = __fmaf_rn(wk, ml[k].y, l);
       acc.x = __fmaf_rn(wk, o[k].x, acc.x);
