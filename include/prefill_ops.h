@@ -393,7 +393,8 @@ int pfop_qk_norm_rope(int32_t itype, const void* q_dev, int64_t q_ld, const void
    pfop_verify_draft_work_bytes(rows, n_seq); it needs no clearing; calls that
    share it may not overlap on the GPU.  Recordable.
    PF_E_ARG: rows outside [0, 2^20], n_seq outside [0, rows]; vocab < 1 or
-   >= 2^30, a row stride below it; missing or misaligned buffers (logits to
+   >= 2^30, a row stride below it; 2^31 chunks of 2 KB of logits or more, target
+   and draft rows together (4 TB: a row's last chunk counts whole); missing or misaligned buffers (logits to
    their element, others to 4 bytes); a scratch too small. */
 int pfop_verify_draft(int32_t ltype, const void* target_dev, int64_t target_ld, const void* draft_dev,
                       int64_t draft_ld, int32_t rows, int32_t n_seq, int32_t vocab, const int32_t* tokens_dev,

@@ -53,11 +53,12 @@ struct VerifyArgs {
   // [target rows, then draft rows][parts]: maximum and sum.  Row r's chunks are
   // r chunks .. (r + 1) chunks - 1 of all; warp w takes per of them from w per on.
   float2* sums;
-  int parts, chunks, per;
-  bool narrow;  // all chunks count to less than 2^31
+  int parts, chunks, per;  // (all rows' chunks are below 2^31)
 
-  __device__ __forceinline__ int64_t over(int64_t x, int d) const {
-    return narrow ? static_cast<int64_t>(static_cast<uint32_t>(x) / static_cast<uint32_t>(d)) : x / d;
+  // the warp that has chunk j of row
+  __device__ __forceinline__ int warp_of(int row, int j) const {
+    return static_cast<int>((static_cast<uint32_t>(row) * static_cast<uint32_t>(chunks) + static_cast<uint32_t>(j)) /
+                            static_cast<uint32_t>(per));
   }
 };
 
@@ -205,11 +206,12 @@ __global__ void __launch_bounds__(32 * VD_SUM_WARPS, VD_SUM_CTAS) draft_sums_ker
   const int lane = threadIdx.x & 31;
   pdl_wait();
   pdl_launch();  // after the wait: what the next kernel reads ahead of its own is there
-  const int64_t w = static_cast<int64_t>(blockIdx.x) * VD_SUM_WARPS + (threadIdx.x >> 5);
+  const int w = static_cast<int>(blockIdx.x) * VD_SUM_WARPS + static_cast<int>(threadIdx.x >> 5);
   const int rows = a.rows + (a.draft ? a.rows - a.n_seq : 0);
-  const int64_t c0 = w * a.per, c1 = min(c0 + a.per, static_cast<int64_t>(rows) * a.chunks);
+  const int64_t c0 = static_cast<int64_t>(w) * a.per, c1 = min(c0 + a.per, static_cast<int64_t>(rows) * a.chunks);
   if (c0 >= c1) return;
-  int r = static_cast<int>(a.over(c0, a.chunks)), j = static_cast<int>(c0 - static_cast<int64_t>(r) * a.chunks);  // row and its chunk
+  int r = static_cast<int>(static_cast<uint32_t>(c0) / static_cast<uint32_t>(a.chunks));  // row and its chunk
+  int j = static_cast<int>(c0 - static_cast<int64_t>(r) * a.chunks);
   int left = static_cast<int>(c1 - c0);
   // a row: logits up to 16 bytes' alignment, vectors, the rest
   const T* x;
@@ -259,7 +261,7 @@ __global__ void __launch_bounds__(32 * VD_SUM_WARPS, VD_SUM_CTAS) draft_sums_ker
     if (ends) {
       if (last != -INFINITY) s.one(last);
       s.join_lanes<32>();
-      const int part = static_cast<int>(w - a.over(static_cast<int64_t>(row) * a.chunks, a.per));
+      const int part = w - a.warp_of(row, 0);
       if (lane == 0) a.sums[static_cast<int64_t>(row) * a.parts + part] = make_float2(s.m, s.z);
       s = VdSum();
     }
@@ -476,13 +478,14 @@ __global__ void __launch_bounds__(VD_THREADS, 2) draft_pick_kernel(const VerifyA
       const bool is = it < items && (!of_draft || base + i < r1 - 1);
       VdSum z;
       if (is) {
-        const int64_t row = of_draft ? a.rows + base + i - s : base + i;
-        const int n = static_cast<int>(a.over((row + 1) * a.chunks - 1, a.per) - a.over(row * a.chunks, a.per)) + 1;
+        const int row = of_draft ? a.rows + base + i - s : base + i;
+        const int n = a.warp_of(row, a.chunks - 1) - a.warp_of(row, 0) + 1;
+        const float2* sums = a.sums + static_cast<int64_t>(row) * a.parts;
         float2 p[VD_PARTS_MAX / 16];
 #pragma unroll
         for (int k = 0; k < VD_PARTS_MAX / 16; ++k) {
           p[k] = make_float2(-INFINITY, 0.f);
-          if ((lane & 15) + 16 * k < n) p[k] = __ldcg(a.sums + row * a.parts + (lane & 15) + 16 * k);
+          if ((lane & 15) + 16 * k < n) p[k] = __ldcg(sums + (lane & 15) + 16 * k);
         }
 #pragma unroll
         for (int k = 0; k < VD_PARTS_MAX / 16; ++k) z.join(p[k].x, p[k].y);
@@ -625,7 +628,6 @@ static cudaError_t launch_verify(VerifyArgs a, cudaStream_t s) {
   const int64_t all = rows * a.chunks, warps = int64_t(sms) * VD_SUM_CTAS * VD_SUM_WARPS;
   a.per = static_cast<int>(std::max((all + warps - 1) / warps, (int64_t(a.chunks) + VD_PARTS_MAX - 2) / (VD_PARTS_MAX - 1)));
   a.parts = static_cast<int>(std::min<int64_t>(VD_PARTS_MAX, (a.chunks - 1) / a.per + 2));
-  a.narrow = all < int64_t(1) << 31;
   const int64_t used = (all + a.per - 1) / a.per;
   e = launch_k(draft_sums_kernel<T>, dim3(static_cast<unsigned>((used + VD_SUM_WARPS - 1) / VD_SUM_WARPS)),
                dim3(32 * VD_SUM_WARPS), 0, s, 1, a);
@@ -668,6 +670,10 @@ extern "C" int pfop_verify_draft(int32_t ltype, const void* target_dev, int64_t 
   if (vocab < 1 || vocab >= (1 << 30) || target_ld < vocab || (draft_dev && draft_ld < vocab))
     return fail(PF_E_ARG, "vocab, or a row stride below it");
   if (n_seq == 0) return PF_OK;
+  // (the kernels count chunks in 32 bits)
+  const int chunk = ltype == PF_L_F32 ? vd_chunk<float>() : vd_chunk<__nv_bfloat16>();
+  if (((vocab - 1) / chunk + 1) * (rows + (draft_dev ? int64_t(rows) - n_seq : 0)) >= int64_t(1) << 31)
+    return fail(PF_E_ARG, "2^31 chunks of logits or more");
   if (!target_dev || !tokens_dev || !first_dev || !u_dev || !noise_dev || !n_accept_dev || !token_dev || !work_dev)
     return fail(PF_E_ARG, "null buffer");
   auto at = [](const void* p) { return reinterpret_cast<uintptr_t>(p); };
@@ -676,7 +682,7 @@ extern "C" int pfop_verify_draft(int32_t ltype, const void* target_dev, int64_t 
     return fail(PF_E_ARG, "misaligned buffer");
   if (work_bytes < pfop_verify_draft_work_bytes(rows, n_seq)) return fail(PF_E_ARG, "the scratch is smaller than these rows need");
   const VerifyArgs a{target_dev, draft_dev, target_ld, draft_ld, rows, n_seq, vocab, tokens_dev, first_dev, u_dev,
-                     noise_dev, n_accept_dev, token_dev, p_accept_dev, static_cast<float2*>(work_dev), 1, 1, 1, false};
+                     noise_dev, n_accept_dev, token_dev, p_accept_dev, static_cast<float2*>(work_dev), 1, 1, 1};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const cudaError_t e = ltype == PF_L_F32 ? launch_verify<float>(a, s) : launch_verify<__nv_bfloat16>(a, s);
   if (e != cudaSuccess) return fail(PF_E_CUDA, std::string("draft verification launch: ") + cudaGetErrorString(e));
