@@ -1,6 +1,6 @@
 """Attention over pages and over cells where queries or keys are no numbers:
 they reach the rows that they belong to, or that see them, and no others, however
-the call is cut."""
+the call is cut.  And rows that see no key at all."""
 import numpy as np
 import pytest
 
@@ -103,3 +103,26 @@ def test_queries_that_are_no_numbers_over_cells(heads, rows, past):
         assert torch.isnan(got[total - 2, 1]).all()
         got[total - 2, 1] = first[total - 2, 1]
         assert torch.equal(got, first)
+
+
+@pytest.mark.parametrize("heads", [(8, 1, 256), (8, 2, 256), (32, 4, 64), (4, 4, 64)])
+@pytest.mark.parametrize("words", [1, 3])
+@pytest.mark.parametrize("rows,past", [([1, 2, 1, 1], [0, 0, 7, 0]), ([1, 1, 2], [0, 40000, 0]), ([1] * 100, [0, 700] * 50)])
+def test_masks_that_leave_nothing_in_calls_of_few_rows(heads, words, rows, past):
+    """Rows without any key give zeros on the kernel of few rows too, in
+    items of their own and between parts of others; every second one sees
+    itself."""
+    c = Paged(heads, 16, rows, past, 109)
+    mask = np.zeros((c.total, words), np.uint64)
+    row, empty = 0, []
+    for i, (n, p) in enumerate(zip(rows, past)):
+        for t in range(n):
+            if i % 4 == 3:
+                mask[row, 0] = 1 << t
+            elif p == 0:
+                empty.append(row)
+            row += 1
+    c.go(np.concatenate([mask, np.zeros((3, words), np.uint64)]))
+    c.plan.check()
+    c.check(mask)
+    assert empty and (c.out[empty] == 0).all()

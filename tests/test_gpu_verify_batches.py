@@ -129,3 +129,23 @@ def test_a_scratch_serves_every_batch_of_no_more_rows():
     c.work = work
     with pytest.raises(binding.PrefillError, match="scratch"):
         c.go()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("model", [True, False])
+@pytest.mark.parametrize("drafts,vocab", [([0], 7), ([1], 1000), ([4], 32000), ([33], 300), ([100], 5000), ([5, 0], 50257)])
+def test_few_sequences_all_compared(drafts, vocab, dtype, model):
+    """Ten batches of one or two sequences: nine in ten decisions have their
+    margin, and those are compared."""
+    sure_of = 0
+    for seed in range(10):
+        c = Draft(drafts, vocab, dtype, 1000 + seed, model=model, near=0.3)
+        c.go()
+        t, d = c.target.cpu(), None if c.draft is None else c.draft.cpu()
+        tok, first, u, noise = c.tokens.tolist(), c.first.tolist(), c.u.tolist(), c.noise.cpu()
+        for s in range(len(drafts)):
+            n, token, _, sure = _expected(t, d, tok, first, u, noise, s)
+            if sure:
+                assert (int(c.n_accept[s]), int(c.token[s])) == (n, token), (seed, s)
+                sure_of += 1
+    assert sure_of >= 9 * len(drafts)
