@@ -349,8 +349,10 @@ int pfop_attention_paged_status(void* work_dev, void* stream);
    V; two rows may not share a slot.  Hkv 0: queries only, as the KV-shared
    layers need them (k, v, slots, k_gain, kc, vc are not looked at).
    pos int32 device, any value (angles are exact to about 2^-24 of a turn
-   everywhere); gains fp32 device [hd].  Norms and rotations are fp32, rounded
-   to fp16 once.  q_out may not overlap its input.
+   everywhere); gains fp32 device [hd].  Norms and products are fp32, sines and
+   cosines good to about 2^-20: a turned value is off by less than 2^-19 of its
+   pair's |y[i]| + |y[i + hd/2]| before it is rounded to fp16, once.  q_out may not
+   overlap its input.
    PF_E_ARG: hd other than 64 or 256; rows outside [0, 2^24], n_head or
    n_head_kv above 1024; a row stride below the row's heads or no multiple of
    16 bytes; eps below 0, rope_base below 1, or not finite; missing buffers;
@@ -377,6 +379,10 @@ int pfop_qk_norm_rope(int32_t itype, const void* q_dev, int64_t q_ld, const void
      p where w is 0 throughout).
    With u uniform in [0, 1) and noise exponential (fp32 [n_seq][vocab],
    positive) the tokens are distributed as the target alone would give them.
+   Probabilities are fp32, good to 2^-17: what lies nearer to a border than that
+   (u q(d) and p(d), or two scores, whose p - q is good to 2^-17 of p) may fall to
+   either side.  Where the two rows are the
+   same, or a shift apart that fp32 does not round, w is 0.
    Logits: ltype PF_L_F32 or PF_L_BF16, row strides target_ld, draft_ld, values
    of -inf allowed (probability 0).  Outputs: n_accept[s] (int32), token[s]
    (int32) and, where p_accept_dev is not NULL, for each row that judges a draft
@@ -394,8 +400,9 @@ int pfop_qk_norm_rope(int32_t itype, const void* q_dev, int64_t q_ld, const void
    share it may not overlap on the GPU.  Recordable.
    PF_E_ARG: rows outside [0, 2^20], n_seq outside [0, rows]; vocab < 1 or
    >= 2^30, a row stride below it; 2^31 chunks of 2 KB of logits or more, target
-   and draft rows together (4 TB: a row's last chunk counts whole); missing or misaligned buffers (logits to
-   their element, others to 4 bytes); a scratch too small. */
+   and draft rows together (4 TB: a row's last chunk counts whole); missing or
+   misaligned buffers (logits to their element, others to 4 bytes); a scratch too
+   small. */
 int pfop_verify_draft(int32_t ltype, const void* target_dev, int64_t target_ld, const void* draft_dev,
                       int64_t draft_ld, int32_t rows, int32_t n_seq, int32_t vocab, const int32_t* tokens_dev,
                       const int32_t* first_dev, const float* u_dev, const float* noise_dev, int32_t* n_accept_dev,

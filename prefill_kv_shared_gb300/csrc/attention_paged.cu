@@ -18,8 +18,11 @@ namespace pf {
 constexpr int few_ctas(int hd, int cols) { return hd == 64 && cols <= 16 ? 2 : 1; }
 // Least tiles of a CTA, and how many more tiles than an even share an item may
 // have for a CTA of its own (beside an eighth of the share), which saves the
-// merge kernel.  `little`: work for less than half of the CTAs.  (hd 64: 64
-// tokens over 500 to 1319 keys, 32 heads over 4, 13.4 us with 64, 18.1 with 32.
+// merge kernel.  `little`: work for less than half of the CTAs.  (hd 64, 32 heads
+// over 4, cost of 64 and of 32: 64 tokens over 100 to 1300 keys at random 12.1 and
+// 15.4 us, 32 over 1000 9.2 and 10.9, 8 over 800 5.5 and 6.1, one over 1000 5.8 and
+// 6.1; one long among short ones, 1200 keys and 63 of 300 8.9 and 9.2, 32 of 400
+// 7.1 and 7.9, but 1500 and 63 of 500 10.8 and 10.6; 48 is between them.
 // hd 256: 16 over 1024 keys, 8 heads over 2, 11.0 with 16 tiles and 24, 12.5
 // with 8; one over 500, 8 heads over 1, 5.5 with 8 and 12, 7.7 with 16 and 24.)
 constexpr int few_min(bool little) { return little ? 8 : 16; }
@@ -49,7 +52,10 @@ static_assert(few_cols(64) <= 24 && few_cols(256) <= 16, "the kernels that are l
 //
 // The online softmax keeps a reference per column that follows the maximum by
 // steps of more than 2^8 (P within fp16), so that most tiles need a vote and no
-// shuffles.  Sums and O are fp32, P fp16.
+// shuffles.  Sums and O are fp32.  P is fp16, what the matrix instruction takes
+// beside V: 2^-11 of a p of 2^-14 and more, 2^-25 in all below, where a key counts
+// in the sum but at the end no more in O (to be seen only where one key outweighs
+// all others, its v is small, and there are more than some 2^16 of them).
 //
 // Work: the items (run, KV head), counted in tiles of 16 keys, lie end to end
 // and every CTA takes the same number of tiles; or a CTA takes an item where
@@ -532,9 +538,15 @@ struct FewPlan {
 };
 
 // Which calls: no run of more columns than the kernel takes, and so few tiles
-// that they can be counted.  (Taken apart from longer runs in the same call,
-// single tokens were slower: 512 rows of 8 heads over 2 of 256 with 13 single
-// tokens and 10 drafted 65.7 us, 44.0 together.)
+// that they can be counted.  One longer run takes the whole call to the other
+// kernel: the two kernels one after the other leave SMs idle twice, which costs
+// more unless the tokens are most of the work.  (Together and apart, us: 8 heads
+// over 2 of 256, 512 rows behind 3584 with 13 tokens over 1000 keys 33.9 and
+// 40.1, 64 behind 500 with 16 over 1000 19.4 and 27.1, 2048 with 63 over 2000 72.9
+// and 76.1, but 64 rows with 64 tokens over 4096 105.3 and 92.8; 32 heads over 4 of
+// 64, 64 behind 500 with 16 over 1000 12.0 and 17.2, but 2048 with 63 over 2000 81.0
+// and 70.8, 64 with 64 over 4096 69.0 and 50.5.  A program with such a batch makes
+// two calls.)
 static bool few_plan(FewPlan& p, const pfop_attn_run* runs, int n_runs, int Hq, int Hkv, int hd) {
   const int group = Hq / Hkv, most = std::min(FEW_ROWS, few_cols(hd) / group);
   p.sh.Hq = Hq, p.sh.Hkv = Hkv, p.sh.log_g = 0;
