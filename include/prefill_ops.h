@@ -381,8 +381,8 @@ int pfop_qk_norm_rope(int32_t itype, const void* q_dev, int64_t q_ld, const void
    positive) the tokens are distributed as the target alone would give them.
    Probabilities are fp32, good to 2^-17: what lies nearer to a border than that
    (u q(d) and p(d), or two scores, whose p - q is good to 2^-17 of p) may fall to
-   either side.  Where the two rows are the
-   same, or a shift apart that fp32 does not round, w is 0.
+   either side.  Where the two rows are the same, or a shift apart that fp32 does
+   not round, w is 0.
    Logits: ltype PF_L_F32 or PF_L_BF16, row strides target_ld, draft_ld, values
    of -inf allowed (probability 0).  Outputs: n_accept[s] (int32), token[s]
    (int32) and, where p_accept_dev is not NULL, for each row that judges a draft
